@@ -22,6 +22,8 @@ import torch
 __all__ = ["gdr2_fwd", "gdr2_bwd", "gdr2_step", "gdr2_fwd_logits", "gdr2_bwd_logits", "gdr2_step_logits",
            "gdr2_fwd_seg", "gdr2_bwd_seg", "gdr2_fwd_noalloc", "gdr2_fwd_workspace_bytes",
            "gdr2_bwd_workspace_bytes", "gdr2_seg_workspace_bytes", "gdr2_strerror", "gdr2_version", "GDR2Function",
+           "gdr2_scalar_fwd", "gdr2_scalar_bwd", "gdr2_scalar_step", "gdr2_scalar_workspace_bytes",
+           "GDR2ScalarFunction", "gdr2_attn_step", "gdr2_attn_workspace_bytes", "gdr2_kv_append",
            "library_path", "load_library"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,7 +35,9 @@ DTYPE_F32, DTYPE_BF16 = 0, 1
 _DT = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16}
 EXPORTED = ["gdr2_fwd", "gdr2_bwd", "gdr2_step", "gdr2_fwd_logits", "gdr2_bwd_logits", "gdr2_step_logits",
             "gdr2_fwd_seg", "gdr2_bwd_seg", "gdr2_fwd_noalloc", "gdr2_fwd_workspace_bytes",
-            "gdr2_bwd_workspace_bytes", "gdr2_seg_workspace_bytes", "gdr2_strerror", "gdr2_version"]
+            "gdr2_bwd_workspace_bytes", "gdr2_seg_workspace_bytes", "gdr2_strerror", "gdr2_version",
+            "gdr2_scalar_fwd", "gdr2_scalar_bwd", "gdr2_scalar_step", "gdr2_scalar_workspace_bytes",
+            "gdr2_attn_step", "gdr2_attn_workspace_bytes", "gdr2_kv_append"]
 NOALLOC_SCRATCH_BYTES = 64 << 20  # GDR2_NOALLOC_SCRATCH_BYTES in include/gdr2.h
 
 
@@ -76,6 +80,20 @@ def load_library():
     lib.gdr2_bwd_seg.restype = i
     lib.gdr2_fwd_noalloc.argtypes = [vp] * 9 + [i] * 7 + [vp]
     lib.gdr2_fwd_noalloc.restype = i
+    lib.gdr2_scalar_workspace_bytes.argtypes = [i] * 9
+    lib.gdr2_scalar_workspace_bytes.restype = sz
+    lib.gdr2_scalar_fwd.argtypes = [vp] * 9 + [i] * 9 + [vp, sz, vp]
+    lib.gdr2_scalar_fwd.restype = i
+    lib.gdr2_scalar_bwd.argtypes = [vp] * 15 + [i] * 9 + [vp, sz, vp]
+    lib.gdr2_scalar_bwd.restype = i
+    lib.gdr2_scalar_step.argtypes = [vp] * 8 + [i] * 8 + [vp]
+    lib.gdr2_scalar_step.restype = i
+    lib.gdr2_attn_workspace_bytes.argtypes = [i] * 5
+    lib.gdr2_attn_workspace_bytes.restype = sz
+    lib.gdr2_attn_step.argtypes = [vp] * 8 + [i] * 7 + [f] + [i] * 2 + [vp, sz, vp]
+    lib.gdr2_attn_step.restype = i
+    lib.gdr2_kv_append.argtypes = [vp] * 8 + [i] * 8 + [vp]
+    lib.gdr2_kv_append.restype = i
     lib.gdr2_strerror.argtypes = [i]
     lib.gdr2_strerror.restype = ctypes.c_char_p
     lib.gdr2_version.argtypes = []
@@ -367,3 +385,302 @@ class GDR2Function(torch.autograd.Function):
                       None if dht is None else dht.contiguous(), ws=ws, fwd_saved=True,
                       need_dh0=ctx.has_h0)
         return gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["db"], gr["dw"], gr["dh0"]
+
+
+# ---------------------------------------------------------------- gated delta rule with scalar gates
+
+
+def gdr2_scalar_workspace_bytes(N, T, Hk, Hv, dk, dv, packed=False, dtype=DTYPE_BF16, save_for_bwd=False) -> int:
+    return int(load_library().gdr2_scalar_workspace_bytes(N, T, Hk, Hv, dk, dv, int(bool(packed)), dtype,
+                                                          int(bool(save_for_bwd))))
+
+
+def _adr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(q, *tensors):
+    for t in tensors:
+        if t is not None and t.device != q.device:
+            raise ValueError("all tensors must be on one device, got %s and %s" % (q.device, t.device))
+
+
+def _index(t, name, shape):
+    _check(t, name, torch.int32, shape)
+
+
+class _on:
+    """The tensors' device as the current one, and the stream to launch on: the given one, or that device's
+    current stream."""
+
+    def __init__(self, t, stream):
+        self.dev, self.stream = t.device.index, stream
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.dev)
+        s = self.stream if self.stream is not None else torch.cuda.current_stream()
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.prev)
+
+
+def _scalar_dims(q, k, v, g, beta, cu_seqlens):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and v must have four dimensions [B,T,H,d]")
+    B, T, Hk, dk = q.shape
+    Hv, dv = v.shape[2], v.shape[3]
+    if q.dtype not in _DT:
+        raise ValueError("unsupported dtype %s" % q.dtype)
+    _check(q, "q", q.dtype, (B, T, Hk, dk))
+    _check(k, "k", q.dtype, (B, T, Hk, dk))
+    _check(v, "v", q.dtype, (B, T, Hv, dv))
+    _check(g, "g", q.dtype, (B, T, Hv))
+    _check(beta, "beta", q.dtype, (B, T, Hv))
+    N = B
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("packed sequences need B = 1, got B = %d" % B)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must have one dimension and at least one entry")
+        _index(cu_seqlens, "cu_seqlens", cu_seqlens.shape)
+        N = cu_seqlens.numel() - 1
+    return B, T, Hk, Hv, dk, dv, N, _DT[q.dtype]
+
+
+def _scalar_workspace(N, T, Hk, Hv, dk, dv, packed, dt, train, device):
+    n = gdr2_scalar_workspace_bytes(N, T, Hk, Hv, dk, dv, packed, dt, train)
+    if n == 0 and N * T * Hv > 0:
+        raise ValueError("unsupported shape/dtype: N=%d T=%d Hk=%d Hv=%d dk=%d dv=%d" % (N, T, Hk, Hv, dk, dv))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def gdr2_scalar_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, save_for_bwd=False, ws=None, o=None,
+                    output_final_state=True, stream=None):
+    """Gated delta rule with scalar gates, chunkwise forward (see include/gdr2.h). q, k: [B,T,Hk,dk];
+    v: [B,T,Hv,dv]; g, beta: [B,T,Hv], all of one dtype (bf16 or fp32); Hv a multiple of Hk. h0:
+    [N,Hv,dk,dv] fp32 or None. cu_seqlens: None (N = B sequences of T tokens) or int32 [N+1] on the
+    device, the bounds of N sequences packed along T with B = 1. Returns (o, ht or None, ws); pass ``ws``
+    back to gdr2_scalar_bwd(..., fwd_saved=True) when save_for_bwd is set. Rows of ``o`` that belong to
+    no sequence are zero, or left as they were in an ``o`` that is passed in."""
+    lib = load_library()
+    B, T, Hk, Hv, dk, dv, N, dt = _scalar_dims(q, k, v, g, beta, cu_seqlens)
+    _check(h0, "h0", torch.float32, (N, Hv, dk, dv))
+    new = []
+    own_o = o is None
+    if own_o:
+        o = torch.empty(B, T, Hv, dv, dtype=q.dtype, device=q.device)
+        new.append(o)
+    _check(o, "o", q.dtype, (B, T, Hv, dv))
+    ht = torch.empty(N, Hv, dk, dv, dtype=torch.float32, device=q.device) if output_final_state else None
+    new.append(ht)
+    if ws is None:
+        ws = _scalar_workspace(N, T, Hk, Hv, dk, dv, cu_seqlens is not None, dt, save_for_bwd, q.device)
+        new.append(ws)
+    _same_device(q, k, v, g, beta, h0, cu_seqlens, o, ws)
+    if own_o and N == 0:
+        o.zero_()  # no sequence, and no kernel
+    _keep_for(stream, *new)
+    with _on(q, stream) as s:
+        st = lib.gdr2_scalar_fwd(_adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(cu_seqlens), _adr(o),
+                                 _adr(ht), N, T, Hk, Hv, dk, dv, dt, int(own_o), int(bool(save_for_bwd)), _adr(ws),
+                                 ws.numel(), s)
+    _raise(st, "gdr2_scalar_fwd")
+    return o, ht, ws
+
+
+def gdr2_scalar_bwd(q, k, v, g, beta, h0, dout, dht=None, *, cu_seqlens=None, ws=None, fwd_saved=False,
+                    need_dh0=True, grads=None, stream=None):
+    """Backward of gdr2_scalar_fwd. Returns a dict with dq, dk, dv, dg, dbeta (input dtype) and dh0 (fp32 or
+    None). With fwd_saved=True, ``ws`` must be the workspace of a gdr2_scalar_fwd(..., save_for_bwd=True)
+    call on the same inputs. ``grads``: a dict of the five token gradients to write into."""
+    lib = load_library()
+    B, T, Hk, Hv, dk, dv, N, dt = _scalar_dims(q, k, v, g, beta, cu_seqlens)
+    _check(dout, "dout", q.dtype, (B, T, Hv, dv))
+    _check(h0, "h0", torch.float32, (N, Hv, dk, dv))
+    _check(dht, "dht", torch.float32, (N, Hv, dk, dv))
+    new = []
+    names = (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))
+    own = grads is None
+    if own:
+        grads = {n: torch.empty_like(x) for n, x in names}
+        new += list(grads.values())
+    else:
+        grads = dict(grads)
+        for n, x in names:
+            if grads.get(n) is None:
+                raise ValueError("grads must hold %s" % n)
+            _check(grads[n], n, q.dtype, tuple(x.shape))
+    grads["dh0"] = torch.empty(N, Hv, dk, dv, dtype=torch.float32, device=q.device) if need_dh0 else None
+    new.append(grads["dh0"])
+    if ws is None:
+        if fwd_saved:
+            raise ValueError("fwd_saved=True needs the forward's workspace")
+        ws = _scalar_workspace(N, T, Hk, Hv, dk, dv, cu_seqlens is not None, dt, True, q.device)
+        new.append(ws)
+    _same_device(q, k, v, g, beta, h0, dout, dht, cu_seqlens, ws, *grads.values())
+    if own and N == 0:
+        for n, _ in names:
+            grads[n].zero_()
+    _keep_for(stream, *new)
+    with _on(q, stream) as s:
+        st = lib.gdr2_scalar_bwd(_adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(dout), _adr(dht),
+                                 _adr(cu_seqlens), _adr(grads["dq"]), _adr(grads["dk"]), _adr(grads["dv"]),
+                                 _adr(grads["dg"]), _adr(grads["dbeta"]), _adr(grads["dh0"]), N, T, Hk, Hv, dk, dv,
+                                 dt, int(own), int(bool(fwd_saved)), _adr(ws), ws.numel(), s)
+    _raise(st, "gdr2_scalar_bwd")
+    return grads
+
+
+def gdr2_scalar_step(q, k, v, g, beta, state, *, slots=None, o=None, stream=None):
+    """Recurrent step (decoding) of the gated delta rule with scalar gates: the T tokens of q, k
+    [B,T,Hk,dk], v [B,T,Hv,dv], g, beta [B,T,Hv], one at a time, on states in a pool: ``state``
+    [S,Hv,dk,dv] fp32, updated in place. Row b uses state slots[b] (int32 [B] on the device), or b
+    without slots. A slot outside the pool marks a padding row (o = 0, no state touched); rows with one
+    slot in common are taken in order, as one sequence. Returns o."""
+    lib = load_library()
+    B, T, Hk, Hv, dk, dv, _, dt = _scalar_dims(q, k, v, g, beta, None)
+    if state is None:
+        raise ValueError("state is required")
+    if state.dim() != 4:
+        raise ValueError("state must have four dimensions [S,Hv,dk,dv]")
+    _check(state, "state", torch.float32, (state.shape[0], Hv, dk, dv))
+    if slots is None:
+        if state.shape[0] < B:
+            raise ValueError("state holds %d states for %d rows" % (state.shape[0], B))
+    else:
+        _index(slots, "slots", (B,))
+    if o is None:
+        o = torch.empty(B, T, Hv, dv, dtype=q.dtype, device=q.device)
+        _keep_for(stream, o)
+    else:
+        _check(o, "o", q.dtype, (B, T, Hv, dv))
+    _same_device(q, k, v, g, beta, state, slots, o)
+    with _on(q, stream) as s:
+        st = lib.gdr2_scalar_step(_adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(state), _adr(slots), _adr(o), B,
+                                  T, Hk, Hv, dk, dv, state.shape[0], dt, s)
+    _raise(st, "gdr2_scalar_step")
+    return o
+
+
+class GDR2ScalarFunction(torch.autograd.Function):
+    """Autograd wrapper: forward saves the chunks' states in the workspace, backward reuses them."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, g, beta, h0=None, cu_seqlens=None):
+        o, ht, ws = gdr2_scalar_fwd(q, k, v, g, beta, h0, cu_seqlens=cu_seqlens, save_for_bwd=True)
+        ctx.save_for_backward(q, k, v, g, beta, h0, cu_seqlens, ws)
+        return o, ht
+
+    @staticmethod
+    def backward(ctx, do, dht):
+        q, k, v, g, beta, h0, cu_seqlens, ws = ctx.saved_tensors
+        gr = gdr2_scalar_bwd(q, k, v, g, beta, h0, do.contiguous(), None if dht is None else dht.contiguous(),
+                             cu_seqlens=cu_seqlens, ws=ws, fwd_saved=True, need_dh0=h0 is not None)
+        return gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["dbeta"], gr["dh0"], None
+
+
+# ---------------------------------------------------------------- attention over a paged cache
+
+
+def gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dtype=DTYPE_BF16) -> int:
+    return int(load_library().gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dtype))
+
+
+def _cache_dims(k_cache, v_cache, block_table, dtype, D):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape [pages,page_size,Hkv,D], got %s and %s"
+                         % (tuple(k_cache.shape), tuple(v_cache.shape)))
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not t.is_cuda:
+            raise ValueError("%s must be a GPU tensor" % n)
+        if t.dtype != dtype:
+            raise ValueError("%s must have dtype %s, got %s" % (n, dtype, t.dtype))
+        if t.shape[3] != D:
+            raise ValueError("%s must have %d channels, got %d" % (n, D, t.shape[3]))
+        if t.stride(3) != 1:
+            raise ValueError("the channels of %s must be contiguous" % n)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have two dimensions [B,max_pages]")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    return (ctypes.c_longlong * 6)(ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+
+
+def gdr2_attn_step(q, k_cache, v_cache, block_table, lengths, *, scale=None, window=0, o=None, lse=None,
+                   return_lse=False, ws=None, stream=None):
+    """Attention of one new token a sequence over a paged key-value cache (see include/gdr2.h). q:
+    [B,Hq,D]; k_cache, v_cache: [pages,page_size,Hkv,D] with any strides but the last; block_table: int32
+    [B,max_pages]; lengths: int32 [B], tokens held with the new one. scale: D ** -0.5 unless given;
+    window: only the last ``window`` tokens (0: all). Returns o, or (o, lse) with return_lse or an
+    ``lse`` tensor (fp32 [B,Hq]). ``ws``: a uint8 workspace of gdr2_attn_workspace_bytes."""
+    lib = load_library()
+    if q.dim() != 3:
+        raise ValueError("q must have three dimensions [B,Hq,D]")
+    B, Hq, D = q.shape
+    if q.dtype not in _DT:
+        raise ValueError("unsupported dtype %s" % q.dtype)
+    dt = _DT[q.dtype]
+    _check(q, "q", q.dtype, (B, Hq, D))
+    strides = _cache_dims(k_cache, v_cache, block_table, q.dtype, D)
+    pages, page, Hkv = k_cache.shape[:3]
+    _index(block_table, "block_table", (B, block_table.shape[1]))
+    _index(lengths, "lengths", (B,))
+    new = []
+    if o is None:
+        o = torch.empty_like(q)
+        new.append(o)
+    else:
+        _check(o, "o", q.dtype, (B, Hq, D))
+    if lse is None:
+        if return_lse:
+            lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+            new.append(lse)
+    else:
+        _check(lse, "lse", torch.float32, (B, Hq))
+    if ws is None:
+        ws = torch.empty(gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dt), dtype=torch.uint8, device=q.device)
+        new.append(ws)
+    _same_device(q, k_cache, v_cache, block_table, lengths, o, lse, ws)
+    _keep_for(stream, *new)
+    with _on(q, stream) as s:
+        st = lib.gdr2_attn_step(_adr(q), _adr(k_cache), _adr(v_cache), strides, _adr(block_table), _adr(lengths),
+                                _adr(o), _adr(lse), B, Hq, Hkv, D, pages, page, block_table.shape[1],
+                                D ** -0.5 if scale is None else scale, window, dt, _adr(ws), ws.numel(), s)
+    _raise(st, "gdr2_attn_step")
+    return o if lse is None else (o, lse)
+
+
+def gdr2_kv_append(k, v, k_cache, v_cache, block_table, starts, *, cu_seqlens=None, stream=None):
+    """Writes the keys and values of new tokens, k and v [tokens,Hkv,D], into a paged cache (layout as
+    gdr2_attn_step) behind the starts[s] tokens (int32 [B]) that each sequence holds. cu_seqlens: int32
+    [B+1], the bounds of the sequences' tokens, or None for one token a sequence. Tokens without a place
+    in block_table are dropped."""
+    lib = load_library()
+    if k.dim() != 3:
+        raise ValueError("k must have three dimensions [tokens,Hkv,D]")
+    tokens, Hkv, D = k.shape
+    if k.dtype not in _DT:
+        raise ValueError("unsupported dtype %s" % k.dtype)
+    _check(k, "k", k.dtype, (tokens, Hkv, D))
+    _check(v, "v", k.dtype, (tokens, Hkv, D))
+    strides = _cache_dims(k_cache, v_cache, block_table, k.dtype, D)
+    if k_cache.shape[2] != Hkv:
+        raise ValueError("k_cache must have %d heads, got %d" % (Hkv, k_cache.shape[2]))
+    B = block_table.shape[0]
+    _index(block_table, "block_table", (B, block_table.shape[1]))
+    _index(starts, "starts", (B,))
+    if cu_seqlens is None:
+        if tokens != B:
+            raise ValueError("without cu_seqlens there is one token a sequence, got %d tokens for %d sequences"
+                             % (tokens, B))
+    else:
+        _index(cu_seqlens, "cu_seqlens", (B + 1,))
+    _same_device(k, v, k_cache, v_cache, block_table, starts, cu_seqlens)
+    with _on(k, stream) as s:
+        st = lib.gdr2_kv_append(_adr(k), _adr(v), _adr(k_cache), _adr(v_cache), strides, _adr(block_table),
+                                _adr(starts), _adr(cu_seqlens), B, tokens, Hkv, D, k_cache.shape[0], k_cache.shape[1],
+                                block_table.shape[1], _DT[k.dtype], s)
+    _raise(st, "gdr2_kv_append")

@@ -1,0 +1,148 @@
+// Gated delta rule with scalar gates: arguments, workspace layout and sequence maps shared by
+// the host launcher and the kernels (internal to libgdr2).
+//
+//     S_t = exp(g_t) (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   o_t = S_t^T q_t
+//
+// with one log-decay g and one write strength beta per token and value head. Inside a chunk of
+// 64 tokens with start state S, gam = running sum of g, D_ri = exp(gam_r - gam_i) (i <= r):
+//
+//     A = strict_lower(beta_r D_ri k_r.k_i)    T = (I + A)^-1    M = lower(D_ri q_r.k_i)
+//     X = beta (V - e^gam K S)    Delta = T X    O = e^gam Q S + M Delta
+//     S' = e^gamC S + K^T (tail Delta),   tail = exp(gamC - gam)
+//
+// The decay is one number per row, so it never enters an operand: the raw k, q, v rows (exact in
+// the operand type) feed the matrix cores as they are, and every decay factor multiplies an fp32
+// accumulator or a row of an intermediate.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gdr2_layout.hpp"
+
+namespace gdr2 {
+
+// Per (chunk slot, value head) arrays, id = slot * Hv + head, in the operand type unless said:
+//   T     : images (fimg) of T, [NS][64][64]: NS = 2 for bf16, a bf16 value and the bf16 value
+//           of what its rounding left over (together 16 bits of mantissa), 1 for fp32
+//   M     : image of M, [64][64]; training with bf16: also its remainder
+//   vec   : fp32 rows of 64: e^gam, beta, tail (all zero in padding rows), gam as a float and its
+//           remainder; element 320 is e^gamC
+//   training only, each a row of 16-column slices [D / 16][rows][16]:
+//   S, dS : chunk start state and end-state gradient, rows = key channels
+//   Delta, dY : rows = tokens
+struct ScLayout {
+    size_t t, m, vec, s, d;                              // element counts per id
+    size_t o_t, o_m, o_vec, o_s, o_ds, o_delta, o_dy;    // byte offsets
+    size_t infer_bytes, train_bytes;
+};
+
+constexpr int SC_E = 0, SC_BETA = 64, SC_TAIL = 128, SC_GHI = 192, SC_GLO = 256, SC_EC = 320, SC_VEC = 384;
+
+inline ScLayout sc_layout(long long ids, int DK, int DV, int esz, bool train) {
+    ScLayout L;
+    const size_t ns = esz == 2 ? 2 : 1;
+    L.t = ns * 64 * 64;
+    L.m = (train ? ns : 1) * 64 * 64;
+    L.vec = SC_VEC;
+    L.s = (size_t)DK * DV;
+    L.d = (size_t)64 * DV;
+    size_t off = 0;
+    auto take = [&](size_t elems, size_t el_bytes) {
+        const size_t o = off;
+        off += align256((size_t)ids * elems * el_bytes);
+        return o;
+    };
+    L.o_t = take(L.t, esz);
+    L.o_m = take(L.m, esz);
+    L.o_vec = take(L.vec, 4);
+    L.infer_bytes = off;
+    L.o_s = take(L.s, esz);
+    L.o_ds = take(L.s, esz);
+    L.o_delta = take(L.d, esz);
+    L.o_dy = take(L.d, esz);
+    L.train_bytes = off;
+    return L;
+}
+
+struct ScArgs {
+    const void *q, *k, *v, *g, *beta;  // [tokens][Hk][DK], [tokens][Hv][DV], [tokens][Hv]
+    const float* h0;                   // [N][Hv][DK][DV] or null
+    const void* dout;                  // [tokens][Hv][DV]
+    const float* dht;                  // [N][Hv][DK][DV] or null
+    void* o;                           // null: forward recompute inside the backward
+    float* ht;
+    void *dq, *dk, *dv, *dg, *dbeta;
+    float* dh0;
+    const int* cu;                     // packed: [N + 1] on the device, else null
+    char* ws;
+    ScLayout L;
+    int N, T;                          // sequences; tokens of each (packed: tokens in all)
+    int Hk, Hv, R;                     // R = Hv / Hk value heads share a key head
+    int DK, DV;
+    int slots;                         // chunk slots (at least one per chunk of every sequence)
+    int zero_rest;                     // packed: 1 sets the outputs' rows of no sequence to zero
+};
+
+// Sequence s: its first token row, token count and first chunk slot. Packed sequences take the
+// slots from start / 64 + s on: as many as they have chunks fit before the next sequence's first.
+// cu is data of the caller's that no host check can see, so its entries are held inside the
+// tensors here: whatever they are, rows stay below T and slots below `slots`.
+struct ScSeq {
+    long long tok0;
+    int len, nt, slot0;
+};
+__host__ __device__ __forceinline__ int sc_clamp(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
+__host__ __device__ __forceinline__ ScSeq sc_seq(const int* cu, int T, int s) {
+    ScSeq q;
+    if (cu) {
+        const int b = sc_clamp(cu[s], 0, T), e = sc_clamp(cu[s + 1], b, T);
+        q.tok0 = b;
+        q.len = e - b;
+        q.slot0 = b / 64 + s;
+    } else {
+        q.tok0 = (long long)s * T;
+        q.len = T;
+        q.slot0 = s * ((T + 63) / 64);
+    }
+    q.nt = (q.len + 63) / 64;
+    return q;
+}
+// The sequence whose chunk a slot holds (false: the slot is spare), c its chunk.
+__device__ __forceinline__ bool sc_slot(const int* cu, int T, int N, int slot, ScSeq& q, int& c) {
+    int s;
+    if (cu) {
+        int lo = 0, hi = N - 1;  // the last s with slot0(s) <= slot
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (sc_clamp(cu[mid], 0, T) / 64 + mid <= slot) lo = mid;
+            else hi = mid - 1;
+        }
+        s = lo;
+    } else {
+        s = slot / ((T + 63) / 64);
+    }
+    q = sc_seq(cu, T, s);
+    c = slot - q.slot0;
+    return c >= 0 && c < q.nt;
+}
+
+hipError_t launch_sc_fwd(const ScArgs& a, bool bf16, bool train, hipStream_t stream);
+hipError_t launch_sc_bwd(const ScArgs& a, bool bf16, hipStream_t stream);
+template <class OT, int DK, int DV>
+hipError_t launch_sc_fwd_chain_t(const ScArgs& a, bool train, hipStream_t stream);
+template <class OT, int DK, int DV>
+hipError_t launch_sc_bwd_chain_t(const ScArgs& a, hipStream_t stream);
+
+struct ScStepArgs {
+    const void *q, *k, *v, *g, *beta;  // [B][T][Hk][DK], [B][T][Hv][DV], [B][T][Hv]
+    float* state;                      // [states][Hv][DK][DV]
+    const int* slots;                  // [B] or null: row b's state is slots[b] (null: b)
+    void* o;
+    int B, T, Hk, Hv, R, states;
+    int DK, DV;
+    int nt_out;
+};
+hipError_t launch_sc_step(const ScStepArgs& a, bool bf16, hipStream_t stream);
+
+}  // namespace gdr2

@@ -1,0 +1,614 @@
+// Gated delta rule with scalar gates: the kernels that are parallel over chunks (see
+// gdr2_scalar.hpp for the equations). Forward: T = (I + A)^-1 and M of every chunk and value
+// head. Backward: the gradients, from the states and their gradients that the chains left.
+#include "gdr2_intra_common.hpp"
+#include "gdr2_scalar_device.hpp"
+
+namespace gdr2 {
+
+// gam = running sum of g over the chunk's rows (lane = row), in 64 bits: the decays are exponentials
+// of differences of gam, and in 32 bits a strong decay early in the chunk (gam of some thousands)
+// would cost a later weak one its digits.
+__device__ __forceinline__ double wave_scan(double x) {
+    const int l = lane_id();
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double y = __shfl_up(x, o);
+        if (l >= o) x += y;
+    }
+    return x;
+}
+
+// upper 16x16 block (R, I), I > R, number u = 0..5
+__device__ __forceinline__ void sc_upper_ri(int u, int& R, int& I) {
+    R = u < 3 ? 0 : (u < 5 ? 1 : 2);
+    I = u < 3 ? u + 1 : (u < 5 ? u - 1 : 3);
+}
+
+// D_ri = exp(gam_r - gam_i) from gam held as a float and its remainder
+template <class OT>
+__device__ __forceinline__ float decay(float rhi, float rlo, float ihi, float ilo) {
+    return exp_op<OT>((rhi - ihi) + (rlo - ilo));
+}
+
+// Inverse T of the unit lower-triangular I + A (A and T fp32 in LDS, 4 waves; the upper blocks of T
+// are zero already). Wave w solves diagonal block w by forward substitution, lane li for column li
+// (substitution, not a product of powers of A: those grow like binomials when keys repeat); then
+// T_RI = -T_RR sum_{K = I}^{R - 1} A_RK T_KI on fp32 MFMA, one level of blocks at a time.
+__device__ __forceinline__ void sc_inverse(const lds_char* sA, lds_char* sT) {
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const Lane ln = fresh_lane();
+    const int li = ln.li, lq = ln.lq;
+    auto A = [&](int r, int c) { return sA + swz<float, CH>(r, c) * 4; };
+    auto Tp = [&](int r, int c) { return sT + swz<float, CH>(r, c) * 4; };
+    {
+        // row r of the block: its chunk i4 / 4 sits at (4 wv + i4 / 4) ^ f(r), f(r) known here
+        const lds_char* base[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) base[j] = sA + 16 * wv * CH * 4 + ((4 * wv) ^ (4 * j)) * 16;
+        float x[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int f = swz_f<float, CH>(r);
+            float acc = r == li ? 1.f : 0.f;
+#pragma unroll
+            for (int i4 = 0; i4 < r; i4 += 4) {
+                const f32x4 row = lds_load<f32x4>(base[f >> 2] + r * CH * 4 + ((i4 / 4) ^ (f & 3)) * 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (i4 + i < r) acc -= row[i] * x[i4 + i];
+            }
+            x[r] = acc;
+        }
+        if (lq == 0) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) lds_store<float>(Tp(16 * wv + r, 16 * wv + li), x[r]);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int lev = 1; lev < NBLK; ++lev) {
+        if (wv < NBLK - lev) {
+            const int I = wv, R = wv + lev;
+            f32x4 z = {0.f, 0.f, 0.f, 0.f}, t = z;
+#pragma unroll
+            for (int k = 0; k < lev; ++k) {
+                float a4[4], b4[4];
+                lds_get4<float>(A(16 * R + li, 16 * (I + k) + 4 * lq), a4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) b4[e] = lds_load<float>(Tp(16 * (I + k) + 4 * lq + e, 16 * I + li));
+                mma_k16_f32(z, a4, b4);
+            }
+            float a4[4];
+            const float b4[4] = {z[0], z[1], z[2], z[3]};
+            lds_get4<float>(Tp(16 * R + li, 16 * R + 4 * lq), a4);
+            mma_k16_f32(t, a4, b4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds_store<float>(Tp(16 * R + 4 * lq + i, 16 * I + li), -t[i]);
+        }
+        __syncthreads();
+    }
+}
+
+// One workgroup of four waves per (chunk slot, key head): k k^T and q k^T once, on the raw rows,
+// then for each value head of the group A, its inverse and M with that head's decay and beta.
+// Bound by HBM traffic in the large (reads q and k, writes T, M and the row factors: 48 KB a chunk
+// and value head at d_k = 128 with Hk = Hv) and by the latency of the blocked inverse in the small.
+template <class OT, int DK, bool TRAIN>
+__global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
+    constexpr int KB = DK / 32, ES = sizeof(OT);
+    constexpr int TILE = CH * DK * ES, SQ = CH * CH * 4;
+    constexpr int BUF = 2 * TILE > 2 * SQ ? 2 * TILE : 2 * SQ;
+    __shared__ __align__(16) char smem_[BUF];
+    __shared__ __align__(16) char svec_[SC_VEC * 4];
+    lds_char* smem = (lds_char*)smem_;
+    lds_char* sV = (lds_char*)svec_;
+    poison_lds(smem, sizeof(smem_));
+    poison_lds(sV, sizeof(svec_));
+    poison_lds_done();
+    const int tid = threadIdx.x, l = tid & 63, li = l & 15, lq = l >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
+    if (a.cu && a.zero_rest && a.o) zero_rest_rows<OT>(a, slot, a.o, a.Hv, hk * a.R, a.R, a.DV);
+    ScSeq q;
+    int c;
+    if (!sc_slot(a.cu, a.T, a.N, slot, q, c)) return;
+    const long long row0 = q.tok0 + 64LL * c;
+    const int nvalid = min(CH, q.len - CH * c);
+    const size_t rsk = (size_t)a.Hk * DK;
+    lds_char* sK = smem;
+    lds_char* sQ = smem + TILE;
+    dma_rows<OT, DK, 4>((const OT*)a.k + row0 * rsk + (size_t)hk * DK, rsk, nvalid, sK, wv);
+    dma_rows<OT, DK, 4>((const OT*)a.q + row0 * rsk + (size_t)hk * DK, rsk, nvalid, sQ, wv);
+    zero_tail_rows<OT, DK, 256>(sK, nvalid);
+    zero_tail_rows<OT, DK, 256>(sQ, nvalid);
+    wait_vm<0>();
+    __syncthreads();
+    // block pairs p = wv, wv + 4, wv + 8 of the lower triangle, as transposed tiles: lane (li, lq)
+    // holds rows 16 R + li, columns 16 I + 4 lq + i
+    const LSwz<OT, DK> vK{sK}, vQ{sQ};
+    f32x4 kk[3], qk[3];
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+        const int p = wv + 4 * n;
+        kk[n] = qk[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (p < NPAIR) {
+            int R, I;
+            pair_ri(p, R, I);
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const auto fi = lfrag_rowk8<OT>(vK, 16 * I, 32 * kb);
+                mma(kk[n], fi, lfrag_rowk8<OT>(vK, 16 * R, 32 * kb));
+                mma(qk[n], fi, lfrag_rowk8<OT>(vQ, 16 * R, 32 * kb));
+            }
+        }
+    }
+    __syncthreads();  // the tiles are dead: A and T take their place
+    lds_char* sA = smem;
+    lds_char* sT = smem + SQ;
+    for (int idx = tid; idx < 6 * 64; idx += 256) {  // the upper blocks of T stay zero
+        int R, I;
+        sc_upper_ri(idx / 64, R, I);
+        const int e = idx % 64;
+        lds_store<f32x4>(sT + swz<float, CH>(16 * R + e / 4, 16 * I + 4 * (e % 4)) * 4, f32x4{});
+    }
+#pragma unroll 1
+    for (int hh = 0; hh < a.R; ++hh) {
+        const int h = hk * a.R + hh;
+        const size_t id = (size_t)slot * a.Hv + h;
+        if (wv == 0) {
+            const bool ok = l < nvalid;
+            const size_t at = (size_t)(row0 + l) * a.Hv + h;
+            const double gam = wave_scan(ok ? (double)to_f(((const OT*)a.g)[at]) : 0.0);
+            const double gc = __shfl(gam, 63);
+            const float hi = (float)gam, lo = (float)(gam - (double)hi);
+            const float v[6] = {ok ? exp_op<OT>(hi) * (1.f + lo) : 0.f, ok ? to_f(((const OT*)a.beta)[at]) : 0.f,
+                                ok ? exp_op<OT>((float)(gc - gam)) : 0.f, hi, lo, exp_op<OT>((float)gc)};
+            float* vec = (float*)(a.ws + a.L.o_vec) + id * a.L.vec;
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+                lds_store<float>(sV + (64 * i + l) * 4, v[i]);
+                vec[64 * i + l] = v[i];
+            }
+        }
+        __syncthreads();
+        OT* m = (OT*)(a.ws + a.L.o_m) + id * a.L.m;
+#pragma unroll
+        for (int n = 0; n < 3; ++n) {
+            const int p = wv + 4 * n;
+            if (p < NPAIR) {
+                int R, I;
+                pair_ri(p, R, I);
+                const int r = 16 * R + li, i0 = 16 * I + 4 * lq;
+                const float rhi = lds_load<float>(sV + (SC_GHI + r) * 4), rlo = lds_load<float>(sV + (SC_GLO + r) * 4);
+                const float beta = lds_load<float>(sV + (SC_BETA + r) * 4);
+                float ihi[4], ilo[4], av[4];
+                lds_get4<float>(sV + (SC_GHI + i0) * 4, ihi);
+                lds_get4<float>(sV + (SC_GLO + i0) * 4, ilo);
+                f32x4 mv;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // above the diagonal the exponent would be positive: there the product is dropped
+                    const float d = i0 + i <= r ? decay<OT>(rhi, rlo, ihi[i], ilo[i]) : 0.f;
+                    mv[i] = d == 0.f ? 0.f : d * qk[n][i];
+                    av[i] = i0 + i < r && d != 0.f ? beta * d * kk[n][i] : 0.f;
+                }
+                f32x4 a4 = {av[0], av[1], av[2], av[3]};
+                lds_store<f32x4>(sA + swz<float, CH>(r, i0) * 4, a4);
+                OT* mp = m + fimg<OT, CH>(r, i0);
+                if constexpr (ES == 2) {
+                    bf16x4 hi, lo;
+                    split4(mv, hi, lo);
+                    *(bf16x4*)mp = hi;
+                    if (TRAIN) *(bf16x4*)(mp + CH * CH) = lo;
+                } else {
+                    *(f32x4*)mp = mv;
+                }
+            }
+        }
+        for (int u = wv; u < 6; u += 4) {
+            int R, I;
+            sc_upper_ri(u, R, I);
+            OT* mp = m + fimg<OT, CH>(16 * R + li, 16 * I + 4 * lq);
+            const float z[4] = {0.f, 0.f, 0.f, 0.f};
+            st4(mp, z);
+            if (TRAIN && ES == 2) st4(mp + CH * CH, z);
+        }
+        __syncthreads();
+        sc_inverse(sA, sT);
+        // T out, a 16-byte piece of the image (8 bf16 or 4 fp32 columns of a row) at a time
+        OT* t = (OT*)(a.ws + a.L.o_t) + id * a.L.t;
+        constexpr int EPP = 16 / ES;
+        for (int idx = tid; idx < CH * CH / EPP; idx += 256) {
+            const int r = idx / (CH / EPP), c0 = EPP * (idx % (CH / EPP));
+            if constexpr (ES == 2) {
+                const f32x4 x0 = lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4);
+                const f32x4 x1 = lds_load<f32x4>(sT + swz<float, CH>(r, c0 + 4) * 4);
+                bf16x4 h0, l0, h1, l1;
+                split4(x0, h0, l0);
+                split4(x1, h1, l1);
+                OT* tp = t + fimg<OT, CH>(r, c0);
+                *(bf16x8*)tp = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
+                *(bf16x8*)(tp + CH * CH) = __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
+            } else {
+                *(f32x4*)(t + fimg<OT, CH>(r, c0)) = lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4);
+            }
+        }
+        __syncthreads();  // A, T and the row factors are free for the next head
+    }
+}
+
+// ============================================================================ gradients
+template <class OT, int DK, int DV>
+struct ScGradLds {
+    static constexpr int ES = sizeof(OT);
+    static constexpr int NW = DK / 16;               // waves, one 16-row tile of key channels each
+    static constexpr int SQ = CH * CH * ES;
+    static constexpr int K = 0;                      // raw k and q rows, swizzled
+    static constexpr int Q = K + CH * DK * ES;
+    static constexpr int DO = Q + CH * DK * ES;      // dO rows, swizzled
+    static constexpr int DEL = DO + CH * DV * ES;    // Delta, dY: slices [DV / 16][64][16]
+    static constexpr int DY = DEL + CH * DV * ES;
+    static constexpr int P = DO;                     // after the pair products: P, R / beta, R [64][64]
+    static constexpr int RP = P + SQ;
+    static constexpr int R = RP + SQ;
+    static_assert(3 * SQ <= 3 * CH * DV * ES, "P and R fit over dO, Delta and dY");
+    static constexpr int VEC = DY + CH * DV * ES;
+    static constexpr int ROWP = VEC + SC_VEC * 4;    // per block pair: row and column sums of N
+    static constexpr int COLP = ROWP + NPAIR * 16 * 4;
+    static constexpr int DOTS = COLP + NPAIR * 16 * 4;  // per wave and row: q.dq_s, k.dx_s, k.dk_s, k.G
+    static constexpr int DOTV = DOTS + 4 * NW * CH * 4; // per row: dY.v
+    static constexpr int SS = DOTV + CH * 4;            // per wave: <dS', S>
+    static constexpr int BYTES = SS + NW * 4;
+};
+
+// One workgroup per (chunk slot, key head), one wave per 16 key channels: the gradients of the
+// group's value heads one after another, dq and dk summed over them in fp32 registers (value heads
+// that share a key head need no second pass and no atomics). Per value head
+//   dq_s = e^gam S dO, dx_s = -e^gam S dY, dk_s = tail dS' Delta   (columns of S, dS': fragments
+//     straight from the workspace; dO, dY, Delta from LDS, which every wave reads whole)
+//   dM = lower(dO Delta^T), dA = -strict(dY Delta^T), q k^T, k k^T in 16x16 block pairs, from which
+//   P = D dM, R = beta D dA and N = P q.k + R k.k, the derivative of every D_ri times D_ri
+//   dq = dq_s + P K,  G = dx_s + (R / beta) K,  dk = P^T Q + R^T K + beta G + dk_s
+//   dv = beta dY,  dbeta = dY.v + k.G
+//   dg_t = sum_{r >= t} (row_r - col_r of N + q.dq_s + beta k.dx_s) + sum_{i < t} k.dk_s + e^gamC <dS', S>
+// The last line sums only terms that carry the decay across t: the diagonal of N, which does not
+// depend on the decay, is left out, so that a strong decay leaves a small dg and no cancellation.
+template <class OT, int DK, int DV>
+__global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
+    using LS = ScGradLds<OT, DK, DV>;
+    using FT = typename Frag<OT>::type;
+    constexpr int ES = sizeof(OT), NW = LS::NW, NTHR = 64 * NW, KB = DK / 32, VB = DV / 32;
+    constexpr int PPW = (NPAIR + NW - 1) / NW;  // block pairs of a wave
+    extern __shared__ __align__(16) char smem_[];
+    lds_char* sm = (lds_char*)smem_;
+    poison_lds(sm, LS::BYTES);
+    poison_lds_done();
+    const int tid = threadIdx.x, l = tid & 63, li = l & 15, lq = l >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
+    if (a.cu && a.zero_rest) {
+        zero_rest_rows<OT>(a, slot, a.dq, a.Hk, hk, 1, DK);
+        zero_rest_rows<OT>(a, slot, a.dk, a.Hk, hk, 1, DK);
+        zero_rest_rows<OT>(a, slot, a.dv, a.Hv, hk * a.R, a.R, DV);
+        zero_rest_rows<OT>(a, slot, a.dg, a.Hv, hk * a.R, a.R, 1);
+        zero_rest_rows<OT>(a, slot, a.dbeta, a.Hv, hk * a.R, a.R, 1);
+    }
+    ScSeq q;
+    int c;
+    if (!sc_slot(a.cu, a.T, a.N, slot, q, c)) return;
+    const long long row0 = q.tok0 + 64LL * c;
+    const int nvalid = min(CH, q.len - CH * c);
+    const size_t rsk = (size_t)a.Hk * DK, rsv = (size_t)a.Hv * DV;
+    const size_t k0 = row0 * rsk + (size_t)hk * DK;
+    const LSwz<OT, DK> vK{sm + LS::K}, vQ{sm + LS::Q};
+    const LSwz<OT, DV> vO{sm + LS::DO};
+    const LSlice<OT, CH> vDel{sm + LS::DEL}, vDy{sm + LS::DY};
+    const LSwz<OT, CH> vP{sm + LS::P}, vRp{sm + LS::RP}, vR{sm + LS::R};
+    dma_rows<OT, DK, NW>((const OT*)a.k + k0, rsk, nvalid, sm + LS::K, wv);
+    dma_rows<OT, DK, NW>((const OT*)a.q + k0, rsk, nvalid, sm + LS::Q, wv);
+    zero_tail_rows<OT, DK, NTHR>(sm + LS::K, nvalid);
+    zero_tail_rows<OT, DK, NTHR>(sm + LS::Q, nvalid);
+    f32x4 dq[4], dk[4];  // transposed tiles: keys 16 wv + 4 lq + i, tokens 16 t + li
+#pragma unroll
+    for (int t = 0; t < 4; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+#pragma unroll 1
+    for (int hh = 0; hh < a.R; ++hh) {
+        const int h = hk * a.R + hh;
+        const size_t id = (size_t)slot * a.Hv + h;
+        const size_t v0 = row0 * rsv + (size_t)h * DV;
+        const OT* gS = (const OT*)(a.ws + a.L.o_s) + id * a.L.s;
+        const OT* gdS = (const OT*)(a.ws + a.L.o_ds) + id * a.L.s;
+        if (hh) __syncthreads();  // the head before is done with LDS
+        dma_rows<OT, DV, NW>((const OT*)a.dout + v0, rsv, nvalid, sm + LS::DO, wv);
+        zero_tail_rows<OT, DV, NTHR>(sm + LS::DO, nvalid);
+        const char* gDel = a.ws + a.L.o_delta + id * a.L.d * ES;
+        const char* gDy = a.ws + a.L.o_dy + id * a.L.d * ES;
+        for (int n = wv; n < CH * DV * ES / 1024; n += NW) {
+            __builtin_amdgcn_global_load_lds(gDel + n * 1024 + l * 16, (lds_void*)(sm + LS::DEL + n * 1024), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds(gDy + n * 1024 + l * 16, (lds_void*)(sm + LS::DY + n * 1024), 16, 0, 0);
+        }
+        for (int i = tid; i < SC_VEC; i += NTHR)
+            lds_store<float>(sm + LS::VEC + i * 4, ((const float*)(a.ws + a.L.o_vec))[id * a.L.vec + i]);
+        FT fS[VB], fdS[VB];  // this wave's key rows of S and dS', K = value column
+#pragma unroll
+        for (int kb = 0; kb < VB; ++kb) {
+            fS[kb] = gfrag_slice<OT, DK>(gS, 16 * wv, kb);
+            fdS[kb] = gfrag_slice<OT, DK>(gdS, 16 * wv, kb);
+        }
+        wait_vm<0>();
+        __syncthreads();
+
+        // ---- the states' parts
+        Lane ln = fresh_lane();
+        float e[4], tail[4], beta[4];  // of tokens 16 t + li
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            e[t] = lds_load<float>(sm + LS::VEC + (SC_E + 16 * t + li) * 4);
+            tail[t] = lds_load<float>(sm + LS::VEC + (SC_TAIL + 16 * t + li) * 4);
+            beta[t] = lds_load<float>(sm + LS::VEC + (SC_BETA + 16 * t + li) * 4);
+        }
+        auto dot_rows = [&](const LSwz<OT, DK>& m, const f32x4& x, int t, int which) {
+            // sum over this wave's keys of m[token][key] x, tokens 16 t + li
+            float y[4];
+            lds_get4<OT>(m.p + m.off(16 * t + li, 16 * wv + 4 * lq), y);
+            float s = (y[0] * x[0] + y[1] * x[1]) + (y[2] * x[2] + y[3] * x[3]);
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (lq == 0) lds_store<float>(sm + LS::DOTS + ((which * NW + wv) * CH + 16 * t + li) * 4, s);
+        };
+        f32x4 G[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x, z = x;
+#pragma unroll
+            for (int kb = 0; kb < VB; ++kb) {
+                mma(x, fS[kb], frag_rows<OT>(ln, vO, 16 * t, 32 * kb));
+                mma(y, fS[kb], frag_rows<OT>(ln, vDy, 16 * t, 32 * kb));
+                mma(z, fdS[kb], frag_rows<OT>(ln, vDel, 16 * t, 32 * kb));
+            }
+            x = x * e[t];
+            G[t] = y * -e[t];
+            z = z * tail[t];
+            dq[t] += x;
+            dk[t] += z;
+            dot_rows(vQ, x, t, 0);
+            dot_rows(vK, G[t], t, 1);
+            dot_rows(vK, z, t, 2);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        {
+            float s = 0.f;
+#pragma unroll
+            for (int kb = 0; kb < VB; ++kb)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += to_f(fS[kb][i]) * to_f(fdS[kb][i]);
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
+            if (l == 0) lds_store<float>(sm + LS::SS + wv * 4, s);
+        }
+
+        // ---- dv = beta dY and dY.v, 16 bytes of a row a lane
+        {
+            constexpr int EPC = 16 / ES, LPR = DV / EPC;
+            typedef OT VT __attribute__((ext_vector_type(16 / ES)));
+#pragma unroll
+            for (int i = 0; i < CH * LPR / NTHR; ++i) {
+                const int u = tid + NTHR * i, r = u / LPR, col = EPC * (u % LPR);
+                const VT y = lds_load<VT>(vDy.p + vDy.off(r, col));
+                float s = 0.f;
+                if (r < nvalid) {
+                    const VT v = *(const VT*)((const OT*)a.v + v0 + r * rsv + col);
+                    const float b = lds_load<float>(sm + LS::VEC + (SC_BETA + r) * 4);
+                    VT d;
+#pragma unroll
+                    for (int j = 0; j < EPC; ++j) {
+                        s += to_f(y[j]) * to_f(v[j]);
+                        d[j] = to_ot<OT>(b * to_f(y[j]));
+                    }
+                    *(VT*)((OT*)a.dv + v0 + r * rsv + col) = d;
+                }
+#pragma unroll
+                for (int m = 1; m < LPR; m <<= 1) s += __shfl_xor(s, m);
+                if (u % LPR == 0) lds_store<float>(sm + LS::DOTV + r * 4, s);
+            }
+        }
+
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- block pairs (rows 16 R + li, columns 16 I + 4 lq + i)
+        f32x4 fP[PPW], fRp[PPW], fR[PPW];
+        ln = fresh_lane();
+#pragma unroll
+        for (int n = 0; n < PPW; ++n) {
+            const int p = wv + NW * n;
+            if (p < NPAIR) {
+                int R, I;
+                pair_ri(p, R, I);
+                f32x4 qk = {0.f, 0.f, 0.f, 0.f}, kk = qk, dm = qk, da = qk;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    const FT f = frag_rows<OT>(ln, vK, 16 * I, 32 * kb);
+                    mma(qk, f, frag_rows<OT>(ln, vQ, 16 * R, 32 * kb));
+                    mma(kk, f, frag_rows<OT>(ln, vK, 16 * R, 32 * kb));
+                }
+#pragma unroll
+                for (int kb = 0; kb < VB; ++kb) {
+                    const FT f = frag_rows<OT>(ln, vDel, 16 * I, 32 * kb);
+                    mma(dm, f, frag_rows<OT>(ln, vO, 16 * R, 32 * kb));
+                    mma(da, f, frag_rows<OT>(ln, vDy, 16 * R, 32 * kb));
+                }
+                const int r = 16 * R + li, i0 = 16 * I + 4 * lq;
+                const float rhi = lds_load<float>(sm + LS::VEC + (SC_GHI + r) * 4);
+                const float rlo = lds_load<float>(sm + LS::VEC + (SC_GLO + r) * 4);
+                const float br = lds_load<float>(sm + LS::VEC + (SC_BETA + r) * 4);
+                float ihi[4], ilo[4], nn[4];
+                lds_get4<float>(sm + LS::VEC + (SC_GHI + i0) * 4, ihi);
+                lds_get4<float>(sm + LS::VEC + (SC_GLO + i0) * 4, ilo);
+                float rows = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float d = i0 + i <= r ? decay<OT>(rhi, rlo, ihi[i], ilo[i]) : 0.f;
+                    const bool strict = i0 + i < r;
+                    fP[n][i] = d == 0.f ? 0.f : d * dm[i];
+                    fRp[n][i] = strict && d != 0.f ? -(d * da[i]) : 0.f;
+                    fR[n][i] = br * fRp[n][i];
+                    nn[i] = strict ? fP[n][i] * qk[i] + fR[n][i] * kk[i] : 0.f;
+                    rows += nn[i];
+                }
+                rows += __shfl_xor(rows, 16);
+                rows += __shfl_xor(rows, 32);
+                if (lq == 0) lds_store<float>(sm + LS::ROWP + (p * 16 + li) * 4, rows);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) nn[i] = row_sum16(nn[i]);
+                if (li == 0) lds_store<f32x4>(sm + LS::COLP + (p * 16 + 4 * lq) * 4, f32x4{nn[0], nn[1], nn[2], nn[3]});
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();  // dO, Delta and dY are dead: P and R take their place
+#pragma unroll
+        for (int n = 0; n < PPW; ++n) {
+            const int p = wv + NW * n;
+            if (p < NPAIR) {
+                int R, I;
+                pair_ri(p, R, I);
+                const int o = swz<OT, CH>(16 * R + li, 16 * I + 4 * lq) * ES;
+                const float x[4] = {fP[n][0], fP[n][1], fP[n][2], fP[n][3]};
+                const float y[4] = {fRp[n][0], fRp[n][1], fRp[n][2], fRp[n][3]};
+                const float z[4] = {fR[n][0], fR[n][1], fR[n][2], fR[n][3]};
+                lds_put4<OT>(sm + LS::P + o, x);
+                lds_put4<OT>(sm + LS::RP + o, y);
+                lds_put4<OT>(sm + LS::R + o, z);
+            }
+        }
+        for (int u = wv; u < 6; u += NW) {
+            int R, I;
+            sc_upper_ri(u, R, I);
+            const int o = swz<OT, CH>(16 * R + li, 16 * I + 4 * lq) * ES;
+            const float z[4] = {0.f, 0.f, 0.f, 0.f};
+            lds_put4<OT>(sm + LS::P + o, z);
+            lds_put4<OT>(sm + LS::RP + o, z);
+            lds_put4<OT>(sm + LS::R + o, z);
+        }
+        __syncthreads();
+
+        // ---- dq += P K, G += (R / beta) K, dk += P^T Q + R^T K + beta G
+        FT fK[2], fQ[2];
+        ln = fresh_lane();
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            fK[kb] = frag_cols<OT>(ln, vK, 16 * wv, 32 * kb);
+            fQ[kb] = frag_cols<OT>(ln, vQ, 16 * wv, 32 * kb);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+                if (kb == 0 || t >= 2) {  // rows of token tile t: columns up to it
+                    mma(dq[t], fK[kb], frag_rows<OT>(ln, vP, 16 * t, 32 * kb));
+                    mma(G[t], fK[kb], frag_rows<OT>(ln, vRp, 16 * t, 32 * kb));
+                }
+                if (kb == 1 || t < 2) {   // columns of token tile t: rows from it on
+                    mma(dk[t], fQ[kb], frag_cols<OT>(ln, vP, 16 * t, 32 * kb));
+                    mma(dk[t], fK[kb], frag_cols<OT>(ln, vR, 16 * t, 32 * kb));
+                }
+            }
+            dot_rows(vK, G[t], t, 3);
+            dk[t] += G[t] * beta[t];
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();
+        // ---- dbeta and dg (lane = row)
+        if (wv == 0) {
+            const int r = l;
+            float d[4] = {0.f, 0.f, 0.f, 0.f}, ss = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) d[j] += lds_load<float>(sm + LS::DOTS + ((j * NW + w) * CH + r) * 4);
+                ss += lds_load<float>(sm + LS::SS + w * 4);
+            }
+            const float b = lds_load<float>(sm + LS::VEC + (SC_BETA + r) * 4);
+            float x = d[0] + b * d[1];
+#pragma unroll
+            for (int o = 0; o < NBLK; ++o) {
+                if (o <= r / 16) x += lds_load<float>(sm + LS::ROWP + (pair_id(r / 16, o) * 16 + r % 16) * 4);
+                if (o >= r / 16) x -= lds_load<float>(sm + LS::COLP + (pair_id(o, r / 16) * 16 + r % 16) * 4);
+            }
+            // suffix sum of x, exclusive prefix sum of k.dk_s
+            float suf = x, pre = d[2];
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const float s = __shfl_down(suf, o), p = __shfl_up(pre, o);
+                if (l + o < 64) suf += s;
+                if (l >= o) pre += p;
+            }
+            pre = __shfl_up(pre, 1);
+            if (l == 0) pre = 0.f;
+            const float ec = lds_load<float>(sm + LS::VEC + SC_EC * 4);
+            if (r < nvalid) {
+                const size_t at = (size_t)(row0 + r) * a.Hv + h;
+                ((OT*)a.dbeta)[at] = to_ot<OT>(lds_load<float>(sm + LS::DOTV + r * 4) + d[3]);
+                ((OT*)a.dg)[at] = to_ot<OT>(suf + pre + ec * ss);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const int r = 16 * t + li;
+        if (r < nvalid) {
+            const float x[4] = {dq[t][0], dq[t][1], dq[t][2], dq[t][3]};
+            const float y[4] = {dk[t][0], dk[t][1], dk[t][2], dk[t][3]};
+            st4((OT*)a.dq + k0 + r * rsk + 16 * wv + 4 * lq, x);
+            st4((OT*)a.dk + k0 + r * rsk + 16 * wv + 4 * lq, y);
+        }
+    }
+}
+
+// ============================================================================ launchers
+template <class OT, int DK, int DV>
+static hipError_t launch_sc_fwd_t(const ScArgs& a, bool train, hipStream_t stream) {
+    const dim3 grid((unsigned)(a.slots * a.Hk));
+    if (train)
+        hipLaunchKernelGGL((k_sc_prep<OT, DK, true>), grid, dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_sc_prep<OT, DK, false>), grid, dim3(256), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return launch_sc_fwd_chain_t<OT, DK, DV>(a, train, stream);
+}
+template <class OT, int DK, int DV>
+static hipError_t launch_sc_bwd_t(const ScArgs& a, hipStream_t stream) {
+    hipError_t e = launch_sc_bwd_chain_t<OT, DK, DV>(a, stream);
+    if (e != hipSuccess) return e;
+    constexpr int lds = ScGradLds<OT, DK, DV>::BYTES;
+    e = hipFuncSetAttribute((const void*)k_sc_grad<OT, DK, DV>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_sc_grad<OT, DK, DV>), dim3((unsigned)(a.slots * a.Hk)), dim3(4 * DK), lds, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_sc_fwd(const ScArgs& a, bool bf16_, bool train, hipStream_t stream) {
+    if (bf16_) {
+        if (a.DK == 64 && a.DV == 64) return launch_sc_fwd_t<bf16, 64, 64>(a, train, stream);
+        if (a.DK == 64 && a.DV == 128) return launch_sc_fwd_t<bf16, 64, 128>(a, train, stream);
+        if (a.DK == 128 && a.DV == 64) return launch_sc_fwd_t<bf16, 128, 64>(a, train, stream);
+        if (a.DK == 128 && a.DV == 128) return launch_sc_fwd_t<bf16, 128, 128>(a, train, stream);
+    } else if (a.DK == 64 && a.DV == 64) {
+        return launch_sc_fwd_t<float, 64, 64>(a, train, stream);
+    }
+    return hipErrorInvalidValue;
+}
+hipError_t launch_sc_bwd(const ScArgs& a, bool bf16_, hipStream_t stream) {
+    if (bf16_) {
+        if (a.DK == 64 && a.DV == 64) return launch_sc_bwd_t<bf16, 64, 64>(a, stream);
+        if (a.DK == 64 && a.DV == 128) return launch_sc_bwd_t<bf16, 64, 128>(a, stream);
+        if (a.DK == 128 && a.DV == 64) return launch_sc_bwd_t<bf16, 128, 64>(a, stream);
+        if (a.DK == 128 && a.DV == 128) return launch_sc_bwd_t<bf16, 128, 128>(a, stream);
+    } else if (a.DK == 64 && a.DV == 64) {
+        return launch_sc_bwd_t<float, 64, 64>(a, stream);
+    }
+    return hipErrorInvalidValue;
+}
+
+}  // namespace gdr2

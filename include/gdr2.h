@@ -212,6 +212,100 @@ int gdr2_fwd_noalloc(const void* q, const void* k, const void* v, const void* g,
                      const float* h0, void* o, float* ht, int B, int T, int H, int dk, int dv, int chunk,
                      int dtype, void* stream);
 
+/* Gated delta rule with scalar gates: one log-decay g and one write strength beta per token and
+ * value head instead of a gate per channel,
+ *
+ *     S_t = exp(g_t) (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   o_t = S_t^T q_t,
+ *
+ * which is gdr2_fwd's recurrence with b = w = beta and g the same in every channel, at a third of its
+ * input bytes. Value heads may share key heads: Hv is a multiple of Hk, and value head h reads the
+ * queries and keys of head h / (Hv / Hk); their gradients are summed over the heads that share them.
+ *
+ * Layouts (contiguous, row-major, element type `dtype` unless said):
+ *   q, k and dq, dk_             : [tokens][Hk][dk]
+ *   v, o, dout and dv_           : [tokens][Hv][dv]
+ *   g, beta and dg, dbeta        : [tokens][Hv]
+ *   h0, ht, dht, dh0             : [N][Hv][dk][dv], always fp32
+ * Sequences: with cu_seqlens NULL, N sequences of T tokens each, one after another (tokens = N T).
+ * Else packed: T tokens in all, sequence s being the tokens cu_seqlens[s] .. cu_seqlens[s + 1] - 1;
+ * cu_seqlens is an int32 array of N + 1 non-decreasing entries in 0 .. T on the device, lengths may be
+ * zero (such a sequence passes its state through). Its entries are data that no check on the host can
+ * see: entries out of order or range give wrong results for the sequences concerned, but no access
+ * outside the tensors. Tokens of no sequence are not read, and their rows of o (dq, dk_, dv_, dg, dbeta)
+ * are left as they were, or set to zero with zero_rest = 1.
+ *
+ * Precision: with bf16, o and the gradients of the token tensors carry a few bf16 roundings; the
+ * states, which are fp32, do not: ht and dh0 are off by less than 1e-5 of what was written into them
+ * (Frobenius norm; writes that cancel one another, as of one key again and again, leave their errors
+ * behind). g <= 0 may be of any finite size, as for gdr2_fwd.
+ *
+ * Supported dtype / dk / dv as gdr2_fwd; chunks are of 64 tokens. Ownership, streams, errors and calls
+ * without tokens as gdr2_fwd / gdr2_bwd; g, beta, dg and dbeta need only their element's alignment; Hv
+ * not a multiple of Hk returns GDR2_ERR_SHAPE. Workspace:
+ * gdr2_scalar_workspace_bytes (packed = 1 when cu_seqlens is given; save_for_bwd = 1 for a forward that
+ * a backward follows, and for the backward). gdr2_scalar_bwd(..., fwd_saved = 1) needs the workspace as
+ * gdr2_scalar_fwd(..., save_for_bwd = 1) left it for the same inputs; fwd_saved = 0 recomputes. */
+size_t gdr2_scalar_workspace_bytes(int N, int T, int Hk, int Hv, int dk, int dv, int packed, int dtype,
+                                   int save_for_bwd);
+
+int gdr2_scalar_fwd(const void* q, const void* k, const void* v, const void* g, const void* beta, const float* h0,
+                    const int* cu_seqlens, void* o, float* ht, int N, int T, int Hk, int Hv, int dk, int dv,
+                    int dtype, int zero_rest, int save_for_bwd, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+int gdr2_scalar_bwd(const void* q, const void* k, const void* v, const void* g, const void* beta, const float* h0,
+                    const void* dout, const float* dht, const int* cu_seqlens, void* dq, void* dk_, void* dv_,
+                    void* dg, void* dbeta, float* dh0, int N, int T, int Hk, int Hv, int dk, int dv, int dtype,
+                    int zero_rest, int fwd_saved, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its recurrent form, for decoding: T tokens for each of B rows (q, k [B][T][Hk][dk], v, o
+ * [B][T][Hv][dv], g, beta [B][T][Hv]) on states in a pool, state fp32 [n_states][Hv][dk][dv], updated
+ * in place. Row b's state is slots[b] (an int32 array on the device), or b when slots is NULL
+ * (n_states >= B then). A row whose slot is outside 0 .. n_states - 1 is padding: its o is zero and
+ * no state is touched. Rows that name the same slot are taken one after another in the order of the
+ * rows, as one sequence. States that no row names are left as they were. */
+int gdr2_scalar_step(const void* q, const void* k, const void* v, const void* g, const void* beta, float* state,
+                     const int* slots, void* o, int B, int T, int Hk, int Hv, int dk, int dv, int n_states, int dtype,
+                     void* stream);
+
+/* Attention of one new token a sequence over a paged key-value cache, the decode step of the
+ * attention layers that a hybrid decoder alternates with the recurrent ones:
+ *
+ *     o = sum_t p_t v_t / sum_t p_t,   p_t = exp(scale q . k_t),   lse = log sum_t p_t
+ *
+ * over the tokens t that the sequence holds (its new token, appended before, included), or the last
+ * `window` of them when window > 0.
+ *   q, o   : [B][Hq][D] in `dtype`, contiguous;   lse : fp32 [B][Hq], or NULL
+ *   caches : [num_pages][page_size][Hkv][D] in `dtype`, the D elements of a row contiguous;
+ *            cache_strides = { page, token, head stride of k_cache, the same of v_cache } in elements
+ *            (a host array), multiples of 16 bytes; Hq is a multiple of Hkv, query head h reading key
+ *            head h / (Hq / Hkv)
+ *   block_table : int32 [B][max_pages] on the device; page i of a sequence holds its tokens
+ *            i page_size .. (i + 1) page_size - 1. Entries outside 0 .. num_pages - 1 are no page:
+ *            their tokens are masked (attention) or dropped (append)
+ *   lengths : int32 [B] on the device, tokens held; taken as 0 .. max_pages page_size where outside
+ * page_size is a power of two from 16 on (else GDR2_ERR_VALUE), D 64 or 128, dtype BF16 or F32. A row
+ * with nothing visible gets o = 0 and lse = -inf. What the cache holds in masked or unused places,
+ * infinities and NaN included, does not matter. Scores, weights' sums and lse are fp32; with bf16 the
+ * weights enter the second product as bf16. Results do not depend on the other rows of the call beyond
+ * the order of fp32 sums, and are repeatable bit for bit. Workspace: gdr2_attn_workspace_bytes, of no
+ * content between calls; calls that may overlap need one each. */
+size_t gdr2_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int dtype);
+
+int gdr2_attn_step(const void* q, const void* k_cache, const void* v_cache, const long long* cache_strides,
+                   const int* block_table, const int* lengths, void* o, float* lse, int B, int Hq, int Hkv, int D,
+                   int num_pages, int page_size, int max_pages, float scale, int window, int dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Writes new tokens' keys and values, k and v [tokens][Hkv][D], into the cache behind the starts[s]
+ * tokens that sequence s holds: its i-th new token goes to position starts[s] + i. cu_seqlens (int32
+ * [B + 1] on the device) gives each sequence's tokens as in gdr2_scalar_fwd, NULL one token a sequence
+ * (tokens = B). Tokens whose position lies outside the table or on no page are dropped, and the rest of
+ * the cache is left as it was. Two tokens of a call must not share a place. */
+int gdr2_kv_append(const void* k, const void* v, void* k_cache, void* v_cache, const long long* cache_strides,
+                   const int* block_table, const int* starts, const int* cu_seqlens, int B, int tokens, int Hkv, int D,
+                   int num_pages, int page_size, int max_pages, int dtype, void* stream);
+
 /* Static description of a status code. */
 const char* gdr2_strerror(int status);
 
