@@ -117,6 +117,20 @@ __device__ __forceinline__ typename Frag<OT>::type frag_cols(const Lane& n, cons
     }
 }
 
+// Sum over the four lanes li + 16 lq of a column, in all of them: two exchanges of half waves and of
+// neighbouring rows in the vector unit, without the LDS round trip of a shuffle.
+__device__ __forceinline__ float sum_lq(float x) {
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// value of lane n (a constant) in every lane
+__device__ __forceinline__ float lane_value(float x, int n) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), n));
+}
+
 // Fragments of a slice array [D / 16][rows][16] (row-K, the contiguous K order): row row0 + li,
 // columns 32 kb + 8 lq .. + 7.
 template <class OT, int ROWS>

@@ -25,6 +25,18 @@ __device__ __forceinline__ void sc_upper_ri(int u, int& R, int& I) {
     I = u < 3 ? u + 1 : (u < 5 ? u - 1 : 3);
 }
 
+// x + the value N lanes up in the row of 16 (zero past its end)
+template <int N>
+__device__ __forceinline__ float row_suffix_step(float x) {
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x100 + N, 0xF, 0xF, false));
+}
+// sum over 8 neighbouring lanes (of those that share l / 8), in the first of them
+__device__ __forceinline__ float row_sum8(float x) {
+    x = row_suffix_step<1>(x);
+    x = row_suffix_step<2>(x);
+    return row_suffix_step<4>(x);
+}
+
 // D_ri = exp(gam_r - gam_i) from gam held as a float and its remainder
 template <class OT>
 __device__ __forceinline__ float decay(float rhi, float rlo, float ihi, float ilo) {
@@ -90,8 +102,10 @@ __device__ __forceinline__ void sc_inverse(const lds_char* sA, lds_char* sT) {
     }
 }
 
-// One workgroup of four waves per (chunk slot, key head): k k^T and q k^T once, on the raw rows,
-// then for each value head of the group A, its inverse and M with that head's decay and beta.
+// One workgroup of four waves per (chunk slot, value head): k k^T and q k^T on the raw rows, then A, its
+// inverse and M with the head's decay and beta. (One workgroup per key head, which would form the
+// products once for all of its value heads, is no faster at 16384 x 16 tokens and heads, 35 us both
+// ways, and twice as slow where few workgroups run.)
 // Bound by HBM traffic in the large (reads q and k, writes T, M and the row factors: 48 KB a chunk
 // and value head at d_k = 128 with Hk = Hv) and by the latency of the blocked inverse in the small.
 template <class OT, int DK, bool TRAIN>
@@ -108,8 +122,8 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
     poison_lds_done();
     const int tid = threadIdx.x, l = tid & 63, li = l & 15, lq = l >> 4;
     const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
-    if (a.cu && a.zero_rest && a.o) zero_rest_rows<OT>(a, slot, a.o, a.Hv, hk * a.R, a.R, a.DV);
+    const int slot = blockIdx.x / a.Hv, h = blockIdx.x % a.Hv, hk = h / a.R;
+    if (a.cu && a.zero_rest && a.o) zero_rest_rows<OT>(a, slot, a.o, a.Hv, h, 1, a.DV);
     ScSeq q;
     int c;
     if (!sc_slot(a.cu, a.T, a.N, slot, q, c)) return;
@@ -152,89 +166,84 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
         const int e = idx % 64;
         lds_store<f32x4>(sT + swz<float, CH>(16 * R + e / 4, 16 * I + 4 * (e % 4)) * 4, f32x4{});
     }
-#pragma unroll 1
-    for (int hh = 0; hh < a.R; ++hh) {
-        const int h = hk * a.R + hh;
-        const size_t id = (size_t)slot * a.Hv + h;
-        if (wv == 0) {
-            const bool ok = l < nvalid;
-            const size_t at = (size_t)(row0 + l) * a.Hv + h;
-            const double gam = wave_scan(ok ? (double)to_f(((const OT*)a.g)[at]) : 0.0);
-            const double gc = __shfl(gam, 63);
-            const float hi = (float)gam, lo = (float)(gam - (double)hi);
-            const float v[6] = {ok ? exp_op<OT>(hi) * (1.f + lo) : 0.f, ok ? to_f(((const OT*)a.beta)[at]) : 0.f,
-                                ok ? exp_op<OT>((float)(gc - gam)) : 0.f, hi, lo, exp_op<OT>((float)gc)};
-            float* vec = (float*)(a.ws + a.L.o_vec) + id * a.L.vec;
+    const size_t id = (size_t)slot * a.Hv + h;
+    if (wv == 0) {
+        const bool ok = l < nvalid;
+        const size_t at = (size_t)(row0 + l) * a.Hv + h;
+        const double gam = wave_scan(ok ? (double)to_f(((const OT*)a.g)[at]) : 0.0);
+        const double gc = __shfl(gam, 63);
+        const float hi = (float)gam, lo = (float)(gam - (double)hi);
+        const float v[6] = {ok ? exp_op<OT>(hi) * (1.f + lo) : 0.f, ok ? to_f(((const OT*)a.beta)[at]) : 0.f,
+                            ok ? exp_op<OT>((float)(gc - gam)) : 0.f, hi, lo, exp_op<OT>((float)gc)};
+        float* vec = (float*)(a.ws + a.L.o_vec) + id * a.L.vec;
 #pragma unroll
-            for (int i = 0; i < 6; ++i) {
-                lds_store<float>(sV + (64 * i + l) * 4, v[i]);
-                vec[64 * i + l] = v[i];
-            }
+        for (int i = 0; i < 6; ++i) {
+            lds_store<float>(sV + (64 * i + l) * 4, v[i]);
+            vec[64 * i + l] = v[i];
         }
-        __syncthreads();
-        OT* m = (OT*)(a.ws + a.L.o_m) + id * a.L.m;
+    }
+    __syncthreads();
+    OT* m = (OT*)(a.ws + a.L.o_m) + id * a.L.m;
 #pragma unroll
-        for (int n = 0; n < 3; ++n) {
-            const int p = wv + 4 * n;
-            if (p < NPAIR) {
-                int R, I;
-                pair_ri(p, R, I);
-                const int r = 16 * R + li, i0 = 16 * I + 4 * lq;
-                const float rhi = lds_load<float>(sV + (SC_GHI + r) * 4), rlo = lds_load<float>(sV + (SC_GLO + r) * 4);
-                const float beta = lds_load<float>(sV + (SC_BETA + r) * 4);
-                float ihi[4], ilo[4], av[4];
-                lds_get4<float>(sV + (SC_GHI + i0) * 4, ihi);
-                lds_get4<float>(sV + (SC_GLO + i0) * 4, ilo);
-                f32x4 mv;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // above the diagonal the exponent would be positive: there the product is dropped
-                    const float d = i0 + i <= r ? decay<OT>(rhi, rlo, ihi[i], ilo[i]) : 0.f;
-                    mv[i] = d == 0.f ? 0.f : d * qk[n][i];
-                    av[i] = i0 + i < r && d != 0.f ? beta * d * kk[n][i] : 0.f;
-                }
-                f32x4 a4 = {av[0], av[1], av[2], av[3]};
-                lds_store<f32x4>(sA + swz<float, CH>(r, i0) * 4, a4);
-                OT* mp = m + fimg<OT, CH>(r, i0);
-                if constexpr (ES == 2) {
-                    bf16x4 hi, lo;
-                    split4(mv, hi, lo);
-                    *(bf16x4*)mp = hi;
-                    if (TRAIN) *(bf16x4*)(mp + CH * CH) = lo;
-                } else {
-                    *(f32x4*)mp = mv;
-                }
-            }
-        }
-        for (int u = wv; u < 6; u += 4) {
+    for (int n = 0; n < 3; ++n) {
+        const int p = wv + 4 * n;
+        if (p < NPAIR) {
             int R, I;
-            sc_upper_ri(u, R, I);
-            OT* mp = m + fimg<OT, CH>(16 * R + li, 16 * I + 4 * lq);
-            const float z[4] = {0.f, 0.f, 0.f, 0.f};
-            st4(mp, z);
-            if (TRAIN && ES == 2) st4(mp + CH * CH, z);
-        }
-        __syncthreads();
-        sc_inverse(sA, sT);
-        // T out, a 16-byte piece of the image (8 bf16 or 4 fp32 columns of a row) at a time
-        OT* t = (OT*)(a.ws + a.L.o_t) + id * a.L.t;
-        constexpr int EPP = 16 / ES;
-        for (int idx = tid; idx < CH * CH / EPP; idx += 256) {
-            const int r = idx / (CH / EPP), c0 = EPP * (idx % (CH / EPP));
+            pair_ri(p, R, I);
+            const int r = 16 * R + li, i0 = 16 * I + 4 * lq;
+            const float rhi = lds_load<float>(sV + (SC_GHI + r) * 4), rlo = lds_load<float>(sV + (SC_GLO + r) * 4);
+            const float beta = lds_load<float>(sV + (SC_BETA + r) * 4);
+            float ihi[4], ilo[4], av[4];
+            lds_get4<float>(sV + (SC_GHI + i0) * 4, ihi);
+            lds_get4<float>(sV + (SC_GLO + i0) * 4, ilo);
+            f32x4 mv;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // above the diagonal the exponent would be positive: there the product is dropped
+                const float d = i0 + i <= r ? decay<OT>(rhi, rlo, ihi[i], ilo[i]) : 0.f;
+                mv[i] = d == 0.f ? 0.f : d * qk[n][i];
+                av[i] = i0 + i < r && d != 0.f ? beta * d * kk[n][i] : 0.f;
+            }
+            f32x4 a4 = {av[0], av[1], av[2], av[3]};
+            lds_store<f32x4>(sA + swz<float, CH>(r, i0) * 4, a4);
+            OT* mp = m + fimg<OT, CH>(r, i0);
             if constexpr (ES == 2) {
-                const f32x4 x0 = lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4);
-                const f32x4 x1 = lds_load<f32x4>(sT + swz<float, CH>(r, c0 + 4) * 4);
-                bf16x4 h0, l0, h1, l1;
-                split4(x0, h0, l0);
-                split4(x1, h1, l1);
-                OT* tp = t + fimg<OT, CH>(r, c0);
-                *(bf16x8*)tp = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
-                *(bf16x8*)(tp + CH * CH) = __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
+                bf16x4 hi, lo;
+                split4(mv, hi, lo);
+                *(bf16x4*)mp = hi;
+                if (TRAIN) *(bf16x4*)(mp + CH * CH) = lo;
             } else {
-                *(f32x4*)(t + fimg<OT, CH>(r, c0)) = lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4);
+                *(f32x4*)mp = mv;
             }
         }
-        __syncthreads();  // A, T and the row factors are free for the next head
+    }
+    for (int u = wv; u < 6; u += 4) {
+        int R, I;
+        sc_upper_ri(u, R, I);
+        OT* mp = m + fimg<OT, CH>(16 * R + li, 16 * I + 4 * lq);
+        const float z[4] = {0.f, 0.f, 0.f, 0.f};
+        st4(mp, z);
+        if (TRAIN && ES == 2) st4(mp + CH * CH, z);
+    }
+    __syncthreads();
+    sc_inverse(sA, sT);
+    // T out, a 16-byte piece of the image (8 bf16 or 4 fp32 columns of a row) at a time
+    OT* t = (OT*)(a.ws + a.L.o_t) + id * a.L.t;
+    constexpr int EPP = 16 / ES;
+    for (int idx = tid; idx < CH * CH / EPP; idx += 256) {
+        const int r = idx / (CH / EPP), c0 = EPP * (idx % (CH / EPP));
+        if constexpr (ES == 2) {
+            const f32x4 x0 = lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4);
+            const f32x4 x1 = lds_load<f32x4>(sT + swz<float, CH>(r, c0 + 4) * 4);
+            bf16x4 h0, l0, h1, l1;
+            split4(x0, h0, l0);
+            split4(x1, h1, l1);
+            OT* tp = t + fimg<OT, CH>(r, c0);
+            *(bf16x8*)tp = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
+            *(bf16x8*)(tp + CH * CH) = __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            *(f32x4*)(t + fimg<OT, CH>(r, c0)) = lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4);
+        }
     }
 }
 
@@ -244,23 +253,41 @@ struct ScGradLds {
     static constexpr int ES = sizeof(OT);
     static constexpr int NW = DK / 16;               // waves, one 16-row tile of key channels each
     static constexpr int SQ = CH * CH * ES;
-    static constexpr int K = 0;                      // raw k and q rows, swizzled
-    static constexpr int Q = K + CH * DK * ES;
-    static constexpr int DO = Q + CH * DK * ES;      // dO rows, swizzled
-    static constexpr int DEL = DO + CH * DV * ES;    // Delta, dY: slices [DV / 16][64][16]
-    static constexpr int DY = DEL + CH * DV * ES;
-    static constexpr int P = DO;                     // after the pair products: P, R / beta, R [64][64]
+    static constexpr int TK = CH * DK * ES, TV = CH * DV * ES;
+    static constexpr int K = 0;             // raw k rows, swizzled
+    static constexpr int DO = K + TK;       // dO rows, swizzled
+    static constexpr int DEL = DO + TV;     // Delta, dY: slices [DV / 16][64][16]
+    static constexpr int DY = DEL + TV;
+    static constexpr int P = DO;            // after the pair products: P, R / beta, R [64][64], raw q rows
     static constexpr int RP = P + SQ;
     static constexpr int R = RP + SQ;
-    static_assert(3 * SQ <= 3 * CH * DV * ES, "P and R fit over dO, Delta and dY");
-    static constexpr int VEC = DY + CH * DV * ES;
+    static constexpr int Q = R + SQ;
+    static constexpr int ODQ = DO;          // at the end: dq and dk rows on their way out
+    static constexpr int ODK = ODQ + TK;
+    static constexpr int REGION = 3 * TV > 3 * SQ + TK ? 3 * TV : 3 * SQ + TK;
+    static_assert(2 * TK <= REGION, "dq and dk fit over what is dead");
+    static constexpr int VEC = DO + REGION;
     static constexpr int ROWP = VEC + SC_VEC * 4;    // per block pair: row and column sums of N
     static constexpr int COLP = ROWP + NPAIR * 16 * 4;
     static constexpr int DOTS = COLP + NPAIR * 16 * 4;  // per wave and row: q.dq_s, k.dx_s, k.dk_s, k.G
     static constexpr int DOTV = DOTS + 4 * NW * CH * 4; // per row: dY.v
     static constexpr int SS = DOTV + CH * 4;            // per wave: <dS', S>
-    static constexpr int BYTES = SS + NW * 4;
+    static constexpr int RED = SS + NW * 4;             // 6 sums a row
+    static constexpr int BYTES = RED + 6 * CH * 4;
 };
+
+// 64 raw rows into a swizzled tile, rows from nvalid on repeating the last (they meet zeros only)
+template <class OT, int RL, int NW>
+__device__ __forceinline__ void dma_rows_clamped(const OT* base, size_t rs, int nvalid, lds_char* tile, int wv) {
+    constexpr int EPC = 16 / (int)sizeof(OT), NCH = RL / EPC, RPI = 64 / NCH, NI = CH / RPI;
+    const int l = lane_id();
+#pragma unroll
+    for (int n = 0; n < NI; n += NW) {
+        const int row = (n + wv) * RPI + l / NCH, c = (l % NCH) ^ swz_f<OT, RL>(row);
+        const char* src = (const char*)(base + (size_t)min(row, nvalid - 1) * rs + c * EPC);
+        __builtin_amdgcn_global_load_lds(src, (lds_void*)(tile + (n + wv) * 1024), 16, 0, 0);
+    }
+}
 
 // One workgroup per (chunk slot, key head), one wave per 16 key channels: the gradients of the
 // group's value heads one after another, dq and dk summed over them in fp32 registers (value heads
@@ -274,8 +301,14 @@ struct ScGradLds {
 //   dg_t = sum_{r >= t} (row_r - col_r of N + q.dq_s + beta k.dx_s) + sum_{i < t} k.dk_s + e^gamC <dS', S>
 // The last line sums only terms that carry the decay across t: the diagonal of N, which does not
 // depend on the decay, is left out, so that a strong decay leaves a small dg and no cancellation.
-template <class OT, int DK, int DV>
-__global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
+//
+// A chunk and head moves 208 KB (d = 128, bf16), which at the rate of HBM is two thirds of the time;
+// two workgroups a compute unit, one loading while the other works, is what the LDS layout (q enters
+// LDS only when dO, Delta and dY have left it) and the register bound are for. MULTI: more than one
+// value head a key head. (One head is a kernel of its own: around a loop over heads the compiler keeps
+// a hundred addresses in registers.)
+template <class OT, int DK, int DV, bool MULTI>
+__global__ __launch_bounds__(4 * DK, DK == 128 && !MULTI ? 4 : 2) void k_sc_grad(ScArgs a) {
     using LS = ScGradLds<OT, DK, DV>;
     using FT = typename Frag<OT>::type;
     constexpr int ES = sizeof(OT), NW = LS::NW, NTHR = 64 * NW, KB = DK / 32, VB = DV / 32;
@@ -284,8 +317,6 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
     lds_char* sm = (lds_char*)smem_;
     poison_lds(sm, LS::BYTES);
     poison_lds_done();
-    const int tid = threadIdx.x, l = tid & 63, li = l & 15, lq = l >> 4;
-    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int slot = blockIdx.x / a.Hk, hk = blockIdx.x % a.Hk;
     if (a.cu && a.zero_rest) {
         zero_rest_rows<OT>(a, slot, a.dq, a.Hk, hk, 1, DK);
@@ -297,6 +328,7 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
     ScSeq q;
     int c;
     if (!sc_slot(a.cu, a.T, a.N, slot, q, c)) return;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const long long row0 = q.tok0 + 64LL * c;
     const int nvalid = min(CH, q.len - CH * c);
     const size_t rsk = (size_t)a.Hk * DK, rsv = (size_t)a.Hv * DV;
@@ -305,29 +337,31 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
     const LSwz<OT, DV> vO{sm + LS::DO};
     const LSlice<OT, CH> vDel{sm + LS::DEL}, vDy{sm + LS::DY};
     const LSwz<OT, CH> vP{sm + LS::P}, vRp{sm + LS::RP}, vR{sm + LS::R};
-    dma_rows<OT, DK, NW>((const OT*)a.k + k0, rsk, nvalid, sm + LS::K, wv);
-    dma_rows<OT, DK, NW>((const OT*)a.q + k0, rsk, nvalid, sm + LS::Q, wv);
-    zero_tail_rows<OT, DK, NTHR>(sm + LS::K, nvalid);
-    zero_tail_rows<OT, DK, NTHR>(sm + LS::Q, nvalid);
+    dma_rows_clamped<OT, DK, NW>((const OT*)a.k + k0, rsk, nvalid, sm + LS::K, wv);
     f32x4 dq[4], dk[4];  // transposed tiles: keys 16 wv + 4 lq + i, tokens 16 t + li
 #pragma unroll
     for (int t = 0; t < 4; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
 #pragma unroll 1
-    for (int hh = 0; hh < a.R; ++hh) {
+    for (int hh = 0; hh < (MULTI ? a.R : 1); ++hh) {
         const int h = hk * a.R + hh;
         const size_t id = (size_t)slot * a.Hv + h;
         const size_t v0 = row0 * rsv + (size_t)h * DV;
         const OT* gS = (const OT*)(a.ws + a.L.o_s) + id * a.L.s;
         const OT* gdS = (const OT*)(a.ws + a.L.o_ds) + id * a.L.s;
-        if (hh) __syncthreads();  // the head before is done with LDS
+        Lane ln = fresh_lane();
+        const int li = ln.li, lq = ln.lq, l = li + 16 * lq, tid = 64 * wv + l;
+        if (MULTI && hh) sync_lds();  // the head before is done with LDS
         dma_rows<OT, DV, NW>((const OT*)a.dout + v0, rsv, nvalid, sm + LS::DO, wv);
         zero_tail_rows<OT, DV, NTHR>(sm + LS::DO, nvalid);
         const char* gDel = a.ws + a.L.o_delta + id * a.L.d * ES;
         const char* gDy = a.ws + a.L.o_dy + id * a.L.d * ES;
-        for (int n = wv; n < CH * DV * ES / 1024; n += NW) {
-            __builtin_amdgcn_global_load_lds(gDel + n * 1024 + l * 16, (lds_void*)(sm + LS::DEL + n * 1024), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds(gDy + n * 1024 + l * 16, (lds_void*)(sm + LS::DY + n * 1024), 16, 0, 0);
+#pragma unroll
+        for (int n = 0; n < LS::TV / 1024; n += NW) {
+            __builtin_amdgcn_global_load_lds(gDel + (n + wv) * 1024 + l * 16, (lds_void*)(sm + LS::DEL + (n + wv) * 1024), 16,
+                                             0, 0);
+            __builtin_amdgcn_global_load_lds(gDy + (n + wv) * 1024 + l * 16, (lds_void*)(sm + LS::DY + (n + wv) * 1024), 16,
+                                             0, 0);
         }
         for (int i = tid; i < SC_VEC; i += NTHR)
             lds_store<float>(sm + LS::VEC + i * 4, ((const float*)(a.ws + a.L.o_vec))[id * a.L.vec + i]);
@@ -337,28 +371,31 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
             fS[kb] = gfrag_slice<OT, DK>(gS, 16 * wv, kb);
             fdS[kb] = gfrag_slice<OT, DK>(gdS, 16 * wv, kb);
         }
+        typename Raw4<OT>::type qv[4];  // q of tokens 16 t + li, keys 16 wv + 4 lq ..
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+            qv[t] = *(const typename Raw4<OT>::type*)((const OT*)a.q + k0 + (size_t)min(16 * t + li, nvalid - 1) * rsk +
+                                                      16 * wv + 4 * lq);
+        // v, 16 bytes of a row a lane (rows past the end: zero)
+        constexpr int EPC = 16 / ES, LPR = DV / EPC, NVL = CH * LPR / NTHR;
+        typedef OT VT __attribute__((ext_vector_type(EPC)));
+        VT gv[NVL];
+#pragma unroll
+        for (int i = 0; i < NVL; ++i) {
+            const int u = tid + NTHR * i, rr = u / LPR;
+            gv[i] = rr < nvalid ? *(const VT*)((const OT*)a.v + v0 + rr * rsv + EPC * (u % LPR)) : VT{};
+        }
         wait_vm<0>();
-        __syncthreads();
+        sync_lds();
 
         // ---- the states' parts
-        Lane ln = fresh_lane();
-        float e[4], tail[4], beta[4];  // of tokens 16 t + li
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            e[t] = lds_load<float>(sm + LS::VEC + (SC_E + 16 * t + li) * 4);
-            tail[t] = lds_load<float>(sm + LS::VEC + (SC_TAIL + 16 * t + li) * 4);
-            beta[t] = lds_load<float>(sm + LS::VEC + (SC_BETA + 16 * t + li) * 4);
-        }
-        auto dot_rows = [&](const LSwz<OT, DK>& m, const f32x4& x, int t, int which) {
-            // sum over this wave's keys of m[token][key] x, tokens 16 t + li
-            float y[4];
-            lds_get4<OT>(m.p + m.off(16 * t + li, 16 * wv + 4 * lq), y);
-            float s = (y[0] * x[0] + y[1] * x[1]) + (y[2] * x[2] + y[3] * x[3]);
-            s += __shfl_xor(s, 16);
-            s += __shfl_xor(s, 32);
+        auto dot4 = [&](const float (&y)[4], const f32x4& x, int t, int which) {
+            // sum over this wave's keys of y x, tokens 16 t + li
+            const float s = sum_lq((y[0] * x[0] + y[1] * x[1]) + (y[2] * x[2] + y[3] * x[3]));
             if (lq == 0) lds_store<float>(sm + LS::DOTS + ((which * NW + wv) * CH + 16 * t + li) * 4, s);
         };
         f32x4 G[4];
+        ln = fresh_lane();
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x, z = x;
@@ -368,14 +405,17 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
                 mma(y, fS[kb], frag_rows<OT>(ln, vDy, 16 * t, 32 * kb));
                 mma(z, fdS[kb], frag_rows<OT>(ln, vDel, 16 * t, 32 * kb));
             }
-            x = x * e[t];
-            G[t] = y * -e[t];
-            z = z * tail[t];
+            x = x * lds_load<float>(sm + LS::VEC + (SC_E + 16 * t + ln.li) * 4);
+            G[t] = y * -lds_load<float>(sm + LS::VEC + (SC_E + 16 * t + ln.li) * 4);
+            z = z * lds_load<float>(sm + LS::VEC + (SC_TAIL + 16 * t + ln.li) * 4);
             dq[t] += x;
             dk[t] += z;
-            dot_rows(vQ, x, t, 0);
-            dot_rows(vK, G[t], t, 1);
-            dot_rows(vK, z, t, 2);
+            float kx[4];
+            const float qx[4] = {to_f(qv[t][0]), to_f(qv[t][1]), to_f(qv[t][2]), to_f(qv[t][3])};
+            lds_get4<OT>(vK.p + vK.off(16 * t + ln.li, 16 * wv + 4 * ln.lq), kx);
+            dot4(qx, x, t, 0);
+            dot4(kx, G[t], t, 1);
+            dot4(kx, z, t, 2);
             __builtin_amdgcn_sched_barrier(0);
         }
         {
@@ -384,40 +424,32 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
             for (int kb = 0; kb < VB; ++kb)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) s += to_f(fS[kb][i]) * to_f(fdS[kb][i]);
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) s += __shfl_xor(s, m);
+            s = row_sum16(s);
+            s = (lane_value(s, 0) + lane_value(s, 16)) + (lane_value(s, 32) + lane_value(s, 48));
             if (l == 0) lds_store<float>(sm + LS::SS + wv * 4, s);
         }
 
         // ---- dv = beta dY and dY.v, 16 bytes of a row a lane
-        {
-            constexpr int EPC = 16 / ES, LPR = DV / EPC;
-            typedef OT VT __attribute__((ext_vector_type(16 / ES)));
 #pragma unroll
-            for (int i = 0; i < CH * LPR / NTHR; ++i) {
-                const int u = tid + NTHR * i, r = u / LPR, col = EPC * (u % LPR);
-                const VT y = lds_load<VT>(vDy.p + vDy.off(r, col));
-                float s = 0.f;
-                if (r < nvalid) {
-                    const VT v = *(const VT*)((const OT*)a.v + v0 + r * rsv + col);
-                    const float b = lds_load<float>(sm + LS::VEC + (SC_BETA + r) * 4);
-                    VT d;
+        for (int i = 0; i < NVL; ++i) {
+            const int u = tid + NTHR * i, rr = u / LPR, col = EPC * (u % LPR);
+            const VT y = lds_load<VT>(vDy.p + vDy.off(rr, col));
+            const float b = lds_load<float>(sm + LS::VEC + (SC_BETA + rr) * 4);
+            float s = 0.f;
+            VT d;
 #pragma unroll
-                    for (int j = 0; j < EPC; ++j) {
-                        s += to_f(y[j]) * to_f(v[j]);
-                        d[j] = to_ot<OT>(b * to_f(y[j]));
-                    }
-                    *(VT*)((OT*)a.dv + v0 + r * rsv + col) = d;
-                }
-#pragma unroll
-                for (int m = 1; m < LPR; m <<= 1) s += __shfl_xor(s, m);
-                if (u % LPR == 0) lds_store<float>(sm + LS::DOTV + r * 4, s);
+            for (int j = 0; j < EPC; ++j) {
+                s += to_f(y[j]) * to_f(gv[i][j]);
+                d[j] = to_ot<OT>(b * to_f(y[j]));
             }
+            if (rr < nvalid) *(VT*)((OT*)a.dv + v0 + rr * rsv + col) = d;
+            s = LPR == 16 ? row_sum16(s) : row_sum8(s);
+            if (u % LPR == 0) lds_store<float>(sm + LS::DOTV + rr * 4, s);
         }
-
         __builtin_amdgcn_sched_barrier(0);
+
         // ---- block pairs (rows 16 R + li, columns 16 I + 4 lq + i)
-        f32x4 fP[PPW], fRp[PPW], fR[PPW];
+        f32x4 fP[PPW], fRp[PPW];
         ln = fresh_lane();
 #pragma unroll
         for (int n = 0; n < PPW; ++n) {
@@ -425,20 +457,32 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
             if (p < NPAIR) {
                 int R, I;
                 pair_ri(p, R, I);
-                f32x4 qk = {0.f, 0.f, 0.f, 0.f}, kk = qk, dm = qk, da = qk;
+                const int r = 16 * R + ln.li, i0 = 16 * I + 4 * ln.lq;
+                // the rows of q come from memory (this chunk's are in cache by now)
+                FT fq[KB];
+                const OT* qp = (const OT*)a.q + k0 + (size_t)min(r, nvalid - 1) * rsk + 8 * ln.lq;
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    const FT f = frag_rows<OT>(ln, vK, 16 * I, 32 * kb);
-                    mma(qk, f, frag_rows<OT>(ln, vQ, 16 * R, 32 * kb));
-                    mma(kk, f, frag_rows<OT>(ln, vK, 16 * R, 32 * kb));
+                    if constexpr (ES == 2) {
+                        fq[kb] = *(const FT*)(qp + 32 * kb);
+                    } else {
+                        const f32x4 x0 = *(const f32x4*)(qp + 32 * kb), x1 = *(const f32x4*)(qp + 32 * kb + 4);
+                        fq[kb] = __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
+                    }
                 }
+                f32x4 qk = {0.f, 0.f, 0.f, 0.f}, kk = qk, dm = qk, da = qk;
 #pragma unroll
                 for (int kb = 0; kb < VB; ++kb) {
                     const FT f = frag_rows<OT>(ln, vDel, 16 * I, 32 * kb);
                     mma(dm, f, frag_rows<OT>(ln, vO, 16 * R, 32 * kb));
                     mma(da, f, frag_rows<OT>(ln, vDy, 16 * R, 32 * kb));
                 }
-                const int r = 16 * R + li, i0 = 16 * I + 4 * lq;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    const FT f = frag_rows<OT>(ln, vK, 16 * I, 32 * kb);
+                    mma(kk, f, frag_rows<OT>(ln, vK, 16 * R, 32 * kb));
+                    mma(qk, f, fq[kb]);
+                }
                 const float rhi = lds_load<float>(sm + LS::VEC + (SC_GHI + r) * 4);
                 const float rlo = lds_load<float>(sm + LS::VEC + (SC_GLO + r) * 4);
                 const float br = lds_load<float>(sm + LS::VEC + (SC_BETA + r) * 4);
@@ -452,30 +496,31 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
                     const bool strict = i0 + i < r;
                     fP[n][i] = d == 0.f ? 0.f : d * dm[i];
                     fRp[n][i] = strict && d != 0.f ? -(d * da[i]) : 0.f;
-                    fR[n][i] = br * fRp[n][i];
-                    nn[i] = strict ? fP[n][i] * qk[i] + fR[n][i] * kk[i] : 0.f;
+                    nn[i] = strict ? fP[n][i] * qk[i] + br * fRp[n][i] * kk[i] : 0.f;
                     rows += nn[i];
                 }
-                rows += __shfl_xor(rows, 16);
-                rows += __shfl_xor(rows, 32);
-                if (lq == 0) lds_store<float>(sm + LS::ROWP + (p * 16 + li) * 4, rows);
+                rows = sum_lq(rows);
+                if (ln.lq == 0) lds_store<float>(sm + LS::ROWP + (p * 16 + ln.li) * 4, rows);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) nn[i] = row_sum16(nn[i]);
-                if (li == 0) lds_store<f32x4>(sm + LS::COLP + (p * 16 + 4 * lq) * 4, f32x4{nn[0], nn[1], nn[2], nn[3]});
+                if (ln.li == 0)
+                    lds_store<f32x4>(sm + LS::COLP + (p * 16 + 4 * ln.lq) * 4, f32x4{nn[0], nn[1], nn[2], nn[3]});
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        __syncthreads();  // dO, Delta and dY are dead: P and R take their place
+        sync_lds();  // dO, Delta and dY are dead: q, P and R take their place
+        dma_rows_clamped<OT, DK, NW>((const OT*)a.q + k0, rsk, nvalid, sm + LS::Q, wv);
 #pragma unroll
         for (int n = 0; n < PPW; ++n) {
             const int p = wv + NW * n;
             if (p < NPAIR) {
                 int R, I;
                 pair_ri(p, R, I);
-                const int o = swz<OT, CH>(16 * R + li, 16 * I + 4 * lq) * ES;
+                const int o = swz<OT, CH>(16 * R + ln.li, 16 * I + 4 * ln.lq) * ES;
+                const float br = lds_load<float>(sm + LS::VEC + (SC_BETA + 16 * R + ln.li) * 4);
                 const float x[4] = {fP[n][0], fP[n][1], fP[n][2], fP[n][3]};
                 const float y[4] = {fRp[n][0], fRp[n][1], fRp[n][2], fRp[n][3]};
-                const float z[4] = {fR[n][0], fR[n][1], fR[n][2], fR[n][3]};
+                const float z[4] = {br * y[0], br * y[1], br * y[2], br * y[3]};
                 lds_put4<OT>(sm + LS::P + o, x);
                 lds_put4<OT>(sm + LS::RP + o, y);
                 lds_put4<OT>(sm + LS::R + o, z);
@@ -484,13 +529,14 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
         for (int u = wv; u < 6; u += NW) {
             int R, I;
             sc_upper_ri(u, R, I);
-            const int o = swz<OT, CH>(16 * R + li, 16 * I + 4 * lq) * ES;
+            const int o = swz<OT, CH>(16 * R + ln.li, 16 * I + 4 * ln.lq) * ES;
             const float z[4] = {0.f, 0.f, 0.f, 0.f};
             lds_put4<OT>(sm + LS::P + o, z);
             lds_put4<OT>(sm + LS::RP + o, z);
             lds_put4<OT>(sm + LS::R + o, z);
         }
-        __syncthreads();
+        wait_vm<0>();
+        sync_lds();
 
         // ---- dq += P K, G += (R / beta) K, dk += P^T Q + R^T K + beta G
         FT fK[2], fQ[2];
@@ -513,54 +559,64 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
                     mma(dk[t], fK[kb], frag_cols<OT>(ln, vR, 16 * t, 32 * kb));
                 }
             }
-            dot_rows(vK, G[t], t, 3);
-            dk[t] += G[t] * beta[t];
+            float kx[4];
+            lds_get4<OT>(vK.p + vK.off(16 * t + ln.li, 16 * wv + 4 * ln.lq), kx);
+            dot4(kx, G[t], t, 3);
+            dk[t] += G[t] * lds_load<float>(sm + LS::VEC + (SC_BETA + 16 * t + ln.li) * 4);
             __builtin_amdgcn_sched_barrier(0);
         }
-        __syncthreads();
-        // ---- dbeta and dg (lane = row)
-        if (wv == 0) {
-            const int r = l;
-            float d[4] = {0.f, 0.f, 0.f, 0.f}, ss = 0.f;
+        sync_lds();
+        // ---- sums over the waves and over the block pairs, lane = row, one task a wave
+        for (int task = wv; task < 6; task += NW) {
+            float x = 0.f;
+            if (task < 4) {
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
+                for (int u = 0; u < NW; ++u) x += lds_load<float>(sm + LS::DOTS + ((task * NW + u) * CH + l) * 4);
+            } else if (task == 4) {
+                const int b = l / 16;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) d[j] += lds_load<float>(sm + LS::DOTS + ((j * NW + w) * CH + r) * 4);
-                ss += lds_load<float>(sm + LS::SS + w * 4);
+                for (int o = 0; o < NBLK; ++o) {
+                    const float rs = lds_load<float>(sm + LS::ROWP + (pair_id(b, min(o, b)) * 16 + l % 16) * 4);
+                    const float cs = lds_load<float>(sm + LS::COLP + (pair_id(max(o, b), b) * 16 + l % 16) * 4);
+                    x += (o <= b ? rs : 0.f) - (o >= b ? cs : 0.f);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < NW; ++u) x += lds_load<float>(sm + LS::SS + u * 4);
             }
-            const float b = lds_load<float>(sm + LS::VEC + (SC_BETA + r) * 4);
-            float x = d[0] + b * d[1];
+            lds_store<float>(sm + LS::RED + (task * CH + l) * 4, x);
+        }
+        if (!MULTI || hh + 1 == a.R) {  // dq and dk, turned to whole rows through LDS
 #pragma unroll
-            for (int o = 0; o < NBLK; ++o) {
-                if (o <= r / 16) x += lds_load<float>(sm + LS::ROWP + (pair_id(r / 16, o) * 16 + r % 16) * 4);
-                if (o >= r / 16) x -= lds_load<float>(sm + LS::COLP + (pair_id(o, r / 16) * 16 + r % 16) * 4);
-            }
-            // suffix sum of x, exclusive prefix sum of k.dk_s
-            float suf = x, pre = d[2];
-#pragma unroll
-            for (int o = 1; o < 64; o <<= 1) {
-                const float s = __shfl_down(suf, o), p = __shfl_up(pre, o);
-                if (l + o < 64) suf += s;
-                if (l >= o) pre += p;
-            }
-            pre = __shfl_up(pre, 1);
-            if (l == 0) pre = 0.f;
-            const float ec = lds_load<float>(sm + LS::VEC + SC_EC * 4);
-            if (r < nvalid) {
-                const size_t at = (size_t)(row0 + r) * a.Hv + h;
-                ((OT*)a.dbeta)[at] = to_ot<OT>(lds_load<float>(sm + LS::DOTV + r * 4) + d[3]);
-                ((OT*)a.dg)[at] = to_ot<OT>(suf + pre + ec * ss);
+            for (int t = 0; t < 4; ++t) {
+                const int o = swz<OT, DK>(16 * t + ln.li, 16 * wv + 4 * ln.lq) * ES;
+                const float x[4] = {dq[t][0], dq[t][1], dq[t][2], dq[t][3]};
+                const float y[4] = {dk[t][0], dk[t][1], dk[t][2], dk[t][3]};
+                lds_put4<OT>(sm + LS::ODQ + o, x);
+                lds_put4<OT>(sm + LS::ODK + o, y);
             }
         }
-    }
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int r = 16 * t + li;
-        if (r < nvalid) {
-            const float x[4] = {dq[t][0], dq[t][1], dq[t][2], dq[t][3]};
-            const float y[4] = {dk[t][0], dk[t][1], dk[t][2], dk[t][3]};
-            st4((OT*)a.dq + k0 + r * rsk + 16 * wv + 4 * lq, x);
-            st4((OT*)a.dk + k0 + r * rsk + 16 * wv + 4 * lq, y);
+        sync_lds();
+        if (!MULTI || hh + 1 == a.R) {
+            store_rows_tiles<OT, DK, NTHR, false>(sm + LS::ODQ, (OT*)a.dq + k0, rsk, nvalid);
+            store_rows_tiles<OT, DK, NTHR, false>(sm + LS::ODK, (OT*)a.dk + k0, rsk, nvalid);
+        }
+        // ---- dbeta and dg
+        if (wv == 0) {
+            auto red = [&](int t) { return lds_load<float>(sm + LS::RED + (t * CH + l) * 4); };
+            const float x = red(0) + lds_load<float>(sm + LS::VEC + (SC_BETA + l) * 4) * red(1) + red(4);
+            // suffix sum of x, exclusive prefix sum of k.dk_s: inside the 16 lanes of a row, then over rows
+            float suf = row_suffix16(x), pre = row_scan16(red(2));
+            const float s1 = lane_value(suf, 16), s2 = lane_value(suf, 32), s3 = lane_value(suf, 48);
+            const float p0 = lane_value(pre, 15), p1 = lane_value(pre, 31), p2 = lane_value(pre, 47);
+            pre = row_shr1(pre);
+            suf += l < 16 ? s1 + (s2 + s3) : l < 32 ? s2 + s3 : l < 48 ? s3 : 0.f;
+            pre += l < 16 ? 0.f : l < 32 ? p0 : l < 48 ? p0 + p1 : (p0 + p1) + p2;
+            if (l < nvalid) {
+                const size_t at = (size_t)(row0 + l) * a.Hv + h;
+                ((OT*)a.dbeta)[at] = to_ot<OT>(lds_load<float>(sm + LS::DOTV + l * 4) + red(3));
+                ((OT*)a.dg)[at] = to_ot<OT>(suf + pre + lds_load<float>(sm + LS::VEC + SC_EC * 4) * red(5));
+            }
         }
     }
 }
@@ -568,7 +624,7 @@ __global__ __launch_bounds__(4 * DK) void k_sc_grad(ScArgs a) {
 // ============================================================================ launchers
 template <class OT, int DK, int DV>
 static hipError_t launch_sc_fwd_t(const ScArgs& a, bool train, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.slots * a.Hk));
+    const dim3 grid((unsigned)(a.slots * a.Hv));
     if (train)
         hipLaunchKernelGGL((k_sc_prep<OT, DK, true>), grid, dim3(256), 0, stream, a);
     else
@@ -582,9 +638,10 @@ static hipError_t launch_sc_bwd_t(const ScArgs& a, hipStream_t stream) {
     hipError_t e = launch_sc_bwd_chain_t<OT, DK, DV>(a, stream);
     if (e != hipSuccess) return e;
     constexpr int lds = ScGradLds<OT, DK, DV>::BYTES;
-    e = hipFuncSetAttribute((const void*)k_sc_grad<OT, DK, DV>, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    auto grad = a.R > 1 ? k_sc_grad<OT, DK, DV, true> : k_sc_grad<OT, DK, DV, false>;
+    e = hipFuncSetAttribute((const void*)grad, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_sc_grad<OT, DK, DV>), dim3((unsigned)(a.slots * a.Hk)), dim3(4 * DK), lds, stream, a);
+    hipLaunchKernelGGL(grad, dim3((unsigned)(a.slots * a.Hk)), dim3(4 * DK), lds, stream, a);
     return hipGetLastError();
 }
 
