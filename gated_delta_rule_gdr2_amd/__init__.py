@@ -15,6 +15,7 @@ every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -390,6 +391,7 @@ class GDR2Function(torch.autograd.Function):
 # ---------------------------------------------------------------- gated delta rule with scalar gates
 
 
+@functools.lru_cache(maxsize=256)
 def gdr2_scalar_workspace_bytes(N, T, Hk, Hv, dk, dv, packed=False, dtype=DTYPE_BF16, save_for_bwd=False) -> int:
     return int(load_library().gdr2_scalar_workspace_bytes(N, T, Hk, Hv, dk, dv, int(bool(packed)), dtype,
                                                           int(bool(save_for_bwd))))
@@ -399,32 +401,36 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
-def _same_device(q, *tensors):
-    for t in tensors:
-        if t is not None and t.device != q.device:
-            raise ValueError("all tensors must be on one device, got %s and %s" % (q.device, t.device))
+def _want(t, name, dtype, shape, dev):
+    """_check and one device for all, at a fraction of the calls into torch: a decode step's kernels take a
+    few microseconds, and so do checks."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _check(t, name, dtype, shape)
+        raise ValueError("all tensors must be on one device: %s is on %s, q or k on cuda:%d" % (name, t.device, dev))
 
 
-def _index(t, name, shape):
-    _check(t, name, torch.int32, shape)
+def _device_of(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be a GPU tensor" % name)
+    return dev
 
 
 class _on:
-    """The tensors' device as the current one, and the stream to launch on: the given one, or that device's
-    current stream."""
+    """Device ``dev`` as the current one, and the stream to launch on: the given one, or the device's current
+    stream."""
 
-    def __init__(self, t, stream):
-        self.dev, self.stream = t.device.index, stream
+    def __init__(self, dev, stream):
+        self.dev, self.stream, self.prev = dev, stream, None
 
     def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.dev:
+        if torch.cuda.current_device() != self.dev:
+            self.prev = torch.cuda.current_device()
             torch.cuda.set_device(self.dev)
-        s = self.stream if self.stream is not None else torch.cuda.current_stream()
-        return s.cuda_stream
+        return (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
 
     def __exit__(self, *exc):
-        if self.prev != self.dev:
+        if self.prev is not None:
             torch.cuda.set_device(self.prev)
 
 
@@ -433,22 +439,24 @@ def _scalar_dims(q, k, v, g, beta, cu_seqlens):
         raise ValueError("q and v must have four dimensions [B,T,H,d]")
     B, T, Hk, dk = q.shape
     Hv, dv = v.shape[2], v.shape[3]
-    if q.dtype not in _DT:
-        raise ValueError("unsupported dtype %s" % q.dtype)
-    _check(q, "q", q.dtype, (B, T, Hk, dk))
-    _check(k, "k", q.dtype, (B, T, Hk, dk))
-    _check(v, "v", q.dtype, (B, T, Hv, dv))
-    _check(g, "g", q.dtype, (B, T, Hv))
-    _check(beta, "beta", q.dtype, (B, T, Hv))
+    t = q.dtype
+    if t not in _DT:
+        raise ValueError("unsupported dtype %s" % t)
+    dev = _device_of(q, "q")
+    _want(q, "q", t, (B, T, Hk, dk), dev)
+    _want(k, "k", t, (B, T, Hk, dk), dev)
+    _want(v, "v", t, (B, T, Hv, dv), dev)
+    _want(g, "g", t, (B, T, Hv), dev)
+    _want(beta, "beta", t, (B, T, Hv), dev)
     N = B
     if cu_seqlens is not None:
         if B != 1:
             raise ValueError("packed sequences need B = 1, got B = %d" % B)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must have one dimension and at least one entry")
-        _index(cu_seqlens, "cu_seqlens", cu_seqlens.shape)
+        _want(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
         N = cu_seqlens.numel() - 1
-    return B, T, Hk, Hv, dk, dv, N, _DT[q.dtype]
+    return B, T, Hk, Hv, dk, dv, N, _DT[t], dev
 
 
 def _scalar_workspace(N, T, Hk, Hv, dk, dv, packed, dt, train, device):
@@ -467,24 +475,27 @@ def gdr2_scalar_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, save_for_bwd=
     back to gdr2_scalar_bwd(..., fwd_saved=True) when save_for_bwd is set. Rows of ``o`` that belong to
     no sequence are zero, or left as they were in an ``o`` that is passed in."""
     lib = load_library()
-    B, T, Hk, Hv, dk, dv, N, dt = _scalar_dims(q, k, v, g, beta, cu_seqlens)
-    _check(h0, "h0", torch.float32, (N, Hv, dk, dv))
+    B, T, Hk, Hv, dk, dv, N, dt, dev = _scalar_dims(q, k, v, g, beta, cu_seqlens)
+    if h0 is not None:
+        _want(h0, "h0", torch.float32, (N, Hv, dk, dv), dev)
     new = []
     own_o = o is None
     if own_o:
         o = torch.empty(B, T, Hv, dv, dtype=q.dtype, device=q.device)
         new.append(o)
-    _check(o, "o", q.dtype, (B, T, Hv, dv))
+    else:
+        _want(o, "o", q.dtype, (B, T, Hv, dv), dev)
     ht = torch.empty(N, Hv, dk, dv, dtype=torch.float32, device=q.device) if output_final_state else None
     new.append(ht)
     if ws is None:
         ws = _scalar_workspace(N, T, Hk, Hv, dk, dv, cu_seqlens is not None, dt, save_for_bwd, q.device)
         new.append(ws)
-    _same_device(q, k, v, g, beta, h0, cu_seqlens, o, ws)
+    else:
+        _want(ws, "ws", torch.uint8, ws.shape, dev)
     if own_o and N == 0:
         o.zero_()  # no sequence, and no kernel
     _keep_for(stream, *new)
-    with _on(q, stream) as s:
+    with _on(dev, stream) as s:
         st = lib.gdr2_scalar_fwd(_adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(cu_seqlens), _adr(o),
                                  _adr(ht), N, T, Hk, Hv, dk, dv, dt, int(own_o), int(bool(save_for_bwd)), _adr(ws),
                                  ws.numel(), s)
@@ -498,10 +509,11 @@ def gdr2_scalar_bwd(q, k, v, g, beta, h0, dout, dht=None, *, cu_seqlens=None, ws
     None). With fwd_saved=True, ``ws`` must be the workspace of a gdr2_scalar_fwd(..., save_for_bwd=True)
     call on the same inputs. ``grads``: a dict of the five token gradients to write into."""
     lib = load_library()
-    B, T, Hk, Hv, dk, dv, N, dt = _scalar_dims(q, k, v, g, beta, cu_seqlens)
-    _check(dout, "dout", q.dtype, (B, T, Hv, dv))
-    _check(h0, "h0", torch.float32, (N, Hv, dk, dv))
-    _check(dht, "dht", torch.float32, (N, Hv, dk, dv))
+    B, T, Hk, Hv, dk, dv, N, dt, dev = _scalar_dims(q, k, v, g, beta, cu_seqlens)
+    _want(dout, "dout", q.dtype, (B, T, Hv, dv), dev)
+    for t, n in ((h0, "h0"), (dht, "dht")):
+        if t is not None:
+            _want(t, n, torch.float32, (N, Hv, dk, dv), dev)
     new = []
     names = (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta))
     own = grads is None
@@ -513,7 +525,7 @@ def gdr2_scalar_bwd(q, k, v, g, beta, h0, dout, dht=None, *, cu_seqlens=None, ws
         for n, x in names:
             if grads.get(n) is None:
                 raise ValueError("grads must hold %s" % n)
-            _check(grads[n], n, q.dtype, tuple(x.shape))
+            _want(grads[n], n, q.dtype, x.shape, dev)
     grads["dh0"] = torch.empty(N, Hv, dk, dv, dtype=torch.float32, device=q.device) if need_dh0 else None
     new.append(grads["dh0"])
     if ws is None:
@@ -521,12 +533,13 @@ def gdr2_scalar_bwd(q, k, v, g, beta, h0, dout, dht=None, *, cu_seqlens=None, ws
             raise ValueError("fwd_saved=True needs the forward's workspace")
         ws = _scalar_workspace(N, T, Hk, Hv, dk, dv, cu_seqlens is not None, dt, True, q.device)
         new.append(ws)
-    _same_device(q, k, v, g, beta, h0, dout, dht, cu_seqlens, ws, *grads.values())
+    else:
+        _want(ws, "ws", torch.uint8, ws.shape, dev)
     if own and N == 0:
         for n, _ in names:
             grads[n].zero_()
     _keep_for(stream, *new)
-    with _on(q, stream) as s:
+    with _on(dev, stream) as s:
         st = lib.gdr2_scalar_bwd(_adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(dout), _adr(dht),
                                  _adr(cu_seqlens), _adr(grads["dq"]), _adr(grads["dk"]), _adr(grads["dv"]),
                                  _adr(grads["dg"]), _adr(grads["dbeta"]), _adr(grads["dh0"]), N, T, Hk, Hv, dk, dv,
@@ -542,26 +555,25 @@ def gdr2_scalar_step(q, k, v, g, beta, state, *, slots=None, o=None, stream=None
     without slots. A slot outside the pool marks a padding row (o = 0, no state touched); rows with one
     slot in common are taken in order, as one sequence. Returns o."""
     lib = load_library()
-    B, T, Hk, Hv, dk, dv, _, dt = _scalar_dims(q, k, v, g, beta, None)
+    B, T, Hk, Hv, dk, dv, _, dt, dev = _scalar_dims(q, k, v, g, beta, None)
     if state is None:
         raise ValueError("state is required")
     if state.dim() != 4:
         raise ValueError("state must have four dimensions [S,Hv,dk,dv]")
-    _check(state, "state", torch.float32, (state.shape[0], Hv, dk, dv))
-    if slots is None:
-        if state.shape[0] < B:
-            raise ValueError("state holds %d states for %d rows" % (state.shape[0], B))
-    else:
-        _index(slots, "slots", (B,))
+    S = state.shape[0]
+    _want(state, "state", torch.float32, (S, Hv, dk, dv), dev)
+    if slots is not None:
+        _want(slots, "slots", torch.int32, (B,), dev)
+    elif S < B:
+        raise ValueError("state holds %d states for %d rows" % (S, B))
     if o is None:
-        o = torch.empty(B, T, Hv, dv, dtype=q.dtype, device=q.device)
+        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
         _keep_for(stream, o)
     else:
-        _check(o, "o", q.dtype, (B, T, Hv, dv))
-    _same_device(q, k, v, g, beta, state, slots, o)
-    with _on(q, stream) as s:
+        _want(o, "o", q.dtype, v.shape, dev)
+    with _on(dev, stream) as s:
         st = lib.gdr2_scalar_step(_adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(state), _adr(slots), _adr(o), B,
-                                  T, Hk, Hv, dk, dv, state.shape[0], dt, s)
+                                  T, Hk, Hv, dk, dv, S, dt, s)
     _raise(st, "gdr2_scalar_step")
     return o
 
@@ -586,18 +598,22 @@ class GDR2ScalarFunction(torch.autograd.Function):
 # ---------------------------------------------------------------- attention over a paged cache
 
 
+@functools.lru_cache(maxsize=256)
 def gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dtype=DTYPE_BF16) -> int:
     return int(load_library().gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dtype))
 
 
-def _cache_dims(k_cache, v_cache, block_table, dtype, D):
+_Strides = ctypes.c_longlong * 6
+
+
+def _cache_strides(k_cache, v_cache, block_table, dtype, D, dev):
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must have one shape [pages,page_size,Hkv,D], got %s and %s"
                          % (tuple(k_cache.shape), tuple(v_cache.shape)))
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not t.is_cuda:
-            raise ValueError("%s must be a GPU tensor" % n)
-        if t.dtype != dtype:
+        if t.get_device() != dev:
+            raise ValueError("%s must be on the GPU of the other tensors" % n)
+        if t.dtype is not dtype:
             raise ValueError("%s must have dtype %s, got %s" % (n, dtype, t.dtype))
         if t.shape[3] != D:
             raise ValueError("%s must have %d channels, got %d" % (n, D, t.shape[3]))
@@ -605,8 +621,7 @@ def _cache_dims(k_cache, v_cache, block_table, dtype, D):
             raise ValueError("the channels of %s must be contiguous" % n)
     if block_table.dim() != 2:
         raise ValueError("block_table must have two dimensions [B,max_pages]")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    return (ctypes.c_longlong * 6)(ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    return _Strides(*k_cache.stride()[:3], *v_cache.stride()[:3])
 
 
 def gdr2_attn_step(q, k_cache, v_cache, block_table, lengths, *, scale=None, window=0, o=None, lse=None,
@@ -622,32 +637,33 @@ def gdr2_attn_step(q, k_cache, v_cache, block_table, lengths, *, scale=None, win
     B, Hq, D = q.shape
     if q.dtype not in _DT:
         raise ValueError("unsupported dtype %s" % q.dtype)
-    dt = _DT[q.dtype]
-    _check(q, "q", q.dtype, (B, Hq, D))
-    strides = _cache_dims(k_cache, v_cache, block_table, q.dtype, D)
+    dt, dev = _DT[q.dtype], _device_of(q, "q")
+    _want(q, "q", q.dtype, (B, Hq, D), dev)
+    strides = _cache_strides(k_cache, v_cache, block_table, q.dtype, D, dev)
     pages, page, Hkv = k_cache.shape[:3]
-    _index(block_table, "block_table", (B, block_table.shape[1]))
-    _index(lengths, "lengths", (B,))
+    max_pages = block_table.shape[1]
+    _want(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    _want(lengths, "lengths", torch.int32, (B,), dev)
     new = []
     if o is None:
         o = torch.empty_like(q)
         new.append(o)
     else:
-        _check(o, "o", q.dtype, (B, Hq, D))
-    if lse is None:
-        if return_lse:
-            lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
-            new.append(lse)
-    else:
-        _check(lse, "lse", torch.float32, (B, Hq))
+        _want(o, "o", q.dtype, (B, Hq, D), dev)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, (B, Hq), dev)
+    elif return_lse:
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device)
+        new.append(lse)
     if ws is None:
         ws = torch.empty(gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dt), dtype=torch.uint8, device=q.device)
         new.append(ws)
-    _same_device(q, k_cache, v_cache, block_table, lengths, o, lse, ws)
+    else:
+        _want(ws, "ws", torch.uint8, ws.shape, dev)
     _keep_for(stream, *new)
-    with _on(q, stream) as s:
+    with _on(dev, stream) as s:
         st = lib.gdr2_attn_step(_adr(q), _adr(k_cache), _adr(v_cache), strides, _adr(block_table), _adr(lengths),
-                                _adr(o), _adr(lse), B, Hq, Hkv, D, pages, page, block_table.shape[1],
+                                _adr(o), _adr(lse), B, Hq, Hkv, D, pages, page, max_pages,
                                 D ** -0.5 if scale is None else scale, window, dt, _adr(ws), ws.numel(), s)
     _raise(st, "gdr2_attn_step")
     return o if lse is None else (o, lse)
@@ -664,23 +680,22 @@ def gdr2_kv_append(k, v, k_cache, v_cache, block_table, starts, *, cu_seqlens=No
     tokens, Hkv, D = k.shape
     if k.dtype not in _DT:
         raise ValueError("unsupported dtype %s" % k.dtype)
-    _check(k, "k", k.dtype, (tokens, Hkv, D))
-    _check(v, "v", k.dtype, (tokens, Hkv, D))
-    strides = _cache_dims(k_cache, v_cache, block_table, k.dtype, D)
+    dev = _device_of(k, "k")
+    _want(k, "k", k.dtype, (tokens, Hkv, D), dev)
+    _want(v, "v", k.dtype, (tokens, Hkv, D), dev)
+    strides = _cache_strides(k_cache, v_cache, block_table, k.dtype, D, dev)
     if k_cache.shape[2] != Hkv:
         raise ValueError("k_cache must have %d heads, got %d" % (Hkv, k_cache.shape[2]))
-    B = block_table.shape[0]
-    _index(block_table, "block_table", (B, block_table.shape[1]))
-    _index(starts, "starts", (B,))
-    if cu_seqlens is None:
-        if tokens != B:
-            raise ValueError("without cu_seqlens there is one token a sequence, got %d tokens for %d sequences"
-                             % (tokens, B))
-    else:
-        _index(cu_seqlens, "cu_seqlens", (B + 1,))
-    _same_device(k, v, k_cache, v_cache, block_table, starts, cu_seqlens)
-    with _on(k, stream) as s:
+    B, max_pages = block_table.shape
+    _want(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    _want(starts, "starts", torch.int32, (B,), dev)
+    if cu_seqlens is not None:
+        _want(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    elif tokens != B:
+        raise ValueError("without cu_seqlens there is one token a sequence, got %d tokens for %d sequences"
+                         % (tokens, B))
+    with _on(dev, stream) as s:
         st = lib.gdr2_kv_append(_adr(k), _adr(v), _adr(k_cache), _adr(v_cache), strides, _adr(block_table),
                                 _adr(starts), _adr(cu_seqlens), B, tokens, Hkv, D, k_cache.shape[0], k_cache.shape[1],
-                                block_table.shape[1], _DT[k.dtype], s)
+                                max_pages, _DT[k.dtype], s)
     _raise(st, "gdr2_kv_append")

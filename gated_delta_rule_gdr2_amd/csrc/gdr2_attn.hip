@@ -16,10 +16,12 @@
 // 4 (lane / 16) + i. Values: a lane loads D / 16 consecutive channels of those same tokens and
 // transposes its 8 x 8 block in registers (one byte permute per pair of elements).
 //
-// Work is split evenly over a fixed number of workgroups whatever the lengths: the units (32 tokens
-// in bf16, 16 in fp32) of all (sequence, head group) rows form one line, and each workgroup takes an
-// equal run of it, its four waves the units in turn. A row inside one run is finished there; a row
-// that crosses runs leaves partial sums, joined in a fixed order by a second kernel.
+// Long rows are split evenly over a fixed number of workgroups whatever the lengths: the units (32
+// tokens in bf16, 16 in fp32) of all (sequence, head group) rows form one line, with ATTN_COST places
+// before each row for what a row costs by itself, and each workgroup takes an equal run of the line,
+// its eight waves the units in turn. A row inside one run is finished there; a row that crosses runs
+// leaves partial sums, joined in a fixed order by a second kernel. Where no row can be long, each
+// workgroup takes one row and there is nothing to join (attn_rows_mode).
 #include "gdr2_attn.hpp"
 #include "gdr2_device.hpp"
 
@@ -27,7 +29,9 @@ namespace gdr2 {
 
 template <class OT>
 constexpr int attn_unit() { return sizeof(OT) == 2 ? 32 : 16; }
-constexpr int ATTN_MIN_UNITS = 4;  // of a workgroup: one for each wave
+constexpr int AW = 8;           // waves of a workgroup
+constexpr int ATTN_COST = 6;    // of a row, in units: its own loads and its waves' join
+constexpr int ATTN_MIN = 14;    // places of the line a workgroup takes at least (ATTN_COST + a unit for each wave)
 
 // The visible tokens of sequence b and its units (at least one, so that every row is written).
 struct AttnSpan {
@@ -46,43 +50,33 @@ __device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, int b) {
     return s;
 }
 
-// Exclusive prefix sums of the sequences' units, by the whole workgroup of 256: thread t holds the
-// sum before its run of `per` consecutive sequences; returns the total.
-struct AttnPrefix {
-    long long before, total;
+// The line of all rows, computed by each wave for itself: lane t holds the place before its run of
+// `per` consecutive sequences. A workgroup takes `share` places. (The host checks that they are fewer
+// than 2^31.)
+struct AttnLine {
+    unsigned before, total, share;
     int per;
 };
 template <class OT>
-__device__ __forceinline__ AttnPrefix attn_prefix(const AttnArgs& a, long long* s4) {
-    const int tid = threadIdx.x, l = tid & 63, wv = tid >> 6;
-    AttnPrefix p;
-    p.per = (a.B + 255) / 256;
-    long long own = 0;
+__device__ __forceinline__ AttnLine attn_line(const AttnArgs& a) {
+    const int l = lane_id(), HR = a.Hkv * a.NG;
+    AttnLine p;
+    p.per = (a.B + 63) / 64;
+    unsigned own = 0;
     for (int i = 0; i < p.per; ++i) {
-        const int b = tid * p.per + i;
-        if (b < a.B) own += attn_span<OT>(a, b).units;
+        const int b = l * p.per + i;
+        if (b < a.B) own += (attn_span<OT>(a, b).units + ATTN_COST) * HR;
     }
-    long long x = own;
+    unsigned x = own;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
-        const long long y = __shfl_up(x, o);
+        const unsigned y = __shfl_up(x, o);
         if (l >= o) x += y;
     }
-    if (l == 63) s4[wv] = x;
-    __syncthreads();
     p.before = x - own;
-    p.total = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        if (w < wv) p.before += s4[w];
-        p.total += s4[w];
-    }
+    p.total = __builtin_amdgcn_readlane(x, 63);
+    p.share = max((p.total + a.wgs - 1) / a.wgs, (unsigned)ATTN_MIN);
     return p;
-}
-// workgroups that take part: no more than leave each its minimum of units
-__device__ __forceinline__ long long attn_parts(const AttnArgs& a, long long total) {
-    const long long n = (total + ATTN_MIN_UNITS - 1) / ATTN_MIN_UNITS;
-    return n < a.wgs ? n : a.wgs;
 }
 
 // One unit's keys and values in registers, as loaded.
@@ -234,155 +228,168 @@ __device__ __forceinline__ void attn_update(const AttnArgs& a, const AttnSpan& s
     }
 }
 
+// One run of a row by the workgroup's waves: units i0 .. i0 + n - 1 of the row's; whole: the whole row,
+// finished here, else its partial sums go to `part`.
 template <class OT, int D>
-__global__ __launch_bounds__(256, 2) void k_attn(AttnArgs a) {
+__device__ __forceinline__ void attn_run(const AttnArgs& a, int b, int hr, const AttnSpan& sp, int i0, int n, bool whole,
+                                         float* part, float (&sml)[2][AW][16], float (&so)[AW][16][D + 4]) {
     constexpr int U = attn_unit<OT>(), EV = D / 16;
     using QT = typename std::conditional<sizeof(OT) == 2, bf16x8, f32x4>::type;
     constexpr int NQ = sizeof(OT) == 2 ? D / 32 : D / 16;
-    __shared__ long long s4[4];
-    __shared__ int sfind[2];
-    __shared__ float sml[2][4][16];
-    __shared__ __align__(16) float so[4][16][D + 4];
+    const int tid = threadIdx.x, l = tid & 63, li = l & 15, lq = l >> 4;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int hkv = hr / a.NG, h0 = hkv * a.G + (hr % a.NG) * a.gh;  // first query head of the row
+    const int heads = min(a.gh, a.G - (hr % a.NG) * a.gh);
+    const int u0 = sp.u0 + i0;
+    const int work = sp.hi > sp.lo ? n : 0;  // a row with nothing to see has a unit, but no page to read
+    auto pages = [&](int i, int (&pg)[2]) {  // pages of unit i of the run
+#pragma unroll
+        for (int s = 0; s < U / 16; ++s) {
+            const int tok = (u0 + i) * U + 16 * s;
+            pg[s] = -1;
+            if (i < work && tok < sp.hi) {
+                const int p = a.c.table[(size_t)b * a.c.max_pages + (tok >> a.c.shift)];
+                pg[s] = (unsigned)p < (unsigned)a.c.pages ? p : -1;
+            }
+        }
+    };
+    int pg[2] = {-1, -1};
+    pages(wv, pg);
+    QT q[NQ];
+    {
+        const OT* qp = (const OT*)a.q + ((size_t)b * a.Hq + h0 + min(li, heads - 1)) * D;
+#pragma unroll
+        for (int kb = 0; kb < NQ; ++kb) {
+            if constexpr (sizeof(OT) == 2) q[kb] = *(const QT*)(qp + 32 * kb + 8 * lq);
+            else q[kb] = *(const QT*)(qp + 16 * kb + 4 * lq);
+        }
+    }
+    AttnState<D> st;
+    st.m = -INFINITY;
+    st.l = 0.f;
+#pragma unroll
+    for (int j = 0; j < EV; ++j) st.acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // the wave's units wv, wv + AW, ..: the next one's keys and values are on their way while this one
+    // is worked on, and the page of the one after that is looked up
+    AttnTile<OT, D> t0, t1;
+    if (wv < work) {
+        attn_load<OT, D>(a, u0 + wv, hkv, pg, t0);
+        pages(wv + AW, pg);
+    }
+#pragma unroll 1
+    for (int i = wv; i < work; i += 2 * AW) {
+        if (i + AW < work) {
+            attn_load<OT, D>(a, u0 + i + AW, hkv, pg, t1);
+            pages(i + 2 * AW, pg);
+        }
+        attn_update<OT, D>(a, sp, u0 + i, t0, q, st);
+        if (i + AW >= work) break;
+        if (i + 2 * AW < work) {
+            attn_load<OT, D>(a, u0 + i + 2 * AW, hkv, pg, t0);
+            pages(i + 3 * AW, pg);
+        }
+        attn_update<OT, D>(a, sp, u0 + i + AW, t1, q, st);
+    }
+    // ---- join the waves
+    st.l += __shfl_xor(st.l, 16);
+    st.l += __shfl_xor(st.l, 32);
+    if (lq == 0) {
+        sml[0][wv][li] = st.m;
+        sml[1][wv][li] = st.l;
+    }
+    __syncthreads();
+    float M = sml[0][0][li];
+#pragma unroll
+    for (int x = 1; x < AW; ++x) M = fmaxf(M, sml[0][x][li]);
+    const float f = __builtin_amdgcn_exp2f(st.m - (M == -INFINITY ? 0.f : M));
+    if (li < heads) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j4 = 0; j4 < EV; j4 += 4) {
+                f32x4 x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = st.acc[j4 + j][i] * f;
+                *(f32x4*)&so[wv][li][EV * (4 * lq + i) + j4] = x;
+            }
+    }
+    __syncthreads();
+    for (int e = tid; e < heads * (D / 4); e += 64 * AW) {
+        const int hd = e / (D / 4), d = 4 * (e % (D / 4));
+        f32x4 x = *(const f32x4*)&so[0][hd][d];
+#pragma unroll
+        for (int y = 1; y < AW; ++y) x += *(const f32x4*)&so[y][hd][d];
+        float Mh = sml[0][0][hd];
+#pragma unroll
+        for (int y = 1; y < AW; ++y) Mh = fmaxf(Mh, sml[0][y][hd]);
+        const float mu = Mh == -INFINITY ? 0.f : Mh;
+        float L = 0.f;
+#pragma unroll
+        for (int y = 0; y < AW; ++y) L += sml[1][y][hd] * __builtin_amdgcn_exp2f(sml[0][y][hd] - mu);
+        if (whole) {
+            const float r = L == 0.f ? 0.f : 1.f / L;  // nothing visible: a row of zeros
+            const float ov[4] = {x[0] * r, x[1] * r, x[2] * r, x[3] * r};
+            st4((OT*)a.o + ((size_t)b * a.Hq + h0 + hd) * D + d, ov);
+            if (a.lse && d == 0)
+                a.lse[(size_t)b * a.Hq + h0 + hd] = L == 0.f ? -INFINITY : (Mh + __log2f(L)) * 0.6931471805599453f;
+        } else {
+            *(f32x4*)(part + (size_t)hd * D + d) = x;
+            if (d == 0) {
+                part[(size_t)a.gh * D + 2 * hd] = Mh;
+                part[(size_t)a.gh * D + 2 * hd + 1] = L;
+            }
+        }
+    }
+}
+
+// SPLIT: the line of rows, an equal run a workgroup; else one row a workgroup.
+template <class OT, int D, bool SPLIT>
+__global__ __launch_bounds__(64 * AW) void k_attn(AttnArgs a) {
+    __shared__ float sml[2][AW][16];
+    __shared__ __align__(16) float so[AW][16][D + 4];
     poison_lds((lds_char*)sml, sizeof(sml));
     poison_lds((lds_char*)so, sizeof(so));
     poison_lds_done();
-    const int tid = threadIdx.x, l = tid & 63, li = l & 15, lq = l >> 4;
-    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int HR = a.Hkv * a.NG;  // rows of a sequence
-    const AttnPrefix pre = attn_prefix<OT>(a, s4);
-    const long long total = pre.total * HR, parts = attn_parts(a, total);
-    const long long w = blockIdx.x;
-    if (w >= parts) return;
-    long long t = w * total / parts;
-    const long long tend = (w + 1) * total / parts;
-    // the sequence that holds unit t: the thread whose run of sequences does finds it
-    {
-        long long at = pre.before * HR;
-        for (int i = 0; i < pre.per; ++i) {
-            const int b = tid * pre.per + i;
-            if (b >= a.B) break;
-            const long long n = (long long)attn_span<OT>(a, b).units * HR;
-            if (t >= at && t < at + n) {
-                sfind[0] = b;
-                sfind[1] = (int)(t - at);
-            }
-            at += n;
-        }
-    }
-    __syncthreads();
-    int b = sfind[0];
-    int off = sfind[1];  // unit inside the sequence's HR x units
-    bool first = true;   // the run's first row (its partial result goes to slot 0, a later one's to 1)
-    while (t < tend) {
+    if constexpr (!SPLIT) {
+        const int b = blockIdx.x / HR, hr = blockIdx.x % HR;
         const AttnSpan sp = attn_span<OT>(a, b);
-        const int hr = off / sp.units, i0 = off % sp.units;
-        const int n = (int)((tend - t) < (long long)(sp.units - i0) ? (tend - t) : (long long)(sp.units - i0));
-        const int hkv = hr / a.NG, h0 = hkv * a.G + (hr % a.NG) * a.gh;  // first query head of the row
-        const int heads = min(a.gh, a.G - (hr % a.NG) * a.gh);
-        QT q[NQ];
-        {
-            const OT* qp = (const OT*)a.q + ((size_t)b * a.Hq + h0 + min(li, heads - 1)) * D;
-#pragma unroll
-            for (int kb = 0; kb < NQ; ++kb) {
-                if constexpr (sizeof(OT) == 2) q[kb] = *(const QT*)(qp + 32 * kb + 8 * lq);
-                else q[kb] = *(const QT*)(qp + 16 * kb + 4 * lq);
-            }
+        attn_run<OT, D>(a, b, hr, sp, 0, sp.units, true, nullptr, sml, so);
+        return;
+    }
+    const AttnLine line = attn_line<OT>(a);
+    unsigned t = blockIdx.x * line.share;
+    if (t >= line.total) return;
+    const unsigned tend = min(t + line.share, line.total);
+    // the sequence that holds place t: the last run of sequences that does not begin behind it, then
+    // through that run
+    const int ln = __popcll(__ballot(line.before <= t && lane_id() * line.per < a.B)) - 1;
+    int b = ln * line.per;
+    unsigned at = __builtin_amdgcn_readlane(line.before, ln);
+    AttnSpan sp = attn_span<OT>(a, b);
+    while (t >= at + (sp.units + ATTN_COST) * HR) {
+        at += (sp.units + ATTN_COST) * HR;
+        sp = attn_span<OT>(a, ++b);
+    }
+    while (t < tend) {
+        const int len = sp.units + ATTN_COST;
+        const int hr = (t - at) / len;
+        const unsigned r0 = at + (unsigned)hr * len;             // the row's first place
+        const unsigned r1 = min(r0 + len, tend);
+        // its units in this run: place r0 + ATTN_COST + i is unit i
+        const int i0 = max(0, (int)(t - r0) - ATTN_COST), i1 = max(0, (int)(r1 - r0) - ATTN_COST);
+        if (i1 > i0) {
+            const bool whole = i1 - i0 == sp.units;
+            // a row that goes on from the workgroup before leaves its sums in slot 0, one that begins
+            // here and goes on in slot 1: there is at most one of each
+            float* part = a.part + (size_t)(2 * blockIdx.x + (i0 > 0 ? 0 : 1)) * ((size_t)a.gh * (D + 4));
+            attn_run<OT, D>(a, b, hr, sp, i0, i1 - i0, whole, part, sml, so);
+            __syncthreads();
         }
-        AttnState<D> st;
-        st.m = -INFINITY;
-        st.l = 0.f;
-#pragma unroll
-        for (int j = 0; j < EV; ++j) st.acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int u0 = sp.u0 + i0;
-        const int work = sp.hi > sp.lo ? n : 0;  // a row with nothing to see has a unit, but no page to read
-        auto pages = [&](int i, int (&pg)[2]) {  // pages of unit i of the segment
-#pragma unroll
-            for (int s = 0; s < U / 16; ++s) {
-                const int tok = (u0 + i) * U + 16 * s;
-                pg[s] = -1;
-                if (i < work && tok < sp.hi) {
-                    const int p = a.c.table[(size_t)b * a.c.max_pages + (tok >> a.c.shift)];
-                    pg[s] = (unsigned)p < (unsigned)a.c.pages ? p : -1;
-                }
-            }
-        };
-        // the wave's units wv, wv + 4, ..: the next one's keys and values are on their way while
-        // this one is worked on, and the page of the one after that is looked up
-        AttnTile<OT, D> cur, nxt;
-        int pg[2] = {-1, -1};
-        if (wv < work) {
-            pages(wv, pg);
-            attn_load<OT, D>(a, u0 + wv, hkv, pg, cur);
-            pages(wv + 4, pg);
-        }
-        for (int i = wv; i < work; i += 4) {
-            if (i + 4 < work) {
-                attn_load<OT, D>(a, u0 + i + 4, hkv, pg, nxt);
-                pages(i + 8, pg);
-            }
-            attn_update<OT, D>(a, sp, u0 + i, cur, q, st);
-            cur = nxt;
-        }
-        // ---- join the four waves
-        st.l += __shfl_xor(st.l, 16);
-        st.l += __shfl_xor(st.l, 32);
-        if (lq == 0) {
-            sml[0][wv][li] = st.m;
-            sml[1][wv][li] = st.l;
-        }
-        __syncthreads();
-        float M = sml[0][0][li];
-#pragma unroll
-        for (int x = 1; x < 4; ++x) M = fmaxf(M, sml[0][x][li]);
-        const float Mu = M == -INFINITY ? 0.f : M;
-        const float f = __builtin_amdgcn_exp2f(st.m - Mu);
-        if (li < heads) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j4 = 0; j4 < EV; j4 += 4) {
-                    f32x4 x;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = st.acc[j4 + j][i] * f;
-                    *(f32x4*)&so[wv][li][EV * (4 * lq + i) + j4] = x;
-                }
-        }
-        __syncthreads();
-        const bool whole = n == sp.units;
-        float* part = a.part + (size_t)(2 * w + (first ? 0 : 1)) * ((size_t)a.gh * (D + 4));
-        for (int e = tid; e < heads * (D / 4); e += 256) {
-            const int hd = e / (D / 4), d = 4 * (e % (D / 4));
-            f32x4 x = *(const f32x4*)&so[0][hd][d];
-#pragma unroll
-            for (int y = 1; y < 4; ++y) x += *(const f32x4*)&so[y][hd][d];
-            float Mh = sml[0][0][hd];
-#pragma unroll
-            for (int y = 1; y < 4; ++y) Mh = fmaxf(Mh, sml[0][y][hd]);
-            const float mu = Mh == -INFINITY ? 0.f : Mh;
-            float L = 0.f;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) L += sml[1][y][hd] * __builtin_amdgcn_exp2f(sml[0][y][hd] - mu);
-            if (whole) {
-                const float r = L == 0.f ? 0.f : 1.f / L;  // nothing visible: a row of zeros
-                const float ov[4] = {x[0] * r, x[1] * r, x[2] * r, x[3] * r};
-                st4((OT*)a.o + ((size_t)b * a.Hq + h0 + hd) * D + d, ov);
-                if (a.lse && d == 0)
-                    a.lse[(size_t)b * a.Hq + h0 + hd] = L == 0.f ? -INFINITY : (Mh + __log2f(L)) * 0.6931471805599453f;
-            } else {
-                *(f32x4*)(part + (size_t)hd * D + d) = x;
-                if (d == 0) {
-                    part[(size_t)a.gh * D + 2 * hd] = Mh;
-                    part[(size_t)a.gh * D + 2 * hd + 1] = L;
-                }
-            }
-        }
-        __syncthreads();
-        first = false;
-        t += n;
-        off += n;
-        if (off == sp.units * HR) {
-            off = 0;
-            ++b;
+        t = r1;
+        if (t < tend && t == at + (unsigned)len * HR) {
+            at = t;
+            sp = attn_span<OT>(a, ++b);
         }
     }
 }
@@ -392,33 +399,26 @@ __global__ __launch_bounds__(256, 2) void k_attn(AttnArgs a) {
 template <class OT, int D>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     constexpr int NGRP = 256 / (D / 4);  // thread groups over the parts
-    __shared__ long long s4[4];
-    __shared__ long long sbase;
     __shared__ float sM[NGRP], sL[NGRP];
     __shared__ __align__(16) float so[NGRP][D];
     const int tid = threadIdx.x;
     const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
     const int hkv = hq / a.G, grp = (hq % a.G) / a.gh, hd = (hq % a.G) % a.gh;
     const int HR = a.Hkv * a.NG, hr = hkv * a.NG + grp;
-    const AttnPrefix pre = attn_prefix<OT>(a, s4);
-    const long long total = pre.total * HR, parts = attn_parts(a, total);
-    if (tid == b / pre.per) {
-        long long at = pre.before;
-        for (int i = tid * pre.per; i < b; ++i) at += attn_span<OT>(a, i).units;
-        sbase = at;
-    }
-    __syncthreads();
+    const AttnLine line = attn_line<OT>(a);
     const AttnSpan sp = attn_span<OT>(a, b);
-    const long long t0 = sbase * HR + (long long)hr * sp.units, t1 = t0 + sp.units;
-    const long long w0 = ((t0 + 1) * parts - 1) / total, w1 = (t1 * parts - 1) / total;
+    const int ln = b / line.per;
+    unsigned at = __builtin_amdgcn_readlane(line.before, ln);
+    for (int i = ln * line.per; i < b; ++i) at += (attn_span<OT>(a, i).units + ATTN_COST) * HR;
+    const unsigned r0 = at + (unsigned)hr * (sp.units + ATTN_COST) + ATTN_COST;  // the place of its unit 0
+    const unsigned w0 = r0 / line.share, w1 = (r0 + sp.units - 1) / line.share;
     if (w0 == w1) return;  // written by the one workgroup that had it
-    const bool w0_first = w0 * total / parts == t0;
     const size_t stride = (size_t)a.gh * (D + 4);
     const int g = tid / (D / 4), d = 4 * (tid % (D / 4));
     float M = -INFINITY, L = 0.f;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    for (long long w = w0 + g; w <= w1; w += NGRP) {
-        const float* p = a.part + (size_t)(2 * w + (w == w0 && !w0_first ? 1 : 0)) * stride;
+    for (unsigned w = w0 + g; w <= w1; w += NGRP) {
+        const float* p = a.part + (size_t)(2 * w + (w == w0 ? 1 : 0)) * stride;
         const float m = p[(size_t)a.gh * D + 2 * hd], lw = p[(size_t)a.gh * D + 2 * hd + 1];
         const f32x4 y = *(const f32x4*)(p + (size_t)hd * D + d);
         const float mn = fmaxf(M, m), mu = mn == -INFINITY ? 0.f : mn;
@@ -453,11 +453,25 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     }
 }
 
+// One row a workgroup, without a second kernel: where a row has at most eight units for each wave
+// (whatever the number of rows, splitting it saves less than the join costs), or up to three times that
+// when there are rows enough for every compute unit.
+inline bool attn_rows_mode(const AttnArgs& a, int unit) {
+    long long tokens = (long long)a.c.max_pages << a.c.shift;
+    if (a.window > 0 && a.window < tokens) tokens = a.window + unit;  // a window may begin inside a unit
+    const long long units = (tokens + unit - 1) / unit, rows = (long long)a.B * a.Hkv * a.NG;
+    return units <= 8 * AW || (rows >= ATTN_WGS && units <= 24 * AW);
+}
+
 template <class OT, int D>
 static hipError_t launch_attn_t(const AttnArgs& a, hipStream_t stream) {
-    hipLaunchKernelGGL((k_attn<OT, D>), dim3(a.wgs), dim3(256), 0, stream, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.wgs == 1) return e;
+    if (attn_rows_mode(a, attn_unit<OT>())) {
+        hipLaunchKernelGGL((k_attn<OT, D, false>), dim3((unsigned)(a.B * a.Hkv * a.NG)), dim3(64 * AW), 0, stream, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((k_attn<OT, D, true>), dim3(a.wgs), dim3(64 * AW), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_attn_join<OT, D>), dim3((unsigned)(a.B * a.Hq)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }

@@ -36,7 +36,7 @@ struct AppendArgs {
     int B, tokens, Hkv, D;
 };
 
-constexpr int ATTN_WGS = 512;  // at most: two workgroups of four waves on each of the 256 compute units
+constexpr int ATTN_WGS = 256;  // one workgroup of eight waves on each of the 256 compute units
 
 // floats of one partial result: gh rows of D sums, then their maxima and weights (padded to 16 bytes)
 inline size_t attn_part_floats(int gh, int D) { return (size_t)gh * (D + 4); }

@@ -223,6 +223,8 @@ int gdr2_attn_step(const void* q, const void* k_cache, const void* v_cache, cons
     if (st != GDR2_OK) return st;
     if (!q || !o || !lengths) return GDR2_ERR_NULL;
     if (!isfinite(scale) || window < 0) return GDR2_ERR_VALUE;
+    // the units of all rows are numbered in 32 bits (units of 16 tokens, and a few more places a row)
+    if ((long long)B * Hq * (((long long)max_pages * page_size >> 4) + 16) > 0x7fffffffLL) return GDR2_ERR_SHAPE;
     const void* const ptrs[] = {q, k_cache, v_cache, o, workspace};
     if (!all_aligned(ptrs)) return GDR2_ERR_ALIGN;
     if (!workspace || workspace_bytes < gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dtype)) return GDR2_ERR_WORKSPACE;
