@@ -55,8 +55,8 @@ int sc_shape(int N, int T, int Hk, int Hv, int dk, int dv, int dtype, bool packe
 
 bool sc_no_tokens(int N, int T, int Hv) { return N == 0 || T == 0 || Hv == 0; }
 
-gdr2::ScLayout sc_layout_for(int N, int T, int Hv, int dk, int dv, int dtype, bool packed, bool train) {
-    return gdr2::sc_layout(sc_slots(N, T, packed) * Hv, dk, dv, esize(dtype), train);
+gdr2::ScLayout sc_layout_for(int N, int T, int Hv, int dk, int dv, int dtype, bool packed) {
+    return gdr2::sc_layout(sc_slots(N, T, packed) * Hv, dk, dv, esize(dtype));
 }
 
 int pass_state(float* dst, const float* src, int N, int Hv, int dk, int dv, void* stream) {
@@ -66,7 +66,7 @@ int pass_state(float* dst, const float* src, int N, int Hv, int dk, int dv, void
 }
 
 void sc_fill(gdr2::ScArgs& a, const int* cu, int N, int T, int Hk, int Hv, int dk, int dv, int dtype, int zero_rest,
-             bool train, void* ws) {
+             void* ws) {
     a.cu = cu;
     a.N = N;
     a.T = T;
@@ -77,7 +77,7 @@ void sc_fill(gdr2::ScArgs& a, const int* cu, int N, int T, int Hk, int Hv, int d
     a.DV = dv;
     a.slots = (int)sc_slots(N, T, cu != nullptr);
     a.zero_rest = zero_rest;
-    a.L = sc_layout_for(N, T, Hv, dk, dv, dtype, cu != nullptr, train);
+    a.L = sc_layout_for(N, T, Hv, dk, dv, dtype, cu != nullptr);
     a.ws = (char*)ws;
 }
 
@@ -127,7 +127,7 @@ extern "C" {
 size_t gdr2_scalar_workspace_bytes(int N, int T, int Hk, int Hv, int dk, int dv, int packed, int dtype,
                                    int save_for_bwd) {
     if (sc_shape(N, T, Hk, Hv, dk, dv, dtype, packed != 0) != GDR2_OK || sc_no_tokens(N, T, Hv)) return 0;
-    const gdr2::ScLayout L = sc_layout_for(N, T, Hv, dk, dv, dtype, packed != 0, save_for_bwd != 0);
+    const gdr2::ScLayout L = sc_layout_for(N, T, Hv, dk, dv, dtype, packed != 0);
     return save_for_bwd ? L.train_bytes : L.infer_bytes;
 }
 
@@ -150,7 +150,7 @@ int gdr2_scalar_fwd(const void* q, const void* k, const void* v, const void* g, 
     gdr2::ScArgs a = {};
     a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta;
     a.h0 = h0; a.o = o; a.ht = ht;
-    sc_fill(a, cu_seqlens, N, T, Hk, Hv, dk, dv, dtype, zero_rest, save_for_bwd != 0, workspace);
+    sc_fill(a, cu_seqlens, N, T, Hk, Hv, dk, dv, dtype, zero_rest, workspace);
     return gdr2::launch_sc_fwd(a, dtype == GDR2_DTYPE_BF16, save_for_bwd != 0, (hipStream_t)stream) == hipSuccess
                ? GDR2_OK : GDR2_ERR_HIP;
 }
@@ -175,7 +175,7 @@ int gdr2_scalar_bwd(const void* q, const void* k, const void* v, const void* g, 
     a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta;
     a.h0 = h0; a.dout = dout; a.dht = dht;
     a.dq = dq; a.dk = dk_; a.dv = dv_; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
-    sc_fill(a, cu_seqlens, N, T, Hk, Hv, dk, dv, dtype, zero_rest, true, workspace);
+    sc_fill(a, cu_seqlens, N, T, Hk, Hv, dk, dv, dtype, zero_rest, workspace);
     const bool bf = dtype == GDR2_DTYPE_BF16;
     hipError_t e = hipSuccess;
     if (!fwd_saved) e = gdr2::launch_sc_fwd(a, bf, true, (hipStream_t)stream);

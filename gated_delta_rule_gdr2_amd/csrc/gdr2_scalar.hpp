@@ -25,25 +25,27 @@ namespace gdr2 {
 // Per (chunk slot, value head) arrays, id = slot * Hv + head, in the operand type unless said:
 //   T     : images (fimg) of T, [NS][64][64]: NS = 2 for bf16, a bf16 value and the bf16 value
 //           of what its rounding left over (together 16 bits of mantissa), 1 for fp32
-//   M     : image of M, [64][64]; training with bf16: also its remainder
+//   M     : image of M, [64][64]
 //   vec   : fp32 rows of 64: e^gam, beta, tail (all zero in padding rows), gam as a float and its
 //           remainder; element 320 is e^gamC
+//   training only: T^T and M^T, [NS][64][64] each (the backward chain reads their rows straight into
+//   registers; transposed out of LDS instead, they took a quarter of its LDS traffic)
 //   training only, each a row of 16-column slices [D / 16][rows][16]:
 //   S, dS : chunk start state and end-state gradient, rows = key channels
 //   Delta, dY : rows = tokens
 struct ScLayout {
     size_t t, m, vec, s, d;                              // element counts per id
-    size_t o_t, o_m, o_vec, o_s, o_ds, o_delta, o_dy;    // byte offsets
+    size_t o_t, o_m, o_vec, o_tt, o_mt, o_s, o_ds, o_delta, o_dy;  // byte offsets (T^T, M^T: counts as T)
     size_t infer_bytes, train_bytes;
 };
 
 constexpr int SC_E = 0, SC_BETA = 64, SC_TAIL = 128, SC_GHI = 192, SC_GLO = 256, SC_EC = 320, SC_VEC = 384;
 
-inline ScLayout sc_layout(long long ids, int DK, int DV, int esz, bool train) {
+inline ScLayout sc_layout(long long ids, int DK, int DV, int esz) {
     ScLayout L;
     const size_t ns = esz == 2 ? 2 : 1;
     L.t = ns * 64 * 64;
-    L.m = (train ? ns : 1) * 64 * 64;
+    L.m = 64 * 64;
     L.vec = SC_VEC;
     L.s = (size_t)DK * DV;
     L.d = (size_t)64 * DV;
@@ -57,6 +59,8 @@ inline ScLayout sc_layout(long long ids, int DK, int DV, int esz, bool train) {
     L.o_m = take(L.m, esz);
     L.o_vec = take(L.vec, 4);
     L.infer_bytes = off;
+    L.o_tt = take(L.t, esz);
+    L.o_mt = take(L.t, esz);
     L.o_s = take(L.s, esz);
     L.o_ds = take(L.s, esz);
     L.o_delta = take(L.d, esz);

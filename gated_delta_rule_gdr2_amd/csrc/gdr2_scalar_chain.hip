@@ -22,6 +22,8 @@
 //
 // The producers stream a chunk's operands into LDS by asynchronous DMA, 16 bytes a lane, into two
 // buffers, the next chunk's while this one's step runs.
+#include <type_traits>
+
 #include "gdr2_intra_common.hpp"
 #include "gdr2_scalar_device.hpp"
 
@@ -32,18 +34,7 @@ constexpr int SC_NP = 2;  // producer waves
 
 __device__ __forceinline__ int sc_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// Producer pi's share of a copy of BYTES (a multiple of 1024) into LDS: 1 KB pieces pi, pi + SC_NP, ...
-template <int BYTES>
-__device__ __forceinline__ void sc_dma(const char* src, lds_char* dst, int pi) {
-    static_assert(BYTES % (1024 * SC_NP) == 0, "the same number of whole kilobytes for each producer");
-    const unsigned lo = lane_id() * 16;
-    src += pi * 1024;
-    dst += pi * 1024;
-#pragma unroll
-    for (int k = 0; k < BYTES / 1024; k += SC_NP)
-        __builtin_amdgcn_global_load_lds(src + k * 1024 + lo, (lds_void*)(dst + k * 1024), 16, 0, 0);
-}
-// ... of the 64 rows of a row-major tensor (row stride rs bytes, RL elements read of each) into a
+// Producer pi's share of a copy of the 64 rows of a row-major tensor (row stride rs bytes, RL elements read of each) into a
 // swizzled tile. A lane's place in a row group, swizzle included, repeats every 16 rows, so the lane
 // part of the addresses is computed once (RowLanes) and a copy costs an addition to a scalar base:
 // the producers' time is issue time, and with addresses computed copy by copy they held up the step.
@@ -110,28 +101,29 @@ __device__ __forceinline__ void sc_chain_map(int gid, int pairs, int NJ, int& s,
     }
 }
 
-template <class OT, int DK, bool BWD>
+// NC: 16-column tiles of the value axis a workgroup walks
+template <class OT, int DK, int NC, bool BWD>
 struct ScChainLds {  // one operand buffer, and the exchange
     static constexpr int ES = sizeof(OT), NS = Split<OT>::NS, NKB = DK / 32;
-    static constexpr int SQ = CH * CH * ES;
     static constexpr int K = 0;
     static constexpr int Q = K + CH * DK * ES;
-    static constexpr int V = Q + CH * DK * ES;        // v (forward) or dO (backward), [64][16]
-    static constexpr int T = V + CH * 16 * ES;        // backward: NS images of T and of M
-    static constexpr int M = T + (BWD ? NS : 0) * SQ;
-    static constexpr int VEC = M + (BWD ? NS : 0) * SQ;
+    static constexpr int V = Q + CH * DK * ES;        // v (forward) or dO (backward), NC tiles [64][16]
+    static constexpr int VT = CH * 16 * ES;
+    static constexpr int VEC = V + NC * VT;
     static constexpr int BYTES = VEC + 2048;          // SC_VEC floats, in whole kilobytes
     static constexpr int F = xfrag<OT>();
-    static constexpr int XS = 0;                      // state slice: NS x NKB fragments
+    // exchange, for each column tile
+    static constexpr int XS = 0;                      // state: NS x NKB fragments
     static constexpr int XX = XS + NS * NKB * F;      // X or dDelta: NS x 2
-    static constexpr int XD = XX + NS * 2 * F;        // tail Delta or beta e^gam dY: NS x 2
+    static constexpr int XD = XX + NS * 2 * F;        // tail Delta or -beta e^gam dY: NS x 2
     static constexpr int XO = XD + NS * 2 * F;        // Delta or dY, one part: 2
-    static constexpr int XBYTES = XO + 2 * F;
+    static constexpr int XP = XO + 2 * F;             // backward: Q^T (e^gam dO), fp32 accumulator tiles
+    static constexpr int XT = XP + (BWD ? DK / 16 * 1024 : 0);
+    static constexpr int XBYTES = NC * XT;
     static_assert(2 * BYTES + XBYTES + 256 <= 160 * 1024, "two operand buffers fit");
 };
 
-// Where a walk finds its data.
-template <class OT>
+// Where a walk finds its data; j: its workgroup among those of the (sequence, value head).
 struct ScWalk {
     ScSeq q;
     int h, hk, j;
@@ -141,83 +133,81 @@ struct ScWalk {
 
 // A producer's side: the operands of chunk index(n), n = 0 .. nt - 1, into buffer n % 2. Takes part
 // in the step's barriers.
-template <class OT, int DK, int DV, bool BWD>
-__device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk<OT>& w, lds_char* b0, lds_char* b1,
-                                           lds_char* pf, int pi) {
-    using B = ScChainLds<OT, DK, BWD>;
+template <class OT, int DK, int DV, int NC, bool BWD>
+__device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds_char* b0, lds_char* b1, lds_char* pf,
+                                           int pi) {
+    using B = ScChainLds<OT, DK, NC, BWD>;
+    constexpr int ES = B::ES, NJ = DV / (16 * NC);
     const int nt = w.q.nt;
-    const size_t rsk = (size_t)a.Hk * DK, rsv = (size_t)a.Hv * DV;
-    const RowLanes<OT, DK> rl(rsk * B::ES);
-    // the operands of chunk index(n), in two parts: k, v (dO), the row factors and T; q and M
-    auto load1 = [&](int n) {
+    const size_t rsk = (size_t)a.Hk * DK * ES, rsv = (size_t)a.Hv * DV * ES;  // row strides, bytes
+    const RowLanes<OT, DK> rl(rsk);
+    struct Chunk {
+        const char *k, *q, *v, *f;
+        int nvalid;
+        size_t id;
+    };
+    auto chunk = [&](int n) {
         const int c = BWD ? nt - 1 - n : n;
-        lds_char* buf = (n & 1) ? b1 : b0;
         const long long row0 = w.q.tok0 + 64LL * c;
-        const int nvalid = min(CH, w.q.len - CH * c);
-        const size_t id = (size_t)(w.q.slot0 + c) * a.Hv + w.h;
-        sc_dma_rows<OT, DK>(rl, (const char*)((const OT*)a.k + row0 * rsk + (size_t)w.hk * DK), rsk * B::ES, nvalid,
-                            buf + B::K, pi);
-        const OT* v = BWD ? (const OT*)a.dout : (const OT*)a.v;
-        sc_dma_slice<OT>((const char*)(v + row0 * rsv + (size_t)w.h * DV + 16 * w.j), rsv * B::ES, nvalid, buf + B::V,
-                         pi);
+        Chunk x;
+        x.nvalid = min(CH, w.q.len - CH * c);
+        x.id = (size_t)(w.q.slot0 + c) * a.Hv + w.h;
+        x.k = (const char*)a.k + row0 * rsk + (size_t)w.hk * DK * ES;
+        x.q = (const char*)a.q + row0 * rsk + (size_t)w.hk * DK * ES;
+        x.v = (const char*)(BWD ? a.dout : a.v) + row0 * rsv + (size_t)w.h * DV * ES;
+        x.f = a.ws + a.L.o_vec + x.id * a.L.vec * 4;
+        return x;
+    };
+    auto load1 = [&](int n) {  // k, v (dO) and the row factors
+        const Chunk x = chunk(n);
+        lds_char* buf = (n & 1) ? b1 : b0;
+        sc_dma_rows<OT, DK>(rl, x.k, rsk, x.nvalid, buf + B::K, pi);
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch)
+            sc_dma_slice<OT>(x.v + 16 * (NC * w.j + ch) * ES, rsv, x.nvalid, buf + B::V + ch * B::VT, pi);
         // the row factors: 1.5 KB of the 2 KB the buffer has for them
-        const char* src = a.ws + a.L.o_vec + id * a.L.vec * 4;
         const unsigned lo = (pi == 0 ? lane_id() : 64 + (lane_id() & 31)) * 16;
-        __builtin_amdgcn_global_load_lds(src + lo, (lds_void*)(buf + B::VEC + pi * 1024), 16, 0, 0);
-        if constexpr (BWD) sc_dma<B::NS * B::SQ>(a.ws + a.L.o_t + id * a.L.t * B::ES, buf + B::T, pi);
+        const char* src = x.f + lo;
+        __builtin_amdgcn_global_load_lds(src, (lds_void*)(buf + B::VEC + pi * 1024), 16, 0, 0);
     };
-    auto load2 = [&](int n) {
+    auto load2 = [&](int n) {  // q
         if (!BWD && !a.o) return;
-        const int c = BWD ? nt - 1 - n : n;
-        lds_char* buf = (n & 1) ? b1 : b0;
-        const long long row0 = w.q.tok0 + 64LL * c;
-        const int nvalid = min(CH, w.q.len - CH * c);
-        const size_t id = (size_t)(w.q.slot0 + c) * a.Hv + w.h;
-        sc_dma_rows<OT, DK>(rl, (const char*)((const OT*)a.q + row0 * rsk + (size_t)w.hk * DK), rsk * B::ES, nvalid,
-                            buf + B::Q, pi);
-        if constexpr (BWD) sc_dma<B::NS * B::SQ>(a.ws + a.L.o_m + id * a.L.m * B::ES, buf + B::M, pi);
+        const Chunk x = chunk(n);
+        sc_dma_rows<OT, DK>(rl, x.q, rsk, x.nvalid, ((n & 1) ? b1 : b0) + B::Q, pi);
     };
-    // L2 prefetch of chunk index(n): one word of every 128-byte line of its operands, into a word of
-    // LDS that nothing reads. The lines are numbered 0 .. LINES - 1 over k, T, [q, M,] v (dO) and the row
-    // factors, and shared between the NJ slices of the (sequence, head), which sit on one L2.
-    constexpr int ES = B::ES, NJ = DV / 16;
-    constexpr int LPK = DK * ES / 128, LPV = DV * ES / 128;  // lines of a row
-    constexpr int LK = CH * LPK, LT = B::NS * B::SQ / 128, LM = (BWD ? B::NS : 1) * B::SQ / 128, LV = CH * LPV;
+    // L2 prefetch of chunk index(n): one word of every 128-byte line of what the workgroup reads of it,
+    // into a word of LDS that nothing reads. The lines are numbered over k, T, v (dO), q, M and the row
+    // factors, and shared between the NJ workgroups of the (sequence, head), which sit on one L2.
+    constexpr int LPK = DK * ES / 128, LPV = DV * ES / 128, SQ = CH * CH * ES;  // lines of a row; a 64 x 64 image
+    constexpr int LK = CH * LPK, LT = B::NS * SQ / 128, LM = (BWD ? B::NS : 1) * SQ / 128, LV = CH * LPV;
     constexpr int LVEC = SC_VEC * 4 / 128, LINES = 2 * LK + LT + LM + LV + LVEC;
     constexpr int NPF = (LINES + NJ * 64 * SC_NP - 1) / (NJ * 64 * SC_NP);
     auto prefetch = [&](int n) {  // (past the last chunk: the last one again, so that their number is fixed)
-        n = min(n, nt - 1);
-        const int c = BWD ? nt - 1 - n : n;
-        const long long row0 = w.q.tok0 + 64LL * c;
-        const int last = min(CH, w.q.len - CH * c) - 1;
-        const size_t id = (size_t)(w.q.slot0 + c) * a.Hv + w.h;
-        const char* kp = (const char*)((const OT*)a.k + row0 * rsk + (size_t)w.hk * DK);
-        const char* qp = (const char*)((const OT*)a.q + row0 * rsk + (size_t)w.hk * DK);
-        const char* vp = (const char*)((BWD ? (const OT*)a.dout : (const OT*)a.v) + row0 * rsv + (size_t)w.h * DV);
-        const char* tp = a.ws + a.L.o_t + id * a.L.t * ES;
-        const char* mp = a.ws + a.L.o_m + id * a.L.m * ES;
-        const char* fp = a.ws + a.L.o_vec + id * a.L.vec * 4;
+        const Chunk x = chunk(min(n, nt - 1));
+        const int last = x.nvalid - 1;
+        const char* tp = a.ws + (BWD ? a.L.o_tt : a.L.o_t) + x.id * a.L.t * ES;
+        const char* mp = a.ws + (BWD ? a.L.o_mt : a.L.o_m) + x.id * (BWD ? a.L.t : a.L.m) * ES;
 #pragma unroll
         for (int i = 0; i < NPF; ++i) {
             int v = ((i * SC_NP + pi) * 64 + lane_id()) * NJ + w.j;
             const char* p;
             if (v < LK) {
-                p = kp + (size_t)min(v / LPK, last) * rsk * ES + (v % LPK) * 128;
+                p = x.k + (size_t)min(v / LPK, last) * rsk + (v % LPK) * 128;
             } else if ((v -= LK) < LT) {
                 p = tp + v * 128;
             } else if ((v -= LT) < LV) {
-                p = vp + (size_t)min(v / LPV, last) * rsv * ES + (v % LPV) * 128;
+                p = x.v + (size_t)min(v / LPV, last) * rsv + (v % LPV) * 128;
             } else if ((v -= LV) < LK) {
-                p = qp + (size_t)min(v / LPK, last) * rsk * ES + (v % LPK) * 128;
+                p = x.q + (size_t)min(v / LPK, last) * rsk + (v % LPK) * 128;
             } else if ((v -= LK) < LM) {
                 p = mp + v * 128;
             } else {
-                p = fp + min(v - LM, LVEC - 1) * 128;
+                p = x.f + min(v - LM, LVEC - 1) * 128;
             }
             __builtin_amdgcn_global_load_lds(p, (lds_void*)(pf), 4, 0, 0);
         }
     };
-    constexpr int AHEAD = 3;  // chunks between a line's prefetch and its copy into LDS
+    constexpr int AHEAD = 3;  // chunks between a line's prefetch and its use
     load1(0);
     load2(0);
     for (int n = 1; n <= AHEAD; ++n) prefetch(n);
@@ -234,385 +224,527 @@ __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk<OT>& w,
     wait_vm<0>();  // no copy into this workgroup's LDS outlives it
 }
 
-// Compute waves: the products that lead from one state to the next, and nothing else. What a step
-// reads from its operand buffer is read as early as the buffer allows (T and K^T behind the reads that
-// the first product waits for), so that behind the barriers B and C only the exchanged fragments are
-// left to wait for.
-template <class OT, int DK, int DV>
-__device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk<OT>& w, int wv, lds_char* b0, lds_char* b1,
-                                            lds_char* xs) {
-    using B = ScChainLds<OT, DK, false>;
-    using FT = typename Frag<OT>::type;
-    constexpr int NS = B::NS, NKB = B::NKB, F = B::F, NT = DK / 64;  // NT: 16-row state tiles of a wave
-    const int l = lane_id(), li = l & 15, lq = l >> 4;
-    const int nt = w.q.nt;
-    // state tile t: key rows 16 (NT wv + t) + 4 lq + i, column 16 j + li
-    f32x4 S[NT];
-    auto publish_state = [&]() {
+// A wave's 16 rows of a pair of [64][64] images, straight from the workspace into registers: the fragments
+// are whole kilobytes there, each read by one wave, and would pass LDS twice for nothing.
+template <class OT, int NS>
+struct ImgRows {
+    typename Frag<OT>::type f[NS][2];
+    __device__ __forceinline__ void load(const OT* p, int wv) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) f[n][kb] = gfrag_img<OT, CH>(p + n * CH * CH, 16 * wv, 32 * kb);
+    }
+};
+
+// One wave's tiles of a state slice: tile t of column tile ch holds key rows 16 (NT wv + t) + 4 lq + i,
+// column 16 ch + li of the walk's columns.
+template <class OT, int DK, int NC, bool BWD>
+struct ScState {
+    using B = ScChainLds<OT, DK, NC, BWD>;
+    static constexpr int NT = DK / 64;
+    f32x4 s[NC][NT];
+    __device__ __forceinline__ void init(const float* m, int ld, int col, int wv) {
+        const int l = lane_id(), li = l & 15, lq = l >> 4;
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[ch][t][i] = m ? m[(size_t)(16 * (NT * wv + t) + 4 * lq + i) * ld + col + 16 * ch + li] : 0.f;
+    }
+    __device__ __forceinline__ void out(float* m, int ld, int col, int wv) const {
+        const int l = lane_id(), li = l & 15, lq = l >> 4;
+        if (!m) return;
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    m[(size_t)(16 * (NT * wv + t) + 4 * lq + i) * ld + col + 16 * ch + li] = s[ch][t][i];
+    }
+    __device__ __forceinline__ void publish(lds_char* xs, int ch, int wv) const {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int rt = NT * wv + t;
-            put_split<OT>(xs + B::XS + (rt >> 1) * F, NKB * F, rt & 1, S[t]);
+            put_split<OT>(xs + ch * B::XT + B::XS + (rt >> 1) * B::F, B::NKB * B::F, rt & 1, s[ch][t]);
         }
-    };
+    }
+};
+
+// Compute waves: the products that lead from one state to the next, and nothing else. What a step
+// reads from its operand buffer is read as early as the buffer allows (K^T behind the reads that the
+// second product waits for), so that behind the barrier C only the exchanged fragments are left to
+// wait for.
+template <class OT, int DK, int DV, int NC>
+__device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk& w, int wv, lds_char* b0, lds_char* b1,
+                                            lds_char* xs) {
+    using B = ScChainLds<OT, DK, NC, false>;
+    using FT = typename Frag<OT>::type;
+    constexpr int NS = B::NS, NKB = B::NKB, F = B::F, NT = DK / 64;
+    const int l = lane_id(), li = l & 15, lq = l >> 4;
+    const int nt = w.q.nt;
+    ScState<OT, DK, NC, false> S;
+    S.init(w.start, DV, 16 * NC * w.j, wv);
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            S[t][i] = w.start ? w.start[(size_t)(16 * (NT * wv + t) + 4 * lq + i) * DV + 16 * w.j + li] : 0.f;
-    publish_state();
-    // this wave's rows of T go from the workspace straight into registers, a step ahead
+    for (int ch = 0; ch < NC; ++ch) S.publish(xs, ch, wv);
     const OT* tp = (const OT*)(a.ws + a.L.o_t) + ((size_t)w.q.slot0 * a.Hv + w.h) * a.L.t;
     const size_t tstep = (size_t)a.Hv * a.L.t;
-    FT Tn[NS][2];
-    auto load_t = [&]() {
-#pragma unroll
-        for (int p = 0; p < NS; ++p)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) Tn[p][kb] = gfrag_img<OT, CH>(tp + p * CH * CH, 16 * wv, 32 * kb);
-    };
-    if (nt > 0) load_t();
+    ImgRows<OT, NS> T;  // a step ahead
+    if (nt > 0) T.load(tp, wv);
 #pragma unroll 1
     for (int n = 0; n < nt; ++n) {
         const lds_char* buf = (n & 1) ? b1 : b0;
         const LSwz<OT, DK> vK{buf + B::K};
         sync_lds();  // A: the state slice is published, the chunk's operands are in
-        FT SB[NS][NKB], Kf[NKB];
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-            Kf[kb] = lfrag_rowk8<OT>(vK, 16 * wv, 32 * kb);
-#pragma unroll
-            for (int p = 0; p < NS; ++p) SB[p][kb] = get_x<OT>(xs + B::XS + (p * NKB + kb) * F);
-        }
-        float e4[4], b4[4], t4[4], v4[4];
+        // X = beta (V - e^gam K S) on this wave's tokens
+        FT Kf[NKB];
+        float e4[4], b4[4], t4[4];
         lds_get4<float>(buf + B::VEC + (SC_E + 16 * wv + 4 * lq) * 4, e4);
         lds_get4<float>(buf + B::VEC + (SC_BETA + 16 * wv + 4 * lq) * 4, b4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v4[i] = lds_get1<OT>(buf + B::V + ((16 * wv + 4 * lq + i) * 16 + li) * B::ES);
+        for (int ch = 0; ch < NC; ++ch) {
+            lds_char* xc = xs + ch * B::XT;
+            FT SB[NS][NKB];
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                if (ch == 0) Kf[kb] = lfrag_rowk8<OT>(vK, 16 * wv, 32 * kb);
+#pragma unroll
+                for (int p = 0; p < NS; ++p) SB[p][kb] = get_x<OT>(xc + B::XS + (p * NKB + kb) * F);
+            }
+            float v4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v4[i] = lds_get1<OT>(buf + B::V + ch * B::VT + ((16 * wv + 4 * lq + i) * 16 + li) * B::ES);
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 Y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+                for (int p = 0; p < NS; ++p) mma(Y[2 * (kb & 1) + p], Kf[kb], SB[p][kb]);
+            Y[0] = (Y[0] + Y[2]) + (Y[1] + Y[3]);
+            f32x4 X;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) X[i] = b4[i] * (v4[i] - e4[i] * Y[0][i]);
+            put_split<OT>(xc + B::XX + (wv >> 1) * F, 2 * F, wv & 1, X);
+        }
         lds_get4<float>(buf + B::VEC + (SC_TAIL + 16 * wv + 4 * lq) * 4, t4);
         const float ec = lds_load<float>(buf + B::VEC + SC_EC * 4);
-        __builtin_amdgcn_sched_barrier(0);
-        // X = beta (V - e^gam K S) on this wave's tokens
-        f32x4 Y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) Y[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-            for (int p = 0; p < NS; ++p) mma(Y[2 * (kb & 1) + p], Kf[kb], SB[p][kb]);
-        Y[0] = (Y[0] + Y[2]) + (Y[1] + Y[3]);
-        f32x4 X;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) X[i] = b4[i] * (v4[i] - e4[i] * Y[0][i]);
-        put_split<OT>(xs + B::XX + (wv >> 1) * F, 2 * F, wv & 1, X);
         sync_lds();  // B: X is published
-        // Delta = T X on this wave's tokens (T is lower triangular: for token tiles 0 and 1 the second
-        // half of the columns is zero)
-        FT XB[NS][2];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int p = 0; p < NS; ++p) XB[p][kb] = get_x<OT>(xs + B::XX + (2 * p + kb) * F);
+        // Delta = T X on this wave's tokens
         FT KT[NT][2];  // K^T, rows: this wave's keys
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int ch = 0; ch < NC; ++ch) {
+            lds_char* xc = xs + ch * B::XT;
+            FT XB[NS][2];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) KT[t][kb] = lfrag_colk8<OT>(vK, 16 * (NT * wv + t), 32 * kb);
-        __builtin_amdgcn_sched_barrier(0);
-        f32x4 D[4];
+            for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) D[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int p = 0; p < NS; ++p) XB[p][kb] = get_x<OT>(xc + B::XX + (2 * p + kb) * F);
+            if (ch == 0) {
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb) KT[t][kb] = lfrag_colk8<OT>(vK, 16 * (NT * wv + t), 32 * kb);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 D[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int p = 0; p < NS; ++p)
+#pragma unroll
+                    for (int r = 0; r < NS; ++r) mma(D[2 * p + r], T.f[r][kb], XB[p][kb]);
+            D[0] = (D[0] + D[1]) + (D[2] + D[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[1][i] = t4[i] * D[0][i];
+            put_split<OT>(xc + B::XD + (wv >> 1) * F, 2 * F, wv & 1, D[1]);
+            put_one<OT>(xc + B::XO + (wv >> 1) * F, wv & 1, D[0]);
+        }
+        sync_lds();  // C: Delta is published
+        // the next T: from here to A the memory path is least busy, and a wave waits where it issues a load
+        if (n + 1 < nt) tp += tstep;  // (past the last chunk: the last again)
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+            const lds_char* xc = xs + ch * B::XT;
+            FT DB[NS][2];
 #pragma unroll
             for (int p = 0; p < NS; ++p)
 #pragma unroll
-                for (int r = 0; r < NS; ++r) mma(D[2 * p + r], Tn[r][kb], XB[p][kb]);
-        if (n + 1 < nt) tp += tstep;  // (past the last chunk: the last again)
-        load_t();
-        D[0] = (D[0] + D[1]) + (D[2] + D[3]);
+                for (int kb = 0; kb < 2; ++kb) DB[p][kb] = get_x<OT>(xc + B::XD + (2 * p + kb) * F);
+            if (ch == 0) T.load(tp, wv);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) D[1][i] = t4[i] * D[0][i];
-        put_split<OT>(xs + B::XD + (wv >> 1) * F, 2 * F, wv & 1, D[1]);
-        put_one<OT>(xs + B::XO + (wv >> 1) * F, wv & 1, D[0]);
-        sync_lds();  // C: Delta is published
-        FT DB[NS][2];
+            for (int t = 0; t < NT; ++t) {
+                f32x4 s0 = S.s[ch][t] * ec, s1 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int p = 0; p < NS; ++p)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) DB[p][kb] = get_x<OT>(xs + B::XD + (2 * p + kb) * F);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            f32x4 s0 = S[t] * ec, s1 = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                mma(s0, KT[t][kb], DB[0][kb]);
-                if constexpr (NS == 2) mma(s1, KT[t][kb], DB[1][kb]);
+                for (int kb = 0; kb < 2; ++kb) {
+                    mma(s0, KT[t][kb], DB[0][kb]);
+                    if constexpr (NS == 2) mma(s1, KT[t][kb], DB[1][kb]);
+                }
+                S.s[ch][t] = s0 + s1;
             }
-            S[t] = s0 + s1;
+            S.publish(xs, ch, wv);
         }
-        publish_state();
     }
-    if (w.end) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w.end[(size_t)(16 * (NT * wv + t) + 4 * lq + i) * DV + 16 * w.j + li] = S[t][i];
-    }
+    S.out(w.end, DV, 16 * NC * w.j, wv);
 }
 
 // The 16-column slice [rows][16] of an exchanged matrix of 16 RT rows (its fragments' first parts, from
-// frag on) to the workspace, by the four side waves.
+// frag on) to the workspace, by the four side waves: read while the exchange holds it, stored later, since
+// a wave waits where it issues a store and the others then wait for it at the next barrier.
 template <class OT, int RT>
-__device__ __forceinline__ void store_slice(const lds_char* frag, OT* dst, int wv) {
-    if constexpr (sizeof(OT) == 2) {
+struct Slice {
+    static constexpr int N = sizeof(OT) == 2 ? (RT + 3) / 4 : 2;
+    typename Raw4<OT>::type x[N];
+    __device__ __forceinline__ void read(const lds_char* frag, int wv) {
+        if constexpr (sizeof(OT) == 2) {
 #pragma unroll
-        for (int t = 0; t < (RT + 3) / 4; ++t) {
-            const int rt = wv + 4 * t;
-            if (RT % 4 == 0 || rt < RT) store_slice_tr(frag + (rt >> 1) * xfrag<OT>(), rt & 1, dst + rt * 256);
-        }
-    } else {
-        const int l = lane_id(), li = l & 15, lq = l >> 4;
-        if (wv < RT / 2) {
-            const auto f = get_x<OT>(frag + wv * xfrag<OT>());
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dst[(32 * wv + 8 * lq + e) * 16 + li] = f[e];
+            for (int t = 0; t < N; ++t) {
+                const int rt = wv + 4 * t;
+                if (RT % 4 == 0 || rt < RT) x[t] = read_slice_tr(frag + (rt >> 1) * xfrag<OT>(), rt & 1);
+            }
+        } else if (wv < RT / 2) {
+            const lds_char* p = frag + wv * xfrag<OT>() + lane_id() * 32;
+            x[0] = lds_load<f32x4>(p);
+            x[1] = lds_load<f32x4>(p + 16);
         }
     }
-}
+    __device__ __forceinline__ void write(OT* dst, int wv) const {
+        const int l = lane_id(), li = l & 15, lq = l >> 4;
+        if constexpr (sizeof(OT) == 2) {
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                const int rt = wv + 4 * t;
+                if (RT % 4 == 0 || rt < RT) store_out<true>((bf16x4*)(dst + rt * 256 + li * 16 + 4 * lq), x[t]);
+            }
+        } else if (wv < RT / 2) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[(32 * wv + 8 * lq + e) * 16 + li] = x[e / 4][e % 4];
+        }
+    }
+};
 
 // Side waves: what a step gives away -- O, and for training the chunk's start state and Delta.
-template <class OT, int DK, int DV, bool TRAIN, bool OUT>
-__device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk<OT>& w, int wv, const lds_char* b0,
+template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT>
+__device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, int wv, const lds_char* b0,
                                             const lds_char* b1, const lds_char* xs) {
-    using B = ScChainLds<OT, DK, false>;
+    using B = ScChainLds<OT, DK, NC, false>;
     using FT = typename Frag<OT>::type;
     constexpr int NKB = B::NKB, F = B::F;
     const int l = lane_id(), li = l & 15, lq = l >> 4;
     const OT* mp = (const OT*)(a.ws + a.L.o_m) + ((size_t)w.q.slot0 * a.Hv + w.h) * a.L.m;
     const size_t mstep = (size_t)a.Hv * a.L.m;
-    FT M[2];  // this wave's rows of M, a step ahead as T in the compute waves
-    auto load_m = [&]() {
+    ImgRows<OT, 1> M;  // a step ahead
+    if (OUT && w.q.nt > 0) M.load(mp, wv);
+    Slice<OT, DK / 16> S[NC];
+    auto store_state = [&](int n) {  // chunk n's start state
+        OT* p = (OT*)(a.ws + a.L.o_s) + ((size_t)(w.q.slot0 + n) * a.Hv + w.h) * a.L.s;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) M[kb] = gfrag_img<OT, CH>(mp, 16 * wv, 32 * kb);
+        for (int ch = 0; ch < NC; ++ch) S[ch].write(p + (size_t)(NC * w.j + ch) * DK * 16, wv);
     };
-    if (OUT && w.q.nt > 0) load_m();
 #pragma unroll 1
     for (int n = 0; n < w.q.nt; ++n) {
         const lds_char* buf = (n & 1) ? b1 : b0;
         const size_t id = (size_t)(w.q.slot0 + n) * a.Hv + w.h;
         sync_lds();  // A
+        if (TRAIN && n > 0) store_state(n - 1);
         sync_lds();  // B: from here to C the compute waves leave LDS mostly idle
         // O^T (rows: value columns, columns: this wave's tokens), the state's part
-        f32x4 O = {0.f, 0.f, 0.f, 0.f};
+        f32x4 O[NC];
         if (OUT) {
             const LSwz<OT, DK> vQ{buf + B::Q};
 #pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) mma(O, get_x<OT>(xs + B::XS + kb * F), lfrag_rowk8<OT>(vQ, 16 * wv, 32 * kb));
-            O = O * lds_load<float>(buf + B::VEC + (SC_E + 16 * wv + li) * 4);
+            for (int ch = 0; ch < NC; ++ch) O[ch] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                const FT q = lfrag_rowk8<OT>(vQ, 16 * wv, 32 * kb);
+#pragma unroll
+                for (int ch = 0; ch < NC; ++ch) mma(O[ch], get_x<OT>(xs + ch * B::XT + B::XS + kb * F), q);
+            }
+            const float e = lds_load<float>(buf + B::VEC + (SC_E + 16 * wv + li) * 4);
+#pragma unroll
+            for (int ch = 0; ch < NC; ++ch) O[ch] = O[ch] * e;
         }
-        if (TRAIN) store_slice<OT, DK / 16>(xs + B::XS, (OT*)(a.ws + a.L.o_s) + id * a.L.s + (size_t)w.j * DK * 16, wv);
+        if (TRAIN) {
+#pragma unroll
+            for (int ch = 0; ch < NC; ++ch) S[ch].read(xs + ch * B::XT + B::XS, wv);
+        }
         sync_lds();  // C
         if (OUT) {
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) mma(O, get_x<OT>(xs + B::XO + kb * F), M[kb]);
+            for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) mma(O[ch], get_x<OT>(xs + ch * B::XT + B::XO + kb * F), M.f[0][kb]);
             if (n + 1 < w.q.nt) mp += mstep;
-            load_m();
+            M.load(mp, wv);
             const int row = 16 * wv + li;
             if (CH * n + row < w.q.len) {
-                const float ov[4] = {O[0], O[1], O[2], O[3]};
-                st4((OT*)a.o + ((size_t)(w.q.tok0 + 64LL * n + row) * a.Hv + w.h) * DV + 16 * w.j + 4 * lq, ov);
-            }
-        }
-        if (TRAIN) store_slice<OT, 4>(xs + B::XO, (OT*)(a.ws + a.L.o_delta) + id * a.L.d + (size_t)w.j * CH * 16, wv);
-    }
-}
-
-template <class OT, int DK, int DV>
-__device__ __forceinline__ void sc_walk_of(const ScArgs& a, ScWalk<OT>& w, size_t& st) {
-    int p;
-    sc_chain_map(blockIdx.x, a.N * a.Hv, DV / 16, p, w.j);
-    const int s = p / a.Hv;
-    w.h = p % a.Hv;
-    w.hk = w.h / a.R;
-    w.q = sc_seq(a.cu, a.T, s);
-    st = (size_t)p * DK * DV;
-}
-
-template <class OT, int DK, int DV, bool TRAIN, bool OUT>
-__global__ __launch_bounds__(64 * (2 * SC_NC + SC_NP)) void k_sc_fwd_chain(ScArgs a) {
-    using B = ScChainLds<OT, DK, false>;
-    __shared__ __align__(16) char buf0[B::BYTES];
-    __shared__ __align__(16) char buf1[B::BYTES];
-    __shared__ __align__(16) char xch[B::XBYTES];
-    __shared__ __align__(16) char pfslot[256];  // target of the prefetches, never read
-    poison_lds((lds_char*)buf0, sizeof(buf0));
-    poison_lds((lds_char*)buf1, sizeof(buf1));
-    poison_lds((lds_char*)xch, sizeof(xch));
-    poison_lds_done();
-    ScWalk<OT> w;
-    size_t st;
-    sc_walk_of<OT, DK, DV>(a, w, st);
-    w.start = a.h0 ? a.h0 + st : nullptr;
-    w.end = a.ht ? a.ht + st : nullptr;
-    const int wv = sc_wave();
-    if (wv < SC_NC)
-        sc_fwd_walk<OT, DK, DV>(a, w, wv, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
-    else if (wv < 2 * SC_NC)
-        sc_fwd_side<OT, DK, DV, TRAIN, OUT>(a, w, wv - SC_NC, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
-    else if (w.q.nt > 0)
-        sc_produce<OT, DK, DV, false>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
-}
-
-template <class OT, int DK, int DV>
-__device__ __forceinline__ void sc_bwd_walk(const ScArgs& a, const ScWalk<OT>& w, lds_char* b0, lds_char* b1,
-                                            lds_char* xs) {
-    using B = ScChainLds<OT, DK, true>;
-    using FT = typename Frag<OT>::type;
-    constexpr int NS = B::NS, NKB = B::NKB, F = B::F, NT = DK / 64;
-    const int wv = sc_wave(), l = lane_id(), li = l & 15, lq = l >> 4;
-    const int nt = w.q.nt;
-    f32x4 dS[NT];
-    auto publish_state = [&]() {
+                OT* o = (OT*)a.o + ((size_t)(w.q.tok0 + 64LL * n + row) * a.Hv + w.h) * DV + 16 * NC * w.j + 4 * lq;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int rt = NT * wv + t;
-            put_split<OT>(xs + B::XS + (rt >> 1) * F, NKB * F, rt & 1, dS[t]);
-        }
-    };
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            dS[t][i] = w.start ? w.start[(size_t)(16 * (NT * wv + t) + 4 * lq + i) * DV + 16 * w.j + li] : 0.f;
-    publish_state();
-#pragma unroll 1
-    for (int n = 0; n < nt; ++n) {
-        const int c = nt - 1 - n;
-        const lds_char* buf = (n & 1) ? b1 : b0;
-        const LSwz<OT, DK> vK{buf + B::K}, vQ{buf + B::Q};
-        const LPad<OT> vO{buf + B::V, 16};
-        const size_t id = (size_t)(w.q.slot0 + c) * a.Hv + w.h;
-        sync_lds();  // A: the end-state gradient is published, the chunk's operands are in
-        float e4[4], b4[4], t4[4];
-        lds_get4<float>(buf + B::VEC + (SC_E + 16 * wv + 4 * lq) * 4, e4);
-        lds_get4<float>(buf + B::VEC + (SC_BETA + 16 * wv + 4 * lq) * 4, b4);
-        lds_get4<float>(buf + B::VEC + (SC_TAIL + 16 * wv + 4 * lq) * 4, t4);
-        // dDelta = tail K dS' + M^T dO on this wave's tokens (M^T is upper triangular: token tiles 2
-        // and 3 need only the last 32 rows)
-        f32x4 Y = {0.f, 0.f, 0.f, 0.f}, Y1 = Y;
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-            const FT k = lfrag_rowk8<OT>(vK, 16 * wv, 32 * kb);
-            mma(Y, k, get_x<OT>(xs + B::XS + kb * F));
-            if constexpr (NS == 2) mma(Y1, k, get_x<OT>(xs + B::XS + (NKB + kb) * F));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) Y[i] = t4[i] * (Y[i] + Y1[i]);
-        FT dO[2];
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) dO[kb] = lfrag_colk8<OT>(vO, 0, 32 * kb);
-        Y1 = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            if (kb == 1 || wv < 2) {
-                mma(Y, lfrag_colk8<OT>(LImg<OT, CH>{buf + B::M}, 16 * wv, 32 * kb), dO[kb]);
-                if constexpr (NS == 2)
-                    mma(Y1, lfrag_colk8<OT>(LImg<OT, CH>{buf + B::M + B::SQ}, 16 * wv, 32 * kb), dO[kb]);
-            }
-        }
-        put_split<OT>(xs + B::XX + (wv >> 1) * F, 2 * F, wv & 1, Y + Y1);
-        {  // the chunk's end-state gradient, this wave's key rows
-            OT* s = (OT*)(a.ws + a.L.o_ds) + id * a.L.s + (size_t)w.j * DK * 16;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const int rt = NT * wv + t;
-                if constexpr (NS == 2) store_slice_tr(xs + B::XS + (rt >> 1) * F, rt & 1, s + rt * 256);
-                else store_slice_acc<OT>(dS[t], s + rt * 256);
-            }
-        }
-        // the part of dS without dY: e^gamC dS' + Q^T (e^gam dO)
-        const float ec = lds_load<float>(buf + B::VEC + SC_EC * 4);
-        f32x4 P[NT], P1[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            P[t] = dS[t] * ec;
-            P1[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            FT hi, lo;
-            float s8[8];
-            lds_get4<float>(buf + B::VEC + (SC_E + 32 * kb + 8 * lq) * 4, s8);
-            lds_get4<float>(buf + B::VEC + (SC_E + 32 * kb + 8 * lq + 4) * 4, s8 + 4);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = s8[e] * to_f(dO[kb][e]);
-                hi[e] = to_ot<OT>(x);
-                lo[e] = to_ot<OT>(x - to_f(hi[e]));
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const FT qt = lfrag_colk8<OT>(vQ, 16 * (NT * wv + t), 32 * kb);
-                mma(P[t], qt, hi);
-                if constexpr (NS == 2) mma(P1[t], qt, lo);
-            }
-        }
-        sync_lds();  // B: dDelta is published
-        f32x4 D = {0.f, 0.f, 0.f, 0.f}, D1 = D;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            if (kb == 1 || wv < 2) {
-#pragma unroll
-                for (int p = 0; p < NS; ++p) {
-                    const FT t = lfrag_colk8<OT>(LImg<OT, CH>{buf + B::T + p * B::SQ}, 16 * wv, 32 * kb);
-                    mma(D, t, get_x<OT>(xs + B::XX + kb * F));
-                    if constexpr (NS == 2) mma(D1, t, get_x<OT>(xs + B::XX + (2 + kb) * F));
+                for (int ch = 0; ch < NC; ++ch) {
+                    const float ov[4] = {O[ch][0], O[ch][1], O[ch][2], O[ch][3]};
+                    st4(o + 16 * ch, ov);
                 }
             }
         }
-        f32x4 Z;
+        if (TRAIN) {
+            OT* p = (OT*)(a.ws + a.L.o_delta) + id * a.L.d;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            D[i] += D1[i];
-            Z[i] = -(b4[i] * e4[i]) * D[i];
-        }
-        put_split<OT>(xs + B::XD + (wv >> 1) * F, 2 * F, wv & 1, Z);
-        put_one<OT>(xs + B::XO + (wv >> 1) * F, wv & 1, D);
-        sync_lds();  // C: dY is published
-        FT DB[NS][2];
-#pragma unroll
-        for (int p = 0; p < NS; ++p)
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) DB[p][kb] = get_x<OT>(xs + B::XD + (2 * p + kb) * F);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-                const FT k = lfrag_colk8<OT>(vK, 16 * (NT * wv + t), 32 * kb);
-                mma(P[t], k, DB[0][kb]);
-                if constexpr (NS == 2) mma(P1[t], k, DB[1][kb]);
+            for (int ch = 0; ch < NC; ++ch) {
+                Slice<OT, 4> D;
+                D.read(xs + ch * B::XT + B::XO, wv);
+                D.write(p + (size_t)(NC * w.j + ch) * CH * 16, wv);
             }
-            dS[t] = P[t] + P1[t];
         }
-        publish_state();
-        OT* d = (OT*)(a.ws + a.L.o_dy) + id * a.L.d + (size_t)w.j * CH * 16 + wv * 256;
-        if constexpr (NS == 2) store_slice_tr(xs + B::XO + (wv >> 1) * F, wv & 1, d);
-        else store_slice_acc<OT>(D, d);
     }
-    if (w.end) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w.end[(size_t)(16 * (NT * wv + t) + 4 * lq + i) * DV + 16 * w.j + li] = dS[t][i];
-    }
+    if (TRAIN && w.q.nt > 0) store_state(w.q.nt - 1);
 }
 
-template <class OT, int DK, int DV>
-__global__ __launch_bounds__(64 * (SC_NC + SC_NP)) void k_sc_bwd_chain(ScArgs a) {
-    using B = ScChainLds<OT, DK, true>;
+// Compute waves of the backward (as sc_fwd_walk). What does not depend on the state, Q^T (e^gam dO), is
+// the side waves'.
+template <class OT, int DK, int DV, int NC>
+__device__ __forceinline__ void sc_bwd_walk(const ScArgs& a, const ScWalk& w, int wv, lds_char* b0, lds_char* b1,
+                                            lds_char* xs) {
+    using B = ScChainLds<OT, DK, NC, true>;
+    using FT = typename Frag<OT>::type;
+    constexpr int NS = B::NS, NKB = B::NKB, F = B::F, NT = DK / 64;
+    const int l = lane_id(), lq = l >> 4;
+    const int nt = w.q.nt;
+    ScState<OT, DK, NC, true> dS;
+    dS.init(w.start, DV, 16 * NC * w.j, wv);
+#pragma unroll
+    for (int ch = 0; ch < NC; ++ch) dS.publish(xs, ch, wv);
+    const size_t tstep = (size_t)a.Hv * a.L.t;
+    const size_t id0 = ((size_t)(w.q.slot0 + max(nt - 1, 0)) * a.Hv + w.h) * a.L.t;
+    const OT* tp = (const OT*)(a.ws + a.L.o_tt) + id0;
+    const OT* mp = (const OT*)(a.ws + a.L.o_mt) + id0;
+    ImgRows<OT, NS> T, M;  // rows of T^T and M^T, a step ahead
+    if (nt > 0) {
+        M.load(mp, wv);
+        T.load(tp, wv);
+    }
+#pragma unroll 1
+    for (int n = 0; n < nt; ++n) {
+        const lds_char* buf = (n & 1) ? b1 : b0;
+        const LSwz<OT, DK> vK{buf + B::K};
+        sync_lds();  // A: the end-state gradient is published, the chunk's operands are in
+        // dDelta = tail K dS' + M^T dO on this wave's tokens
+        FT Kf[NKB];
+        float e4[4], b4[4], t4[4];
+        lds_get4<float>(buf + B::VEC + (SC_TAIL + 16 * wv + 4 * lq) * 4, t4);
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+            lds_char* xc = xs + ch * B::XT;
+            const LPad<OT> vO{buf + B::V + ch * B::VT, 16};
+            FT SB[NS][NKB], dO[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) dO[kb] = lfrag_colk8<OT>(vO, 0, 32 * kb);
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) {
+                if (ch == 0) Kf[kb] = lfrag_rowk8<OT>(vK, 16 * wv, 32 * kb);
+#pragma unroll
+                for (int p = 0; p < NS; ++p) SB[p][kb] = get_x<OT>(xc + B::XS + (p * NKB + kb) * F);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 Y[4], Z[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Y[i] = Z[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int p = 0; p < NS; ++p) mma(Z[2 * kb + p], M.f[p][kb], dO[kb]);
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+                for (int p = 0; p < NS; ++p) mma(Y[2 * (kb & 1) + p], Kf[kb], SB[p][kb]);
+            Y[0] = (Y[0] + Y[2]) + (Y[1] + Y[3]);
+            Z[0] = (Z[0] + Z[2]) + (Z[1] + Z[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) Z[0][i] += t4[i] * Y[0][i];
+            put_split<OT>(xc + B::XX + (wv >> 1) * F, 2 * F, wv & 1, Z[0]);
+        }
+        lds_get4<float>(buf + B::VEC + (SC_E + 16 * wv + 4 * lq) * 4, e4);
+        lds_get4<float>(buf + B::VEC + (SC_BETA + 16 * wv + 4 * lq) * 4, b4);
+        const float ec = lds_load<float>(buf + B::VEC + SC_EC * 4);
+        sync_lds();  // B: dDelta is published
+        FT KT[NT][2];
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+            lds_char* xc = xs + ch * B::XT;
+            FT XB[NS][2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int p = 0; p < NS; ++p) XB[p][kb] = get_x<OT>(xc + B::XX + (2 * p + kb) * F);
+            if (ch == 0) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb) KT[t][kb] = lfrag_colk8<OT>(vK, 16 * (NT * wv + t), 32 * kb);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            f32x4 D[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int p = 0; p < NS; ++p)
+#pragma unroll
+                    for (int r = 0; r < NS; ++r) mma(D[2 * p + r], T.f[r][kb], XB[p][kb]);
+            D[0] = (D[0] + D[1]) + (D[2] + D[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[1][i] = -(b4[i] * e4[i]) * D[0][i];
+            put_split<OT>(xc + B::XD + (wv >> 1) * F, 2 * F, wv & 1, D[1]);
+            put_one<OT>(xc + B::XO + (wv >> 1) * F, wv & 1, D[0]);
+        }
+        sync_lds();  // C: dY is published, and the side waves' part of dS
+        if (n + 1 < nt) {
+            tp -= tstep;
+            mp -= tstep;
+        }
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+            const lds_char* xc = xs + ch * B::XT;
+            FT DB[NS][2];
+            f32x4 P[NT];
+#pragma unroll
+            for (int p = 0; p < NS; ++p)
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) DB[p][kb] = get_x<OT>(xc + B::XD + (2 * p + kb) * F);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) P[t] = lds_load<f32x4>(xc + B::XP + ((NT * wv + t) * 64 + l) * 16);
+            if (ch == 0) {
+                M.load(mp, wv);
+                T.load(tp, wv);
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                f32x4 s0 = dS.s[ch][t] * ec, s1 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    mma(s0, KT[t][kb], DB[0][kb]);
+                    if constexpr (NS == 2) mma(s1, KT[t][kb], DB[1][kb]);
+                }
+                dS.s[ch][t] = (s0 + s1) + P[t];
+            }
+            dS.publish(xs, ch, wv);
+        }
+    }
+    dS.out(w.end, DV, 16 * NC * w.j, wv);
+}
+
+template <class OT, int DK, int DV, int NC>
+__device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, int wv, const lds_char* b0,
+                                            const lds_char* b1, lds_char* xs) {
+    using B = ScChainLds<OT, DK, NC, true>;
+    using FT = typename Frag<OT>::type;
+    constexpr int NS = B::NS, NT = DK / 64;
+    const int l = lane_id(), lq = l >> 4;
+    Slice<OT, DK / 16> S[NC];
+    auto store_state = [&](int n) {  // the end-state gradient of walk index n
+        OT* p = (OT*)(a.ws + a.L.o_ds) + ((size_t)(w.q.slot0 + (w.q.nt - 1 - n)) * a.Hv + w.h) * a.L.s;
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) S[ch].write(p + (size_t)(NC * w.j + ch) * DK * 16, wv);
+    };
+#pragma unroll 1
+    for (int n = 0; n < w.q.nt; ++n) {
+        const lds_char* buf = (n & 1) ? b1 : b0;
+        const LSwz<OT, DK> vQ{buf + B::Q};
+        const size_t id = (size_t)(w.q.slot0 + (w.q.nt - 1 - n)) * a.Hv + w.h;
+        sync_lds();  // A
+        if (n > 0) store_state(n - 1);
+        sync_lds();  // B: from here to C the compute waves leave LDS mostly idle
+        // Q^T (e^gam dO), rows: the keys of compute wave wv
+        f32x4 P[NC][NT][2];
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) P[ch][t][0] = P[ch][t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            float s8[8];
+            lds_get4<float>(buf + B::VEC + (SC_E + 32 * kb + 8 * lq) * 4, s8);
+            lds_get4<float>(buf + B::VEC + (SC_E + 32 * kb + 8 * lq + 4) * 4, s8 + 4);
+            FT qt[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) qt[t] = lfrag_colk8<OT>(vQ, 16 * (NT * wv + t), 32 * kb);
+#pragma unroll
+            for (int ch = 0; ch < NC; ++ch) {
+                const FT dO = lfrag_colk8<OT>(LPad<OT>{buf + B::V + ch * B::VT, 16}, 0, 32 * kb);
+                FT hi, lo;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x = s8[e] * to_f(dO[e]);
+                    hi[e] = to_ot<OT>(x);
+                    lo[e] = to_ot<OT>(x - to_f(hi[e]));
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma(P[ch][t][0], qt[t], hi);
+                    if constexpr (NS == 2) mma(P[ch][t][1], qt[t], lo);
+                }
+            }
+        }
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                lds_store<f32x4>(xs + ch * B::XT + B::XP + ((NT * wv + t) * 64 + l) * 16, P[ch][t][0] + P[ch][t][1]);
+            S[ch].read(xs + ch * B::XT + B::XS, wv);
+        }
+        sync_lds();  // C
+        OT* p = (OT*)(a.ws + a.L.o_dy) + id * a.L.d;
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch) {
+            Slice<OT, 4> Y;
+            Y.read(xs + ch * B::XT + B::XO, wv);
+            Y.write(p + (size_t)(NC * w.j + ch) * CH * 16, wv);
+        }
+    }
+    if (w.q.nt > 0) store_state(w.q.nt - 1);
+}
+
+// The sequence of rank r by length, the longest first (up to 64 packed sequences; more, and sequences of
+// one length, are taken as they come): a long one started last would run on alone.
+__device__ __forceinline__ int sc_ranked(const ScArgs& a, int r) {
+    if (!a.cu || a.N > 64) return r;
+    const int l = lane_id();
+    const int len = l < a.N ? sc_seq(a.cu, a.T, l).len : -1;
+    int rank = 0;
+    for (int u = 0; u < a.N; ++u) {
+        const int x = __builtin_amdgcn_readlane(len, u);
+        rank += x > len || (x == len && u < l);
+    }
+    return __ffsll((unsigned long long)__ballot(l < a.N && rank == r)) - 1;
+}
+
+template <class OT, int DK, int DV, int NC>
+__device__ __forceinline__ ScWalk sc_walk_of(const ScArgs& a, const float* starts, float* ends) {
+    ScWalk w;
+    int p;
+    sc_chain_map(blockIdx.x, a.N * a.Hv, DV / (16 * NC), p, w.j);
+    w.h = p % a.Hv;
+    w.hk = w.h / a.R;
+    const int s = sc_ranked(a, p / a.Hv);
+    w.q = sc_seq(a.cu, a.T, s);
+    const size_t st = ((size_t)s * a.Hv + w.h) * DK * DV;
+    w.start = starts ? starts + st : nullptr;
+    w.end = ends ? ends + st : nullptr;
+    return w;
+}
+
+constexpr int SC_THREADS = 64 * (2 * SC_NC + SC_NP);
+
+template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT>
+__global__ __launch_bounds__(SC_THREADS) void k_sc_fwd_chain(ScArgs a) {
+    using B = ScChainLds<OT, DK, NC, false>;
     __shared__ __align__(16) char buf0[B::BYTES];
     __shared__ __align__(16) char buf1[B::BYTES];
     __shared__ __align__(16) char xch[B::XBYTES];
@@ -621,35 +753,74 @@ __global__ __launch_bounds__(64 * (SC_NC + SC_NP)) void k_sc_bwd_chain(ScArgs a)
     poison_lds((lds_char*)buf1, sizeof(buf1));
     poison_lds((lds_char*)xch, sizeof(xch));
     poison_lds_done();
-    ScWalk<OT> w;
-    size_t st;
-    sc_walk_of<OT, DK, DV>(a, w, st);
-    w.start = a.dht ? a.dht + st : nullptr;
-    w.end = a.dh0 ? a.dh0 + st : nullptr;
+    const ScWalk w = sc_walk_of<OT, DK, DV, NC>(a, a.h0, a.ht);
     const int wv = sc_wave();
-    if (wv >= SC_NC) {
-        if (w.q.nt > 0) sc_produce<OT, DK, DV, true>(a, w, (lds_char*)buf0, (lds_char*)buf1,
-                                                   (lds_char*)pfslot, wv - SC_NC);
-        return;
-    }
-    sc_bwd_walk<OT, DK, DV>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
+    if (wv < SC_NC)
+        sc_fwd_walk<OT, DK, DV, NC>(a, w, wv, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
+    else if (wv < 2 * SC_NC)
+        sc_fwd_side<OT, DK, DV, NC, TRAIN, OUT>(a, w, wv - SC_NC, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
+    else if (w.q.nt > 0)
+        sc_produce<OT, DK, DV, NC, false>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
+}
+
+template <class OT, int DK, int DV, int NC>
+__global__ __launch_bounds__(SC_THREADS) void k_sc_bwd_chain(ScArgs a) {
+    using B = ScChainLds<OT, DK, NC, true>;
+    __shared__ __align__(16) char buf0[B::BYTES];
+    __shared__ __align__(16) char buf1[B::BYTES];
+    __shared__ __align__(16) char xch[B::XBYTES];
+    __shared__ __align__(16) char pfslot[256];  // target of the prefetches, never read
+    poison_lds((lds_char*)buf0, sizeof(buf0));
+    poison_lds((lds_char*)buf1, sizeof(buf1));
+    poison_lds((lds_char*)xch, sizeof(xch));
+    poison_lds_done();
+    const ScWalk w = sc_walk_of<OT, DK, DV, NC>(a, a.dht, a.dh0);
+    const int wv = sc_wave();
+    if (wv < SC_NC)
+        sc_bwd_walk<OT, DK, DV, NC>(a, w, wv, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
+    else if (wv < 2 * SC_NC)
+        sc_bwd_side<OT, DK, DV, NC>(a, w, wv - SC_NC, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
+    else if (w.q.nt > 0)
+        sc_produce<OT, DK, DV, NC, true>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
+}
+
+// Column tiles a workgroup: with at most one 16-column walk for each compute unit, one; with two or more,
+// walks queue, and two tiles to a workgroup share its operands, its barriers and their latencies (a step
+// takes 1.4 times as long for twice the columns). Packed sequences may be uneven, and then the longest
+// walk, not their sum, sets the time: two tiles only from five walks a compute unit on. Measured, forward
+// chain: 24 sequences of 18 to 700 tokens, 6 walks a unit: 30 us with two tiles, 44 with one; 9 sequences
+// of 103 to 4000 tokens, 4.5 walks a unit: 140 with two, 117 with one.
+static hipError_t sc_column_tiles(const ScArgs& a, long long walks16, int& nc) {
+    int dev = 0, cus = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    nc = e == hipSuccess && walks16 >= (a.cu ? 5LL : 2LL) * cus ? 2 : 1;
+    return e;
 }
 
 template <class OT, int DK, int DV>
 hipError_t launch_sc_fwd_chain_t(const ScArgs& a, bool train, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.N * a.Hv * (DV / 16))), block(64 * (2 * SC_NC + SC_NP));
-    if (train && a.o)
-        hipLaunchKernelGGL((k_sc_fwd_chain<OT, DK, DV, true, true>), grid, block, 0, stream, a);
-    else if (train)
-        hipLaunchKernelGGL((k_sc_fwd_chain<OT, DK, DV, true, false>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((k_sc_fwd_chain<OT, DK, DV, false, true>), grid, block, 0, stream, a);
+    int nc;
+    const long long walks = (long long)a.N * a.Hv * (DV / 16);
+    const hipError_t e = sc_column_tiles(a, walks, nc);
+    if (e != hipSuccess) return e;
+    auto pick = [&](auto n) {
+        constexpr int NC = decltype(n)::value;
+        return !train ? k_sc_fwd_chain<OT, DK, DV, NC, false, true>
+               : a.o  ? k_sc_fwd_chain<OT, DK, DV, NC, true, true> : k_sc_fwd_chain<OT, DK, DV, NC, true, false>;
+    };
+    auto k = nc == 2 ? pick(std::integral_constant<int, 2>{}) : pick(std::integral_constant<int, 1>{});
+    hipLaunchKernelGGL(k, dim3((unsigned)(walks / nc)), dim3(SC_THREADS), 0, stream, a);
     return hipGetLastError();
 }
 template <class OT, int DK, int DV>
 hipError_t launch_sc_bwd_chain_t(const ScArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(a.N * a.Hv * (DV / 16))), block(64 * (SC_NC + SC_NP));
-    hipLaunchKernelGGL((k_sc_bwd_chain<OT, DK, DV>), grid, block, 0, stream, a);
+    int nc;
+    const long long walks = (long long)a.N * a.Hv * (DV / 16);
+    const hipError_t e = sc_column_tiles(a, walks, nc);
+    if (e != hipSuccess) return e;
+    auto k = nc == 2 ? k_sc_bwd_chain<OT, DK, DV, 2> : k_sc_bwd_chain<OT, DK, DV, 1>;
+    hipLaunchKernelGGL(k, dim3((unsigned)(walks / nc)), dim3(SC_THREADS), 0, stream, a);
     return hipGetLastError();
 }
 

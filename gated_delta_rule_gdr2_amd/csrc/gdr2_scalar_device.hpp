@@ -62,22 +62,12 @@ __device__ __forceinline__ typename Frag<OT>::type get_x(const lds_char* frag) {
     return lds_load<typename Frag<OT>::type>(frag + lane_id() * 8 * (int)sizeof(OT));
 }
 
-// Rows 16 kt .. + 15 (K rows) of an exchange fragment out to a 16-column slice [rows][16] of the
-// workspace, from the fragment's first part: a transposing read gives each lane four consecutive
-// columns of one row (bf16 only; fp32 slices are stored from the accumulators).
-// kt is the row tile inside the fragment (0 or 1); dst points at the tile's first row.
-__device__ __forceinline__ void store_slice_tr(const lds_char* frag, int kt, bf16* dst) {
+// Rows 16 kt .. + 15 (K rows, kt = 0 or 1) of an exchange fragment's first part (bf16), turned for a
+// 16-column slice [rows][16]: a transposing read gives lane (li, lq) columns 4 lq .. + 3 of row 16 kt + li.
+__device__ __forceinline__ bf16x4 read_slice_tr(const lds_char* frag, int kt) {
     const int l = lane_id(), li = l & 15, lq = l >> 4;
     const int r = 4 * lq + (li >> 2), c = 16 * kt + 4 * (li & 3);  // column r, K index c .. c + 3
-    const bf16x4 x = lds_read_tr16(frag + ((r + 16 * (c >> 3)) * 8 + (c & 7)) * 2);
-    *(bf16x4*)(dst + li * 16 + 4 * lq) = x;
-}
-// accumulator tile (rows 4 lq + i, column li) to a [16][16] tile of a slice, element by element
-template <class OT>
-__device__ __forceinline__ void store_slice_acc(const f32x4& d, OT* dst) {
-    const int l = lane_id(), li = l & 15, lq = l >> 4;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) dst[(4 * lq + i) * 16 + li] = to_ot<OT>(d[i]);
+    return lds_read_tr16(frag + ((r + 16 * (c >> 3)) * 8 + (c & 7)) * 2);
 }
 
 // This lane's row and K group, as values the compiler cannot trace back to the thread index. The

@@ -102,6 +102,19 @@ __device__ __forceinline__ void sc_inverse(const lds_char* sA, lds_char* sT) {
     }
 }
 
+// four elements and their remainders to a pair of images
+template <class OT>
+__device__ __forceinline__ void put_parts(OT* p, const f32x4& x) {
+    if constexpr (sizeof(OT) == 2) {
+        bf16x4 hi, lo;
+        split4(x, hi, lo);
+        *(bf16x4*)p = hi;
+        *(bf16x4*)(p + CH * CH) = lo;
+    } else {
+        *(f32x4*)p = x;
+    }
+}
+
 // One workgroup of four waves per (chunk slot, value head): k k^T and q k^T on the raw rows, then A, its
 // inverse and M with the head's decay and beta. (One workgroup per key head, which would form the
 // products once for all of its value heads, is no faster at 16384 x 16 tokens and heads, 35 us both
@@ -141,11 +154,11 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
     // block pairs p = wv, wv + 4, wv + 8 of the lower triangle, as transposed tiles: lane (li, lq)
     // holds rows 16 R + li, columns 16 I + 4 lq + i
     const LSwz<OT, DK> vK{sK}, vQ{sQ};
-    f32x4 kk[3], qk[3];
+    f32x4 kk[3], qk[3], kq[3];  // kq: training, the tile of q k^T itself (rows 16 R + 4 lq + i, columns 16 I + li)
 #pragma unroll
     for (int n = 0; n < 3; ++n) {
         const int p = wv + 4 * n;
-        kk[n] = qk[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        kk[n] = qk[n] = kq[n] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (p < NPAIR) {
             int R, I;
             pair_ri(p, R, I);
@@ -153,7 +166,9 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
             for (int kb = 0; kb < KB; ++kb) {
                 const auto fi = lfrag_rowk8<OT>(vK, 16 * I, 32 * kb);
                 mma(kk[n], fi, lfrag_rowk8<OT>(vK, 16 * R, 32 * kb));
-                mma(qk[n], fi, lfrag_rowk8<OT>(vQ, 16 * R, 32 * kb));
+                const auto fq = lfrag_rowk8<OT>(vQ, 16 * R, 32 * kb);
+                mma(qk[n], fi, fq);
+                if (TRAIN) mma(kq[n], fq, fi);
             }
         }
     }
@@ -184,6 +199,7 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
     }
     __syncthreads();
     OT* m = (OT*)(a.ws + a.L.o_m) + id * a.L.m;
+    OT* mt = (OT*)(a.ws + a.L.o_mt) + id * a.L.t;
 #pragma unroll
     for (int n = 0; n < 3; ++n) {
         const int p = wv + 4 * n;
@@ -206,43 +222,47 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
             }
             f32x4 a4 = {av[0], av[1], av[2], av[3]};
             lds_store<f32x4>(sA + swz<float, CH>(r, i0) * 4, a4);
-            OT* mp = m + fimg<OT, CH>(r, i0);
-            if constexpr (ES == 2) {
-                bf16x4 hi, lo;
-                split4(mv, hi, lo);
-                *(bf16x4*)mp = hi;
-                if (TRAIN) *(bf16x4*)(mp + CH * CH) = lo;
-            } else {
-                *(f32x4*)mp = mv;
+            const float mv4[4] = {mv[0], mv[1], mv[2], mv[3]};
+            st4(m + fimg<OT, CH>(r, i0), mv4);
+            if (TRAIN) {  // M^T: row 16 I + li, columns 16 R + 4 lq ..
+                const int ti = 16 * I + li, r0 = 16 * R + 4 * lq;
+                const float chi = lds_load<float>(sV + (SC_GHI + ti) * 4), clo = lds_load<float>(sV + (SC_GLO + ti) * 4);
+                float qhi[4], qlo[4];
+                lds_get4<float>(sV + (SC_GHI + r0) * 4, qhi);
+                lds_get4<float>(sV + (SC_GLO + r0) * 4, qlo);
+                f32x4 x;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float d = ti <= r0 + i ? decay<OT>(qhi[i], qlo[i], chi, clo) : 0.f;
+                    x[i] = d == 0.f ? 0.f : d * kq[n][i];
+                }
+                put_parts<OT>(mt + fimg<OT, CH>(ti, r0), x);
             }
         }
     }
     for (int u = wv; u < 6; u += 4) {
         int R, I;
         sc_upper_ri(u, R, I);
-        OT* mp = m + fimg<OT, CH>(16 * R + li, 16 * I + 4 * lq);
         const float z[4] = {0.f, 0.f, 0.f, 0.f};
-        st4(mp, z);
-        if (TRAIN && ES == 2) st4(mp + CH * CH, z);
+        st4(m + fimg<OT, CH>(16 * R + li, 16 * I + 4 * lq), z);
+        if (TRAIN) put_parts<OT>(mt + fimg<OT, CH>(16 * I + li, 16 * R + 4 * lq), f32x4{0.f, 0.f, 0.f, 0.f});
     }
     __syncthreads();
     sc_inverse(sA, sT);
-    // T out, a 16-byte piece of the image (8 bf16 or 4 fp32 columns of a row) at a time
+    // T out (and for training T^T), 4 columns of a row at a time
     OT* t = (OT*)(a.ws + a.L.o_t) + id * a.L.t;
-    constexpr int EPP = 16 / ES;
-    for (int idx = tid; idx < CH * CH / EPP; idx += 256) {
-        const int r = idx / (CH / EPP), c0 = EPP * (idx % (CH / EPP));
-        if constexpr (ES == 2) {
-            const f32x4 x0 = lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4);
-            const f32x4 x1 = lds_load<f32x4>(sT + swz<float, CH>(r, c0 + 4) * 4);
-            bf16x4 h0, l0, h1, l1;
-            split4(x0, h0, l0);
-            split4(x1, h1, l1);
-            OT* tp = t + fimg<OT, CH>(r, c0);
-            *(bf16x8*)tp = __builtin_shufflevector(h0, h1, 0, 1, 2, 3, 4, 5, 6, 7);
-            *(bf16x8*)(tp + CH * CH) = __builtin_shufflevector(l0, l1, 0, 1, 2, 3, 4, 5, 6, 7);
-        } else {
-            *(f32x4*)(t + fimg<OT, CH>(r, c0)) = lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4);
+    OT* tt = (OT*)(a.ws + a.L.o_tt) + id * a.L.t;
+#pragma unroll
+    for (int i = 0; i < CH * CH / 4 / 256; ++i) {
+        const int idx = tid + 256 * i, r = idx / 16, c0 = 4 * (idx % 16);
+        put_parts<OT>(t + fimg<OT, CH>(r, c0), lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4));
+        if (TRAIN) {
+            // lanes on 16 neighbouring columns of four rows: row c of T^T, columns r0 ..
+            const int ct = 16 * (idx / 64 % 4) + idx % 16, r0 = 16 * (idx / 256) + 4 * (idx / 16 % 4);
+            f32x4 x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = lds_load<float>(sT + swz<float, CH>(r0 + e, ct) * 4);
+            put_parts<OT>(tt + fimg<OT, CH>(ct, r0), x);
         }
     }
 }
@@ -251,7 +271,9 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
 template <class OT, int DK, int DV>
 struct ScGradLds {
     static constexpr int ES = sizeof(OT);
-    static constexpr int NW = DK / 16;               // waves, one 16-row tile of key channels each
+    static constexpr int NW = 8;               // waves
+    static constexpr int KW = DK / 16;         // 16-row tiles of key channels, one a wave;
+    static constexpr int TPW = 4 * KW / NW;    // token tiles of a wave: all four, or half of them where KW = 4
     static constexpr int SQ = CH * CH * ES;
     static constexpr int TK = CH * DK * ES, TV = CH * DV * ES;
     static constexpr int K = 0;             // raw k rows, swizzled
@@ -269,10 +291,10 @@ struct ScGradLds {
     static constexpr int VEC = DO + REGION;
     static constexpr int ROWP = VEC + SC_VEC * 4;    // per block pair: row and column sums of N
     static constexpr int COLP = ROWP + NPAIR * 16 * 4;
-    static constexpr int DOTS = COLP + NPAIR * 16 * 4;  // per wave and row: q.dq_s, k.dx_s, k.dk_s, k.G
-    static constexpr int DOTV = DOTS + 4 * NW * CH * 4; // per row: dY.v
-    static constexpr int SS = DOTV + CH * 4;            // per wave: <dS', S>
-    static constexpr int RED = SS + NW * 4;             // 6 sums a row
+    static constexpr int DOTS = COLP + NPAIR * 16 * 4;  // per key tile and row: q.dq_s, k.dx_s, k.dk_s, k.G
+    static constexpr int DOTV = DOTS + 4 * KW * CH * 4; // per row: dY.v
+    static constexpr int SS = DOTV + CH * 4;            // per key tile: <dS', S>
+    static constexpr int RED = SS + KW * 4;             // 6 sums a row
     static constexpr int BYTES = RED + 6 * CH * 4;
 };
 
@@ -289,7 +311,8 @@ __device__ __forceinline__ void dma_rows_clamped(const OT* base, size_t rs, int 
     }
 }
 
-// One workgroup per (chunk slot, key head), one wave per 16 key channels: the gradients of the
+// One workgroup of eight waves per (chunk slot, key head), each wave a 16-row tile of key channels
+// (two waves to a tile, half the tokens each, where d_k = 64): the gradients of the
 // group's value heads one after another, dq and dk summed over them in fp32 registers (value heads
 // that share a key head need no second pass and no atomics). Per value head
 //   dq_s = e^gam S dO, dx_s = -e^gam S dY, dk_s = tail dS' Delta   (columns of S, dS': fragments
@@ -308,10 +331,10 @@ __device__ __forceinline__ void dma_rows_clamped(const OT* base, size_t rs, int 
 // value head a key head. (One head is a kernel of its own: around a loop over heads the compiler keeps
 // a hundred addresses in registers.)
 template <class OT, int DK, int DV, bool MULTI>
-__global__ __launch_bounds__(4 * DK, DK == 128 && !MULTI ? 4 : 2) void k_sc_grad(ScArgs a) {
+__global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_grad(ScArgs a) {
     using LS = ScGradLds<OT, DK, DV>;
     using FT = typename Frag<OT>::type;
-    constexpr int ES = sizeof(OT), NW = LS::NW, NTHR = 64 * NW, KB = DK / 32, VB = DV / 32;
+    constexpr int ES = sizeof(OT), NW = LS::NW, KW = LS::KW, TPW = LS::TPW, NTHR = 64 * NW, KB = DK / 32, VB = DV / 32;
     constexpr int PPW = (NPAIR + NW - 1) / NW;  // block pairs of a wave
     extern __shared__ __align__(16) char smem_[];
     lds_char* sm = (lds_char*)smem_;
@@ -338,9 +361,10 @@ __global__ __launch_bounds__(4 * DK, DK == 128 && !MULTI ? 4 : 2) void k_sc_grad
     const LSlice<OT, CH> vDel{sm + LS::DEL}, vDy{sm + LS::DY};
     const LSwz<OT, CH> vP{sm + LS::P}, vRp{sm + LS::RP}, vR{sm + LS::R};
     dma_rows_clamped<OT, DK, NW>((const OT*)a.k + k0, rsk, nvalid, sm + LS::K, wv);
-    f32x4 dq[4], dk[4];  // transposed tiles: keys 16 wv + 4 lq + i, tokens 16 t + li
+    const int kw = wv % KW, t0 = TPW * (wv / KW);  // this wave's key tile and first token tile
+    f32x4 dq[TPW], dk[TPW];  // transposed tiles: keys 16 kw + 4 lq + i, tokens 16 (t0 + t) + li
 #pragma unroll
-    for (int t = 0; t < 4; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < TPW; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
 #pragma unroll 1
     for (int hh = 0; hh < (MULTI ? a.R : 1); ++hh) {
@@ -368,14 +392,14 @@ __global__ __launch_bounds__(4 * DK, DK == 128 && !MULTI ? 4 : 2) void k_sc_grad
         FT fS[VB], fdS[VB];  // this wave's key rows of S and dS', K = value column
 #pragma unroll
         for (int kb = 0; kb < VB; ++kb) {
-            fS[kb] = gfrag_slice<OT, DK>(gS, 16 * wv, kb);
-            fdS[kb] = gfrag_slice<OT, DK>(gdS, 16 * wv, kb);
+            fS[kb] = gfrag_slice<OT, DK>(gS, 16 * kw, kb);
+            fdS[kb] = gfrag_slice<OT, DK>(gdS, 16 * kw, kb);
         }
-        typename Raw4<OT>::type qv[4];  // q of tokens 16 t + li, keys 16 wv + 4 lq ..
+        typename Raw4<OT>::type qv[TPW];  // q of this wave's tokens and keys
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-            qv[t] = *(const typename Raw4<OT>::type*)((const OT*)a.q + k0 + (size_t)min(16 * t + li, nvalid - 1) * rsk +
-                                                      16 * wv + 4 * lq);
+        for (int t = 0; t < TPW; ++t)
+            qv[t] = *(const typename Raw4<OT>::type*)((const OT*)a.q + k0 +
+                                                      (size_t)min(16 * (t0 + t) + li, nvalid - 1) * rsk + 16 * kw + 4 * lq);
         // v, 16 bytes of a row a lane (rows past the end: zero)
         constexpr int EPC = 16 / ES, LPR = DV / EPC, NVL = CH * LPR / NTHR;
         typedef OT VT __attribute__((ext_vector_type(EPC)));
@@ -390,29 +414,30 @@ __global__ __launch_bounds__(4 * DK, DK == 128 && !MULTI ? 4 : 2) void k_sc_grad
 
         // ---- the states' parts
         auto dot4 = [&](const float (&y)[4], const f32x4& x, int t, int which) {
-            // sum over this wave's keys of y x, tokens 16 t + li
+            // sum over this wave's keys of y x, tokens 16 (t0 + t) + li
             const float s = sum_lq((y[0] * x[0] + y[1] * x[1]) + (y[2] * x[2] + y[3] * x[3]));
-            if (lq == 0) lds_store<float>(sm + LS::DOTS + ((which * NW + wv) * CH + 16 * t + li) * 4, s);
+            if (lq == 0) lds_store<float>(sm + LS::DOTS + ((which * KW + kw) * CH + 16 * (t0 + t) + li) * 4, s);
         };
-        f32x4 G[4];
+        f32x4 G[TPW];
         ln = fresh_lane();
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < TPW; ++t) {
+            const int tt = t0 + t;
             f32x4 x = {0.f, 0.f, 0.f, 0.f}, y = x, z = x;
 #pragma unroll
             for (int kb = 0; kb < VB; ++kb) {
-                mma(x, fS[kb], frag_rows<OT>(ln, vO, 16 * t, 32 * kb));
-                mma(y, fS[kb], frag_rows<OT>(ln, vDy, 16 * t, 32 * kb));
-                mma(z, fdS[kb], frag_rows<OT>(ln, vDel, 16 * t, 32 * kb));
+                mma(x, fS[kb], frag_rows<OT>(ln, vO, 16 * tt, 32 * kb));
+                mma(y, fS[kb], frag_rows<OT>(ln, vDy, 16 * tt, 32 * kb));
+                mma(z, fdS[kb], frag_rows<OT>(ln, vDel, 16 * tt, 32 * kb));
             }
-            x = x * lds_load<float>(sm + LS::VEC + (SC_E + 16 * t + ln.li) * 4);
-            G[t] = y * -lds_load<float>(sm + LS::VEC + (SC_E + 16 * t + ln.li) * 4);
-            z = z * lds_load<float>(sm + LS::VEC + (SC_TAIL + 16 * t + ln.li) * 4);
+            x = x * lds_load<float>(sm + LS::VEC + (SC_E + 16 * tt + ln.li) * 4);
+            G[t] = y * -lds_load<float>(sm + LS::VEC + (SC_E + 16 * tt + ln.li) * 4);
+            z = z * lds_load<float>(sm + LS::VEC + (SC_TAIL + 16 * tt + ln.li) * 4);
             dq[t] += x;
             dk[t] += z;
             float kx[4];
             const float qx[4] = {to_f(qv[t][0]), to_f(qv[t][1]), to_f(qv[t][2]), to_f(qv[t][3])};
-            lds_get4<OT>(vK.p + vK.off(16 * t + ln.li, 16 * wv + 4 * ln.lq), kx);
+            lds_get4<OT>(vK.p + vK.off(16 * tt + ln.li, 16 * kw + 4 * ln.lq), kx);
             dot4(qx, x, t, 0);
             dot4(kx, G[t], t, 1);
             dot4(kx, z, t, 2);
@@ -426,7 +451,7 @@ __global__ __launch_bounds__(4 * DK, DK == 128 && !MULTI ? 4 : 2) void k_sc_grad
                 for (int i = 0; i < 8; ++i) s += to_f(fS[kb][i]) * to_f(fdS[kb][i]);
             s = row_sum16(s);
             s = (lane_value(s, 0) + lane_value(s, 16)) + (lane_value(s, 32) + lane_value(s, 48));
-            if (l == 0) lds_store<float>(sm + LS::SS + wv * 4, s);
+            if (l == 0) lds_store<float>(sm + LS::SS + kw * 4, s);  // (the same from both waves of a key tile)
         }
 
         // ---- dv = beta dY and dY.v, 16 bytes of a row a lane
@@ -543,26 +568,27 @@ __global__ __launch_bounds__(4 * DK, DK == 128 && !MULTI ? 4 : 2) void k_sc_grad
         ln = fresh_lane();
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            fK[kb] = frag_cols<OT>(ln, vK, 16 * wv, 32 * kb);
-            fQ[kb] = frag_cols<OT>(ln, vQ, 16 * wv, 32 * kb);
+            fK[kb] = frag_cols<OT>(ln, vK, 16 * kw, 32 * kb);
+            fQ[kb] = frag_cols<OT>(ln, vQ, 16 * kw, 32 * kb);
         }
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int t = 0; t < TPW; ++t) {
+            const int tt = t0 + t;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
-                if (kb == 0 || t >= 2) {  // rows of token tile t: columns up to it
-                    mma(dq[t], fK[kb], frag_rows<OT>(ln, vP, 16 * t, 32 * kb));
-                    mma(G[t], fK[kb], frag_rows<OT>(ln, vRp, 16 * t, 32 * kb));
+                if (kb == 0 || tt >= 2) {  // rows of token tile t: columns up to it
+                    mma(dq[t], fK[kb], frag_rows<OT>(ln, vP, 16 * tt, 32 * kb));
+                    mma(G[t], fK[kb], frag_rows<OT>(ln, vRp, 16 * tt, 32 * kb));
                 }
-                if (kb == 1 || t < 2) {   // columns of token tile t: rows from it on
-                    mma(dk[t], fQ[kb], frag_cols<OT>(ln, vP, 16 * t, 32 * kb));
-                    mma(dk[t], fK[kb], frag_cols<OT>(ln, vR, 16 * t, 32 * kb));
+                if (kb == 1 || tt < 2) {   // columns of token tile t: rows from it on
+                    mma(dk[t], fQ[kb], frag_cols<OT>(ln, vP, 16 * tt, 32 * kb));
+                    mma(dk[t], fK[kb], frag_cols<OT>(ln, vR, 16 * tt, 32 * kb));
                 }
             }
             float kx[4];
-            lds_get4<OT>(vK.p + vK.off(16 * t + ln.li, 16 * wv + 4 * ln.lq), kx);
+            lds_get4<OT>(vK.p + vK.off(16 * tt + ln.li, 16 * kw + 4 * ln.lq), kx);
             dot4(kx, G[t], t, 3);
-            dk[t] += G[t] * lds_load<float>(sm + LS::VEC + (SC_BETA + 16 * t + ln.li) * 4);
+            dk[t] += G[t] * lds_load<float>(sm + LS::VEC + (SC_BETA + 16 * tt + ln.li) * 4);
             __builtin_amdgcn_sched_barrier(0);
         }
         sync_lds();
@@ -571,7 +597,7 @@ __global__ __launch_bounds__(4 * DK, DK == 128 && !MULTI ? 4 : 2) void k_sc_grad
             float x = 0.f;
             if (task < 4) {
 #pragma unroll
-                for (int u = 0; u < NW; ++u) x += lds_load<float>(sm + LS::DOTS + ((task * NW + u) * CH + l) * 4);
+                for (int u = 0; u < KW; ++u) x += lds_load<float>(sm + LS::DOTS + ((task * KW + u) * CH + l) * 4);
             } else if (task == 4) {
                 const int b = l / 16;
 #pragma unroll
@@ -582,14 +608,14 @@ __global__ __launch_bounds__(4 * DK, DK == 128 && !MULTI ? 4 : 2) void k_sc_grad
                 }
             } else {
 #pragma unroll
-                for (int u = 0; u < NW; ++u) x += lds_load<float>(sm + LS::SS + u * 4);
+                for (int u = 0; u < KW; ++u) x += lds_load<float>(sm + LS::SS + u * 4);
             }
             lds_store<float>(sm + LS::RED + (task * CH + l) * 4, x);
         }
         if (!MULTI || hh + 1 == a.R) {  // dq and dk, turned to whole rows through LDS
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int o = swz<OT, DK>(16 * t + ln.li, 16 * wv + 4 * ln.lq) * ES;
+            for (int t = 0; t < TPW; ++t) {
+                const int o = swz<OT, DK>(16 * (t0 + t) + ln.li, 16 * kw + 4 * ln.lq) * ES;
                 const float x[4] = {dq[t][0], dq[t][1], dq[t][2], dq[t][3]};
                 const float y[4] = {dk[t][0], dk[t][1], dk[t][2], dk[t][3]};
                 lds_put4<OT>(sm + LS::ODQ + o, x);
@@ -641,7 +667,7 @@ static hipError_t launch_sc_bwd_t(const ScArgs& a, hipStream_t stream) {
     auto grad = a.R > 1 ? k_sc_grad<OT, DK, DV, true> : k_sc_grad<OT, DK, DV, false>;
     e = hipFuncSetAttribute((const void*)grad, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(grad, dim3((unsigned)(a.slots * a.Hk)), dim3(4 * DK), lds, stream, a);
+    hipLaunchKernelGGL(grad, dim3((unsigned)(a.slots * a.Hk)), dim3(512), lds, stream, a);
     return hipGetLastError();
 }
 
