@@ -454,19 +454,22 @@ __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, in
         const size_t id = (size_t)(w.q.slot0 + n) * a.Hv + w.h;
         sync_lds();  // A
         if (TRAIN && n > 0) store_state(n - 1);
+        FT Q[NKB];
+        if (OUT) {
+            const LSwz<OT, DK> vQ{buf + B::Q};
+#pragma unroll
+            for (int kb = 0; kb < NKB; ++kb) Q[kb] = lfrag_rowk8<OT>(vQ, 16 * wv, 32 * kb);
+        }
         sync_lds();  // B: from here to C the compute waves leave LDS mostly idle
         // O^T (rows: value columns, columns: this wave's tokens), the state's part
         f32x4 O[NC];
         if (OUT) {
-            const LSwz<OT, DK> vQ{buf + B::Q};
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) O[ch] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int kb = 0; kb < NKB; ++kb) {
-                const FT q = lfrag_rowk8<OT>(vQ, 16 * wv, 32 * kb);
+            for (int kb = 0; kb < NKB; ++kb)
 #pragma unroll
-                for (int ch = 0; ch < NC; ++ch) mma(O[ch], get_x<OT>(xs + ch * B::XT + B::XS + kb * F), q);
-            }
+                for (int ch = 0; ch < NC; ++ch) mma(O[ch], get_x<OT>(xs + ch * B::XT + B::XS + kb * F), Q[kb]);
             const float e = lds_load<float>(buf + B::VEC + (SC_E + 16 * wv + li) * 4);
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) O[ch] = O[ch] * e;
@@ -660,15 +663,14 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
         const size_t id = (size_t)(w.q.slot0 + (w.q.nt - 1 - n)) * a.Hv + w.h;
         sync_lds();  // A
         if (n > 0) store_state(n - 1);
-        sync_lds();  // B: from here to C the compute waves leave LDS mostly idle
-        // Q^T (e^gam dO), rows: the keys of compute wave wv
+        // Q^T (e^gam dO), rows: the keys of compute wave wv; one half of the tokens before B, the other after
+        // it, so that neither barrier waits for these waves
         f32x4 P[NC][NT][2];
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch)
 #pragma unroll
             for (int t = 0; t < NT; ++t) P[ch][t][0] = P[ch][t][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+        auto half = [&](int kb) {
             float s8[8];
             lds_get4<float>(buf + B::VEC + (SC_E + 32 * kb + 8 * lq) * 4, s8);
             lds_get4<float>(buf + B::VEC + (SC_E + 32 * kb + 8 * lq + 4) * 4, s8 + 4);
@@ -691,7 +693,10 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
                     if constexpr (NS == 2) mma(P[ch][t][1], qt[t], lo);
                 }
             }
-        }
+        };
+        half(0);
+        sync_lds();  // B
+        half(1);
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
 #pragma unroll
