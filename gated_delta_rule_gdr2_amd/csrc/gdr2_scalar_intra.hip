@@ -268,7 +268,7 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
 }
 
 // ============================================================================ gradients
-template <class OT, int DK, int DV>
+template <class OT, int DK, int DV, bool MULTI>
 struct ScGradLds {
     static constexpr int ES = sizeof(OT);
     static constexpr int NW = 8;               // waves
@@ -277,19 +277,23 @@ struct ScGradLds {
     static constexpr int SQ = CH * CH * ES;
     static constexpr int TK = CH * DK * ES, TV = CH * DV * ES;
     static constexpr int K = 0;             // raw k rows, swizzled
-    static constexpr int DO = K + TK;       // dO rows, swizzled
+    static constexpr int Q = K + TK;        // raw q rows: MULTI
+    static constexpr int HEAD = MULTI ? Q + TK : Q;  // a head's region (MULTI: two of them). In it:
+    static constexpr int DO = 0;            // dO rows, swizzled
     static constexpr int DEL = DO + TV;     // Delta, dY: slices [DV / 16][64][16]
     static constexpr int DY = DEL + TV;
-    static constexpr int P = DO;            // after the pair products: P, R / beta, R [64][64], raw q rows
+    static constexpr int P = DO;            // after the pair products: P, R / beta, R [64][64]
     static constexpr int RP = P + SQ;
     static constexpr int R = RP + SQ;
-    static constexpr int Q = R + SQ;
+    static constexpr int QL = R + SQ;       // and raw q rows: one head
     static constexpr int ODQ = DO;          // at the end: dq and dk rows on their way out
     static constexpr int ODK = ODQ + TK;
-    static constexpr int REGION = 3 * TV > 3 * SQ + TK ? 3 * TV : 3 * SQ + TK;
-    static_assert(2 * TK <= REGION, "dq and dk fit over what is dead");
-    static constexpr int VEC = DO + REGION;
-    static constexpr int ROWP = VEC + SC_VEC * 4;    // per block pair: row and column sums of N
+    static constexpr int AFTER = MULTI ? 3 * SQ : 3 * SQ + TK;
+    static constexpr int MX = 3 * TV > AFTER ? 3 * TV : AFTER;
+    static constexpr int VEC = MX > 2 * TK ? MX : 2 * TK;  // the row factors (copied by two waves, 1 KB each)
+    static constexpr int REGION = VEC + 2048;
+    static_assert(SC_VEC * 4 > 1024 && SC_VEC * 4 <= 2048, "the row factors are two waves' copies");
+    static constexpr int ROWP = HEAD + (MULTI ? 2 : 1) * REGION;  // per block pair: row and column sums of N
     static constexpr int COLP = ROWP + NPAIR * 16 * 4;
     static constexpr int DOTS = COLP + NPAIR * 16 * 4;  // per key tile and row: q.dq_s, k.dx_s, k.dk_s, k.G
     static constexpr int DOTV = DOTS + 4 * KW * CH * 4; // per row: dY.v
@@ -325,14 +329,16 @@ __device__ __forceinline__ void dma_rows_clamped(const OT* base, size_t rs, int 
 // The last line sums only terms that carry the decay across t: the diagonal of N, which does not
 // depend on the decay, is left out, so that a strong decay leaves a small dg and no cancellation.
 //
-// A chunk and head moves 208 KB (d = 128, bf16), which at the rate of HBM is two thirds of the time;
-// two workgroups a compute unit, one loading while the other works, is what the LDS layout (q enters
-// LDS only when dO, Delta and dY have left it) and the register bound are for. MULTI: more than one
-// value head a key head. (One head is a kernel of its own: around a loop over heads the compiler keeps
-// a hundred addresses in registers.)
+// A chunk and head moves 208 KB (d = 128, bf16), which at the rate of HBM is two thirds of the time.
+// One value head a key head: two workgroups a compute unit, one loading while the other works, which
+// is what the LDS layout (q enters LDS only when dO, Delta and dY have left it) and the register bound
+// are for. MULTI, more than one: around a loop over heads the registers are not enough for two workgroups
+// (84 spilled), so one has the compute unit, keeps q in LDS and loads the next head while this one is
+// worked on. Measured, d = 128, bf16: 97 us at 2 x 4096 tokens, 16 heads (4.5 TB/s); 129 us at 8859 packed
+// tokens, 8 key heads with 2 value heads each (3.1 TB/s; without the loads ahead 144 us).
 template <class OT, int DK, int DV, bool MULTI>
 __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_grad(ScArgs a) {
-    using LS = ScGradLds<OT, DK, DV>;
+    using LS = ScGradLds<OT, DK, DV, MULTI>;
     using FT = typename Frag<OT>::type;
     constexpr int ES = sizeof(OT), NW = LS::NW, KW = LS::KW, TPW = LS::TPW, NTHR = 64 * NW, KB = DK / 32, VB = DV / 32;
     constexpr int PPW = (NPAIR + NW - 1) / NW;  // block pairs of a wave
@@ -356,61 +362,80 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
     const int nvalid = min(CH, q.len - CH * c);
     const size_t rsk = (size_t)a.Hk * DK, rsv = (size_t)a.Hv * DV;
     const size_t k0 = row0 * rsk + (size_t)hk * DK;
-    const LSwz<OT, DK> vK{sm + LS::K}, vQ{sm + LS::Q};
-    const LSwz<OT, DV> vO{sm + LS::DO};
-    const LSlice<OT, CH> vDel{sm + LS::DEL}, vDy{sm + LS::DY};
-    const LSwz<OT, CH> vP{sm + LS::P}, vRp{sm + LS::RP}, vR{sm + LS::R};
+    const LSwz<OT, DK> vK{sm + LS::K};
     dma_rows_clamped<OT, DK, NW>((const OT*)a.k + k0, rsk, nvalid, sm + LS::K, wv);
+    if (MULTI) dma_rows_clamped<OT, DK, NW>((const OT*)a.q + k0, rsk, nvalid, sm + LS::Q, wv);
     const int kw = wv % KW, t0 = TPW * (wv / KW);  // this wave's key tile and first token tile
     f32x4 dq[TPW], dk[TPW];  // transposed tiles: keys 16 kw + 4 lq + i, tokens 16 (t0 + t) + li
 #pragma unroll
     for (int t = 0; t < TPW; ++t) dq[t] = dk[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-#pragma unroll 1
-    for (int hh = 0; hh < (MULTI ? a.R : 1); ++hh) {
-        const int h = hk * a.R + hh;
+    // What a value head brings: dO, Delta, dY and the row factors to LDS; this wave's key rows of S and dS'
+    // (K = value column) and v (16 bytes of a row a lane, rows past the end zero) to registers
+    constexpr int EPC = 16 / ES, LPR = DV / EPC, NVL = CH * LPR / NTHR;
+    typedef OT VT __attribute__((ext_vector_type(EPC)));
+    FT fS[VB], fdS[VB];
+    VT gv[NVL];
+    auto load_lds = [&](int h, lds_char* hd) {
         const size_t id = (size_t)slot * a.Hv + h;
-        const size_t v0 = row0 * rsv + (size_t)h * DV;
-        const OT* gS = (const OT*)(a.ws + a.L.o_s) + id * a.L.s;
-        const OT* gdS = (const OT*)(a.ws + a.L.o_ds) + id * a.L.s;
-        Lane ln = fresh_lane();
-        const int li = ln.li, lq = ln.lq, l = li + 16 * lq, tid = 64 * wv + l;
-        if (MULTI && hh) sync_lds();  // the head before is done with LDS
-        dma_rows<OT, DV, NW>((const OT*)a.dout + v0, rsv, nvalid, sm + LS::DO, wv);
-        zero_tail_rows<OT, DV, NTHR>(sm + LS::DO, nvalid);
+        const int l = lane_id();
+        dma_rows<OT, DV, NW>((const OT*)a.dout + row0 * rsv + (size_t)h * DV, rsv, nvalid, hd + LS::DO, wv);
+        zero_tail_rows<OT, DV, NTHR>(hd + LS::DO, nvalid);
         const char* gDel = a.ws + a.L.o_delta + id * a.L.d * ES;
         const char* gDy = a.ws + a.L.o_dy + id * a.L.d * ES;
 #pragma unroll
         for (int n = 0; n < LS::TV / 1024; n += NW) {
-            __builtin_amdgcn_global_load_lds(gDel + (n + wv) * 1024 + l * 16, (lds_void*)(sm + LS::DEL + (n + wv) * 1024), 16,
+            __builtin_amdgcn_global_load_lds(gDel + (n + wv) * 1024 + l * 16, (lds_void*)(hd + LS::DEL + (n + wv) * 1024), 16,
                                              0, 0);
-            __builtin_amdgcn_global_load_lds(gDy + (n + wv) * 1024 + l * 16, (lds_void*)(sm + LS::DY + (n + wv) * 1024), 16,
+            __builtin_amdgcn_global_load_lds(gDy + (n + wv) * 1024 + l * 16, (lds_void*)(hd + LS::DY + (n + wv) * 1024), 16,
                                              0, 0);
         }
-        for (int i = tid; i < SC_VEC; i += NTHR)
-            lds_store<float>(sm + LS::VEC + i * 4, ((const float*)(a.ws + a.L.o_vec))[id * a.L.vec + i]);
-        FT fS[VB], fdS[VB];  // this wave's key rows of S and dS', K = value column
+        if (wv < 2) {  // (the second wave's upper lanes: again what its lower lanes copy)
+            const char* src = a.ws + a.L.o_vec + id * a.L.vec * 4 + (wv == 0 ? l : 64 + l % ((SC_VEC * 4 - 1024) / 16)) * 16;
+            __builtin_amdgcn_global_load_lds(src, (lds_void*)(hd + LS::VEC + wv * 1024), 16, 0, 0);
+        }
+    };
+    auto load_s = [&](int h) {
+        const size_t id = (size_t)slot * a.Hv + h;
 #pragma unroll
         for (int kb = 0; kb < VB; ++kb) {
-            fS[kb] = gfrag_slice<OT, DK>(gS, 16 * kw, kb);
-            fdS[kb] = gfrag_slice<OT, DK>(gdS, 16 * kw, kb);
+            fS[kb] = gfrag_slice<OT, DK>((const OT*)(a.ws + a.L.o_s) + id * a.L.s, 16 * kw, kb);
+            fdS[kb] = gfrag_slice<OT, DK>((const OT*)(a.ws + a.L.o_ds) + id * a.L.s, 16 * kw, kb);
         }
-        typename Raw4<OT>::type qv[TPW];  // q of this wave's tokens and keys
-#pragma unroll
-        for (int t = 0; t < TPW; ++t)
-            qv[t] = *(const typename Raw4<OT>::type*)((const OT*)a.q + k0 +
-                                                      (size_t)min(16 * (t0 + t) + li, nvalid - 1) * rsk + 16 * kw + 4 * lq);
-        // v, 16 bytes of a row a lane (rows past the end: zero)
-        constexpr int EPC = 16 / ES, LPR = DV / EPC, NVL = CH * LPR / NTHR;
-        typedef OT VT __attribute__((ext_vector_type(EPC)));
-        VT gv[NVL];
+    };
+    auto load_v = [&](int h) {
 #pragma unroll
         for (int i = 0; i < NVL; ++i) {
-            const int u = tid + NTHR * i, rr = u / LPR;
-            gv[i] = rr < nvalid ? *(const VT*)((const OT*)a.v + v0 + rr * rsv + EPC * (u % LPR)) : VT{};
+            const int u = threadIdx.x + NTHR * i, rr = u / LPR;
+            gv[i] = rr < nvalid ? *(const VT*)((const OT*)a.v + row0 * rsv + (size_t)h * DV + rr * rsv + EPC * (u % LPR)) : VT{};
+        }
+    };
+    load_lds(hk * a.R, sm + LS::HEAD);
+    load_s(hk * a.R);
+    load_v(hk * a.R);
+
+#pragma unroll 1
+    for (int hh = 0; hh < (MULTI ? a.R : 1); ++hh) {
+        const int h = hk * a.R + hh;
+        const size_t v0 = row0 * rsv + (size_t)h * DV;
+        lds_char* hd = sm + LS::HEAD + (MULTI ? (hh & 1) * LS::REGION : 0);
+        const LSwz<OT, DK> vQ{MULTI ? sm + LS::Q : hd + LS::QL};
+        const LSwz<OT, DV> vO{hd + LS::DO};
+        const LSlice<OT, CH> vDel{hd + LS::DEL}, vDy{hd + LS::DY};
+        const LSwz<OT, CH> vP{hd + LS::P}, vRp{hd + LS::RP}, vR{hd + LS::R};
+        Lane ln = fresh_lane();
+        const int li = ln.li, lq = ln.lq, l = li + 16 * lq, tid = 64 * wv + l;
+        const bool more = MULTI && hh + 1 < a.R;
+        typename Raw4<OT>::type qv[TPW];  // q of this wave's tokens and keys
+        if (!MULTI) {
+#pragma unroll
+            for (int t = 0; t < TPW; ++t)
+                qv[t] = *(const typename Raw4<OT>::type*)((const OT*)a.q + k0 +
+                                                          (size_t)min(16 * (t0 + t) + li, nvalid - 1) * rsk + 16 * kw + 4 * lq);
         }
         wait_vm<0>();
-        sync_lds();
+        sync_lds();  // this head is in LDS, and the head before is done with its region
+        if (more) load_lds(h + 1, sm + LS::HEAD + ((hh + 1) & 1) * LS::REGION);
 
         // ---- the states' parts
         auto dot4 = [&](const float (&y)[4], const f32x4& x, int t, int which) {
@@ -430,13 +455,19 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
                 mma(y, fS[kb], frag_rows<OT>(ln, vDy, 16 * tt, 32 * kb));
                 mma(z, fdS[kb], frag_rows<OT>(ln, vDel, 16 * tt, 32 * kb));
             }
-            x = x * lds_load<float>(sm + LS::VEC + (SC_E + 16 * tt + ln.li) * 4);
-            G[t] = y * -lds_load<float>(sm + LS::VEC + (SC_E + 16 * tt + ln.li) * 4);
-            z = z * lds_load<float>(sm + LS::VEC + (SC_TAIL + 16 * tt + ln.li) * 4);
+            x = x * lds_load<float>(hd + LS::VEC + (SC_E + 16 * tt + ln.li) * 4);
+            G[t] = y * -lds_load<float>(hd + LS::VEC + (SC_E + 16 * tt + ln.li) * 4);
+            z = z * lds_load<float>(hd + LS::VEC + (SC_TAIL + 16 * tt + ln.li) * 4);
             dq[t] += x;
             dk[t] += z;
             float kx[4];
-            const float qx[4] = {to_f(qv[t][0]), to_f(qv[t][1]), to_f(qv[t][2]), to_f(qv[t][3])};
+            float qx[4];
+            if (MULTI) {
+                lds_get4<OT>(vQ.p + vQ.off(16 * tt + ln.li, 16 * kw + 4 * ln.lq), qx);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) qx[i] = to_f(qv[t][i]);
+            }
             lds_get4<OT>(vK.p + vK.off(16 * tt + ln.li, 16 * kw + 4 * ln.lq), kx);
             dot4(qx, x, t, 0);
             dot4(kx, G[t], t, 1);
@@ -453,13 +484,17 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             s = (lane_value(s, 0) + lane_value(s, 16)) + (lane_value(s, 32) + lane_value(s, 48));
             if (l == 0) lds_store<float>(sm + LS::SS + kw * 4, s);  // (the same from both waves of a key tile)
         }
+        if (more) {
+            __builtin_amdgcn_sched_barrier(0);
+            load_s(h + 1);
+        }
 
         // ---- dv = beta dY and dY.v, 16 bytes of a row a lane
 #pragma unroll
         for (int i = 0; i < NVL; ++i) {
             const int u = tid + NTHR * i, rr = u / LPR, col = EPC * (u % LPR);
             const VT y = lds_load<VT>(vDy.p + vDy.off(rr, col));
-            const float b = lds_load<float>(sm + LS::VEC + (SC_BETA + rr) * 4);
+            const float b = lds_load<float>(hd + LS::VEC + (SC_BETA + rr) * 4);
             float s = 0.f;
             VT d;
 #pragma unroll
@@ -471,6 +506,7 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             s = LPR == 16 ? row_sum16(s) : row_sum8(s);
             if (u % LPR == 0) lds_store<float>(sm + LS::DOTV + rr * 4, s);
         }
+        if (more) load_v(h + 1);
         __builtin_amdgcn_sched_barrier(0);
 
         // ---- block pairs (rows 16 R + li, columns 16 I + 4 lq + i)
@@ -483,12 +519,14 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
                 int R, I;
                 pair_ri(p, R, I);
                 const int r = 16 * R + ln.li, i0 = 16 * I + 4 * ln.lq;
-                // the rows of q come from memory (this chunk's are in cache by now)
+                // one head: the rows of q come from memory (this chunk's are in cache by now)
                 FT fq[KB];
                 const OT* qp = (const OT*)a.q + k0 + (size_t)min(r, nvalid - 1) * rsk + 8 * ln.lq;
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb) {
-                    if constexpr (ES == 2) {
+                    if constexpr (MULTI) {
+                        fq[kb] = frag_rows<OT>(ln, vQ, 16 * R, 32 * kb);
+                    } else if constexpr (ES == 2) {
                         fq[kb] = *(const FT*)(qp + 32 * kb);
                     } else {
                         const f32x4 x0 = *(const f32x4*)(qp + 32 * kb), x1 = *(const f32x4*)(qp + 32 * kb + 4);
@@ -508,12 +546,12 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
                     mma(kk, f, frag_rows<OT>(ln, vK, 16 * R, 32 * kb));
                     mma(qk, f, fq[kb]);
                 }
-                const float rhi = lds_load<float>(sm + LS::VEC + (SC_GHI + r) * 4);
-                const float rlo = lds_load<float>(sm + LS::VEC + (SC_GLO + r) * 4);
-                const float br = lds_load<float>(sm + LS::VEC + (SC_BETA + r) * 4);
+                const float rhi = lds_load<float>(hd + LS::VEC + (SC_GHI + r) * 4);
+                const float rlo = lds_load<float>(hd + LS::VEC + (SC_GLO + r) * 4);
+                const float br = lds_load<float>(hd + LS::VEC + (SC_BETA + r) * 4);
                 float ihi[4], ilo[4], nn[4];
-                lds_get4<float>(sm + LS::VEC + (SC_GHI + i0) * 4, ihi);
-                lds_get4<float>(sm + LS::VEC + (SC_GLO + i0) * 4, ilo);
+                lds_get4<float>(hd + LS::VEC + (SC_GHI + i0) * 4, ihi);
+                lds_get4<float>(hd + LS::VEC + (SC_GLO + i0) * 4, ilo);
                 float rows = 0.f;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -533,8 +571,8 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        sync_lds();  // dO, Delta and dY are dead: q, P and R take their place
-        dma_rows_clamped<OT, DK, NW>((const OT*)a.q + k0, rsk, nvalid, sm + LS::Q, wv);
+        sync_lds();  // dO, Delta and dY are dead: P and R (and q) take their place
+        if (!MULTI) dma_rows_clamped<OT, DK, NW>((const OT*)a.q + k0, rsk, nvalid, hd + LS::QL, wv);
 #pragma unroll
         for (int n = 0; n < PPW; ++n) {
             const int p = wv + NW * n;
@@ -542,13 +580,13 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
                 int R, I;
                 pair_ri(p, R, I);
                 const int o = swz<OT, CH>(16 * R + ln.li, 16 * I + 4 * ln.lq) * ES;
-                const float br = lds_load<float>(sm + LS::VEC + (SC_BETA + 16 * R + ln.li) * 4);
+                const float br = lds_load<float>(hd + LS::VEC + (SC_BETA + 16 * R + ln.li) * 4);
                 const float x[4] = {fP[n][0], fP[n][1], fP[n][2], fP[n][3]};
                 const float y[4] = {fRp[n][0], fRp[n][1], fRp[n][2], fRp[n][3]};
                 const float z[4] = {br * y[0], br * y[1], br * y[2], br * y[3]};
-                lds_put4<OT>(sm + LS::P + o, x);
-                lds_put4<OT>(sm + LS::RP + o, y);
-                lds_put4<OT>(sm + LS::R + o, z);
+                lds_put4<OT>(hd + LS::P + o, x);
+                lds_put4<OT>(hd + LS::RP + o, y);
+                lds_put4<OT>(hd + LS::R + o, z);
             }
         }
         for (int u = wv; u < 6; u += NW) {
@@ -556,11 +594,11 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             sc_upper_ri(u, R, I);
             const int o = swz<OT, CH>(16 * R + ln.li, 16 * I + 4 * ln.lq) * ES;
             const float z[4] = {0.f, 0.f, 0.f, 0.f};
-            lds_put4<OT>(sm + LS::P + o, z);
-            lds_put4<OT>(sm + LS::RP + o, z);
-            lds_put4<OT>(sm + LS::R + o, z);
+            lds_put4<OT>(hd + LS::P + o, z);
+            lds_put4<OT>(hd + LS::RP + o, z);
+            lds_put4<OT>(hd + LS::R + o, z);
         }
-        wait_vm<0>();
+        if (!MULTI) wait_vm<0>();
         sync_lds();
 
         // ---- dq += P K, G += (R / beta) K, dk += P^T Q + R^T K + beta G
@@ -588,7 +626,7 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             float kx[4];
             lds_get4<OT>(vK.p + vK.off(16 * tt + ln.li, 16 * kw + 4 * ln.lq), kx);
             dot4(kx, G[t], t, 3);
-            dk[t] += G[t] * lds_load<float>(sm + LS::VEC + (SC_BETA + 16 * tt + ln.li) * 4);
+            dk[t] += G[t] * lds_load<float>(hd + LS::VEC + (SC_BETA + 16 * tt + ln.li) * 4);
             __builtin_amdgcn_sched_barrier(0);
         }
         sync_lds();
@@ -618,19 +656,19 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
                 const int o = swz<OT, DK>(16 * (t0 + t) + ln.li, 16 * kw + 4 * ln.lq) * ES;
                 const float x[4] = {dq[t][0], dq[t][1], dq[t][2], dq[t][3]};
                 const float y[4] = {dk[t][0], dk[t][1], dk[t][2], dk[t][3]};
-                lds_put4<OT>(sm + LS::ODQ + o, x);
-                lds_put4<OT>(sm + LS::ODK + o, y);
+                lds_put4<OT>(hd + LS::ODQ + o, x);
+                lds_put4<OT>(hd + LS::ODK + o, y);
             }
         }
         sync_lds();
         if (!MULTI || hh + 1 == a.R) {
-            store_rows_tiles<OT, DK, NTHR, false>(sm + LS::ODQ, (OT*)a.dq + k0, rsk, nvalid);
-            store_rows_tiles<OT, DK, NTHR, false>(sm + LS::ODK, (OT*)a.dk + k0, rsk, nvalid);
+            store_rows_tiles<OT, DK, NTHR, false>(hd + LS::ODQ, (OT*)a.dq + k0, rsk, nvalid);
+            store_rows_tiles<OT, DK, NTHR, false>(hd + LS::ODK, (OT*)a.dk + k0, rsk, nvalid);
         }
         // ---- dbeta and dg
         if (wv == 0) {
             auto red = [&](int t) { return lds_load<float>(sm + LS::RED + (t * CH + l) * 4); };
-            const float x = red(0) + lds_load<float>(sm + LS::VEC + (SC_BETA + l) * 4) * red(1) + red(4);
+            const float x = red(0) + lds_load<float>(hd + LS::VEC + (SC_BETA + l) * 4) * red(1) + red(4);
             // suffix sum of x, exclusive prefix sum of k.dk_s: inside the 16 lanes of a row, then over rows
             float suf = row_suffix16(x), pre = row_scan16(red(2));
             const float s1 = lane_value(suf, 16), s2 = lane_value(suf, 32), s3 = lane_value(suf, 48);
@@ -641,7 +679,7 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             if (l < nvalid) {
                 const size_t at = (size_t)(row0 + l) * a.Hv + h;
                 ((OT*)a.dbeta)[at] = to_ot<OT>(lds_load<float>(sm + LS::DOTV + l * 4) + red(3));
-                ((OT*)a.dg)[at] = to_ot<OT>(suf + pre + lds_load<float>(sm + LS::VEC + SC_EC * 4) * red(5));
+                ((OT*)a.dg)[at] = to_ot<OT>(suf + pre + lds_load<float>(hd + LS::VEC + SC_EC * 4) * red(5));
             }
         }
     }
@@ -663,7 +701,7 @@ template <class OT, int DK, int DV>
 static hipError_t launch_sc_bwd_t(const ScArgs& a, hipStream_t stream) {
     hipError_t e = launch_sc_bwd_chain_t<OT, DK, DV>(a, stream);
     if (e != hipSuccess) return e;
-    constexpr int lds = ScGradLds<OT, DK, DV>::BYTES;
+    const int lds = a.R > 1 ? ScGradLds<OT, DK, DV, true>::BYTES : ScGradLds<OT, DK, DV, false>::BYTES;
     auto grad = a.R > 1 ? k_sc_grad<OT, DK, DV, true> : k_sc_grad<OT, DK, DV, false>;
     e = hipFuncSetAttribute((const void*)grad, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
