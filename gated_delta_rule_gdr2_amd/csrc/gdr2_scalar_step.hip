@@ -5,10 +5,12 @@
 // so one pass over the old state gives both sums over the key axis, and the update needs no second
 // reduction. Bound by HBM: the state is read and written once a call.
 //
-// k_sc_step: one workgroup of WR x WC waves per (row, value head, 32 WC columns); the WR waves of a
-// column group split the key axis and join u and p through LDS. Lane l holds columns 4 (l % 8) .. + 3
-// of rows l / 8 + 8 i, so each row segment a wave moves is one 128-byte line. The state stays in
-// registers for all tokens of the call.
+// k_sc_step: one workgroup of two waves per (row, value head, 64 columns), a wave on 32 columns. Lane l
+// holds columns 4 (l % 8) .. + 3 of rows l / 8 + 8 i, so each row segment a wave moves is one 128-byte
+// line, and the sums over the key axis stay inside a wave. The state stays in registers for all tokens
+// of the call. Measured at d = 128, 16 value heads: 512 rows (1.08 GB) in 180 - 190 us, 5.7 - 6.0 TB/s;
+// one row (2.1 MB) in 5.0 us, a launch and the latency of one read, and no less with the key axis split
+// over four waves that join their sums in LDS (5.1 us).
 #include "gdr2_device.hpp"
 #include "gdr2_scalar.hpp"
 
@@ -22,32 +24,28 @@ __device__ __forceinline__ f32x4 sum_row_groups(f32x4 x) {  // over lanes l ^ 8,
     return x;
 }
 
-template <class OT, int DK, int DV, int WR, int WC, bool NT>
-__global__ __launch_bounds__(64 * WR * WC) void k_sc_step(ScStepArgs a) {
-    constexpr int NTHR = 64 * WR * WC, NI = DK / (8 * WR), NJ = DV / (32 * WC);
-    __shared__ float sk[DK], sq[DK], sv[32 * WC], skq[WR * WC];
-    __shared__ f32x4 sred[2][WR][WC][8];
+template <class OT, int DK, int DV, bool NT>
+__global__ __launch_bounds__(128) void k_sc_step(ScStepArgs a) {
+    constexpr int NTHR = 128, NI = DK / 8, NJ = DV / 64;
+    __shared__ float sk[DK], sq[DK], sv[64];
     poison_lds((lds_char*)sk, sizeof(sk));
     poison_lds((lds_char*)sq, sizeof(sq));
     poison_lds((lds_char*)sv, sizeof(sv));
-    poison_lds((lds_char*)skq, sizeof(skq));
-    poison_lds((lds_char*)sred, sizeof(sred));
     poison_lds_done();
     const int tid = threadIdx.x, wv = tid >> 6, l = tid & 63, cq = l & 7, rg = l >> 3;
-    const int wr = wv / WC, wc = wv % WC;
     const int jb = blockIdx.x % NJ, hb = blockIdx.x / NJ;
     const int h = hb % a.Hv, b0 = hb / a.Hv, hk = h / a.R;
     const int slot = a.slots ? a.slots[b0] : b0;
-    const int col0 = 32 * WC * jb, col = col0 + 32 * wc + 4 * cq;
+    const int col0 = 64 * jb, col = col0 + 32 * wv + 4 * cq;
     if (slot < 0 || slot >= a.states) {  // a padding row: no state, zero output
         for (int t = 0; t < a.T; ++t)
-            if (tid < 32 * WC) ((OT*)a.o)[(((size_t)b0 * a.T + t) * a.Hv + h) * DV + col0 + tid] = to_ot<OT>(0.f);
+            if (tid < 64) ((OT*)a.o)[(((size_t)b0 * a.T + t) * a.Hv + h) * DV + col0 + tid] = to_ot<OT>(0.f);
         return;
     }
     float* hs = a.state + ((size_t)slot * a.Hv + h) * DK * DV + col;
-    f32x4 S[NI];  // S[i]: row wr DK / WR + rg + 8 i
+    f32x4 S[NI];  // S[i]: row rg + 8 i
 #pragma unroll
-    for (int i = 0; i < NI; ++i) S[i] = *(const f32x4*)(hs + (size_t)(wr * (DK / WR) + rg + 8 * i) * DV);
+    for (int i = 0; i < NI; ++i) S[i] = *(const f32x4*)(hs + (size_t)(rg + 8 * i) * DV);
     // Rows that name the same state are one sequence, in the order of the rows: the first of them
     // does the work of all.
     int more = 0;
@@ -69,15 +67,15 @@ __global__ __launch_bounds__(64 * WR * WC) void k_sc_step(ScStepArgs a) {
                 sk[i] = to_f(((const OT*)a.k)[kr + i]);
                 sq[i] = to_f(((const OT*)a.q)[kr + i]);
             }
-            if (tid < 32 * WC) sv[tid] = to_f(((const OT*)a.v)[vr + col0 + tid]);
+            if (tid < 64) sv[tid] = to_f(((const OT*)a.v)[vr + col0 + tid]);
             const float e = expf(to_f(((const OT*)a.g)[tok * a.Hv + h]));
             const float beta = to_f(((const OT*)a.beta)[tok * a.Hv + h]);
             __syncthreads();
             f32x4 u = {0.f, 0.f, 0.f, 0.f}, p = u;
-            float kq = 0.f;  // this wave's rows of k.q, the same in all lanes of a row group
+            float kq = 0.f;  // k.q, the same in all lanes of a row group
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int r = wr * (DK / WR) + rg + 8 * i;
+                const int r = rg + 8 * i;
                 const float k = sk[r], q = sq[r];
                 u += k * S[i];
                 p += q * S[i];
@@ -87,28 +85,12 @@ __global__ __launch_bounds__(64 * WR * WC) void k_sc_step(ScStepArgs a) {
             p = sum_row_groups(p);
 #pragma unroll
             for (int m = 8; m < 64; m <<= 1) kq += __shfl_xor(kq, m, 64);
-            if constexpr (WR > 1) {
-                if (rg == 0) {
-                    sred[0][wr][wc][cq] = u;
-                    sred[1][wr][wc][cq] = p;
-                }
-                if (l == 0) skq[wv] = kq;
-                __syncthreads();
-                u = p = f32x4{0.f, 0.f, 0.f, 0.f};
-                kq = 0.f;
-#pragma unroll
-                for (int w = 0; w < WR; ++w) {
-                    u += sred[0][w][wc][cq];
-                    p += sred[1][w][wc][cq];
-                    kq += skq[w * WC + wc];
-                }
-            }
             f32x4 d;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = beta * (sv[32 * wc + 4 * cq + j] - e * u[j]);
+            for (int j = 0; j < 4; ++j) d[j] = beta * (sv[32 * wv + 4 * cq + j] - e * u[j]);
 #pragma unroll
-            for (int i = 0; i < NI; ++i) S[i] = e * S[i] + sk[wr * (DK / WR) + rg + 8 * i] * d;
-            if (rg == 0 && wr == 0) {
+            for (int i = 0; i < NI; ++i) S[i] = e * S[i] + sk[rg + 8 * i] * d;
+            if (rg == 0) {
                 const f32x4 o = e * p + kq * d;
                 const float ov[4] = {o[0], o[1], o[2], o[3]};
                 st4((OT*)a.o + vr + col, ov);
@@ -119,16 +101,16 @@ __global__ __launch_bounds__(64 * WR * WC) void k_sc_step(ScStepArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i)
-        store_out<NT>((f32x4*)(hs + (size_t)(wr * (DK / WR) + rg + 8 * i) * DV), S[i]);
+        store_out<NT>((f32x4*)(hs + (size_t)(rg + 8 * i) * DV), S[i]);
 }
 
 template <class OT, int DK, int DV>
 static hipError_t launch_sc_step_t(const ScStepArgs& a, hipStream_t stream) {
-    const unsigned pairs = (unsigned)a.B * a.Hv;
+    const unsigned groups = (unsigned)a.B * a.Hv * (DV / 64);
     if (a.nt_out)
-        hipLaunchKernelGGL((k_sc_step<OT, DK, DV, 1, 2, true>), dim3(pairs * (DV / 64)), dim3(128), 0, stream, a);
+        hipLaunchKernelGGL((k_sc_step<OT, DK, DV, true>), dim3(groups), dim3(128), 0, stream, a);
     else
-        hipLaunchKernelGGL((k_sc_step<OT, DK, DV, 1, 2, false>), dim3(pairs * (DV / 64)), dim3(128), 0, stream, a);
+        hipLaunchKernelGGL((k_sc_step<OT, DK, DV, false>), dim3(groups), dim3(128), 0, stream, a);
     return hipGetLastError();
 }
 
