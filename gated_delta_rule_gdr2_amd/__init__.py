@@ -19,6 +19,7 @@ import functools
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 __all__ = ["gdr2_fwd", "gdr2_bwd", "gdr2_step", "gdr2_fwd_logits", "gdr2_bwd_logits", "gdr2_step_logits",
            "gdr2_fwd_seg", "gdr2_bwd_seg", "gdr2_fwd_noalloc", "gdr2_fwd_workspace_bytes",
@@ -578,18 +579,38 @@ def gdr2_scalar_step(q, k, v, g, beta, state, *, slots=None, o=None, stream=None
     return o
 
 
+def _accumulation_streams(leaves):
+    """Of each leaf that wants a gradient, what its accumulation node carries. A node lives as long as any
+    graph that was built on the leaf, and the engine runs it on the stream of the first."""
+    return [torch.autograd.graph.get_gradient_edge(t).node.metadata
+            for t in leaves if t is not None and t.is_leaf and t.requires_grad]
+
+
 class GDR2ScalarFunction(torch.autograd.Function):
-    """Autograd wrapper: forward saves the chunks' states in the workspace, backward reuses them."""
+    """Autograd wrapper: forward saves the chunks' states in the workspace, backward reuses them.
+
+    Forward and backward may be captured into a graph together, but not while an earlier graph of the same
+    leaves, built on another stream, is still alive: their gradients would be accumulated on that stream,
+    outside the capture. Such a backward is refused."""
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, h0=None, cu_seqlens=None):
+        here = torch.cuda.current_stream(q.device).cuda_stream
+        for m in _accumulation_streams((q, k, v, g, beta, h0)):
+            m.setdefault("gdr2_stream", here)
         o, ht, ws = gdr2_scalar_fwd(q, k, v, g, beta, h0, cu_seqlens=cu_seqlens, save_for_bwd=True)
         ctx.save_for_backward(q, k, v, g, beta, h0, cu_seqlens, ws)
         return o, ht
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dht):
         q, k, v, g, beta, h0, cu_seqlens, ws = ctx.saved_tensors
+        if torch.cuda.is_current_stream_capturing():
+            here = torch.cuda.current_stream(q.device).cuda_stream
+            if any(m.get("gdr2_stream", here) != here for m in _accumulation_streams((q, k, v, g, beta, h0))):
+                raise RuntimeError("cannot capture this backward: a graph of the same leaves from another stream is "
+                                   "still alive (drop its outputs first, or capture gdr2_scalar_bwd)")
         gr = gdr2_scalar_bwd(q, k, v, g, beta, h0, do.contiguous(), None if dht is None else dht.contiguous(),
                              cu_seqlens=cu_seqlens, ws=ws, fwd_saved=True, need_dh0=h0 is not None)
         return gr["dq"], gr["dk"], gr["dv"], gr["dg"], gr["dbeta"], gr["dh0"], None
@@ -619,6 +640,8 @@ def _cache_strides(k_cache, v_cache, block_table, dtype, D, dev):
             raise ValueError("%s must have %d channels, got %d" % (n, D, t.shape[3]))
         if t.stride(3) != 1:
             raise ValueError("the channels of %s must be contiguous" % n)
+    if k_cache.shape[0] > 0x7fffffff or k_cache.shape[1] > 0x7fffffff:
+        raise ValueError("k_cache has too many pages or tokens a page")
     if block_table.dim() != 2:
         raise ValueError("block_table must have two dimensions [B,max_pages]")
     return _Strides(*k_cache.stride()[:3], *v_cache.stride()[:3])
@@ -664,7 +687,8 @@ def gdr2_attn_step(q, k_cache, v_cache, block_table, lengths, *, scale=None, win
     with _on(dev, stream) as s:
         st = lib.gdr2_attn_step(_adr(q), _adr(k_cache), _adr(v_cache), strides, _adr(block_table), _adr(lengths),
                                 _adr(o), _adr(lse), B, Hq, Hkv, D, pages, page, max_pages,
-                                D ** -0.5 if scale is None else scale, window, dt, _adr(ws), ws.numel(), s)
+                                D ** -0.5 if scale is None else scale, max(-1, min(window, 0x7fffffff)), dt,
+                                _adr(ws), ws.numel(), s)
     _raise(st, "gdr2_attn_step")
     return o if lse is None else (o, lse)
 

@@ -325,13 +325,14 @@ const char* gdr2_strerror(int status) {
     switch (status) {
         case GDR2_OK: return "ok";
         case GDR2_ERR_NULL: return "a required pointer is NULL";
-        case GDR2_ERR_SHAPE: return "invalid shape (B, T and H must be >= 0; sizes must fit)";
+        case GDR2_ERR_SHAPE: return "invalid shape (B, T and H must be >= 0; heads that share must divide evenly; sizes must fit)";
         case GDR2_ERR_UNSUPPORTED: return "unsupported dk/dv/chunk/dtype combination";
         case GDR2_ERR_ALIGN: return "a pointer is not 16-byte aligned";
         case GDR2_ERR_WORKSPACE: return "workspace is NULL or too small";
         case GDR2_ERR_HIP: return "HIP launch failed";
         case GDR2_ERR_VALUE:
-            return "a scalar argument is out of range (g_scale > 0 finite, 0 < b_scale <= 2, segments >= 1)";
+            return "a scalar argument is out of range (g_scale > 0 finite, 0 < b_scale <= 2, segments >= 1, page_size a "
+                   "power of two >= 16, scale finite, window >= 0)";
         case GDR2_ERR_SCRATCH:
             return "the call needs more workspace than the library's fixed device array "
                    "(GDR2_NOALLOC_SCRATCH_BYTES) holds";

@@ -44,7 +44,7 @@ long long sc_slots(int N, int T, bool packed) {
 int sc_shape(int N, int T, int Hk, int Hv, int dk, int dv, int dtype, bool packed) {
     if (N < 0 || T < 0 || Hk < 0 || Hv < 0) return GDR2_ERR_SHAPE;
     if (!sc_supported(dk, dv, dtype)) return GDR2_ERR_UNSUPPORTED;
-    if (Hk == 0 ? Hv != 0 : Hv % Hk != 0) return GDR2_ERR_SHAPE;
+    if (Hk == 0 ? Hv != 0 : Hv == 0 || Hv % Hk != 0) return GDR2_ERR_SHAPE;
     const long long tokens = packed ? T : (long long)N * T;
     // the grids (slots x key heads, sequences x value heads x slices) and token rows fit in 32 bits
     if (tokens > 0x7fffffffLL - 64 || (tokens * Hv) > (1LL << 40)) return GDR2_ERR_SHAPE;
@@ -223,7 +223,9 @@ int gdr2_attn_step(const void* q, const void* k_cache, const void* v_cache, cons
     if (st != GDR2_OK) return st;
     if (!q || !o || !lengths) return GDR2_ERR_NULL;
     if (!isfinite(scale) || window < 0) return GDR2_ERR_VALUE;
-    // the units of all rows are numbered in 32 bits (units of 16 tokens, and a few more places a row)
+    // token numbers, and those of the units of all rows (of 16 tokens, and a few more places a row), fit in 32
+    // bits
+    if ((long long)max_pages * page_size > 0x7fffffffLL - 64) return GDR2_ERR_SHAPE;
     if ((long long)B * Hq * (((long long)max_pages * page_size >> 4) + 16) > 0x7fffffffLL) return GDR2_ERR_SHAPE;
     const void* const ptrs[] = {q, k_cache, v_cache, o, workspace};
     if (!all_aligned(ptrs)) return GDR2_ERR_ALIGN;

@@ -65,12 +65,13 @@ enum gdr2_dtype { GDR2_DTYPE_F32 = 0, GDR2_DTYPE_BF16 = 1 };
 enum gdr2_status {
     GDR2_OK = 0,
     GDR2_ERR_NULL = -1,        /* a required pointer is NULL */
-    GDR2_ERR_SHAPE = -2,       /* B, T or H negative, or sizes overflow */
+    GDR2_ERR_SHAPE = -2,       /* B, T or H negative, heads that do not divide, or sizes overflow */
     GDR2_ERR_UNSUPPORTED = -3, /* dk/dv/chunk/dtype combination not built */
     GDR2_ERR_ALIGN = -4,       /* a pointer is not 16-byte aligned */
     GDR2_ERR_WORKSPACE = -5,   /* workspace NULL or smaller than required */
     GDR2_ERR_HIP = -6,         /* a HIP launch failed */
-    GDR2_ERR_VALUE = -7,       /* a scalar argument is out of range (gate scales, segments) */
+    GDR2_ERR_VALUE = -7,       /* a scalar argument is out of range (gate scales, segments, page size,
+                                  attention scale, window) */
     GDR2_ERR_SCRATCH = -8      /* gdr2_fwd_noalloc: the call needs more than the fixed scratch */
 };
 
@@ -232,7 +233,7 @@ int gdr2_fwd_noalloc(const void* q, const void* k, const void* v, const void* g,
  * zero (such a sequence passes its state through). Its entries are data that no check on the host can
  * see: entries out of order or range give wrong results for the sequences concerned, but no access
  * outside the tensors. Tokens of no sequence are not read, and their rows of o (dq, dk_, dv_, dg, dbeta)
- * are left as they were, or set to zero with zero_rest = 1.
+ * are left as they were, or set to zero with zero_rest = 1 (N = 0 writes nothing).
  *
  * Precision: with bf16, o and the gradients of the token tensors carry a few bf16 roundings; the
  * states, which are fp32, do not: ht and dh0 are off by less than 1e-5 of what was written into them
@@ -241,7 +242,9 @@ int gdr2_fwd_noalloc(const void* q, const void* k, const void* v, const void* g,
  *
  * Supported dtype / dk / dv as gdr2_fwd; chunks are of 64 tokens. Ownership, streams, errors and calls
  * without tokens as gdr2_fwd / gdr2_bwd; g, beta, dg and dbeta need only their element's alignment; Hv
- * not a multiple of Hk returns GDR2_ERR_SHAPE. Workspace:
+ * that is no multiple of Hk, 0 included unless Hk is 0, returns GDR2_ERR_SHAPE. Outputs must not overlap
+ * one another or the inputs. The workspace has no content between calls but for what fwd_saved = 1 reads;
+ * calls that may overlap need one each:
  * gdr2_scalar_workspace_bytes (packed = 1 when cu_seqlens is given; save_for_bwd = 1 for a forward that
  * a backward follows, and for the backward). gdr2_scalar_bwd(..., fwd_saved = 1) needs the workspace as
  * gdr2_scalar_fwd(..., save_for_bwd = 1) left it for the same inputs; fwd_saved = 0 recomputes. */
@@ -286,7 +289,8 @@ int gdr2_scalar_step(const void* q, const void* k, const void* v, const void* g,
  *   lengths : int32 [B] on the device, tokens held; taken as 0 .. max_pages page_size where outside
  * page_size is a power of two from 16 on (else GDR2_ERR_VALUE), D 64 or 128, dtype BF16 or F32. A row
  * with nothing visible gets o = 0 and lse = -inf. What the cache holds in masked or unused places,
- * infinities and NaN included, does not matter. Scores, weights' sums and lse are fp32; with bf16 the
+ * infinities and NaN included, does not matter. max_pages page_size of 2^31 - 64 and more returns
+ * GDR2_ERR_SHAPE. o must not overlap q. Scores, weights' sums and lse are fp32; with bf16 the
  * weights enter the second product as bf16. Results do not depend on the other rows of the call beyond
  * the order of fp32 sums, and are repeatable bit for bit. Workspace: gdr2_attn_workspace_bytes, of no
  * content between calls; calls that may overlap need one each. */

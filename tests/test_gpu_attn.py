@@ -177,6 +177,56 @@ def test_graph_and_streams():
     assert all(torch.equal(x, want) for x in outs)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("window", [0, 2500])
+def test_ragged_rows_on_shared_workgroups(dtype, window):
+    # tables wide enough for long rows: rows of any length share the line of workgroups
+    lens = [0, 4000, 1, 17, 0, 900, 31, 2600, 64] + [5] * 20
+    check(*make(lens, 4, 2, 64, 16, dtype, seed=15, width=600), window=window)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_more_rows_than_lanes_on_shared_workgroups(dtype):
+    gen = torch.Generator().manual_seed(16)
+    lens = [n if n > 20 else 0 for n in torch.randint(0, 150, (150,), generator=gen).tolist()]
+    check(*make(lens, 3, 3, 64, 16, dtype, seed=16, width=700))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_heads_of_a_long_row(dtype):
+    check(*make([2100, 700], 34, 2, 128, 32, dtype, seed=17, width=200))
+
+
+def test_offsets_past_32_bits():
+    P, page, H, D = 2100, 1024, 8, 128  # 2.2e9 elements a cache
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.empty(P, page, H, D, dtype=BF, device="cuda") for _ in range(2))
+    ids = [2099, 7, 2060]
+    for c in (kc, vc):
+        for p in ids:
+            c[p] = torch.randn(page, H, D, generator=gen, device="cuda")
+    small_k, small_v = kc[ids], vc[ids]
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 16, D, generator=gen, device="cuda").to(BF)
+    far, near = ints([2099, 7], [2060, -1]), ints([0, 1], [2, -1])
+    held = ints(1500, 700)
+    k, v = (torch.randn(2, H, D, generator=gen, device="cuda").to(BF) for _ in range(2))
+    g2.gdr2_kv_append(k, v, kc, vc, far, held)
+    g2.gdr2_kv_append(k, v, small_k, small_v, near, held)
+    assert torch.equal(kc[ids], small_k) and torch.equal(vc[ids], small_v)
+    for a, b in zip(g2.gdr2_attn_step(q, kc, vc, far, held + 1, return_lse=True),
+                    g2.gdr2_attn_step(q, small_k, small_v, near, held + 1, return_lse=True)):
+        assert torch.equal(a, b)
+
+
+def test_windows_past_32_bits():
+    q, kc, vc, table, dev, lengths = make([40], 2, 2, 64, 16, BF, seed=18)
+    assert torch.equal(g2.gdr2_attn_step(q, kc, vc, dev, lengths, window=2 ** 32 + 5),
+                       g2.gdr2_attn_step(q, kc, vc, dev, lengths))
+    with pytest.raises(RuntimeError):
+        g2.gdr2_attn_step(q, kc, vc, dev, lengths, window=-2 ** 32 + 5)
+
+
 # ---------------------------------------------------------------- the cache's writer
 
 

@@ -323,6 +323,112 @@ def test_another_stream():
         assert torch.equal(gr[n], want[n]), n
 
 
+def many(lo, hi, n, seed):
+    gen = torch.Generator().manual_seed(seed)
+    return torch.randint(lo, hi + 1, (n,), generator=gen).tolist()
+
+
+@pytest.mark.parametrize("case", [
+    # chains enough for two column tiles a workgroup, at equal and at ragged lengths; more sequences
+    # than a wave has lanes, with and without that
+    ([70] * 4, False, 8, 16, 128, 128, BF), ([129] * 8, False, 4, 16, 64, 64, F32),
+    ([66] * 9, False, 2, 8, 64, 128, BF), (many(0, 90, 70, 1), True, 5, 5, 64, 64, BF),
+    (many(0, 70, 80, 2), True, 1, 4, 64, 64, F32), (many(0, 20, 100, 3), True, 1, 1, 128, 64, BF),
+    (many(1, 3, 300, 4), True, 1, 2, 64, 64, F32)])
+def test_many_chains(case):
+    lens, packed, hk, hv, dk, dv, dtype = case
+    x, cu = inputs(lens, packed, hk, hv, dk, dv, dtype, seed=30)
+    check(train(x, cu), x, cu, dtype)
+
+
+def test_many_value_heads_of_a_key_head():
+    x, cu = inputs([130], False, 2, 14, 64, 64, BF, seed=31)
+    check(train(x, cu), x, cu, BF)
+
+
+def test_backward_twice():
+    x, cu = inputs([50, 90], True, 1, 2, 64, 64, BF, seed=32)
+    leaves = [x[n].clone().requires_grad_() for n in ("q", "k", "v", "g", "beta", "h0")]
+    o, ht = g2.GDR2ScalarFunction.apply(*leaves, device_cu(cu))
+    run = lambda: torch.autograd.grad([o, ht], leaves, [x["do"], x["dht"]], retain_graph=True)
+    a, b = run(), run()
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    # an output's gradient that is one number, broadcast
+    c = torch.autograd.grad(o.sum(), leaves[:5])
+    want = train(dict(x, do=torch.ones_like(x["do"]), dht=torch.zeros_like(x["dht"])), cu)
+    for t, n in zip(c, ("dq", "dk", "dv", "dg", "dbeta")):
+        assert torch.equal(t, want[n]), n
+
+
+def test_autograd_in_a_graph():
+    x, cu = inputs([64, 40], True, 1, 2, 128, 128, BF, seed=33)
+    dcu = device_cu(cu)
+    want = train(x, cu)
+    leaves = [x[n].clone().requires_grad_() for n in ("q", "k", "v", "g", "beta", "h0")]
+
+    def step():
+        o, ht = g2.GDR2ScalarFunction.apply(*leaves, dcu)
+        return (o.detach(), ht.detach(), *torch.autograd.grad([o, ht], leaves, [x["do"], x["dht"]]))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.fill_(3)
+        train(x, cu)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for t, n in zip(got, ("o", "ht", "dq", "dk", "dv", "dg", "dbeta", "dh0")):
+            assert torch.equal(t, want[n]), n
+
+
+def test_two_calls_at_once():
+    x, cu = inputs([300, 200], True, 2, 4, 128, 128, BF, seed=34)
+    want = train(x, cu)
+    args, dcu = [x[n] for n in ("q", "k", "v", "g", "beta", "h0")], device_cu(cu)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    res = []
+    for s in streams:
+        o, ht, ws = g2.gdr2_scalar_fwd(*args, cu_seqlens=dcu, save_for_bwd=True, stream=s)
+        res.append(dict(o=o, ht=ht, **g2.gdr2_scalar_bwd(*args, x["do"], x["dht"], cu_seqlens=dcu, ws=ws, fwd_saved=True,
+                                                         stream=s)))
+    torch.cuda.synchronize()
+    for r in res:
+        for n in want:
+            assert torch.equal(r[n], want[n]), n
+
+
+def test_packed_without_tokens():
+    h0 = torch.randn(2, 3, 64, 64, device="cuda")
+    e = lambda *s: torch.empty(1, 0, *s, dtype=BF, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    a = (e(1, 64), e(1, 64), e(3, 64), e(3), e(3), h0)
+    o, ht, ws = g2.gdr2_scalar_fwd(*a, cu_seqlens=cu, save_for_bwd=True)
+    gr = g2.gdr2_scalar_bwd(*a, e(3, 64), h0 * 2, cu_seqlens=cu, ws=ws, fwd_saved=True)
+    assert torch.equal(ht, h0) and torch.equal(gr["dh0"], h0 * 2)
+
+
+def test_offsets_past_32_bits():
+    # 2.2e9 elements of v; the last sequence against a call of its own
+    n, T, hv, d = 520, 256, 128, 128
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda", dtype=BF)
+    x = dict(q=rnd(n, T, 1, d) * d ** -0.5, k=rnd(n, T, 1, d) * d ** -0.5, v=rnd(n, T, hv, d),
+             g=-rnd(n, T, hv).abs() * 0.1, beta=torch.sigmoid(rnd(n, T, hv)), do=rnd(n, T, hv, d), h0=None, dht=None)
+    got = train(x, None)
+    want = train({m: t if t is None else t[-1:].contiguous() for m, t in x.items()}, None)
+    for m in want:
+        assert torch.equal(got[m][-1], want[m][0]), m
+
+
 # ---------------------------------------------------------------- the recurrent step
 
 
@@ -395,6 +501,19 @@ def test_step_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, want_o) and torch.equal(state, want_s)
+
+
+def test_step_offsets_past_32_bits():
+    hv, d, S = 16, 128, 8300  # 2.2e9 elements of state
+    x, _ = inputs([1] * 3, False, 8, hv, d, d, BF, seed=24)
+    state = torch.zeros(S, hv, d, d, device="cuda")
+    slots = torch.tensor([8299, 0, 4100], dtype=torch.int32, device="cuda")
+    state[slots.long()] = x["h0"]
+    o = g2.gdr2_scalar_step(*[x[n] for n in ("q", "k", "v", "g", "beta")], state, slots=slots)
+    want = ref.run_recurrence(x, None)
+    assert ref.normwise(o, torch.stack(want["o"])) <= 2.0 ** -8
+    assert ref.normwise(state[slots.long()], want["ht"]) <= 1e-5
+    assert int(torch.count_nonzero(state.view(S, -1).any(1))) == 3
 
 
 # ---------------------------------------------------------------- refusals (before any launch)

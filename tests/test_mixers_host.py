@@ -1,6 +1,7 @@
 """Host-only checks (no GPU) of the scalar-gate and paged-attention entry points: sizes, refusals
 before any launch, and the maps from tokens to chunk slots for any cu_seqlens."""
 import ctypes
+import gc
 import os
 import random
 
@@ -166,3 +167,60 @@ def test_packed_maps_stay_inside():
                 c = slot - slot0
                 found = (s, c) if 0 <= c < (rows + 63) // 64 else None
                 assert found == used.get(slot), (cu, slot)
+
+
+def test_key_heads_without_value_heads_are_refused(lib):
+    # their gradients would have no kernel to write them
+    assert scalar(lib, Hk=2, Hv=0) == SHAPE and scalar(lib, True, Hk=2, Hv=0) == SHAPE and step(lib, Hk=2, Hv=0) == SHAPE
+
+
+def test_token_numbers_fit_in_32_bits(lib):
+    assert attn(lib, page=1 << 20, max_pages=2047, ws_bytes=0) == WS  # past the check of sizes
+    assert attn(lib, page=1 << 20, max_pages=2048) == SHAPE
+
+
+def test_marks_of_leaves_live_as_long_as_their_graphs():
+    import torch
+    a, b = torch.randn(3, requires_grad=True), torch.randn(3)
+    marks = lambda: g2._accumulation_streams((a, b, None, a * 2))
+    assert len(marks()) == 1  # leaves that want a gradient
+    y = a * 3
+    marks()[0].setdefault("gdr2_stream", 7)
+    assert marks()[0]["gdr2_stream"] == 7
+    y.sum().backward()
+    assert marks()[0]["gdr2_stream"] == 7
+    del y
+    assert "gdr2_stream" not in marks()[0]
+
+
+def test_a_captured_backward_with_a_foreign_graph_is_refused(monkeypatch):
+    # the check alone, on the CPU: the GPU calls are stand-ins, the stream a number
+    import types
+
+    import torch
+    now = types.SimpleNamespace(cuda_stream=1)
+    capturing = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: now)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: bool(capturing))
+    names = ("dq", "dk", "dv", "dg", "dbeta")
+    monkeypatch.setattr(g2, "gdr2_scalar_fwd", lambda q, *a, **kw: (q * 1, torch.zeros(1), torch.zeros(1)))
+    monkeypatch.setattr(g2, "gdr2_scalar_bwd",
+                        lambda *a, **kw: dict({n: torch.ones(2) for n in names}, dh0=None))
+    leaves = [torch.randn(2, requires_grad=True) for _ in range(5)]
+    eager, _ = g2.GDR2ScalarFunction.apply(*leaves)
+    now.cuda_stream = 2
+    capturing.append(True)
+    o, _ = g2.GDR2ScalarFunction.apply(*leaves)
+    with pytest.raises(RuntimeError, match="cannot capture"):
+        o.sum().backward()
+    del eager, o, _
+    gc.collect()  # the error's traceback held the refused graph
+    o, _ = g2.GDR2ScalarFunction.apply(*leaves)
+    o.sum().backward()
+    assert all(torch.equal(t.grad, torch.ones(2)) for t in leaves)
+    # and no second derivative, rather than one without this operator's part
+    capturing.clear()
+    o, _ = g2.GDR2ScalarFunction.apply(*leaves)
+    gr, = torch.autograd.grad(o.sum(), leaves[:1], create_graph=True)
+    with pytest.raises(RuntimeError):
+        gr.sum().backward()
