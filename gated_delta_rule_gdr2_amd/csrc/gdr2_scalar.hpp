@@ -26,6 +26,8 @@ namespace gdr2 {
 //   T     : images (fimg) of T, [NS][64][64]: NS = 2 for bf16, a bf16 value and the bf16 value
 //           of what its rounding left over (together 16 bits of mantissa), 1 for fp32
 //   M     : image of M, [64][64]
+//           (of these triangles' eight fragments of 16 rows and 32 columns, the two that are zero are
+//           neither written nor read: sc_img_zero)
 //   vec   : fp32 rows of 64: e^gam, beta, tail (all zero in padding rows), gam as a float and its
 //           remainder; element 320 is e^gamC
 //   training only: T^T and M^T, [NS][64][64] each (the backward chain reads their rows straight into
@@ -38,6 +40,10 @@ struct ScLayout {
     size_t o_t, o_m, o_vec, o_tt, o_mt, o_s, o_ds, o_delta, o_dy;  // byte offsets (T^T, M^T: counts as T)
     size_t infer_bytes, train_bytes;
 };
+
+// Fragment (row tile, half of the columns) of a lower (TR: upper) triangular image that is zero.
+template <bool TR>
+__host__ __device__ constexpr bool sc_img_zero(int rt, int kb) { return TR ? rt >= 2 && kb == 0 : rt < 2 && kb == 1; }
 
 constexpr int SC_E = 0, SC_BETA = 64, SC_TAIL = 128, SC_GHI = 192, SC_GLO = 256, SC_EC = 320, SC_VEC = 384;
 

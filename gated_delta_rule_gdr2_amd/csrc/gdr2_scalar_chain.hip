@@ -178,8 +178,13 @@ __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds
     // L2 prefetch of chunk index(n): one word of every 128-byte line of what the workgroup reads of it,
     // into a word of LDS that nothing reads. The lines are numbered over k, T, v (dO), q, M and the row
     // factors, and shared between the NJ workgroups of the (sequence, head), which sit on one L2.
-    constexpr int LPK = DK * ES / 128, LPV = DV * ES / 128, SQ = CH * CH * ES;  // lines of a row; a 64 x 64 image
-    constexpr int LK = CH * LPK, LT = B::NS * SQ / 128, LM = (BWD ? B::NS : 1) * SQ / 128, LV = CH * LPV;
+    constexpr int LPK = DK * ES / 128, LPV = DV * ES / 128;  // lines of a row
+    constexpr int LF = 512 * ES / 128;                       // of an image's fragment, six of eight to read
+    constexpr int LK = CH * LPK, LT = B::NS * 6 * LF, LM = (BWD ? B::NS : 1) * 6 * LF, LV = CH * LPV;
+    auto img_line = [](int v) {
+        const int p = v / (6 * LF), f = v / LF % 6;
+        return (8 * p + (BWD ? (f < 4 ? f : 2 * f - 3) : (f < 2 ? 2 * f : f + 2))) * LF + v % LF;
+    };
     constexpr int LVEC = SC_VEC * 4 / 128, LINES = 2 * LK + LT + LM + LV + LVEC;
     constexpr int NPF = (LINES + NJ * 64 * SC_NP - 1) / (NJ * 64 * SC_NP);
     auto prefetch = [&](int n) {  // (past the last chunk: the last one again, so that their number is fixed)
@@ -194,13 +199,13 @@ __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds
             if (v < LK) {
                 p = x.k + (size_t)min(v / LPK, last) * rsk + (v % LPK) * 128;
             } else if ((v -= LK) < LT) {
-                p = tp + v * 128;
+                p = tp + img_line(v) * 128;
             } else if ((v -= LT) < LV) {
                 p = x.v + (size_t)min(v / LPV, last) * rsv + (v % LPV) * 128;
             } else if ((v -= LV) < LK) {
                 p = x.q + (size_t)min(v / LPK, last) * rsk + (v % LPK) * 128;
             } else if ((v -= LK) < LM) {
-                p = mp + v * 128;
+                p = mp + img_line(v) * 128;
             } else {
                 p = x.f + min(v - LM, LVEC - 1) * 128;
             }
@@ -224,16 +229,21 @@ __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds
     wait_vm<0>();  // no copy into this workgroup's LDS outlives it
 }
 
-// A wave's 16 rows of a pair of [64][64] images, straight from the workspace into registers: the fragments
-// are whole kilobytes there, each read by one wave, and would pass LDS twice for nothing.
-template <class OT, int NS>
+// A wave's 16 rows of a pair of [64][64] triangular images (TR: upper), straight from the workspace into
+// registers: the fragments are whole kilobytes there, each read by one wave, and would pass LDS twice for
+// nothing. Of the eight, the two above (below) the diagonal are not read.
+template <class OT, int NS, bool TR>
 struct ImgRows {
     typename Frag<OT>::type f[NS][2];
     __device__ __forceinline__ void load(const OT* p, int wv) {
 #pragma unroll
         for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) f[n][kb] = gfrag_img<OT, CH>(p + n * CH * CH, 16 * wv, 32 * kb);
+            for (int kb = 0; kb < 2; ++kb)
+                if (sc_img_zero<TR>(wv, kb))
+                    f[n][kb] = {};
+                else
+                    f[n][kb] = gfrag_img<OT, CH>(p + n * CH * CH, 16 * wv, 32 * kb);
     }
 };
 
@@ -292,7 +302,7 @@ __device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk& w, in
     for (int ch = 0; ch < NC; ++ch) S.publish(xs, ch, wv);
     const OT* tp = (const OT*)(a.ws + a.L.o_t) + ((size_t)w.q.slot0 * a.Hv + w.h) * a.L.t;
     const size_t tstep = (size_t)a.Hv * a.L.t;
-    ImgRows<OT, NS> T;  // a step ahead
+    ImgRows<OT, NS, false> T;  // a step ahead
     if (nt > 0) T.load(tp, wv);
 #pragma unroll 1
     for (int n = 0; n < nt; ++n) {
@@ -440,7 +450,7 @@ __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, in
     const int l = lane_id(), li = l & 15, lq = l >> 4;
     const OT* mp = (const OT*)(a.ws + a.L.o_m) + ((size_t)w.q.slot0 * a.Hv + w.h) * a.L.m;
     const size_t mstep = (size_t)a.Hv * a.L.m;
-    ImgRows<OT, 1> M;  // a step ahead
+    ImgRows<OT, 1, false> M;  // a step ahead
     if (OUT && w.q.nt > 0) M.load(mp, wv);
     Slice<OT, DK / 16> S[NC];
     auto store_state = [&](int n) {  // chunk n's start state
@@ -527,7 +537,7 @@ __device__ __forceinline__ void sc_bwd_walk(const ScArgs& a, const ScWalk& w, in
     const size_t id0 = ((size_t)(w.q.slot0 + max(nt - 1, 0)) * a.Hv + w.h) * a.L.t;
     const OT* tp = (const OT*)(a.ws + a.L.o_tt) + id0;
     const OT* mp = (const OT*)(a.ws + a.L.o_mt) + id0;
-    ImgRows<OT, NS> T, M;  // rows of T^T and M^T, a step ahead
+    ImgRows<OT, NS, true> T, M;  // rows of T^T and M^T, a step ahead
     if (nt > 0) {
         M.load(mp, wv);
         T.load(tp, wv);

@@ -240,9 +240,8 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
             }
         }
     }
-    for (int u = wv; u < 6; u += 4) {
-        int R, I;
-        sc_upper_ri(u, R, I);
+    if (wv < 2) {  // the two zero blocks in the fragments that are read (sc_img_zero)
+        const int R = 2 * wv, I = R + 1;
         const float z[4] = {0.f, 0.f, 0.f, 0.f};
         st4(m + fimg<OT, CH>(16 * R + li, 16 * I + 4 * lq), z);
         if (TRAIN) put_parts<OT>(mt + fimg<OT, CH>(16 * I + li, 16 * R + 4 * lq), f32x4{0.f, 0.f, 0.f, 0.f});
@@ -255,14 +254,14 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
 #pragma unroll
     for (int i = 0; i < CH * CH / 4 / 256; ++i) {
         const int idx = tid + 256 * i, r = idx / 16, c0 = 4 * (idx % 16);
-        put_parts<OT>(t + fimg<OT, CH>(r, c0), lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4));
+        if (!sc_img_zero<false>(i, c0 / 32)) put_parts<OT>(t + fimg<OT, CH>(r, c0), lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4));
         if (TRAIN) {
             // lanes on 16 neighbouring columns of four rows: row c of T^T, columns r0 ..
             const int ct = 16 * (idx / 64 % 4) + idx % 16, r0 = 16 * (idx / 256) + 4 * (idx / 16 % 4);
             f32x4 x;
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = lds_load<float>(sT + swz<float, CH>(r0 + e, ct) * 4);
-            put_parts<OT>(tt + fimg<OT, CH>(ct, r0), x);
+            if (!sc_img_zero<true>(ct / 16, r0 / 32)) put_parts<OT>(tt + fimg<OT, CH>(ct, r0), x);
         }
     }
 }
