@@ -453,14 +453,17 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     }
 }
 
-// One row a workgroup, without a second kernel: where a row has at most eight units for each wave
-// (whatever the number of rows, splitting it saves less than the join costs), or up to three times that
-// when there are rows enough for every compute unit.
+// One row a workgroup, without a second kernel: where the table (or the window) leaves a row at most four
+// units for each wave, 1024 tokens in bf16. Measured in a graph, bf16, 4 key heads of 128, one row a
+// workgroup against the line of runs and its join:
+//   1 sequence of 100 tokens   4.7 and 11.7 us     1 of 777   11.4 and 13.8     1 of 2048   22.4 and 14.0
+//   8 of 1000                 18.4 and 16.7       32 of 1000  20.8 and 22.9    32 of 2048   40.1 and 36.2
+//   200 of 500                53.3 and 56.8      200 of 2048 174.7 and 162.5  200 of 4096  340.4 and 305.3
+// (the last 5.5 TB/s; long rows one a workgroup leave compute units idle at the end).
 inline bool attn_rows_mode(const AttnArgs& a, int unit) {
     long long tokens = (long long)a.c.max_pages << a.c.shift;
-    if (a.window > 0 && a.window < tokens) tokens = a.window + unit;  // a window may begin inside a unit
-    const long long units = (tokens + unit - 1) / unit, rows = (long long)a.B * a.Hkv * a.NG;
-    return units <= 8 * AW || (rows >= ATTN_WGS && units <= 24 * AW);
+    if (a.window > 0 && a.window < tokens) tokens = (long long)a.window + unit;  // a window may begin inside a unit
+    return (tokens + unit - 1) / unit <= 4 * AW;
 }
 
 template <class OT, int D>
