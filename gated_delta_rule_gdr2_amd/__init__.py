@@ -417,6 +417,12 @@ def _device_of(t, name):
     return dev
 
 
+def _raw_stream(dev):
+    """The current stream of a device as a number, without an object around it where torch offers that."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(dev).cuda_stream if get is None else get(dev)
+
+
 class _on:
     """Device ``dev`` as the current one, and the stream to launch on: the given one, or the device's current
     stream."""
@@ -428,7 +434,7 @@ class _on:
         if torch.cuda.current_device() != self.dev:
             self.prev = torch.cuda.current_device()
             torch.cuda.set_device(self.dev)
-        return (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
+        return _raw_stream(self.dev) if self.stream is None else self.stream.cuda_stream
 
     def __exit__(self, *exc):
         if self.prev is not None:
@@ -436,6 +442,18 @@ class _on:
 
 
 def _scalar_dims(q, k, v, g, beta, cu_seqlens):
+    if cu_seqlens is None:  # what is as it should be is found so by one expression, at half the cost
+        qs, vs, t, dev = q.shape, v.shape, q.dtype, q.get_device()
+        if len(qs) == 4 and len(vs) == 4 and dev >= 0 and t in _DT:
+            B, T, Hk, dk = qs
+            _, _, Hv, dv = vs
+            gs = (B, T, Hv)
+            if (k.shape == qs and vs == (B, T, Hv, dv) and g.shape == gs and beta.shape == gs
+                    and k.dtype is t and v.dtype is t and g.dtype is t and beta.dtype is t
+                    and k.get_device() == dev and v.get_device() == dev and g.get_device() == dev
+                    and beta.get_device() == dev and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+                    and g.is_contiguous() and beta.is_contiguous()):
+                return B, T, Hk, Hv, dk, dv, B, _DT[t], dev
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("q and v must have four dimensions [B,T,H,d]")
     B, T, Hk, dk = q.shape
@@ -568,13 +586,13 @@ def gdr2_scalar_step(q, k, v, g, beta, state, *, slots=None, o=None, stream=None
     elif S < B:
         raise ValueError("state holds %d states for %d rows" % (S, B))
     if o is None:
-        o = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        o = torch.empty_like(v)
         _keep_for(stream, o)
     else:
         _want(o, "o", q.dtype, v.shape, dev)
     with _on(dev, stream) as s:
-        st = lib.gdr2_scalar_step(_adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(state), _adr(slots), _adr(o), B,
-                                  T, Hk, Hv, dk, dv, S, dt, s)
+        st = lib.gdr2_scalar_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                                  state.data_ptr(), _adr(slots), o.data_ptr(), B, T, Hk, Hv, dk, dv, S, dt, s)
     _raise(st, "gdr2_scalar_step")
     return o
 
@@ -627,7 +645,19 @@ def gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dtype=DTYPE_BF16) -> int:
 _Strides = ctypes.c_longlong * 6
 
 
+@functools.lru_cache(maxsize=64)
+def _strides(ks, vs):
+    return _Strides(*ks[:3], *vs[:3])
+
+
 def _cache_strides(k_cache, v_cache, block_table, dtype, D, dev):
+    """Checks a cache. Returns its strides, pages, page size and heads."""
+    shape, ks, vs = k_cache.shape, k_cache.stride(), v_cache.stride()
+    if (len(shape) == 4 and v_cache.shape == shape and shape[3] == D and ks[3] == 1 and vs[3] == 1
+            and k_cache.dtype is dtype and v_cache.dtype is dtype and k_cache.get_device() == dev
+            and v_cache.get_device() == dev and shape[0] <= 0x7fffffff and shape[1] <= 0x7fffffff
+            and block_table.dim() == 2):
+        return _strides(ks, vs), shape[0], shape[1], shape[2]
     if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
         raise ValueError("k_cache and v_cache must have one shape [pages,page_size,Hkv,D], got %s and %s"
                          % (tuple(k_cache.shape), tuple(v_cache.shape)))
@@ -640,11 +670,9 @@ def _cache_strides(k_cache, v_cache, block_table, dtype, D, dev):
             raise ValueError("%s must have %d channels, got %d" % (n, D, t.shape[3]))
         if t.stride(3) != 1:
             raise ValueError("the channels of %s must be contiguous" % n)
-    if k_cache.shape[0] > 0x7fffffff or k_cache.shape[1] > 0x7fffffff:
-        raise ValueError("k_cache has too many pages or tokens a page")
     if block_table.dim() != 2:
         raise ValueError("block_table must have two dimensions [B,max_pages]")
-    return _Strides(*k_cache.stride()[:3], *v_cache.stride()[:3])
+    raise ValueError("k_cache has too many pages or tokens a page")
 
 
 def gdr2_attn_step(q, k_cache, v_cache, block_table, lengths, *, scale=None, window=0, o=None, lse=None,
@@ -661,9 +689,9 @@ def gdr2_attn_step(q, k_cache, v_cache, block_table, lengths, *, scale=None, win
     if q.dtype not in _DT:
         raise ValueError("unsupported dtype %s" % q.dtype)
     dt, dev = _DT[q.dtype], _device_of(q, "q")
-    _want(q, "q", q.dtype, (B, Hq, D), dev)
-    strides = _cache_strides(k_cache, v_cache, block_table, q.dtype, D, dev)
-    pages, page, Hkv = k_cache.shape[:3]
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    strides, pages, page, Hkv = _cache_strides(k_cache, v_cache, block_table, q.dtype, D, dev)
     max_pages = block_table.shape[1]
     _want(block_table, "block_table", torch.int32, (B, max_pages), dev)
     _want(lengths, "lengths", torch.int32, (B,), dev)
@@ -685,10 +713,10 @@ def gdr2_attn_step(q, k_cache, v_cache, block_table, lengths, *, scale=None, win
         _want(ws, "ws", torch.uint8, ws.shape, dev)
     _keep_for(stream, *new)
     with _on(dev, stream) as s:
-        st = lib.gdr2_attn_step(_adr(q), _adr(k_cache), _adr(v_cache), strides, _adr(block_table), _adr(lengths),
-                                _adr(o), _adr(lse), B, Hq, Hkv, D, pages, page, max_pages,
+        st = lib.gdr2_attn_step(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), strides, block_table.data_ptr(),
+                                lengths.data_ptr(), o.data_ptr(), _adr(lse), B, Hq, Hkv, D, pages, page, max_pages,
                                 D ** -0.5 if scale is None else scale, max(-1, min(window, 0x7fffffff)), dt,
-                                _adr(ws), ws.numel(), s)
+                                ws.data_ptr(), ws.numel(), s)
     _raise(st, "gdr2_attn_step")
     return o if lse is None else (o, lse)
 
@@ -705,11 +733,12 @@ def gdr2_kv_append(k, v, k_cache, v_cache, block_table, starts, *, cu_seqlens=No
     if k.dtype not in _DT:
         raise ValueError("unsupported dtype %s" % k.dtype)
     dev = _device_of(k, "k")
-    _want(k, "k", k.dtype, (tokens, Hkv, D), dev)
+    if not k.is_contiguous():
+        raise ValueError("k must be contiguous")
     _want(v, "v", k.dtype, (tokens, Hkv, D), dev)
-    strides = _cache_strides(k_cache, v_cache, block_table, k.dtype, D, dev)
-    if k_cache.shape[2] != Hkv:
-        raise ValueError("k_cache must have %d heads, got %d" % (Hkv, k_cache.shape[2]))
+    strides, pages, page, heads = _cache_strides(k_cache, v_cache, block_table, k.dtype, D, dev)
+    if heads != Hkv:
+        raise ValueError("k_cache must have %d heads, got %d" % (Hkv, heads))
     B, max_pages = block_table.shape
     _want(block_table, "block_table", torch.int32, (B, max_pages), dev)
     _want(starts, "starts", torch.int32, (B,), dev)
@@ -719,7 +748,7 @@ def gdr2_kv_append(k, v, k_cache, v_cache, block_table, starts, *, cu_seqlens=No
         raise ValueError("without cu_seqlens there is one token a sequence, got %d tokens for %d sequences"
                          % (tokens, B))
     with _on(dev, stream) as s:
-        st = lib.gdr2_kv_append(_adr(k), _adr(v), _adr(k_cache), _adr(v_cache), strides, _adr(block_table),
-                                _adr(starts), _adr(cu_seqlens), B, tokens, Hkv, D, k_cache.shape[0], k_cache.shape[1],
-                                max_pages, _DT[k.dtype], s)
+        st = lib.gdr2_kv_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), strides,
+                                block_table.data_ptr(), starts.data_ptr(), _adr(cu_seqlens), B, tokens, Hkv, D,
+                                pages, page, max_pages, _DT[k.dtype], s)
     _raise(st, "gdr2_kv_append")

@@ -22,6 +22,11 @@
 // its eight waves the units in turn. A row inside one run is finished there; a row that crosses runs
 // leaves partial sums, joined in a fixed order by a second kernel. Where no row can be long, each
 // workgroup takes one row and there is nothing to join (attn_rows_mode).
+//
+// Measured: 64 sequences of 200 to 16384 tokens, 32 heads over 8 key heads of 128, bf16 (1.02 GB) 192 us
+// and 6 us for the join, 5.2 TB/s together; 24 windows of up to 2048 tokens, 16 heads of 64, fp32 (134 MB)
+// 38 us a pass, 3.5 TB/s, of which about 12 us are what even short rows take on the line (two launches,
+// the line, the join).
 #include "gdr2_attn.hpp"
 #include "gdr2_device.hpp"
 
@@ -484,6 +489,7 @@ hipError_t launch_attn(const AttnArgs& a, bool bf16_, hipStream_t stream) {
 }
 
 // ============================================================================ writing the cache
+// Bound by HBM: 56 MB of prompts in 11.8 us, 4.7 TB/s; one token for each of 96 sequences 2.9 us, a launch.
 // A copy, 16 bytes a thread for the keys and the values each; a token's row (all its heads) by
 // consecutive threads. Tokens whose place lies past the table or on an invalid page are dropped.
 template <class OT>

@@ -117,10 +117,13 @@ __device__ __forceinline__ void put_parts(OT* p, const f32x4& x) {
 
 // One workgroup of four waves per (chunk slot, value head): k k^T and q k^T on the raw rows, then A, its
 // inverse and M with the head's decay and beta. (One workgroup per key head, which would form the
-// products once for all of its value heads, is no faster at 16384 x 16 tokens and heads, 35 us both
-// ways, and twice as slow where few workgroups run.)
-// Bound by HBM traffic in the large (reads q and k, writes T, M and the row factors: 48 KB a chunk
-// and value head at d_k = 128 with Hk = Hv) and by the latency of the blocked inverse in the small.
+// products once for all of its value heads, was no faster where many run, 36 and 35 us for 2 x 4096 tokens
+// and 16 heads before T^T and M^T were written, and slower where few do, 15.7 and 10 us for three chunks
+// in fp32.)
+// Bound by HBM traffic in the large: reads q and k, writes T, M and the row factors, for training T^T and
+// M^T too, 52 (training 76) KB a chunk and value head at d_k = 128 with Hk = Hv; 51 us for 16384 tokens and
+// 16 heads, 38 us for 2 x 4096 in training, 4.1 TB/s both. In the small by the latency of the blocked
+// inverse: 11.5 us for three chunks.
 template <class OT, int DK, bool TRAIN>
 __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
     constexpr int KB = DK / 32, ES = sizeof(OT);
@@ -254,7 +257,8 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
 #pragma unroll
     for (int i = 0; i < CH * CH / 4 / 256; ++i) {
         const int idx = tid + 256 * i, r = idx / 16, c0 = 4 * (idx % 16);
-        if (!sc_img_zero<false>(i, c0 / 32)) put_parts<OT>(t + fimg<OT, CH>(r, c0), lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4));
+        if (!sc_img_zero<false>(i, c0 / 32))
+            put_parts<OT>(t + fimg<OT, CH>(r, c0), lds_load<f32x4>(sT + swz<float, CH>(r, c0) * 4));
         if (TRAIN) {
             // lanes on 16 neighbouring columns of four rows: row c of T^T, columns r0 ..
             const int ct = 16 * (idx / 64 % 4) + idx % 16, r0 = 16 * (idx / 256) + 4 * (idx / 16 % 4);
@@ -333,8 +337,9 @@ __device__ __forceinline__ void dma_rows_clamped(const OT* base, size_t rs, int 
 // is what the LDS layout (q enters LDS only when dO, Delta and dY have left it) and the register bound
 // are for. MULTI, more than one: around a loop over heads the registers are not enough for two workgroups
 // (84 spilled), so one has the compute unit, keeps q in LDS and loads the next head while this one is
-// worked on. Measured, d = 128, bf16: 97 us at 2 x 4096 tokens, 16 heads (4.5 TB/s); 129 us at 8859 packed
-// tokens, 8 key heads with 2 value heads each (3.1 TB/s; without the loads ahead 144 us).
+// worked on. Measured, d = 128, bf16: 98 us at 2 x 4096 tokens, 16 heads (4.5 TB/s); 129 us at 8859 packed
+// tokens, 8 key heads with 2 value heads each (3.1 TB/s, five rounds of workgroups of which the last is half
+// empty; without the loads ahead 144 us).
 template <class OT, int DK, int DV, bool MULTI>
 __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_grad(ScArgs a) {
     using LS = ScGradLds<OT, DK, DV, MULTI>;
@@ -384,13 +389,13 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
         const char* gDy = a.ws + a.L.o_dy + id * a.L.d * ES;
 #pragma unroll
         for (int n = 0; n < LS::TV / 1024; n += NW) {
-            __builtin_amdgcn_global_load_lds(gDel + (n + wv) * 1024 + l * 16, (lds_void*)(hd + LS::DEL + (n + wv) * 1024), 16,
-                                             0, 0);
-            __builtin_amdgcn_global_load_lds(gDy + (n + wv) * 1024 + l * 16, (lds_void*)(hd + LS::DY + (n + wv) * 1024), 16,
-                                             0, 0);
+            const int kb = (n + wv) * 1024;
+            __builtin_amdgcn_global_load_lds(gDel + kb + l * 16, (lds_void*)(hd + LS::DEL + kb), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds(gDy + kb + l * 16, (lds_void*)(hd + LS::DY + kb), 16, 0, 0);
         }
         if (wv < 2) {  // (the second wave's upper lanes: again what its lower lanes copy)
-            const char* src = a.ws + a.L.o_vec + id * a.L.vec * 4 + (wv == 0 ? l : 64 + l % ((SC_VEC * 4 - 1024) / 16)) * 16;
+            const int piece = wv == 0 ? l : 64 + l % ((SC_VEC * 4 - 1024) / 16);
+            const char* src = a.ws + a.L.o_vec + id * a.L.vec * 4 + piece * 16;
             __builtin_amdgcn_global_load_lds(src, (lds_void*)(hd + LS::VEC + wv * 1024), 16, 0, 0);
         }
     };
@@ -406,7 +411,8 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
 #pragma unroll
         for (int i = 0; i < NVL; ++i) {
             const int u = threadIdx.x + NTHR * i, rr = u / LPR;
-            gv[i] = rr < nvalid ? *(const VT*)((const OT*)a.v + row0 * rsv + (size_t)h * DV + rr * rsv + EPC * (u % LPR)) : VT{};
+            const OT* p = (const OT*)a.v + (row0 + rr) * rsv + (size_t)h * DV + EPC * (u % LPR);
+            gv[i] = rr < nvalid ? *(const VT*)p : VT{};
         }
     };
     load_lds(hk * a.R, sm + LS::HEAD);
@@ -429,8 +435,8 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
         if (!MULTI) {
 #pragma unroll
             for (int t = 0; t < TPW; ++t)
-                qv[t] = *(const typename Raw4<OT>::type*)((const OT*)a.q + k0 +
-                                                          (size_t)min(16 * (t0 + t) + li, nvalid - 1) * rsk + 16 * kw + 4 * lq);
+                qv[t] = *(const typename Raw4<OT>::type*)(
+                    (const OT*)a.q + k0 + (size_t)min(16 * (t0 + t) + li, nvalid - 1) * rsk + 16 * kw + 4 * lq);
         }
         wait_vm<0>();
         sync_lds();  // this head is in LDS, and the head before is done with its region
