@@ -38,6 +38,7 @@ namespace gdr2 {
 struct ScLayout {
     size_t t, m, vec, s, d;                              // element counts per id
     size_t o_t, o_m, o_vec, o_tt, o_mt, o_s, o_ds, o_delta, o_dy;  // byte offsets (T^T, M^T: counts as T)
+    size_t o_seg;                                        // segments' ends and transitions, fp32
     size_t infer_bytes, train_bytes;
 };
 
@@ -47,7 +48,8 @@ __host__ __device__ constexpr bool sc_img_zero(int rt, int kb) { return TR ? rt 
 
 constexpr int SC_E = 0, SC_BETA = 64, SC_TAIL = 128, SC_GHI = 192, SC_GLO = 256, SC_EC = 320, SC_VEC = 384;
 
-inline ScLayout sc_layout(long long ids, int DK, int DV, int esz) {
+// segs: segments of all (sequence, value head)s together, 0 where chains are whole
+inline ScLayout sc_layout(long long ids, long long segs, int DK, int DV, int esz) {
     ScLayout L;
     const size_t ns = esz == 2 ? 2 : 1;
     L.t = ns * 64 * 64;
@@ -64,6 +66,8 @@ inline ScLayout sc_layout(long long ids, int DK, int DV, int esz) {
     L.o_t = take(L.t, esz);
     L.o_m = take(L.m, esz);
     L.o_vec = take(L.vec, 4);
+    L.o_seg = off;
+    off += align256((size_t)segs * DK * (DV + DK) * sizeof(float));
     L.infer_bytes = off;
     L.o_tt = take(L.t, esz);
     L.o_mt = take(L.t, esz);
@@ -91,8 +95,33 @@ struct ScArgs {
     int Hk, Hv, R;                     // R = Hv / Hk value heads share a key head
     int DK, DV;
     int slots;                         // chunk slots (at least one per chunk of every sequence)
+    int nseg, seglen;                  // segments that a sequence's chains are cut in, and their chunks
     int zero_rest;                     // packed: 1 sets the outputs' rows of no sequence to zero
 };
+
+// Segments that chains are cut in, and their chunks: each segment's end from a zero start and its transition
+// are found at the same time, joined, and the segments walked together. That is two walks and twice the
+// columns (where DK = DV) instead of one, so it pays where walks are few and long: up to 64 of 16 columns,
+// with at least 16 chunks a segment, as many segments as give 256 workgroups something, up to 8.
+// (Packed sequences, whose lengths only the device knows, are walked whole.) Measured, one sequence, bf16,
+// d = 128, forward and training step, in segments and whole:
+//   16384 tokens  1 head    104 and 295 us,  231 and 645     4 heads   133 and 307,  351 and 679
+//                 8 heads   218 and 337,     581 and 771
+//    4096 tokens  1 head     56 and 86,      133 and 192     8 heads    74 and 91,   176 and 209
+//    2048 tokens  2 heads    52 and 50,      119 and 113 (two segments of 16)
+inline void sc_segments(int N, int T, int Hv, int DV, bool packed, int& nseg, int& seglen) {
+    const long long walks = (long long)N * Hv * (DV / 16);
+    const int nt = (int)(((long long)T + 63) / 64);
+    nseg = 1;
+    seglen = nt;
+    if (packed || walks < 1 || walks > 64) return;
+    int n = (int)(256 / walks);
+    if (n > 8) n = 8;
+    if (n > nt / 16) n = nt / 16;
+    if (n < 3) return;  // two walks of half the chunks are no shorter
+    seglen = (nt + n - 1) / n;
+    nseg = (nt + seglen - 1) / seglen;
+}
 
 // Sequence s: its first token row, token count and first chunk slot. Packed sequences take the
 // slots from start / 64 + s on: as many as they have chunks fit before the next sequence's first.

@@ -25,6 +25,11 @@
 // lane, into two buffers, the next chunk's while this one's step runs, and call what the workgroups of a head
 // will read three chunks later into their L2, each a share of it. T and M go from L2 straight to registers.
 //
+// Few long sequences are cut in segments (sc_segments): the state at a segment's end is affine in the one at
+// its start, E + P S, and one launch finds E and P of all segments with the same walk (SUM: P from the unit
+// matrix, with the values counted as zero), k_sc_join carries them forward, and the walks proper start from
+// there.
+//
 // Bound by the latency of a step: 256 walks of 64 steps (2 x 4096 tokens, 16 heads, d = 128, one walk on each
 // compute unit) take 93 us forward with what training saves and 100 us backward, 1.5 us a step; 128 walks
 // of 256 steps (one prompt of 16384 tokens) 283 us, 1.1 us or 2700 cycles a step, of which the three
@@ -133,17 +138,21 @@ struct ScChainLds {  // one operand buffer, and the exchange
     static_assert(2 * BYTES + XBYTES + 256 <= 160 * 1024, "two operand buffers fit");
 };
 
-// Where a walk finds its data; j: its workgroup among those of the (sequence, value head).
+// Where a walk finds its data; j: its workgroup among those of the (sequence, value head). Its states are
+// columns col .. of matrices with ld columns; unit: it starts from those columns of the unit matrix, and the
+// values (dO) count as zero.
 struct ScWalk {
     ScSeq q;
-    int h, hk, j;
+    int h, hk, j, ld, col;
+    bool unit;
     const float* start;
     float* end;
 };
 
 // A producer's side: the operands of chunk index(n), n = 0 .. nt - 1, into buffer n % 2. Takes part
 // in the step's barriers.
-template <class OT, int DK, int DV, int NC, bool BWD>
+// (FULL: backward, and forward with outputs, which alone read q and M.)
+template <class OT, int DK, int DV, int NC, bool BWD, bool FULL>
 __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds_char* b0, lds_char* b1, lds_char* pf,
                                            int pi) {
     using B = ScChainLds<OT, DK, NC, BWD>;
@@ -181,7 +190,7 @@ __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds
         __builtin_amdgcn_global_load_lds(src, (lds_void*)(buf + B::VEC + pi * 1024), 16, 0, 0);
     };
     auto load2 = [&](int n) {  // q
-        if (!BWD && !a.o) return;
+        if (!FULL) return;
         const Chunk x = chunk(n);
         sc_dma_rows<OT, DK>(rl, x.q, rsk, x.nvalid, ((n & 1) ? b1 : b0) + B::Q, pi);
     };
@@ -195,7 +204,7 @@ __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds
         const int p = v / (6 * LF), f = v / LF % 6;
         return (8 * p + (BWD ? (f < 4 ? f : 2 * f - 3) : (f < 2 ? 2 * f : f + 2))) * LF + v % LF;
     };
-    constexpr int LVEC = SC_VEC * 4 / 128, LINES = 2 * LK + LT + LM + LV + LVEC;
+    constexpr int LVEC = SC_VEC * 4 / 128, LINES = LK + LT + LV + (FULL ? LK + LM : 0) + LVEC;
     constexpr int NPF = (LINES + NJ * 64 * SC_NP - 1) / (NJ * 64 * SC_NP);
     auto prefetch = [&](int n) {  // (past the last chunk: the last one again, so that their number is fixed)
         const Chunk x = chunk(min(n, nt - 1));
@@ -212,12 +221,12 @@ __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds
                 p = tp + img_line(v) * 128;
             } else if ((v -= LT) < LV) {
                 p = x.v + (size_t)min(v / LPV, last) * rsv + (v % LPV) * 128;
-            } else if ((v -= LV) < LK) {
+            } else if (FULL && (v -= LV) < LK) {
                 p = x.q + (size_t)min(v / LPK, last) * rsk + (v % LPK) * 128;
-            } else if ((v -= LK) < LM) {
+            } else if (FULL && (v -= LK) < LM) {
                 p = mp + img_line(v) * 128;
             } else {
-                p = x.f + min(v - LM, LVEC - 1) * 128;
+                p = x.f + min(v - (FULL ? LM : LV), LVEC - 1) * 128;
             }
             __builtin_amdgcn_global_load_lds(p, (lds_void*)(pf), 4, 0, 0);
         }
@@ -264,26 +273,28 @@ struct ScState {
     using B = ScChainLds<OT, DK, NC, BWD>;
     static constexpr int NT = DK / 64;
     f32x4 s[NC][NT];
-    __device__ __forceinline__ void init(const float* m, int ld, int col, int wv) {
+    __device__ __forceinline__ void init(const ScWalk& w, int wv) {
         const int l = lane_id(), li = l & 15, lq = l >> 4;
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[ch][t][i] = m ? m[(size_t)(16 * (NT * wv + t) + 4 * lq + i) * ld + col + 16 * ch + li] : 0.f;
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 16 * (NT * wv + t) + 4 * lq + i, c = w.col + 16 * ch + li;
+                    s[ch][t][i] = w.unit ? (r == c ? 1.f : 0.f) : w.start ? w.start[(size_t)r * w.ld + c] : 0.f;
+                }
     }
-    __device__ __forceinline__ void out(float* m, int ld, int col, int wv) const {
+    __device__ __forceinline__ void out(const ScWalk& w, int wv) const {
         const int l = lane_id(), li = l & 15, lq = l >> 4;
-        if (!m) return;
+        if (!w.end) return;
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    m[(size_t)(16 * (NT * wv + t) + 4 * lq + i) * ld + col + 16 * ch + li] = s[ch][t][i];
+                    w.end[(size_t)(16 * (NT * wv + t) + 4 * lq + i) * w.ld + w.col + 16 * ch + li] = s[ch][t][i];
     }
     __device__ __forceinline__ void publish(lds_char* xs, int ch, int wv) const {
 #pragma unroll
@@ -298,7 +309,7 @@ struct ScState {
 // reads from its operand buffer is read as early as the buffer allows (K^T behind the reads that the
 // second product waits for), so that behind the barrier C only the exchanged fragments are left to
 // wait for.
-template <class OT, int DK, int DV, int NC>
+template <class OT, int DK, int DV, int NC, bool SUM>
 __device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk& w, int wv, lds_char* b0, lds_char* b1,
                                             lds_char* xs) {
     using B = ScChainLds<OT, DK, NC, false>;
@@ -307,7 +318,7 @@ __device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk& w, in
     const int l = lane_id(), li = l & 15, lq = l >> 4;
     const int nt = w.q.nt;
     ScState<OT, DK, NC, false> S;
-    S.init(w.start, DV, 16 * NC * w.j, wv);
+    S.init(w, wv);
 #pragma unroll
     for (int ch = 0; ch < NC; ++ch) S.publish(xs, ch, wv);
     const OT* tp = (const OT*)(a.ws + a.L.o_t) + ((size_t)w.q.slot0 * a.Hv + w.h) * a.L.t;
@@ -349,7 +360,7 @@ __device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk& w, in
             Y[0] = (Y[0] + Y[2]) + (Y[1] + Y[3]);
             f32x4 X;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) X[i] = b4[i] * (v4[i] - e4[i] * Y[0][i]);
+            for (int i = 0; i < 4; ++i) X[i] = b4[i] * ((SUM && w.unit ? 0.f : v4[i]) - e4[i] * Y[0][i]);
             put_split<OT>(xc + B::XX + (wv >> 1) * F, 2 * F, wv & 1, X);
         }
         lds_get4<float>(buf + B::VEC + (SC_TAIL + 16 * wv + 4 * lq) * 4, t4);
@@ -412,7 +423,7 @@ __device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk& w, in
             S.publish(xs, ch, wv);
         }
     }
-    S.out(w.end, DV, 16 * NC * w.j, wv);
+    S.out(w, wv);
 }
 
 // The 16-column slice [rows][16] of an exchanged matrix of 16 RT rows (its fragments' first parts, from
@@ -531,7 +542,7 @@ __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, in
 
 // Compute waves of the backward (as sc_fwd_walk). What does not depend on the state, Q^T (e^gam dO), is
 // the side waves'.
-template <class OT, int DK, int DV, int NC>
+template <class OT, int DK, int DV, int NC, bool SUM>
 __device__ __forceinline__ void sc_bwd_walk(const ScArgs& a, const ScWalk& w, int wv, lds_char* b0, lds_char* b1,
                                             lds_char* xs) {
     using B = ScChainLds<OT, DK, NC, true>;
@@ -540,7 +551,7 @@ __device__ __forceinline__ void sc_bwd_walk(const ScArgs& a, const ScWalk& w, in
     const int l = lane_id(), lq = l >> 4;
     const int nt = w.q.nt;
     ScState<OT, DK, NC, true> dS;
-    dS.init(w.start, DV, 16 * NC * w.j, wv);
+    dS.init(w, wv);
 #pragma unroll
     for (int ch = 0; ch < NC; ++ch) dS.publish(xs, ch, wv);
     const size_t tstep = (size_t)a.Hv * a.L.t;
@@ -589,7 +600,7 @@ __device__ __forceinline__ void sc_bwd_walk(const ScArgs& a, const ScWalk& w, in
             Y[0] = (Y[0] + Y[2]) + (Y[1] + Y[3]);
             Z[0] = (Z[0] + Z[2]) + (Z[1] + Z[3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) Z[0][i] += t4[i] * Y[0][i];
+            for (int i = 0; i < 4; ++i) Z[0][i] = (SUM && w.unit ? 0.f : Z[0][i]) + t4[i] * Y[0][i];
             put_split<OT>(xc + B::XX + (wv >> 1) * F, 2 * F, wv & 1, Z[0]);
         }
         lds_get4<float>(buf + B::VEC + (SC_E + 16 * wv + 4 * lq) * 4, e4);
@@ -660,10 +671,10 @@ __device__ __forceinline__ void sc_bwd_walk(const ScArgs& a, const ScWalk& w, in
             dS.publish(xs, ch, wv);
         }
     }
-    dS.out(w.end, DV, 16 * NC * w.j, wv);
+    dS.out(w, wv);
 }
 
-template <class OT, int DK, int DV, int NC>
+template <class OT, int DK, int DV, int NC, bool SUM>
 __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, int wv, const lds_char* b0,
                                             const lds_char* b1, lds_char* xs) {
     using B = ScChainLds<OT, DK, NC, true>;
@@ -682,7 +693,7 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
         const LSwz<OT, DK> vQ{buf + B::Q};
         const size_t id = (size_t)(w.q.slot0 + (w.q.nt - 1 - n)) * a.Hv + w.h;
         sync_lds();  // A
-        if (n > 0) store_state(n - 1);
+        if (!SUM && n > 0) store_state(n - 1);
         // Q^T (e^gam dO), rows: the keys of compute wave wv; one half of the tokens before B, the other after
         // it, so that neither barrier waits for these waves
         f32x4 P[NC][NT][2];
@@ -721,10 +732,12 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
         for (int ch = 0; ch < NC; ++ch) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
-                lds_store<f32x4>(xs + ch * B::XT + B::XP + ((NT * wv + t) * 64 + l) * 16, P[ch][t][0] + P[ch][t][1]);
-            S[ch].read(xs + ch * B::XT + B::XS, wv);
+                lds_store<f32x4>(xs + ch * B::XT + B::XP + ((NT * wv + t) * 64 + l) * 16,
+                                 SUM && w.unit ? f32x4{0.f, 0.f, 0.f, 0.f} : P[ch][t][0] + P[ch][t][1]);
+            if (!SUM) S[ch].read(xs + ch * B::XT + B::XS, wv);
         }
         sync_lds();  // C
+        if (SUM) continue;
         OT* p = (OT*)(a.ws + a.L.o_dy) + id * a.L.d;
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
@@ -733,7 +746,7 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
             Y.write(p + (size_t)(NC * w.j + ch) * CH * 16, wv);
         }
     }
-    if (w.q.nt > 0) store_state(w.q.nt - 1);
+    if (!SUM && w.q.nt > 0) store_state(w.q.nt - 1);
 }
 
 // The sequence of rank r by length, the longest first (up to 64 packed sequences; more, and sequences of
@@ -751,25 +764,52 @@ __device__ __forceinline__ int sc_ranked(const ScArgs& a, int r) {
     return __ffsll((unsigned long long)__ballot(l < a.N && rank == r)) - 1;
 }
 
-template <class OT, int DK, int DV, int NC>
-__device__ __forceinline__ ScWalk sc_walk_of(const ScArgs& a, const float* starts, float* ends) {
-    ScWalk w;
-    int p;
-    sc_chain_map(blockIdx.x, a.N * a.Hv, DV / (16 * NC), p, w.j);
-    w.h = p % a.Hv;
+// Workgroup -> walk. Sequences of one length may be cut in a.nseg segments of a.seglen chunks (sc_segments),
+// number i along the walk's direction. seg_e[.., i]: where segment i's walk ends; seg_p[.., i]: its transition,
+// the end of a walk from the unit matrix. SUM: the walks that find those, of all segments but the last, each
+// from zero (the first from the sequence's own start), DV columns and for all but the first DK of the
+// transition. Else: the segments themselves, from the ends that k_sc_join has carried forward.
+template <class OT, int DK, int DV, int NC, bool BWD, bool SUM>
+__device__ __forceinline__ bool sc_walk_of(const ScArgs& a, const float* starts, float* ends, ScWalk& w) {
+    constexpr int NJ = DV / (16 * NC), NJK = DK / (16 * NC);
+    const int nseg = SUM ? a.nseg - 1 : a.nseg;
+    int p, j;
+    sc_chain_map(blockIdx.x, a.N * a.Hv * nseg, SUM ? NJ + NJK : NJ, p, j);
+    const int i = p % nseg, pair = p / nseg;
+    w.h = pair % a.Hv;
     w.hk = w.h / a.R;
-    const int s = sc_ranked(a, p / a.Hv);
+    const int s = sc_ranked(a, pair / a.Hv);
     w.q = sc_seq(a.cu, a.T, s);
-    const size_t st = ((size_t)s * a.Hv + w.h) * DK * DV;
-    w.start = starts ? starts + st : nullptr;
-    w.end = ends ? ends + st : nullptr;
-    return w;
+    w.unit = SUM && j >= NJ;
+    if (w.unit && i == 0) return false;
+    w.j = w.unit ? (j - NJ) % NJ : j;
+    w.col = 16 * NC * (w.unit ? j - NJ : j);
+    w.ld = w.unit ? DK : DV;
+    const size_t st = (size_t)s * a.Hv + w.h, sg = st * a.nseg + i;
+    float* const seg_e = (float*)(a.ws + a.L.o_seg);
+    float* const seg_p = seg_e + (size_t)a.N * a.Hv * a.nseg * DK * DV;
+    if (SUM) {
+        w.start = i == 0 && starts ? starts + st * DK * DV : nullptr;
+        w.end = w.unit ? seg_p + sg * DK * DK : seg_e + sg * DK * DV;
+    } else {
+        w.start = i > 0 ? seg_e + (sg - 1) * DK * DV : starts ? starts + st * DK * DV : nullptr;
+        w.end = i + 1 == a.nseg && ends ? ends + st * DK * DV : nullptr;
+    }
+    if (a.nseg > 1) {
+        const int c = a.seglen * (BWD ? a.nseg - 1 - i : i);  // its first chunk
+        w.q.tok0 += 64LL * c;
+        w.q.len = min(w.q.len - 64 * c, 64 * a.seglen);
+        w.q.slot0 += c;
+        w.q.nt = (w.q.len + 63) / 64;
+    }
+    return true;
 }
 
 constexpr int SC_THREADS = 64 * (2 * SC_NC + SC_NP);
 
 template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT>
 __global__ __launch_bounds__(SC_THREADS) void k_sc_fwd_chain(ScArgs a) {
+    constexpr bool SUM = !TRAIN && !OUT;
     using B = ScChainLds<OT, DK, NC, false>;
     __shared__ __align__(16) char buf0[B::BYTES];
     __shared__ __align__(16) char buf1[B::BYTES];
@@ -779,17 +819,18 @@ __global__ __launch_bounds__(SC_THREADS) void k_sc_fwd_chain(ScArgs a) {
     poison_lds((lds_char*)buf1, sizeof(buf1));
     poison_lds((lds_char*)xch, sizeof(xch));
     poison_lds_done();
-    const ScWalk w = sc_walk_of<OT, DK, DV, NC>(a, a.h0, a.ht);
+    ScWalk w;
+    if (!sc_walk_of<OT, DK, DV, NC, false, SUM>(a, a.h0, a.ht, w)) return;
     const int wv = sc_wave();
     if (wv < SC_NC)
-        sc_fwd_walk<OT, DK, DV, NC>(a, w, wv, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
+        sc_fwd_walk<OT, DK, DV, NC, SUM>(a, w, wv, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
     else if (wv < 2 * SC_NC)
         sc_fwd_side<OT, DK, DV, NC, TRAIN, OUT>(a, w, wv - SC_NC, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
     else if (w.q.nt > 0)
-        sc_produce<OT, DK, DV, NC, false>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
+        sc_produce<OT, DK, DV, NC, false, OUT>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
 }
 
-template <class OT, int DK, int DV, int NC>
+template <class OT, int DK, int DV, int NC, bool SUM>
 __global__ __launch_bounds__(SC_THREADS) void k_sc_bwd_chain(ScArgs a) {
     using B = ScChainLds<OT, DK, NC, true>;
     __shared__ __align__(16) char buf0[B::BYTES];
@@ -800,14 +841,54 @@ __global__ __launch_bounds__(SC_THREADS) void k_sc_bwd_chain(ScArgs a) {
     poison_lds((lds_char*)buf1, sizeof(buf1));
     poison_lds((lds_char*)xch, sizeof(xch));
     poison_lds_done();
-    const ScWalk w = sc_walk_of<OT, DK, DV, NC>(a, a.dht, a.dh0);
+    ScWalk w;
+    if (!sc_walk_of<OT, DK, DV, NC, true, SUM>(a, a.dht, a.dh0, w)) return;
     const int wv = sc_wave();
     if (wv < SC_NC)
-        sc_bwd_walk<OT, DK, DV, NC>(a, w, wv, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
+        sc_bwd_walk<OT, DK, DV, NC, SUM>(a, w, wv, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
     else if (wv < 2 * SC_NC)
-        sc_bwd_side<OT, DK, DV, NC>(a, w, wv - SC_NC, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
+        sc_bwd_side<OT, DK, DV, NC, SUM>(a, w, wv - SC_NC, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
     else if (w.q.nt > 0)
-        sc_produce<OT, DK, DV, NC, true>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
+        sc_produce<OT, DK, DV, NC, true, true>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
+}
+
+// Carries the segments' ends forward: E_i += P_i E_(i - 1) for i = 1 .. nseg - 2, so that E_i is where segment
+// i + 1 starts. One workgroup of DK / 16 waves per (sequence, value head, 16 columns), wave w on rows
+// 16 w .. + 15, E_(i - 1) in LDS. fp32 throughout, as the states are.
+template <int DK, int DV>
+__global__ __launch_bounds__(4 * DK) void k_sc_join(ScArgs a) {
+    __shared__ __align__(16) float sE[DK * 17];
+    poison_lds((lds_char*)sE, sizeof(sE));
+    poison_lds_done();
+    const int st = blockIdx.x / (DV / 16), col = 16 * (blockIdx.x % (DV / 16));
+    const int l = lane_id(), li = l & 15, lq = l >> 4, r0 = 16 * sc_wave();
+    float* const e0 = (float*)(a.ws + a.L.o_seg) + (size_t)st * a.nseg * DK * DV + col + li;
+    const float* const p0 = (const float*)(a.ws + a.L.o_seg) + (size_t)a.N * a.Hv * a.nseg * DK * DV +
+                            (size_t)st * a.nseg * DK * DK + (size_t)(r0 + li) * DK + 4 * lq;
+    f32x4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = e0[(size_t)(r0 + 4 * lq + i) * DV];
+    for (int n = 1; n + 1 < a.nseg; ++n) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sE[(r0 + 4 * lq + i) * 17 + li] = x[i];
+        __syncthreads();
+        float* e = e0 + (size_t)n * DK * DV;
+        const float* p = p0 + (size_t)n * DK * DK;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = e[(size_t)(r0 + 4 * lq + i) * DV];
+#pragma unroll
+        for (int kb = 0; kb < DK / 16; ++kb) {
+            const f32x4 pr = *(const f32x4*)(p + 16 * kb);
+            const float a4[4] = {pr[0], pr[1], pr[2], pr[3]};
+            float b4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b4[i] = sE[(16 * kb + 4 * lq + i) * 17 + li];
+            mma_k16_f32(x, a4, b4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[(size_t)(r0 + 4 * lq + i) * DV] = x[i];
+    }
 }
 
 // Column tiles a workgroup: with at most one 16-column walk for each compute unit, one; with two or more,
@@ -824,11 +905,29 @@ static hipError_t sc_column_tiles(const ScArgs& a, long long walks16, int& nc) {
     return e;
 }
 
+// The segments' ends, where there is more than one: summarise runs the SUM walks of nc column tiles.
+template <int DK, int DV, class F>
+static hipError_t sc_segment_ends(const ScArgs& a, hipStream_t stream, F summarise) {
+    if (a.nseg <= 1) return hipSuccess;
+    const long long tiles = (long long)a.N * a.Hv * (a.nseg - 1) * ((DV + DK) / 16);
+    const int nc = tiles > 256 ? 2 : 1;
+    summarise(nc, dim3((unsigned)(tiles / nc)));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.nseg == 2) return e;
+    hipLaunchKernelGGL((k_sc_join<DK, DV>), dim3((unsigned)(a.N * a.Hv * (DV / 16))), dim3(4 * DK), 0, stream, a);
+    return hipGetLastError();
+}
+
 template <class OT, int DK, int DV>
 hipError_t launch_sc_fwd_chain_t(const ScArgs& a, bool train, hipStream_t stream) {
     int nc;
-    const long long walks = (long long)a.N * a.Hv * (DV / 16);
-    const hipError_t e = sc_column_tiles(a, walks, nc);
+    const long long walks = (long long)a.N * a.Hv * a.nseg * (DV / 16);
+    hipError_t e = sc_column_tiles(a, walks, nc);
+    if (e != hipSuccess) return e;
+    e = sc_segment_ends<DK, DV>(a, stream, [&](int n, dim3 grid) {
+        auto k = n == 2 ? k_sc_fwd_chain<OT, DK, DV, 2, false, false> : k_sc_fwd_chain<OT, DK, DV, 1, false, false>;
+        hipLaunchKernelGGL(k, grid, dim3(SC_THREADS), 0, stream, a);
+    });
     if (e != hipSuccess) return e;
     auto pick = [&](auto n) {
         constexpr int NC = decltype(n)::value;
@@ -842,10 +941,15 @@ hipError_t launch_sc_fwd_chain_t(const ScArgs& a, bool train, hipStream_t stream
 template <class OT, int DK, int DV>
 hipError_t launch_sc_bwd_chain_t(const ScArgs& a, hipStream_t stream) {
     int nc;
-    const long long walks = (long long)a.N * a.Hv * (DV / 16);
-    const hipError_t e = sc_column_tiles(a, walks, nc);
+    const long long walks = (long long)a.N * a.Hv * a.nseg * (DV / 16);
+    hipError_t e = sc_column_tiles(a, walks, nc);
     if (e != hipSuccess) return e;
-    auto k = nc == 2 ? k_sc_bwd_chain<OT, DK, DV, 2> : k_sc_bwd_chain<OT, DK, DV, 1>;
+    e = sc_segment_ends<DK, DV>(a, stream, [&](int n, dim3 grid) {
+        auto k = n == 2 ? k_sc_bwd_chain<OT, DK, DV, 2, true> : k_sc_bwd_chain<OT, DK, DV, 1, true>;
+        hipLaunchKernelGGL(k, grid, dim3(SC_THREADS), 0, stream, a);
+    });
+    if (e != hipSuccess) return e;
+    auto k = nc == 2 ? k_sc_bwd_chain<OT, DK, DV, 2, false> : k_sc_bwd_chain<OT, DK, DV, 1, false>;
     hipLaunchKernelGGL(k, dim3((unsigned)(walks / nc)), dim3(SC_THREADS), 0, stream, a);
     return hipGetLastError();
 }

@@ -238,7 +238,9 @@ int gdr2_fwd_noalloc(const void* q, const void* k, const void* v, const void* g,
  * Precision: with bf16, o and the gradients of the token tensors carry a few bf16 roundings; the
  * states, which are fp32, do not: ht and dh0 are off by less than 1e-5 of what was written into them
  * (Frobenius norm; writes that cancel one another, as of one key again and again, leave their errors
- * behind). g <= 0 may be of any finite size, as for gdr2_fwd.
+ * behind). g <= 0 may be of any finite size, as for gdr2_fwd. Results repeat bit for bit; few long
+ * sequences of one length are walked in segments, so that their last bits differ from those of a call
+ * with more sequences, or a packed one.
  *
  * Supported dtype / dk / dv as gdr2_fwd; chunks are of 64 tokens. Ownership, streams, errors and calls
  * without tokens as gdr2_fwd / gdr2_bwd; g, beta, dg and dbeta need only their element's alignment; Hv

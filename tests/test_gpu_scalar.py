@@ -341,6 +341,32 @@ def test_many_chains(case):
     check(train(x, cu), x, cu, dtype)
 
 
+@pytest.mark.parametrize("case", [
+    # few chains and long: whole, and cut in three to eight segments, the last ones ragged
+    ([2100], 1, 1, 64, 64, F32), ([4133], 1, 2, 64, 64, F32), ([2050, 2050], 2, 2, 128, 128, BF),
+    ([3300, 3300], 2, 2, 128, 128, BF),
+    ([4200], 1, 2, 128, 64, BF), ([5500], 1, 1, 64, 128, BF), ([8300], 1, 1, 64, 64, BF), ([4096], 4, 4, 128, 128, BF)])
+@pytest.mark.parametrize("h0", [True, False])
+def test_long_sequences(case, h0):
+    # weak decays and writes, so that what one segment leaves still counts in the next ones
+    lens, hk, hv, dk, dv, dtype = case
+    x, cu = inputs(lens, False, hk, hv, dk, dv, dtype, g_scale=0.0005, beta_scale=0.05, h0=h0, seed=35)
+    check(train(x, cu), x, cu, dtype)
+
+
+def test_long_sequences_repeat_and_recompute():
+    x, _ = inputs([3300], False, 2, 4, 128, 64, BF, g_scale=0.001, beta_scale=0.1, seed=36)
+    args = [x[n] for n in ("q", "k", "v", "g", "beta", "h0")]
+    a, b = train(x, None), train(x, None)
+    o, ht, _ = g2.gdr2_scalar_fwd(*args)
+    c = g2.gdr2_scalar_bwd(*args, x["do"], x["dht"])
+    assert torch.equal(o, a["o"]) and torch.equal(ht, a["ht"])
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+    for n in c:
+        assert torch.equal(a[n], c[n]), n
+
+
 def test_many_value_heads_of_a_key_head():
     x, cu = inputs([130], False, 2, 14, 64, 64, BF, seed=31)
     check(train(x, cu), x, cu, BF)
