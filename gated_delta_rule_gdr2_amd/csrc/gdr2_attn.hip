@@ -23,8 +23,8 @@
 // leaves partial sums, joined in a fixed order by a second kernel. Where no row can be long, each
 // workgroup takes one row and there is nothing to join (attn_rows_mode).
 //
-// Measured: 64 sequences of 200 to 16384 tokens, 32 heads over 8 key heads of 128, bf16 (1.02 GB) 192 us
-// and 6 us for the join, 5.2 TB/s together; 24 windows of up to 2048 tokens, 16 heads of 64, fp32 (134 MB)
+// Measured: 64 sequences of 200 to 16384 tokens, 32 heads over 8 key heads of 128, bf16 (1.02 GB) 198 us
+// with the join, 5.15 TB/s, and 4096 of 300 tokens (5 GB) 1.10 ms, 4.6 TB/s; 24 windows of up to 2048 tokens, 16 heads of 64, fp32 (134 MB)
 // 38 us a pass, 3.5 TB/s, of which about 12 us are what even short rows take on the line (two launches,
 // the line, the join).
 #include "gdr2_attn.hpp"
@@ -82,6 +82,28 @@ __device__ __forceinline__ AttnLine attn_line(const AttnArgs& a) {
     p.total = __builtin_amdgcn_readlane(x, 63);
     p.share = max((p.total + a.wgs - 1) / a.wgs, (unsigned)ATTN_MIN);
     return p;
+}
+
+// The sequence that holds place t (below total): its number, first place and tokens.
+struct AttnAt {
+    int b;
+    unsigned at;
+    AttnSpan sp;
+};
+template <class OT>
+__device__ __forceinline__ AttnAt attn_find(const AttnArgs& a, const AttnLine& line, unsigned t) {
+    const int HR = a.Hkv * a.NG;
+    // the last run of sequences that does not begin behind it, then through that run
+    const int ln = __popcll(__ballot(line.before <= t && lane_id() * line.per < a.B)) - 1;
+    AttnAt f;
+    f.b = ln * line.per;
+    f.at = __builtin_amdgcn_readlane(line.before, ln);
+    f.sp = attn_span<OT>(a, f.b);
+    while (t >= f.at + (f.sp.units + ATTN_COST) * HR) {
+        f.at += (f.sp.units + ATTN_COST) * HR;
+        f.sp = attn_span<OT>(a, ++f.b);
+    }
+    return f;
 }
 
 // One unit's keys and values in registers, as loaded.
@@ -366,16 +388,10 @@ __global__ __launch_bounds__(64 * AW) void k_attn(AttnArgs a) {
     unsigned t = blockIdx.x * line.share;
     if (t >= line.total) return;
     const unsigned tend = min(t + line.share, line.total);
-    // the sequence that holds place t: the last run of sequences that does not begin behind it, then
-    // through that run
-    const int ln = __popcll(__ballot(line.before <= t && lane_id() * line.per < a.B)) - 1;
-    int b = ln * line.per;
-    unsigned at = __builtin_amdgcn_readlane(line.before, ln);
-    AttnSpan sp = attn_span<OT>(a, b);
-    while (t >= at + (sp.units + ATTN_COST) * HR) {
-        at += (sp.units + ATTN_COST) * HR;
-        sp = attn_span<OT>(a, ++b);
-    }
+    AttnAt f = attn_find<OT>(a, line, t);
+    int b = f.b;
+    unsigned at = f.at;
+    AttnSpan sp = f.sp;
     while (t < tend) {
         const int len = sp.units + ATTN_COST;
         const int hr = (t - at) / len;
@@ -399,25 +415,32 @@ __global__ __launch_bounds__(64 * AW) void k_attn(AttnArgs a) {
     }
 }
 
-// Joins the partial results of the rows that cross workgroups: one workgroup per (sequence, query
-// head), the workgroups' parts of the row in order.
+// Joins the partial results of the rows that cross workgroups, the workgroups' parts of a row in order. One
+// workgroup for each run of the line but the last and each head of a group: at most one row begins in a run
+// and goes on behind it. (With one for each row, each of which walked the line, 4096 sequences took 4.9 ms.)
 template <class OT, int D>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     constexpr int NGRP = 256 / (D / 4);  // thread groups over the parts
     __shared__ float sM[NGRP], sL[NGRP];
     __shared__ __align__(16) float so[NGRP][D];
+    poison_lds((lds_char*)sM, sizeof(sM));
+    poison_lds((lds_char*)sL, sizeof(sL));
+    poison_lds((lds_char*)so, sizeof(so));
+    poison_lds_done();
     const int tid = threadIdx.x;
-    const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq;
-    const int hkv = hq / a.G, grp = (hq % a.G) / a.gh, hd = (hq % a.G) % a.gh;
-    const int HR = a.Hkv * a.NG, hr = hkv * a.NG + grp;
+    const unsigned w0 = blockIdx.x / a.gh;
+    const int hd = blockIdx.x % a.gh;
     const AttnLine line = attn_line<OT>(a);
-    const AttnSpan sp = attn_span<OT>(a, b);
-    const int ln = b / line.per;
-    unsigned at = __builtin_amdgcn_readlane(line.before, ln);
-    for (int i = ln * line.per; i < b; ++i) at += (attn_span<OT>(a, i).units + ATTN_COST) * HR;
-    const unsigned r0 = at + (unsigned)hr * (sp.units + ATTN_COST) + ATTN_COST;  // the place of its unit 0
-    const unsigned w0 = r0 / line.share, w1 = (r0 + sp.units - 1) / line.share;
-    if (w0 == w1) return;  // written by the one workgroup that had it
+    const unsigned t = (w0 + 1) * line.share;  // the first place behind the run
+    if (t >= line.total) return;
+    const AttnAt f = attn_find<OT>(a, line, t);
+    const int b = f.b, len = f.sp.units + ATTN_COST, hr = (t - f.at) / len;
+    const unsigned r0 = f.at + (unsigned)hr * len + ATTN_COST;  // the place of the row's unit 0
+    if (r0 >= t || r0 / line.share != w0) return;  // it begins behind the run, or before it
+    const unsigned w1 = (r0 + f.sp.units - 1) / line.share;
+    const int hkv = hr / a.NG, hg = (hr % a.NG) * a.gh + hd;
+    if (hg >= a.G) return;
+    const int hq = hkv * a.G + hg;
     const size_t stride = (size_t)a.gh * (D + 4);
     const int g = tid / (D / 4), d = 4 * (tid % (D / 4));
     float M = -INFINITY, L = 0.f;
@@ -480,7 +503,7 @@ static hipError_t launch_attn_t(const AttnArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((k_attn<OT, D, true>), dim3(a.wgs), dim3(64 * AW), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_attn_join<OT, D>), dim3((unsigned)(a.B * a.Hq)), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((k_attn_join<OT, D>), dim3((unsigned)((a.wgs - 1) * a.gh)), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 hipError_t launch_attn(const AttnArgs& a, bool bf16_, hipStream_t stream) {

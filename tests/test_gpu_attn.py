@@ -193,6 +193,14 @@ def test_more_rows_than_lanes_on_shared_workgroups(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_thousands_of_rows_on_shared_workgroups(dtype):
+    gen = torch.Generator().manual_seed(19)
+    lens = torch.randint(0, 5, (2500,), generator=gen).tolist()
+    lens[1234] = 3000
+    check(*make(lens, 2, 1, 64, 16, dtype, seed=19, width=300))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_heads_of_a_long_row(dtype):
     check(*make([2100, 700], 34, 2, 128, 32, dtype, seed=17, width=200))
 
