@@ -8,9 +8,11 @@ Attention", anthology record LIT-802, takeaway 1; paper Sec. 3.1 Eqs. 8-10)
 
 runs entirely in the HIP kernels of ``libgdr2.so`` (built from ``csrc/`` by
 ``python -m gated_delta_rule_gdr2_amd.build``); see ``include/gdr2.h`` for the
-C ABI. This module only marshals torch tensors (device memory and the current
-HIP stream) into those calls. There is no fallback: if the library is missing
-every call raises.
+C ABI. So do the same recurrence with scalar gates (``gdr2_scalar_*``) and, for
+the other layers of a hybrid decoder, attention over a paged key-value cache
+(``gdr2_attn_step``) and the cache's writer (``gdr2_kv_append``). This module
+only marshals torch tensors (device memory and the current HIP stream) into
+those calls. There is no fallback: if the library is missing every call raises.
 """
 from __future__ import annotations
 
