@@ -419,28 +419,17 @@ def _device_of(t, name):
     return dev
 
 
-def _raw_stream(dev):
-    """The current stream of a device as a number, without an object around it where torch offers that."""
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return torch.cuda.current_stream(dev).cuda_stream if get is None else get(dev)
+# the current stream of a device as a number, without an object around it where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-class _on:
-    """Device ``dev`` as the current one, and the stream to launch on: the given one, or the device's current
-    stream."""
-
-    def __init__(self, dev, stream):
-        self.dev, self.stream, self.prev = dev, stream, None
-
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev:
-            self.prev = torch.cuda.current_device()
-            torch.cuda.set_device(self.dev)
-        return _raw_stream(self.dev) if self.stream is None else self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
+def _launch(f, dev, stream, *args):
+    """f(*args, stream) with device ``dev`` as the current one, on the given stream or the device's current one."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _launch(f, dev, stream, *args)
+    return f(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
 
 
 def _scalar_dims(q, k, v, g, beta, cu_seqlens):
@@ -516,10 +505,9 @@ def gdr2_scalar_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, save_for_bwd=
     if own_o and N == 0:
         o.zero_()  # no sequence, and no kernel
     _keep_for(stream, *new)
-    with _on(dev, stream) as s:
-        st = lib.gdr2_scalar_fwd(_adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(cu_seqlens), _adr(o),
-                                 _adr(ht), N, T, Hk, Hv, dk, dv, dt, int(own_o), int(bool(save_for_bwd)), _adr(ws),
-                                 ws.numel(), s)
+    st = _launch(lib.gdr2_scalar_fwd, dev, stream, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0),
+                 _adr(cu_seqlens), _adr(o), _adr(ht), N, T, Hk, Hv, dk, dv, dt, int(own_o), int(bool(save_for_bwd)),
+                 _adr(ws), ws.numel())
     _raise(st, "gdr2_scalar_fwd")
     return o, ht, ws
 
@@ -560,11 +548,10 @@ def gdr2_scalar_bwd(q, k, v, g, beta, h0, dout, dht=None, *, cu_seqlens=None, ws
         for n, _ in names:
             grads[n].zero_()
     _keep_for(stream, *new)
-    with _on(dev, stream) as s:
-        st = lib.gdr2_scalar_bwd(_adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0), _adr(dout), _adr(dht),
-                                 _adr(cu_seqlens), _adr(grads["dq"]), _adr(grads["dk"]), _adr(grads["dv"]),
-                                 _adr(grads["dg"]), _adr(grads["dbeta"]), _adr(grads["dh0"]), N, T, Hk, Hv, dk, dv,
-                                 dt, int(own), int(bool(fwd_saved)), _adr(ws), ws.numel(), s)
+    st = _launch(lib.gdr2_scalar_bwd, dev, stream, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0),
+                 _adr(dout), _adr(dht), _adr(cu_seqlens), _adr(grads["dq"]), _adr(grads["dk"]), _adr(grads["dv"]),
+                 _adr(grads["dg"]), _adr(grads["dbeta"]), _adr(grads["dh0"]), N, T, Hk, Hv, dk, dv, dt, int(own),
+                 int(bool(fwd_saved)), _adr(ws), ws.numel())
     _raise(st, "gdr2_scalar_bwd")
     return grads
 
@@ -592,9 +579,8 @@ def gdr2_scalar_step(q, k, v, g, beta, state, *, slots=None, o=None, stream=None
         _keep_for(stream, o)
     else:
         _want(o, "o", q.dtype, v.shape, dev)
-    with _on(dev, stream) as s:
-        st = lib.gdr2_scalar_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                                  state.data_ptr(), _adr(slots), o.data_ptr(), B, T, Hk, Hv, dk, dv, S, dt, s)
+    st = _launch(lib.gdr2_scalar_step, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+                 beta.data_ptr(), state.data_ptr(), _adr(slots), o.data_ptr(), B, T, Hk, Hv, dk, dv, S, dt)
     _raise(st, "gdr2_scalar_step")
     return o
 
@@ -714,11 +700,10 @@ def gdr2_attn_step(q, k_cache, v_cache, block_table, lengths, *, scale=None, win
     else:
         _want(ws, "ws", torch.uint8, ws.shape, dev)
     _keep_for(stream, *new)
-    with _on(dev, stream) as s:
-        st = lib.gdr2_attn_step(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), strides, block_table.data_ptr(),
-                                lengths.data_ptr(), o.data_ptr(), _adr(lse), B, Hq, Hkv, D, pages, page, max_pages,
-                                D ** -0.5 if scale is None else scale, max(-1, min(window, 0x7fffffff)), dt,
-                                ws.data_ptr(), ws.numel(), s)
+    st = _launch(lib.gdr2_attn_step, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), strides,
+                 block_table.data_ptr(), lengths.data_ptr(), o.data_ptr(), _adr(lse), B, Hq, Hkv, D, pages, page,
+                 max_pages, D ** -0.5 if scale is None else scale, max(-1, min(window, 0x7fffffff)), dt, ws.data_ptr(),
+                 ws.numel())
     _raise(st, "gdr2_attn_step")
     return o if lse is None else (o, lse)
 
@@ -749,8 +734,7 @@ def gdr2_kv_append(k, v, k_cache, v_cache, block_table, starts, *, cu_seqlens=No
     elif tokens != B:
         raise ValueError("without cu_seqlens there is one token a sequence, got %d tokens for %d sequences"
                          % (tokens, B))
-    with _on(dev, stream) as s:
-        st = lib.gdr2_kv_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), strides,
-                                block_table.data_ptr(), starts.data_ptr(), _adr(cu_seqlens), B, tokens, Hkv, D,
-                                pages, page, max_pages, _DT[k.dtype], s)
+    st = _launch(lib.gdr2_kv_append, dev, stream, k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                 strides, block_table.data_ptr(), starts.data_ptr(), _adr(cu_seqlens), B, tokens, Hkv, D, pages, page,
+                 max_pages, _DT[k.dtype])
     _raise(st, "gdr2_kv_append")
