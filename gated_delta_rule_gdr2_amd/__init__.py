@@ -588,6 +588,8 @@ def gdr2_scalar_step(q, k, v, g, beta, state, *, slots=None, o=None, stream=None
 def _accumulation_streams(leaves):
     """Of each leaf that wants a gradient, what its accumulation node carries. A node lives as long as any
     graph that was built on the leaf, and the engine runs it on the stream of the first."""
+    if torch.is_inference_mode_enabled():
+        return []  # no graph is built, and there are no nodes to ask for
     return [torch.autograd.graph.get_gradient_edge(t).node.metadata
             for t in leaves if t is not None and t.is_leaf and t.requires_grad]
 

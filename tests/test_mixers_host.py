@@ -191,6 +191,8 @@ def test_marks_of_leaves_live_as_long_as_their_graphs():
     assert marks()[0]["gdr2_stream"] == 7
     del y
     assert "gdr2_stream" not in marks()[0]
+    with torch.inference_mode():
+        assert marks() == []
 
 
 def test_a_captured_backward_with_a_foreign_graph_is_refused(monkeypatch):
