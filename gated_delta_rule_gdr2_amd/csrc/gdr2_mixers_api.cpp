@@ -56,8 +56,8 @@ int sc_shape(int N, int T, int Hk, int Hv, int dk, int dv, int dtype, bool packe
 bool sc_no_tokens(int N, int T, int Hv) { return N == 0 || T == 0 || Hv == 0; }
 
 gdr2::ScLayout sc_layout_for(int N, int T, int Hv, int dk, int dv, int dtype, bool packed) {
-    int nseg, seglen;
-    gdr2::sc_segments(N, T, Hv, dv, packed, nseg, seglen);
+    int nseg, seglen, lead;
+    gdr2::sc_segments(N, T, Hv, dv, packed, nseg, seglen, lead);
     return gdr2::sc_layout(sc_slots(N, T, packed) * Hv, nseg > 1 ? (long long)N * Hv * nseg : 0, dk, dv, esize(dtype));
 }
 
@@ -79,7 +79,7 @@ void sc_fill(gdr2::ScArgs& a, const int* cu, int N, int T, int Hk, int Hv, int d
     a.DV = dv;
     a.slots = (int)sc_slots(N, T, cu != nullptr);
     a.zero_rest = zero_rest;
-    gdr2::sc_segments(N, T, Hv, dv, cu != nullptr, a.nseg, a.seglen);
+    gdr2::sc_segments(N, T, Hv, dv, cu != nullptr, a.nseg, a.seglen, a.lead);
     a.L = sc_layout_for(N, T, Hv, dk, dv, dtype, cu != nullptr);
     a.ws = (char*)ws;
 }

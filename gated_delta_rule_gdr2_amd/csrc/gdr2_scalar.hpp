@@ -95,32 +95,39 @@ struct ScArgs {
     int Hk, Hv, R;                     // R = Hv / Hk value heads share a key head
     int DK, DV;
     int slots;                         // chunk slots (at least one per chunk of every sequence)
-    int nseg, seglen;                  // segments that a sequence's chains are cut in, and their chunks
+    int nseg, seglen, lead;            // segments of a sequence's chains, their chunks, the first one ahead
     int zero_rest;                     // packed: 1 sets the outputs' rows of no sequence to zero
 };
 
 // Segments that chains are cut in, and their chunks: each segment's end from a zero start and its transition
 // are found at the same time, joined, and the segments walked together. That is two walks and twice the
-// columns (where DK = DV) instead of one, so it pays where walks are few and long: up to 64 of 16 columns,
-// with at least 16 chunks a segment, as many segments as give 256 workgroups something, up to 8.
+// columns (where DK = DV) instead of one, so it pays where walks are few and long: up to 128 of 16 columns,
+// with at least 16 chunks a segment, as many segments as give 256 workgroups something, up to 8. lead: the
+// first segment is walked in full along with the others' ends, one less to walk after the join, where
+// workgroups are short (the ends alone are quicker to find).
 // (Packed sequences, whose lengths only the device knows, are walked whole.) Measured, one sequence, bf16,
 // d = 128, forward and training step, in segments and whole:
-//   16384 tokens  1 head    104 and 295 us,  231 and 645     4 heads   133 and 307,  351 and 679
-//                 8 heads   218 and 337,     581 and 771
-//    4096 tokens  1 head     56 and 86,      133 and 192     8 heads    74 and 91,   176 and 209
+//   16384 tokens  1 head    102 and 295 us,  233 and 645     4 heads   133 and 307,  324 and 679
+//                 8 heads   200 and 337,     516 and 771    12 heads   304 and 316,  795 and 910
+//    4096 tokens  1 head     57 and 86,      133 and 192     8 heads    79 and 91,   184 and 209
 //    2048 tokens  2 heads    52 and 50,      119 and 113 (two segments of 16)
-inline void sc_segments(int N, int T, int Hv, int DV, bool packed, int& nseg, int& seglen) {
+// 8 heads of 16384 tokens without the first segment ahead (four segments): 218 us and 581 us; 1 head with
+// it 110 and 241.
+inline void sc_segments(int N, int T, int Hv, int DV, bool packed, int& nseg, int& seglen, int& lead) {
     const long long walks = (long long)N * Hv * (DV / 16);
     const int nt = (int)(((long long)T + 63) / 64);
     nseg = 1;
     seglen = nt;
-    if (packed || walks < 1 || walks > 64) return;
-    int n = (int)(256 / walks);
+    lead = 0;
+    if (packed || walks < 1 || walks > 128) return;
+    const int ahead = walks >= 64;
+    int n = (int)(256 / walks) + ahead;
     if (n > 8) n = 8;
     if (n > nt / 16) n = nt / 16;
     if (n < 3) return;  // two walks of half the chunks are no shorter
     seglen = (nt + n - 1) / n;
     nseg = (nt + seglen - 1) / seglen;
+    lead = ahead;
 }
 
 // Sequence s: its first token row, token count and first chunk slot. Packed sequences take the

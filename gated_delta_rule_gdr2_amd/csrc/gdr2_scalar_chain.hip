@@ -28,11 +28,11 @@
 // Few long sequences are cut in segments (sc_segments): the state at a segment's end is affine in the one at
 // its start, E + P S, and one launch finds E and P of all segments with the same walk (SUM: P from the unit
 // matrix, with the values counted as zero), k_sc_join carries them forward, and the walks proper start from
-// there.
+// there. (With 64 walks and more the first segment is walked in full at once: ScArgs::lead.)
 //
 // Bound by the latency of a step: 256 walks of 64 steps (2 x 4096 tokens, 16 heads, d = 128, one walk on each
 // compute unit) take 93 us forward with what training saves and 100 us backward, 1.5 us a step; 128 walks
-// of 256 steps (one prompt of 16384 tokens) 283 us, 1.1 us or 2700 cycles a step, of which the three
+// of 256 steps (one prompt of 16384 tokens, walked whole) 283 us, 1.1 us or 2700 cycles a step, of which the three
 // barriers with the exchange behind each are most. Measured and not taken: T through LDS like the rest
 // (forward 104 -> 111 us at the time), q straight to the side waves' registers (104 -> 113), the keys of K S
 // split over the waves and summed through LDS (97 -> 108; the prompt 288 -> 333), a higher wave priority
@@ -104,12 +104,17 @@ __device__ __forceinline__ void sc_dma_slice(const char* base, size_t rs, int nv
 
 // chain workgroup -> (sequence, value head, slice): workgroups go to the 8 XCDs round-robin, so
 // that the slices of a (sequence, head), which read the same q, k, T and M, share an L2, as far as
-// their number allows
-__device__ __forceinline__ void sc_chain_map(int gid, int pairs, int NJ, int& s, int& j) {
+// their number allows. even: walks of one length, so that an XCD may take consecutive ones (uneven ones
+// come longest first, and that order is kept)
+__device__ __forceinline__ void sc_chain_map(int gid, int pairs, int NJ, bool even, int& s, int& j) {
+    const int x = gid % 8, rest = gid / 8;
     if (pairs % 8 == 0) {
-        const int x = gid % 8, rest = gid / 8;
         j = rest % NJ;
         s = (rest / NJ) * 8 + x;
+    } else if (even) {
+        const int all = pairs * NJ, n = x * (all / 8) + min(x, all % 8) + rest;
+        s = n / NJ;
+        j = n % NJ;
     } else {
         s = gid / NJ;
         j = gid % NJ;
@@ -140,19 +145,19 @@ struct ScChainLds {  // one operand buffer, and the exchange
 
 // Where a walk finds its data; j: its workgroup among those of the (sequence, value head). Its states are
 // columns col .. of matrices with ld columns; unit: it starts from those columns of the unit matrix, and the
-// values (dO) count as zero.
+// values (dO) count as zero. full: what its steps give away is wanted, not only where it ends.
 struct ScWalk {
     ScSeq q;
     int h, hk, j, ld, col;
-    bool unit;
+    bool unit, full;
     const float* start;
     float* end;
 };
 
 // A producer's side: the operands of chunk index(n), n = 0 .. nt - 1, into buffer n % 2. Takes part
 // in the step's barriers.
-// (FULL: backward, and forward with outputs, which alone read q and M.)
-template <class OT, int DK, int DV, int NC, bool BWD, bool FULL>
+// (FULL: backward, and forward with outputs, which alone read q and M; with SUM, of full walks.)
+template <class OT, int DK, int DV, int NC, bool BWD, bool FULL, bool SUM>
 __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds_char* b0, lds_char* b1, lds_char* pf,
                                            int pi) {
     using B = ScChainLds<OT, DK, NC, BWD>;
@@ -190,7 +195,7 @@ __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds
         __builtin_amdgcn_global_load_lds(src, (lds_void*)(buf + B::VEC + pi * 1024), 16, 0, 0);
     };
     auto load2 = [&](int n) {  // q
-        if (!FULL) return;
+        if (!FULL || (SUM && !BWD && !w.full)) return;
         const Chunk x = chunk(n);
         sc_dma_rows<OT, DK>(rl, x.q, rsk, x.nvalid, ((n & 1) ? b1 : b0) + B::Q, pi);
     };
@@ -221,6 +226,8 @@ __device__ __forceinline__ void sc_produce(const ScArgs& a, const ScWalk& w, lds
                 p = tp + img_line(v) * 128;
             } else if ((v -= LT) < LV) {
                 p = x.v + (size_t)min(v / LPV, last) * rsv + (v % LPV) * 128;
+            } else if (FULL && SUM && !BWD && !w.full) {
+                p = x.f + min(max(v - LV - LK - LM, 0), LVEC - 1) * 128;
             } else if (FULL && (v -= LV) < LK) {
                 p = x.q + (size_t)min(v / LPK, last) * rsk + (v % LPK) * 128;
             } else if (FULL && (v -= LK) < LM) {
@@ -462,9 +469,14 @@ struct Slice {
 };
 
 // Side waves: what a step gives away -- O, and for training the chunk's start state and Delta.
-template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT>
+template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT, bool SUM>
 __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, int wv, const lds_char* b0,
                                             const lds_char* b1, const lds_char* xs) {
+    if (SUM && !w.full) {
+#pragma unroll 1
+        for (int n = 0; n < 3 * w.q.nt; ++n) sync_lds();  // A, B, C
+        return;
+    }
     using B = ScChainLds<OT, DK, NC, false>;
     using FT = typename Frag<OT>::type;
     constexpr int NKB = B::NKB, F = B::F;
@@ -693,7 +705,8 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
         const LSwz<OT, DK> vQ{buf + B::Q};
         const size_t id = (size_t)(w.q.slot0 + (w.q.nt - 1 - n)) * a.Hv + w.h;
         sync_lds();  // A
-        if (!SUM && n > 0) store_state(n - 1);
+        const bool give = !SUM || w.full;
+        if (give && n > 0) store_state(n - 1);
         // Q^T (e^gam dO), rows: the keys of compute wave wv; one half of the tokens before B, the other after
         // it, so that neither barrier waits for these waves
         f32x4 P[NC][NT][2];
@@ -734,10 +747,10 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
             for (int t = 0; t < NT; ++t)
                 lds_store<f32x4>(xs + ch * B::XT + B::XP + ((NT * wv + t) * 64 + l) * 16,
                                  SUM && w.unit ? f32x4{0.f, 0.f, 0.f, 0.f} : P[ch][t][0] + P[ch][t][1]);
-            if (!SUM) S[ch].read(xs + ch * B::XT + B::XS, wv);
+            if (give) S[ch].read(xs + ch * B::XT + B::XS, wv);
         }
         sync_lds();  // C
-        if (SUM) continue;
+        if (!give) continue;
         OT* p = (OT*)(a.ws + a.L.o_dy) + id * a.L.d;
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) {
@@ -746,7 +759,7 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
             Y.write(p + (size_t)(NC * w.j + ch) * CH * 16, wv);
         }
     }
-    if (!SUM && w.q.nt > 0) store_state(w.q.nt - 1);
+    if ((!SUM || w.full) && w.q.nt > 0) store_state(w.q.nt - 1);
 }
 
 // The sequence of rank r by length, the longest first (up to 64 packed sequences; more, and sequences of
@@ -767,21 +780,23 @@ __device__ __forceinline__ int sc_ranked(const ScArgs& a, int r) {
 // Workgroup -> walk. Sequences of one length may be cut in a.nseg segments of a.seglen chunks (sc_segments),
 // number i along the walk's direction. seg_e[.., i]: where segment i's walk ends; seg_p[.., i]: its transition,
 // the end of a walk from the unit matrix. SUM: the walks that find those, of all segments but the last, each
-// from zero (the first from the sequence's own start), DV columns and for all but the first DK of the
-// transition. Else: the segments themselves, from the ends that k_sc_join has carried forward.
+// from zero (the first from the sequence's own start, and in full with a.lead), DV columns and for all but
+// the first DK of the transition. Else: the segments themselves (with a.lead, all but the first), from the ends
+// that k_sc_join has carried forward.
 template <class OT, int DK, int DV, int NC, bool BWD, bool SUM>
 __device__ __forceinline__ bool sc_walk_of(const ScArgs& a, const float* starts, float* ends, ScWalk& w) {
     constexpr int NJ = DV / (16 * NC), NJK = DK / (16 * NC);
-    const int nseg = SUM ? a.nseg - 1 : a.nseg;
+    const int count = a.nseg - (SUM ? 1 : a.lead);
     int p, j;
-    sc_chain_map(blockIdx.x, a.N * a.Hv * nseg, SUM ? NJ + NJK : NJ, p, j);
-    const int i = p % nseg, pair = p / nseg;
+    sc_chain_map(blockIdx.x, a.N * a.Hv * count, SUM ? NJ + NJK : NJ, !a.cu, p, j);
+    const int i = p % count + (SUM ? 0 : a.lead), pair = p / count;
     w.h = pair % a.Hv;
     w.hk = w.h / a.R;
     const int s = sc_ranked(a, pair / a.Hv);
     w.q = sc_seq(a.cu, a.T, s);
     w.unit = SUM && j >= NJ;
     if (w.unit && i == 0) return false;
+    w.full = !SUM || (i == 0 && a.lead);
     w.j = w.unit ? (j - NJ) % NJ : j;
     w.col = 16 * NC * (w.unit ? j - NJ : j);
     w.ld = w.unit ? DK : DV;
@@ -807,9 +822,8 @@ __device__ __forceinline__ bool sc_walk_of(const ScArgs& a, const float* starts,
 
 constexpr int SC_THREADS = 64 * (2 * SC_NC + SC_NP);
 
-template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT>
+template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT, bool SUM>
 __global__ __launch_bounds__(SC_THREADS) void k_sc_fwd_chain(ScArgs a) {
-    constexpr bool SUM = !TRAIN && !OUT;
     using B = ScChainLds<OT, DK, NC, false>;
     __shared__ __align__(16) char buf0[B::BYTES];
     __shared__ __align__(16) char buf1[B::BYTES];
@@ -825,9 +839,9 @@ __global__ __launch_bounds__(SC_THREADS) void k_sc_fwd_chain(ScArgs a) {
     if (wv < SC_NC)
         sc_fwd_walk<OT, DK, DV, NC, SUM>(a, w, wv, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
     else if (wv < 2 * SC_NC)
-        sc_fwd_side<OT, DK, DV, NC, TRAIN, OUT>(a, w, wv - SC_NC, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
+        sc_fwd_side<OT, DK, DV, NC, TRAIN, OUT, SUM>(a, w, wv - SC_NC, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
     else if (w.q.nt > 0)
-        sc_produce<OT, DK, DV, NC, false, OUT>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
+        sc_produce<OT, DK, DV, NC, false, OUT, SUM>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
 }
 
 template <class OT, int DK, int DV, int NC, bool SUM>
@@ -849,7 +863,7 @@ __global__ __launch_bounds__(SC_THREADS) void k_sc_bwd_chain(ScArgs a) {
     else if (wv < 2 * SC_NC)
         sc_bwd_side<OT, DK, DV, NC, SUM>(a, w, wv - SC_NC, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)xch);
     else if (w.q.nt > 0)
-        sc_produce<OT, DK, DV, NC, true, true>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
+        sc_produce<OT, DK, DV, NC, true, true, SUM>(a, w, (lds_char*)buf0, (lds_char*)buf1, (lds_char*)pfslot, wv - 2 * SC_NC);
 }
 
 // Carries the segments' ends forward: E_i += P_i E_(i - 1) for i = 1 .. nseg - 2, so that E_i is where segment
@@ -905,7 +919,8 @@ static hipError_t sc_column_tiles(const ScArgs& a, long long walks16, int& nc) {
     return e;
 }
 
-// The segments' ends, where there is more than one: summarise runs the SUM walks of nc column tiles.
+// The first segment and the others' ends, where there is more than one: summarise runs the SUM walks of nc
+// column tiles.
 template <int DK, int DV, class F>
 static hipError_t sc_segment_ends(const ScArgs& a, hipStream_t stream, F summarise) {
     if (a.nseg <= 1) return hipSuccess;
@@ -913,7 +928,7 @@ static hipError_t sc_segment_ends(const ScArgs& a, hipStream_t stream, F summari
     const int nc = tiles > 256 ? 2 : 1;
     summarise(nc, dim3((unsigned)(tiles / nc)));
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.nseg == 2) return e;
+    if (e != hipSuccess) return e;
     hipLaunchKernelGGL((k_sc_join<DK, DV>), dim3((unsigned)(a.N * a.Hv * (DV / 16))), dim3(4 * DK), 0, stream, a);
     return hipGetLastError();
 }
@@ -921,27 +936,30 @@ static hipError_t sc_segment_ends(const ScArgs& a, hipStream_t stream, F summari
 template <class OT, int DK, int DV>
 hipError_t launch_sc_fwd_chain_t(const ScArgs& a, bool train, hipStream_t stream) {
     int nc;
-    const long long walks = (long long)a.N * a.Hv * a.nseg * (DV / 16);
+    const long long walks = (long long)a.N * a.Hv * (a.nseg - a.lead) * (DV / 16);
     hipError_t e = sc_column_tiles(a, walks, nc);
     if (e != hipSuccess) return e;
+    auto pick2 = [&](auto n, auto sum) {
+        constexpr int NC = decltype(n)::value;
+        constexpr bool SUM = decltype(sum)::value;
+        return !train ? k_sc_fwd_chain<OT, DK, DV, NC, false, true, SUM>
+               : a.o  ? k_sc_fwd_chain<OT, DK, DV, NC, true, true, SUM> : k_sc_fwd_chain<OT, DK, DV, NC, true, false, SUM>;
+    };
+    auto pick = [&](int n, auto sum) {
+        return n == 2 ? pick2(std::integral_constant<int, 2>{}, sum) : pick2(std::integral_constant<int, 1>{}, sum);
+    };
     e = sc_segment_ends<DK, DV>(a, stream, [&](int n, dim3 grid) {
-        auto k = n == 2 ? k_sc_fwd_chain<OT, DK, DV, 2, false, false> : k_sc_fwd_chain<OT, DK, DV, 1, false, false>;
-        hipLaunchKernelGGL(k, grid, dim3(SC_THREADS), 0, stream, a);
+        hipLaunchKernelGGL(pick(n, std::true_type{}), grid, dim3(SC_THREADS), 0, stream, a);
     });
     if (e != hipSuccess) return e;
-    auto pick = [&](auto n) {
-        constexpr int NC = decltype(n)::value;
-        return !train ? k_sc_fwd_chain<OT, DK, DV, NC, false, true>
-               : a.o  ? k_sc_fwd_chain<OT, DK, DV, NC, true, true> : k_sc_fwd_chain<OT, DK, DV, NC, true, false>;
-    };
-    auto k = nc == 2 ? pick(std::integral_constant<int, 2>{}) : pick(std::integral_constant<int, 1>{});
+    auto k = pick(nc, std::false_type{});
     hipLaunchKernelGGL(k, dim3((unsigned)(walks / nc)), dim3(SC_THREADS), 0, stream, a);
     return hipGetLastError();
 }
 template <class OT, int DK, int DV>
 hipError_t launch_sc_bwd_chain_t(const ScArgs& a, hipStream_t stream) {
     int nc;
-    const long long walks = (long long)a.N * a.Hv * a.nseg * (DV / 16);
+    const long long walks = (long long)a.N * a.Hv * (a.nseg - a.lead) * (DV / 16);
     hipError_t e = sc_column_tiles(a, walks, nc);
     if (e != hipSuccess) return e;
     e = sc_segment_ends<DK, DV>(a, stream, [&](int n, dim3 grid) {

@@ -345,7 +345,8 @@ def test_many_chains(case):
     # few chains and long: whole, and cut in three to eight segments, the last ones ragged
     ([2100], 1, 1, 64, 64, F32), ([4133], 1, 2, 64, 64, F32), ([2050, 2050], 2, 2, 128, 128, BF),
     ([3300, 3300], 2, 2, 128, 128, BF),
-    ([4200], 1, 2, 128, 64, BF), ([5500], 1, 1, 64, 128, BF), ([8300], 1, 1, 64, 64, BF), ([4096], 4, 4, 128, 128, BF)])
+    ([4200], 1, 2, 128, 64, BF), ([5500], 1, 1, 64, 128, BF), ([8300], 1, 1, 64, 64, BF), ([4096], 4, 4, 128, 128, BF),
+    ([4160], 2, 8, 64, 128, BF), ([3300], 16, 16, 64, 64, F32)])
 @pytest.mark.parametrize("h0", [True, False])
 def test_long_sequences(case, h0):
     # weak decays and writes, so that what one segment leaves still counts in the next ones
@@ -354,8 +355,9 @@ def test_long_sequences(case, h0):
     check(train(x, cu), x, cu, dtype)
 
 
-def test_long_sequences_repeat_and_recompute():
-    x, _ = inputs([3300], False, 2, 4, 128, 64, BF, g_scale=0.001, beta_scale=0.1, seed=36)
+@pytest.mark.parametrize("hv", [4, 16])
+def test_long_sequences_repeat_and_recompute(hv):
+    x, _ = inputs([3300], False, 2, hv, 128, 64, BF, g_scale=0.001, beta_scale=0.1, seed=36)
     args = [x[n] for n in ("q", "k", "v", "g", "beta", "h0")]
     a, b = train(x, None), train(x, None)
     o, ht, _ = g2.gdr2_scalar_fwd(*args)
