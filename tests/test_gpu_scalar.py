@@ -369,6 +369,29 @@ def test_long_sequences_repeat_and_recompute(hv):
         assert torch.equal(a[n], c[n]), n
 
 
+@pytest.mark.parametrize("hv", [2, 16])
+def test_long_sequences_in_a_graph(hv):
+    # segments, found and joined in the workspace: nothing of it may count between calls
+    x, _ = inputs([3300], False, 2, hv, 64, 64, BF, g_scale=0.001, beta_scale=0.1, seed=37)
+    args = [x[n] for n in ("q", "k", "v", "g", "beta", "h0")]
+    want = train(x, None)
+    ws = torch.empty(g2.gdr2_scalar_workspace_bytes(1, 3300, 2, hv, 64, 64, save_for_bwd=True), dtype=torch.uint8,
+                     device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, ht, _ = g2.gdr2_scalar_fwd(*args, save_for_bwd=True, ws=ws)
+        gr = g2.gdr2_scalar_bwd(*args, x["do"], x["dht"], ws=ws, fwd_saved=True)
+    for _ in range(3):
+        for t in (o, ht, ws, *gr.values()):
+            t.fill_(3)
+        train(x, None)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for n, t in dict(gr, o=o, ht=ht).items():
+            assert torch.equal(t, want[n]), n
+
+
 def test_many_value_heads_of_a_key_head():
     x, cu = inputs([130], False, 2, 14, 64, 64, BF, seed=31)
     check(train(x, cu), x, cu, BF)
