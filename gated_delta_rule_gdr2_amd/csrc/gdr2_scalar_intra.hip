@@ -6,6 +6,13 @@
 
 namespace gdr2 {
 
+// A log-decay as it enters the running sum: e^-256 is zero in 32 bits (the smallest number there is e^-103),
+// so a stronger one says no more, and every decay across the token, gradients included, is the same exact
+// zero. Left as it is, -1e18 would take the digits of all later sums of its chunk, and two of the type's
+// lowest value would pass the range in which gam is kept (both gave wrong results and NaN). Each at -256 at
+// least, gam stays above -2^14. NaN passes through.
+__device__ __forceinline__ double log_decay(float g) { return g < -256.f ? -256.0 : (double)g; }
+
 // gam = running sum of g over the chunk's rows (lane = row), in 64 bits: the decays are exponentials
 // of differences of gam, and in 32 bits a strong decay early in the chunk (gam of some thousands)
 // would cost a later weak one its digits.
@@ -188,7 +195,7 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
     if (wv == 0) {
         const bool ok = l < nvalid;
         const size_t at = (size_t)(row0 + l) * a.Hv + h;
-        const double gam = wave_scan(ok ? (double)to_f(((const OT*)a.g)[at]) : 0.0);
+        const double gam = wave_scan(ok ? log_decay(to_f(((const OT*)a.g)[at])) : 0.0);
         const double gc = __shfl(gam, 63);
         const float hi = (float)gam, lo = (float)(gam - (double)hi);
         const float v[6] = {ok ? exp_op<OT>(hi) * (1.f + lo) : 0.f, ok ? to_f(((const OT*)a.beta)[at]) : 0.f,

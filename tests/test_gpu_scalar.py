@@ -119,6 +119,24 @@ def test_weak_decay_after_a_strong_one(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("at", [[5], [3, 40], [0, 1, 63, 64], list(range(20, 90))])
+@pytest.mark.parametrize("g", [-1000.0, -1e18, None])
+def test_decays_that_reset_the_state(dtype, at, g):
+    # a log-decay of any finite size, the type's lowest value among them (a usual mark of a new document):
+    # nothing of the state is left, and the weak decays behind it count as they would without it
+    x, cu = inputs([150], False, 1, 2, 64, 64, dtype, seed=41)
+    x["g"][:, at] = torch.finfo(dtype).min if g is None else g
+    got = train(x, cu)
+    check(got, x, cu, dtype)
+    # the recurrent step says the same: each is within its own bound of the exact result
+    state = x["h0"].clone()
+    o = g2.gdr2_scalar_step(*[x[n] for n in ("q", "k", "v", "g", "beta")], state)
+    tok, step = (2.0 ** -7, 2.0 ** -8) if dtype == BF else (1e-5, 1e-5)
+    assert ref.normwise(got["o"], o.cpu().double()) <= tok + step
+    assert ref.normwise(got["ht"], state.cpu().double()) <= 2e-5
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_repeated_keys_and_full_writes(dtype):
     # one key throughout and beta = 1: the powers of A grow like binomials, its inverse does not.
     # The corrections Delta_i = v_i - e^g v_(i-1) are sqrt(2) as large as a write and telescope to the
