@@ -306,7 +306,7 @@ struct ScGradLds {
     static constexpr int ROWP = HEAD + (MULTI ? 2 : 1) * REGION;  // per block pair: row and column sums of N
     static constexpr int COLP = ROWP + NPAIR * 16 * 4;
     static constexpr int DOTS = COLP + NPAIR * 16 * 4;  // per key tile and row: q.dq_s, k.dx_s, k.dk_s, k.G
-    static constexpr int DOTV = DOTS + 4 * KW * CH * 4; // per row: dY.v
+    static constexpr int DOTV = DOTS + 4 * KW * CH * 4; // per row: dY.Delta / beta, or dY.v
     static constexpr int SS = DOTV + CH * 4;            // per key tile: <dS', S>
     static constexpr int RED = SS + KW * 4;             // 6 sums a row
     static constexpr int BYTES = RED + 6 * CH * 4;
@@ -325,6 +325,13 @@ __device__ __forceinline__ void dma_rows_clamped(const OT* base, size_t rs, int 
     }
 }
 
+// dbeta = dY.(v - k^T X) with X the state before the token, decayed, and beta (v - k^T X) is Delta. The other
+// form, dY.v + k.G, is a difference of terms of the size of v: where the state already predicts v, as a trained
+// one does, the bf16 roundings of S and of the intermediates in G would stay at that size (normwise errors in
+// bf16 where v - k^T X is a tenth and a thirtieth of v: 1.2e-2 and 3.9e-2 against 2.6e-3 and less). It is left
+// for a beta so small that Delta, a product with it, would leave the normal numbers.
+__device__ __forceinline__ bool sc_dbeta_by_delta(float beta) { return fabsf(beta) >= 0x1p-32f; }
+
 // One workgroup of eight waves per (chunk slot, key head), each wave a 16-row tile of key channels
 // (two waves to a tile, half the tokens each, where d_k = 64): the gradients of the
 // group's value heads one after another, dq and dk summed over them in fp32 registers (value heads
@@ -334,7 +341,7 @@ __device__ __forceinline__ void dma_rows_clamped(const OT* base, size_t rs, int 
 //   dM = lower(dO Delta^T), dA = -strict(dY Delta^T), q k^T, k k^T in 16x16 block pairs, from which
 //   P = D dM, R = beta D dA and N = P q.k + R k.k, the derivative of every D_ri times D_ri
 //   dq = dq_s + P K,  G = dx_s + (R / beta) K,  dk = P^T Q + R^T K + beta G + dk_s
-//   dv = beta dY,  dbeta = dY.v + k.G
+//   dv = beta dY,  dbeta = dY.Delta / beta, or dY.v + k.G where beta is next to nothing (sc_dbeta_by_delta)
 //   dg_t = sum_{r >= t} (row_r - col_r of N + q.dq_s + beta k.dx_s) + sum_{i < t} k.dk_s + e^gamC <dS', S>
 // The last line sums only terms that carry the decay across t: the diagonal of N, which does not
 // depend on the decay, is left out, so that a strong decay leaves a small dg and no cancellation.
@@ -501,22 +508,24 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             load_s(h + 1);
         }
 
-        // ---- dv = beta dY and dY.v, 16 bytes of a row a lane
+        // ---- dv = beta dY and the row's part of dbeta, 16 bytes of a row a lane
 #pragma unroll
         for (int i = 0; i < NVL; ++i) {
             const int u = tid + NTHR * i, rr = u / LPR, col = EPC * (u % LPR);
             const VT y = lds_load<VT>(vDy.p + vDy.off(rr, col));
+            const VT del = lds_load<VT>(vDel.p + vDel.off(rr, col));
             const float b = lds_load<float>(hd + LS::VEC + (SC_BETA + rr) * 4);
+            const bool by_delta = sc_dbeta_by_delta(b);
             float s = 0.f;
             VT d;
 #pragma unroll
             for (int j = 0; j < EPC; ++j) {
-                s += to_f(y[j]) * to_f(gv[i][j]);
+                s += to_f(y[j]) * to_f(by_delta ? del[j] : gv[i][j]);
                 d[j] = to_ot<OT>(b * to_f(y[j]));
             }
             if (rr < nvalid) *(VT*)((OT*)a.dv + v0 + rr * rsv + col) = d;
             s = LPR == 16 ? row_sum16(s) : row_sum8(s);
-            if (u % LPR == 0) lds_store<float>(sm + LS::DOTV + rr * 4, s);
+            if (u % LPR == 0) lds_store<float>(sm + LS::DOTV + rr * 4, by_delta ? s / b : s);
         }
         if (more) load_v(h + 1);
         __builtin_amdgcn_sched_barrier(0);
@@ -680,7 +689,8 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
         // ---- dbeta and dg
         if (wv == 0) {
             auto red = [&](int t) { return lds_load<float>(sm + LS::RED + (t * CH + l) * 4); };
-            const float x = red(0) + lds_load<float>(hd + LS::VEC + (SC_BETA + l) * 4) * red(1) + red(4);
+            const float b = lds_load<float>(hd + LS::VEC + (SC_BETA + l) * 4);
+            const float x = red(0) + b * red(1) + red(4);
             // suffix sum of x, exclusive prefix sum of k.dk_s: inside the 16 lanes of a row, then over rows
             float suf = row_suffix16(x), pre = row_scan16(red(2));
             const float s1 = lane_value(suf, 16), s2 = lane_value(suf, 32), s3 = lane_value(suf, 48);
@@ -690,7 +700,7 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             pre += l < 16 ? 0.f : l < 32 ? p0 : l < 48 ? p0 + p1 : (p0 + p1) + p2;
             if (l < nvalid) {
                 const size_t at = (size_t)(row0 + l) * a.Hv + h;
-                ((OT*)a.dbeta)[at] = to_ot<OT>(lds_load<float>(sm + LS::DOTV + l * 4) + red(3));
+                ((OT*)a.dbeta)[at] = to_ot<OT>(lds_load<float>(sm + LS::DOTV + l * 4) + (sc_dbeta_by_delta(b) ? 0.f : red(3)));
                 ((OT*)a.dg)[at] = to_ot<OT>(suf + pre + lds_load<float>(hd + LS::VEC + SC_EC * 4) * red(5));
             }
         }

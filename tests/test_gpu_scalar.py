@@ -156,6 +156,38 @@ def test_write_strength_two_and_zero():
     check(train(x, cu), x, cu, F32)
 
 
+@pytest.mark.parametrize("noise", [0.1, 0.03])
+@pytest.mark.parametrize("case", [(130, 1, 2, 64, 64, F32), (130, 1, 2, 64, 64, BF), (200, 2, 2, 128, 128, BF),
+                                  (130, 1, 4, 128, 64, BF)])
+def test_gradients_where_the_state_predicts_the_values(case, noise):
+    # v = what the state holds for k, and a little noise: dbeta = dY.(v - k^T X) is small against dY.v
+    T, hk, hv, dk, dv, dtype = case
+    x, _ = inputs([T], False, hk, hv, dk, dv, dtype, g_scale=0.01, seed=42)
+    gen = torch.Generator().manual_seed(42)
+    rnd = lambda *s: torch.randn(*s, generator=gen, dtype=torch.float64)
+    S = rnd(hv, dk, dv).float().double()
+    x["h0"] = S[None].float().cuda()
+    k, g, beta = (ref.sequences(x[n], None)[0] for n in ("k", "g", "beta"))
+    k = k.repeat_interleave(hv // hk, 1)
+    v = torch.empty(T, hv, dv, dtype=torch.float64)
+    for t in range(T):
+        X = S * torch.exp(g[t])[:, None, None]
+        seen = (k[t][:, :, None] * X).sum(1)
+        v[t] = (seen + noise * rnd(hv, dv)).to(dtype).double()
+        S = X + k[t][:, :, None] * (beta[t][:, None] * (v[t] - seen))[:, None, :]
+    x["v"] = v[None].to(dtype).cuda()
+    check(train(x, None), x, None, dtype)
+
+
+@pytest.mark.parametrize("beta", [0.0, 1e-30, 1e-12, 1e-8])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_write_strengths_next_to_nothing(dtype, beta):
+    x, cu = inputs([130], False, 1, 2, 64, 64, dtype, seed=43)
+    x["beta"][:, ::3] = beta
+    x["beta"][:, 1::5] = -0.25
+    check(train(x, cu), x, cu, dtype)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_inference_forward_recompute_and_repeats(dtype):
     x, cu = inputs([100, 64, 7], True, 2, 4, 64, 64, dtype, seed=9)
