@@ -432,6 +432,13 @@ def _launch(f, dev, stream, *args):
     return f(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
 
 
+def _zero(stream, *tensors):
+    """Sets tensors to zero on the stream that the call's kernels would run on."""
+    with torch.cuda.stream(stream):  # None: the current one
+        for t in tensors:
+            t.zero_()
+
+
 def _scalar_dims(q, k, v, g, beta, cu_seqlens):
     if cu_seqlens is None:  # what is as it should be is found so by one expression, at half the cost
         qs, vs, t, dev = q.shape, v.shape, q.dtype, q.get_device()
@@ -502,9 +509,9 @@ def gdr2_scalar_fwd(q, k, v, g, beta, h0=None, *, cu_seqlens=None, save_for_bwd=
         new.append(ws)
     else:
         _want(ws, "ws", torch.uint8, ws.shape, dev)
-    if own_o and N == 0:
-        o.zero_()  # no sequence, and no kernel
     _keep_for(stream, *new)
+    if own_o and N == 0:
+        _zero(stream, o)  # no sequence, and no kernel
     st = _launch(lib.gdr2_scalar_fwd, dev, stream, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0),
                  _adr(cu_seqlens), _adr(o), _adr(ht), N, T, Hk, Hv, dk, dv, dt, int(own_o), int(bool(save_for_bwd)),
                  _adr(ws), ws.numel())
@@ -544,10 +551,9 @@ def gdr2_scalar_bwd(q, k, v, g, beta, h0, dout, dht=None, *, cu_seqlens=None, ws
         new.append(ws)
     else:
         _want(ws, "ws", torch.uint8, ws.shape, dev)
-    if own and N == 0:
-        for n, _ in names:
-            grads[n].zero_()
     _keep_for(stream, *new)
+    if own and N == 0:
+        _zero(stream, *(grads[n] for n, _ in names))
     st = _launch(lib.gdr2_scalar_bwd, dev, stream, _adr(q), _adr(k), _adr(v), _adr(g), _adr(beta), _adr(h0),
                  _adr(dout), _adr(dht), _adr(cu_seqlens), _adr(grads["dq"]), _adr(grads["dk"]), _adr(grads["dv"]),
                  _adr(grads["dg"]), _adr(grads["dbeta"]), _adr(grads["dh0"]), N, T, Hk, Hv, dk, dv, dt, int(own),

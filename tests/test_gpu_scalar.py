@@ -279,6 +279,25 @@ def test_no_tokens():
     assert (o == 0).all() and ht.shape[0] == 0
 
 
+def test_no_sequences_on_another_stream():
+    # the zeros are written on the stream that was asked for, not on one that is busy with other work
+    x, _ = inputs([4000], True, 1, 3, 64, 64, BF, h0=False)
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    a = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    busy, s = torch.randn(8192, 8192, device="cuda"), torch.cuda.Stream()
+    marks = [torch.full_like(x[n], 7.0) for n in ("q", "k", "v", "v", "g", "beta")]
+    torch.cuda.synchronize()
+    del marks  # their memory is what the outputs are likely to get
+    for _ in range(4):
+        busy @ busy
+    o, _, _ = g2.gdr2_scalar_fwd(*a, cu_seqlens=cu, stream=s)
+    gr = g2.gdr2_scalar_bwd(*a, None, x["do"], cu_seqlens=cu, stream=s)
+    with torch.cuda.stream(s):
+        got = [t.cpu() for t in (o, *(gr[n] for n in TOK[1:]))]
+    torch.cuda.synchronize()
+    assert all((t == 0).all() for t in got)
+
+
 def test_gradients_against_differences():
     x, cu = inputs([70], False, 1, 2, 64, 64, F32, seed=14)
     got = train(x, cu)
