@@ -33,9 +33,8 @@
 namespace gdr2 {
 
 template <class OT>
-constexpr int attn_unit() { return sizeof(OT) == 2 ? 32 : 16; }
+constexpr int attn_unit() { return attn_unit_tokens(sizeof(OT) == 2); }
 constexpr int AW = 8;           // waves of a workgroup
-constexpr int ATTN_COST = 6;    // of a row, in units: its own loads and its waves' join
 constexpr int ATTN_MIN = 14;    // places of the line a workgroup takes at least (ATTN_COST + a unit for each wave)
 
 // The visible tokens of sequence b and its units (at least one, so that every row is written).
@@ -488,11 +487,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 //   8 of 1000                 18.4 and 16.7       32 of 1000  20.8 and 22.9    32 of 2048   40.1 and 36.2
 //   200 of 500                53.3 and 56.8      200 of 2048 174.7 and 162.5  200 of 4096  340.4 and 305.3
 // (the last 5.5 TB/s; long rows one a workgroup leave compute units idle at the end).
-inline bool attn_rows_mode(const AttnArgs& a, int unit) {
-    long long tokens = (long long)a.c.max_pages << a.c.shift;
-    if (a.window > 0 && a.window < tokens) tokens = (long long)a.window + unit;  // a window may begin inside a unit
-    return (tokens + unit - 1) / unit <= 4 * AW;
-}
+inline bool attn_rows_mode(const AttnArgs& a, int unit) { return attn_max_units(a.c, a.window, unit) <= 4 * AW; }
 
 template <class OT, int D>
 static hipError_t launch_attn_t(const AttnArgs& a, hipStream_t stream) {

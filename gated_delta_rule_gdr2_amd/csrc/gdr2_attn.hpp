@@ -37,6 +37,21 @@ struct AppendArgs {
 };
 
 constexpr int ATTN_WGS = 256;  // one workgroup of eight waves on each of the 256 compute units
+constexpr int ATTN_COST = 6;   // of a row, in units: its own loads and its waves' join
+
+// Tokens of a unit, the piece that a wave takes at a time, and the units that a row has at most, by its table
+// or its window (which may begin inside a unit).
+constexpr int attn_unit_tokens(bool bf16) { return bf16 ? 32 : 16; }
+inline long long attn_max_units(const Cache& c, int window, int unit) {
+    long long tokens = (long long)c.max_pages << c.shift;
+    if (window > 0 && window < tokens) tokens = (long long)window + unit;
+    return (tokens + unit - 1) / unit;
+}
+// The most places that the line of all rows can have (gdr2_attn.hip); an empty row has a unit too.
+inline long long attn_line_places(const AttnArgs& a, int unit) {
+    const long long units = attn_max_units(a.c, a.window, unit);
+    return (long long)a.B * a.Hkv * a.NG * ((units > 0 ? units : 1) + ATTN_COST);
+}
 
 // floats of one partial result: gh rows of D sums, then their maxima and weights (padded to 16 bytes)
 inline size_t attn_part_floats(int gh, int D) { return (size_t)gh * (D + 4); }

@@ -226,13 +226,8 @@ int gdr2_attn_step(const void* q, const void* k_cache, const void* v_cache, cons
     if (st != GDR2_OK) return st;
     if (!q || !o || !lengths) return GDR2_ERR_NULL;
     if (!isfinite(scale) || window < 0) return GDR2_ERR_VALUE;
-    // token numbers, and those of the units of all rows (of 16 tokens, and a few more places a row), fit in 32
-    // bits
+    // token numbers, and the places of all rows' units, fit in 32 bits
     if ((long long)max_pages * page_size > 0x7fffffffLL - 64) return GDR2_ERR_SHAPE;
-    if ((long long)B * Hq * (((long long)max_pages * page_size >> 4) + 16) > 0x7fffffffLL) return GDR2_ERR_SHAPE;
-    const void* const ptrs[] = {q, k_cache, v_cache, o, workspace};
-    if (!all_aligned(ptrs)) return GDR2_ERR_ALIGN;
-    if (!workspace || workspace_bytes < gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dtype)) return GDR2_ERR_WORKSPACE;
     gdr2::AttnArgs a = {};
     a.q = q; a.o = o; a.lse = lse; a.lengths = lengths;
     a.part = (float*)workspace;
@@ -244,6 +239,11 @@ int gdr2_attn_step(const void* q, const void* k_cache, const void* v_cache, cons
     a.window = window;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     a.wgs = gdr2::ATTN_WGS;
+    if (gdr2::attn_line_places(a, gdr2::attn_unit_tokens(dtype == GDR2_DTYPE_BF16)) > 0x7fffffffLL)
+        return GDR2_ERR_SHAPE;
+    const void* const ptrs[] = {q, k_cache, v_cache, o, workspace};
+    if (!all_aligned(ptrs)) return GDR2_ERR_ALIGN;
+    if (!workspace || workspace_bytes < gdr2_attn_workspace_bytes(B, Hq, Hkv, D, dtype)) return GDR2_ERR_WORKSPACE;
     return gdr2::launch_attn(a, dtype == GDR2_DTYPE_BF16, (hipStream_t)stream) == hipSuccess ? GDR2_OK : GDR2_ERR_HIP;
 }
 

@@ -291,8 +291,9 @@ int gdr2_scalar_step(const void* q, const void* k, const void* v, const void* g,
  *   lengths : int32 [B] on the device, tokens held; taken as 0 .. max_pages page_size where outside
  * page_size is a power of two from 16 on (else GDR2_ERR_VALUE), D 64 or 128, dtype BF16 or F32. A row
  * with nothing visible gets o = 0 and lse = -inf. What the cache holds in masked or unused places,
- * infinities and NaN included, does not matter. max_pages page_size of 2^31 - 64 and more returns
- * GDR2_ERR_SHAPE. o must not overlap q. Scores, weights' sums and lse are fp32; with bf16 the
+ * infinities and NaN included, does not matter. GDR2_ERR_SHAPE: max_pages page_size of more than
+ * 2^31 - 65, or more than 2^31 - 1 places of B Hkv ceil(Hq / Hkv / 16) rows, each of which takes 6 and one for
+ * every 32 tokens (fp32: 16) of the table, or of the window and 32 (16) more where that is less. o must not overlap q. Scores, weights' sums and lse are fp32; with bf16 the
  * weights enter the second product as bf16. Results do not depend on the other rows of the call beyond
  * the order of fp32 sums, and are repeatable bit for bit. Workspace: gdr2_attn_workspace_bytes, of no
  * content between calls; calls that may overlap need one each. */

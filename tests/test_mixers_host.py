@@ -180,6 +180,20 @@ def test_token_numbers_fit_in_32_bits(lib):
     assert attn(lib, page=1 << 20, max_pages=2048) == SHAPE
 
 
+def test_long_tables_of_many_rows(lib):
+    # as many places as the line of rows can number, and one row more
+    past = lambda **kw: attn(lib, page=1024, strides=(1 << 20, 128, 64) * 2, ws_bytes=0, **kw)
+    assert past(B=512, Hq=64, Hkv=8, max_pages=1024) == WS   # 4096 rows of 2^20 tokens
+    assert past(B=2048, Hq=64, Hkv=8, max_pages=256) == WS
+    rows = (2 ** 31 - 1) // (2 ** 15 + 6)
+    assert past(B=rows, Hq=16, Hkv=1, max_pages=1024) == WS
+    assert past(B=rows + 1, Hq=16, Hkv=1, max_pages=1024) == SHAPE
+    assert past(B=rows // 2 + 1, Hq=17, Hkv=1, max_pages=1024) == SHAPE  # two groups of heads
+    assert past(B=rows, Hq=1, Hkv=1, max_pages=1024, dtype=F32) == SHAPE  # units of 16 tokens
+    assert past(B=rows + 1, Hq=1, Hkv=1, max_pages=1024, window=5000) == WS  # what the window leaves of them
+    assert past(B=2 ** 31 // 7, Hq=1, Hkv=1, max_pages=0) == WS and past(B=2 ** 31 // 7 + 1, Hq=1, max_pages=0) == SHAPE
+
+
 def test_marks_of_leaves_live_as_long_as_their_graphs():
     import torch
     a, b = torch.randn(3, requires_grad=True), torch.randn(3)
