@@ -486,8 +486,12 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
 //   1 sequence of 100 tokens   4.7 and 11.7 us     1 of 777   11.4 and 13.8     1 of 2048   22.4 and 14.0
 //   8 of 1000                 18.4 and 16.7       32 of 1000  20.8 and 22.9    32 of 2048   40.1 and 36.2
 //   200 of 500                53.3 and 56.8      200 of 2048 174.7 and 162.5  200 of 4096  340.4 and 305.3
-// (the last 5.5 TB/s; long rows one a workgroup leave compute units idle at the end).
-inline bool attn_rows_mode(const AttnArgs& a, int unit) { return attn_max_units(a.c, a.window, unit) <= 4 * AW; }
+// (the last 5.5 TB/s; long rows one a workgroup leave compute units idle at the end). A launch takes fewer than
+// 2^32 threads: 2^23 rows and more go to the line.
+inline bool attn_rows_mode(const AttnArgs& a, int unit) {
+    const long long rows = (long long)a.B * a.Hkv * a.NG;
+    return attn_max_units(a.c, a.window, unit) <= 4 * AW && rows < (1LL << 32) / (64 * AW);
+}
 
 template <class OT, int D>
 static hipError_t launch_attn_t(const AttnArgs& a, hipStream_t stream) {

@@ -36,6 +36,9 @@ bool sc_supported(int dk, int dv, int dtype) {
     return dtype == GDR2_DTYPE_F32 && dk == 64 && dv == 64;
 }
 
+// a launch takes fewer than 2^32 threads
+bool grid_fits(long long groups, int threads) { return groups < (1LL << 32) / threads; }
+
 // chunk slots: one per chunk, packed also up to one spare per sequence
 long long sc_slots(int N, int T, bool packed) {
     return packed ? (long long)T / 64 + N : (long long)N * (((long long)T + 63) / 64);
@@ -46,11 +49,20 @@ int sc_shape(int N, int T, int Hk, int Hv, int dk, int dv, int dtype, bool packe
     if (!sc_supported(dk, dv, dtype)) return GDR2_ERR_UNSUPPORTED;
     if (Hk == 0 ? Hv != 0 : Hv == 0 || Hv % Hk != 0) return GDR2_ERR_SHAPE;
     const long long tokens = packed ? T : (long long)N * T;
-    // the grids (slots x key heads, sequences x value heads x slices) and token rows fit in 32 bits
+    // token rows and (sequence, value head, slice)s fit in 32 bits
     if (tokens > 0x7fffffffLL - 64 || (tokens * Hv) > (1LL << 40)) return GDR2_ERR_SHAPE;
-    if (sc_slots(N, T, packed) * (Hv > Hk ? Hv : Hk) > 0x7fffffffLL) return GDR2_ERR_SHAPE;
     if ((long long)N * Hv * (dv / 16) > 0x7fffffffLL) return GDR2_ERR_SHAPE;
     return GDR2_OK;
+}
+
+// ... and for the chunkwise kernels: preparation, gradients and chains (of many walks, two column tiles each)
+int sc_chunk_shape(int N, int T, int Hk, int Hv, int dk, int dv, int dtype, bool packed) {
+    const int st = sc_shape(N, T, Hk, Hv, dk, dv, dtype, packed);
+    if (st != GDR2_OK) return st;
+    const long long slots = sc_slots(N, T, packed);
+    return slots * Hv <= 0x7fffffffLL && grid_fits(slots * Hv, 256) && grid_fits(slots * Hk, 512) &&
+                   grid_fits((long long)N * Hv * (dv / 32), gdr2::SC_CHAIN_THREADS)
+               ? GDR2_OK : GDR2_ERR_SHAPE;
 }
 
 bool sc_no_tokens(int N, int T, int Hv) { return N == 0 || T == 0 || Hv == 0; }
@@ -129,7 +141,7 @@ extern "C" {
 
 size_t gdr2_scalar_workspace_bytes(int N, int T, int Hk, int Hv, int dk, int dv, int packed, int dtype,
                                    int save_for_bwd) {
-    if (sc_shape(N, T, Hk, Hv, dk, dv, dtype, packed != 0) != GDR2_OK || sc_no_tokens(N, T, Hv)) return 0;
+    if (sc_chunk_shape(N, T, Hk, Hv, dk, dv, dtype, packed != 0) != GDR2_OK || sc_no_tokens(N, T, Hv)) return 0;
     const gdr2::ScLayout L = sc_layout_for(N, T, Hv, dk, dv, dtype, packed != 0);
     return save_for_bwd ? L.train_bytes : L.infer_bytes;
 }
@@ -139,7 +151,7 @@ int gdr2_scalar_fwd(const void* q, const void* k, const void* v, const void* g, 
                     int dtype, int zero_rest, int save_for_bwd, void* workspace, size_t workspace_bytes,
                     void* stream) {
     const bool packed = cu_seqlens != nullptr;
-    const int st = sc_shape(N, T, Hk, Hv, dk, dv, dtype, packed);
+    const int st = sc_chunk_shape(N, T, Hk, Hv, dk, dv, dtype, packed);
     if (st != GDR2_OK) return st;
     const bool none = sc_no_tokens(N, T, Hv);
     if (!none && (!q || !k || !v || !g || !beta || !o)) return GDR2_ERR_NULL;
@@ -163,7 +175,7 @@ int gdr2_scalar_bwd(const void* q, const void* k, const void* v, const void* g, 
                     void* dg, void* dbeta, float* dh0, int N, int T, int Hk, int Hv, int dk, int dv, int dtype,
                     int zero_rest, int fwd_saved, void* workspace, size_t workspace_bytes, void* stream) {
     const bool packed = cu_seqlens != nullptr;
-    const int st = sc_shape(N, T, Hk, Hv, dk, dv, dtype, packed);
+    const int st = sc_chunk_shape(N, T, Hk, Hv, dk, dv, dtype, packed);
     if (st != GDR2_OK) return st;
     const bool none = sc_no_tokens(N, T, Hv);
     if (!none && (!q || !k || !v || !g || !beta || !dout || !dq || !dk_ || !dv_ || !dg || !dbeta))
@@ -191,6 +203,7 @@ int gdr2_scalar_step(const void* q, const void* k, const void* v, const void* g,
                      void* stream) {
     const int st = sc_shape(B, T, Hk, Hv, dk, dv, dtype, false);
     if (st != GDR2_OK) return st;
+    if (!grid_fits((long long)B * Hv * (dv / 64), 128)) return GDR2_ERR_SHAPE;
     if (n_states < 0 || (!slots && n_states < B)) return GDR2_ERR_SHAPE;
     const bool none = sc_no_tokens(B, T, Hv);
     if (!none && (!q || !k || !v || !g || !beta || !o)) return GDR2_ERR_NULL;
@@ -254,7 +267,7 @@ int gdr2_kv_append(const void* k, const void* v, void* k_cache, void* v_cache, c
     if (st != GDR2_OK) return st;
     if (tokens < 0 || (!cu_seqlens && tokens != B)) return GDR2_ERR_SHAPE;
     if (B == 0 || tokens == 0 || Hkv == 0) return GDR2_OK;
-    if ((long long)tokens * Hkv * (D / (16 / esize(dtype))) > 0x7fffffffLL * 256) return GDR2_ERR_SHAPE;
+    if ((long long)tokens * Hkv >= (1LL << 32) / (D / (16 / esize(dtype)))) return GDR2_ERR_SHAPE;  // a thread each
     st = cache_check(k_cache, v_cache, cache_strides, block_table, B, num_pages, page_size, max_pages, esize(dtype));
     if (st != GDR2_OK) return st;
     if (!k || !v || !starts) return GDR2_ERR_NULL;

@@ -48,6 +48,8 @@ __host__ __device__ constexpr bool sc_img_zero(int rt, int kb) { return TR ? rt 
 
 constexpr int SC_E = 0, SC_BETA = 64, SC_TAIL = 128, SC_GHI = 192, SC_GLO = 256, SC_EC = 320, SC_VEC = 384;
 
+constexpr int SC_CHAIN_THREADS = 640;  // of a chain's workgroup: four compute, four side and two producer waves
+
 // segs: segments of all (sequence, value head)s together, 0 where chains are whole
 inline ScLayout sc_layout(long long ids, long long segs, int DK, int DV, int esz) {
     ScLayout L;

@@ -821,6 +821,7 @@ __device__ __forceinline__ bool sc_walk_of(const ScArgs& a, const float* starts,
 }
 
 constexpr int SC_THREADS = 64 * (2 * SC_NC + SC_NP);
+static_assert(SC_THREADS == SC_CHAIN_THREADS, "as the host counts them");
 
 template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT, bool SUM>
 __global__ __launch_bounds__(SC_THREADS) void k_sc_fwd_chain(ScArgs a) {

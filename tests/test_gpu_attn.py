@@ -227,6 +227,25 @@ def test_offsets_past_32_bits():
         assert torch.equal(a, b)
 
 
+def test_more_rows_than_a_launch_takes_workgroups():
+    # 2^23 rows and some: short rows, but one launch of a workgroup each would pass 2^32 threads
+    B, H, D = 2 ** 19 + 3, 16, 64
+    lens = {0: 5, 77: 16, B // 2: 31, B - 1: 1}
+    q, kc, vc, table, _, _ = make(list(lens.values()), H, H, D, 16, BF, seed=20, width=2)
+    wide = torch.zeros(B, H, D, dtype=BF, device="cuda")
+    dev = torch.full((B, 2), -1, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
+    rows = torch.tensor(list(lens), device="cuda")
+    wide[rows], dev[rows] = q, torch.tensor(table, dtype=torch.int32).cuda()
+    lengths[rows] = torch.tensor(list(lens.values()), dtype=torch.int32).cuda()
+    o, lse = g2.gdr2_attn_step(wide, kc, vc, dev, lengths, return_lse=True)
+    wo, wl = ref.attention(q, kc, vc, table, list(lens.values()), D ** -0.5, 0)
+    assert ref.normwise(o[rows], wo) <= TOL[BF] and (lse[rows].cpu().double() - wl).abs().max() <= 1e-5 * wl.abs().max()
+    empty = torch.ones(B, dtype=torch.bool, device="cuda")
+    empty[rows] = False
+    assert not o[empty].any() and (lse[empty] == -float("inf")).all()
+
+
 def test_windows_past_32_bits():
     q, kc, vc, table, dev, lengths = make([40], 2, 2, 64, 16, BF, seed=18)
     assert torch.equal(g2.gdr2_attn_step(q, kc, vc, dev, lengths, window=2 ** 32 + 5),

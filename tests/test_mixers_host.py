@@ -194,6 +194,22 @@ def test_long_tables_of_many_rows(lib):
     assert past(B=2 ** 31 // 7, Hq=1, Hkv=1, max_pages=0) == WS and past(B=2 ** 31 // 7 + 1, Hq=1, max_pages=0) == SHAPE
 
 
+def test_launches_fit_in_32_bits_of_threads(lib):
+    # past that a launch fails, after earlier ones of the same call perhaps: such sizes are refused before any
+    odd = FAKE + 8  # not aligned: the next refusal, so that no call here gets as far as a launch
+    pieces = lambda n, **kw: append(lib, k=odd, cu=FAKE, tokens=n, Hkv=8, D=128, **kw)
+    assert pieces(2 ** 25 - 1) == ALIGN and pieces(2 ** 25) == SHAPE           # 128 pieces of 16 bytes a token
+    assert pieces(2 ** 24 - 1, dtype=F32) == ALIGN and pieces(2 ** 24, dtype=F32) == SHAPE
+    assert append(lib, cu=FAKE, tokens=2 ** 31 - 1, Hkv=2 ** 31 - 1, D=128) == SHAPE
+    rows = lambda b: step(lib, [odd] + [FAKE] * 6, B=b, dk=128, dv=128, states=1)
+    assert rows(2 ** 24 - 1) == ALIGN and rows(2 ** 24) == SHAPE               # two workgroups of 128 threads a row
+    for bwd in (False, True):
+        chains = lambda n, **kw: scalar(lib, bwd, N=n, T=1, dk=128, dv=128, ws=0, **kw)
+        most = 2 ** 32 // 640 // 4                                             # four workgroups of 640 threads
+        assert chains(most - 1) == WS and chains(most + 1) == SHAPE
+    assert g2.gdr2_scalar_workspace_bytes(2 ** 32 // 640 // 4 + 1, 1, 1, 1, 128, 128) == 0
+
+
 def test_marks_of_leaves_live_as_long_as_their_graphs():
     import torch
     a, b = torch.randn(3, requires_grad=True), torch.randn(3)
