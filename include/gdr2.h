@@ -294,7 +294,7 @@ int gdr2_scalar_step(const void* q, const void* k, const void* v, const void* g,
  * infinities and NaN included, does not matter. GDR2_ERR_SHAPE: max_pages page_size of more than
  * 2^31 - 65, or more than 2^31 - 1 places of B Hkv ceil(Hq / Hkv / 16) rows, each of which takes 6 and one for
  * every 32 tokens (fp32: 16) of the table, or of the window and 32 (16) more where that is less. o must not overlap q. Scores, weights' sums and lse are fp32; with bf16 the
- * weights enter the second product as bf16. Results do not depend on the other rows of the call beyond
+ * weights enter the second product in two bf16 parts, 16 bits together. Results do not depend on the other rows of the call beyond
  * the order of fp32 sums, and are repeatable bit for bit. Workspace: gdr2_attn_workspace_bytes, of no
  * content between calls; calls that may overlap need one each. */
 size_t gdr2_attn_workspace_bytes(int B, int Hq, int Hkv, int D, int dtype);

@@ -109,6 +109,22 @@ def test_large_scores(dtype):
     assert ref.normwise(o, wo) <= tol and (lse.cpu().double() - wl).abs().max() <= 1e-5 * wl.abs().max()
 
 
+@pytest.mark.parametrize("lens", [[2], [3], [40, 7], [777], [4000]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_keep_their_digits(lens, D):
+    # bf16: every element of o is off by its own rounding, 2^-8 of it, and by what the weights are off by:
+    # a score by up to 2^-24 (D + 3) |q||k| scale, in the weight and in the sum of the weights, and a weight
+    # held in two bf16 parts by 2^-17 and less of it, with 2^-20 for the sums; that of sum p |v| / sum p
+    q, kc, vc, table, dev, lengths = make(lens, 4, 2, D, 64, BF, seed=50)
+    o = g2.gdr2_attn_step(q, kc, vc, dev, lengths)
+    wo, _ = ref.attention(q, kc, vc, table, lens, D ** -0.5, 0)
+    size, _ = ref.attention(q, kc, vc.abs(), table, lens, D ** -0.5, 0)
+    kn = torch.where(torch.isnan(kc), torch.zeros_like(kc), kc).double().norm(dim=-1).max()
+    score = 2.0 ** -24 * (D + 3) * float(q.double().norm(dim=-1).max() * kn) * D ** -0.5
+    room = 2.0 ** -8 * wo.abs() + (2 * score + 2.0 ** -17 + 2.0 ** -20) * size * (1 + 2.0 ** -8)
+    assert ((o.cpu().double() - wo).abs() <= room).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_pages_that_are_none(dtype):
     # holes in the table, ids past the pool, lengths past the table and below zero
