@@ -435,7 +435,10 @@ __device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk& w, in
 
 // The 16-column slice [rows][16] of an exchanged matrix of 16 RT rows (its fragments' first parts, from
 // frag on) to the workspace, by the four side waves: read while the exchange holds it, stored later, since
-// a wave waits where it issues a store and the others then wait for it at the next barrier.
+// a wave waits where it issues a store and the others then wait for it at the next barrier. What is saved for
+// the gradients (S, dS', Delta, dY) is one bf16 each: the gradients end in bf16, off by 2 to 3e-3, and a second
+// part would add half as much again to the 208 KB a chunk and head that their kernel waits for. The chains
+// themselves carry both parts on.
 template <class OT, int RT>
 struct Slice {
     static constexpr int N = sizeof(OT) == 2 ? (RT + 3) / 4 : 2;
@@ -468,7 +471,10 @@ struct Slice {
     }
 };
 
-// Side waves: what a step gives away -- O, and for training the chunk's start state and Delta.
+// Side waves: what a step gives away -- O, and for training the chunk's start state and Delta. In bf16 O takes
+// the first parts of S and Delta, and M in one part: nothing is carried on from it, and it is rounded to bf16
+// itself. It is off by 2.4e-3 (its own rounding 1.7e-3). With both parts of all three it was off by 1.65e-3, and
+// a prompt of 16384 tokens took 357 us instead of 322, a training step of 2 x 4096 345 instead of 331.
 template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT, bool SUM>
 __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, int wv, const lds_char* b0,
                                             const lds_char* b1, const lds_char* xs) {
@@ -762,9 +768,11 @@ __device__ __forceinline__ void sc_bwd_side(const ScArgs& a, const ScWalk& w, in
     if ((!SUM || w.full) && w.q.nt > 0) store_state(w.q.nt - 1);
 }
 
-// The sequence of rank r by length, the longest first (up to 64 packed sequences; more, and sequences of
-// one length, are taken as they come): a long one started last would run on alone. Measured, 9 sequences of
-// 103 to 4000 tokens, 16 heads of 128: 115 us forward, 124 backward; as they come 144 and 156.
+// The sequence of rank r by length, the longest first (up to 64 packed sequences, one to a lane; more, and
+// sequences of one length, are taken as they come): a long one started last would run on alone. Measured, 9
+// sequences of 103 to 4000 tokens, 16 heads of 128: 115 us forward, 124 backward; as they come 144 and 156. What
+// more than 64 lose by their order, forward, as they come and handed in longest first: 100 sequences of 20 to
+// 2600 tokens, 4 heads of 128: 230 and 200 us, 16 heads 761 and 751; 300 sequences, 4 heads 595 and 545.
 __device__ __forceinline__ int sc_ranked(const ScArgs& a, int r) {
     if (!a.cu || a.N > 64) return r;
     const int l = lane_id();
@@ -908,10 +916,15 @@ __global__ __launch_bounds__(4 * DK) void k_sc_join(ScArgs a) {
 
 // Column tiles a workgroup: with at most one 16-column walk for each compute unit, one; with two or more,
 // walks queue, and two tiles to a workgroup share its operands, its barriers and their latencies (a step
-// takes 1.4 times as long for twice the columns). Packed sequences may be uneven, and then the longest
-// walk, not their sum, sets the time: two tiles only from five walks a compute unit on. Measured, forward
-// chain: 24 sequences of 18 to 700 tokens, 6 walks a unit: 30 us with two tiles, 44 with one; 9 sequences
-// of 103 to 4000 tokens, 4.5 walks a unit: 140 with two, 117 with one.
+// takes 1.4 times as long for twice the columns). Packed sequences may be uneven, which the host does not
+// see, and then the longest walk, not their sum, sets the time: two tiles only from five walks a compute unit
+// on, where they lose for neither kind. Measured, forward and training step in us, with two tiles and with one,
+// 16 heads of 128, for sequences of 512 tokens and for log-uniform ones of 100 to 4000 with one of 4000:
+//   2 walks a unit    38 and 44,   98 and 106      139 and  98,  346 and 255
+//   4 walks a unit    59 and 71,  167 and 187      154 and 136,  441 and 402
+//   4.5               81 and 87,  220 and 230      158 and 160,  491 and 479
+//   5                 83 and 89,  228 and 237      187 and 223,  619 and 683
+//   8                112 and 136, 330 and 381      259 and 305,  819 and 907
 static hipError_t sc_column_tiles(const ScArgs& a, long long walks16, int& nc) {
     int dev = 0, cus = 0;
     hipError_t e = hipGetDevice(&dev);

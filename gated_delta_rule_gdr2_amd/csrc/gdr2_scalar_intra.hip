@@ -129,8 +129,9 @@ __device__ __forceinline__ void put_parts(OT* p, const f32x4& x) {
 // in fp32.)
 // Bound by HBM traffic in the large: reads q and k, writes T, M and the row factors, for training T^T and
 // M^T too, 52 (training 76) KB a chunk and value head at d_k = 128 with Hk = Hv; 51 us for 16384 tokens and
-// 16 heads, 38 us for 2 x 4096 in training, 4.1 TB/s both. In the small by the latency of the blocked
-// inverse: 11.5 us for three chunks.
+// 16 heads, 38 us for 2 x 4096 in training, 4.1 TB/s both. In the small by latencies one behind the other, the
+// tiles' copies, the products, the gates (loaded and scanned in 64 bits by one wave while three wait) and the
+// blocked inverse: 11.5 us for three chunks.
 template <class OT, int DK, bool TRAIN>
 __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
     constexpr int KB = DK / 32, ES = sizeof(OT);
@@ -328,8 +329,8 @@ __device__ __forceinline__ void dma_rows_clamped(const OT* base, size_t rs, int 
 // dbeta = dY.(v - k^T X) with X the state before the token, decayed, and beta (v - k^T X) is Delta. The other
 // form, dY.v + k.G, is a difference of terms of the size of v: where the state already predicts v, as a trained
 // one does, the bf16 roundings of S and of the intermediates in G would stay at that size (normwise errors in
-// bf16 where v - k^T X is a tenth and a thirtieth of v: 1.2e-2 and 3.9e-2 against 2.6e-3 and less). It is left
-// for a beta so small that Delta, a product with it, would leave the normal numbers.
+// bf16 where v - k^T X is a tenth and a thirtieth of v: 1.2e-2 and 3.9e-2 against 2.9e-3). It is left for a
+// beta so small that Delta, a product with it, would leave the normal numbers.
 __device__ __forceinline__ bool sc_dbeta_by_delta(float beta) { return fabsf(beta) >= 0x1p-32f; }
 
 // One workgroup of eight waves per (chunk slot, key head), each wave a 16-row tile of key channels
@@ -343,6 +344,8 @@ __device__ __forceinline__ bool sc_dbeta_by_delta(float beta) { return fabsf(bet
 //   dq = dq_s + P K,  G = dx_s + (R / beta) K,  dk = P^T Q + R^T K + beta G + dk_s
 //   dv = beta dY,  dbeta = dY.Delta / beta, or dY.v + k.G where beta is next to nothing (sc_dbeta_by_delta)
 //   dg_t = sum_{r >= t} (row_r - col_r of N + q.dq_s + beta k.dx_s) + sum_{i < t} k.dk_s + e^gamC <dS', S>
+// (P, R and R / beta are rounded to bf16 as the operands of the last products, as q, k and the saved arrays are;
+// N and all sums stay in 32 bits.)
 // The last line sums only terms that carry the decay across t: the diagonal of N, which does not
 // depend on the decay, is left out, so that a strong decay leaves a small dg and no cancellation.
 //

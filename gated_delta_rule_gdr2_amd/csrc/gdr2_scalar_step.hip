@@ -8,7 +8,9 @@
 // k_sc_step: one workgroup of two waves per (row, value head, 64 columns), a wave on 32 columns. Lane l
 // holds columns 4 (l % 8) .. + 3 of rows l / 8 + 8 i, so each row segment a wave moves is one 128-byte
 // line, and the sums over the key axis stay inside a wave. The state stays in registers for all tokens
-// of the call. Measured at d = 128, 16 value heads: 512 rows (1.08 GB) in 180 - 190 us, 5.7 - 6.0 TB/s;
+// of the call. Measured at d = 128, 16 value heads: 512 rows (1.08 GB) in 222 us, 4.8 TB/s, where each call has
+// another pool (214 us with the states in order), and in 184 us, 5.8 TB/s, on one pool again and again, part of
+// which the Infinity Cache still holds from the call before (written there with ordinary stores: 225 and 226 us);
 // one row (2.1 MB) in 5.0 us, a launch and the latency of one read, and no less with the key axis split
 // over four waves that join their sums in LDS (5.1 us).
 #include "gdr2_device.hpp"
