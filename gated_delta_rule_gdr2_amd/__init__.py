@@ -601,11 +601,20 @@ def _accumulation_streams(leaves):
 
 
 class GDR2ScalarFunction(torch.autograd.Function):
-    """Autograd wrapper: forward saves the chunks' states in the workspace, backward reuses them.
+    """Autograd wrapper: forward saves the chunks' states in the workspace, backward reuses them. Where no
+    gradient is wanted (no_grad, or no input that requires one) it is gdr2_scalar_fwd and saves nothing.
 
     Forward and backward may be captured into a graph together, but not while an earlier graph of the same
     leaves, built on another stream, is still alive: their gradients would be accumulated on that stream,
-    outside the capture. Such a backward is refused."""
+    outside the capture. Such a backward is refused where the earlier graph went through this function; a
+    graph that other operations built on the leaves, and leaves further back than the inputs, are not seen
+    here and are the caller's to drop before a capture."""
+
+    @classmethod
+    def apply(cls, q, k, v, g, beta, h0=None, cu_seqlens=None):
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, v, g, beta, h0)):
+            return super().apply(q, k, v, g, beta, h0, cu_seqlens)
+        return gdr2_scalar_fwd(q, k, v, g, beta, h0, cu_seqlens=cu_seqlens)[:2]
 
     @staticmethod
     def forward(ctx, q, k, v, g, beta, h0=None, cu_seqlens=None):

@@ -226,6 +226,30 @@ def test_marks_of_leaves_live_as_long_as_their_graphs():
         assert marks() == []
 
 
+def test_nothing_is_saved_where_no_gradient_is_wanted(monkeypatch):
+    import types
+
+    import torch
+    saved = []
+
+    def forward(q, *a, save_for_bwd=False, **kw):
+        saved.append(save_for_bwd)
+        return q * 1, torch.zeros(1), torch.zeros(1)
+
+    monkeypatch.setattr(g2, "gdr2_scalar_fwd", forward)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=1))
+    plain, wants = torch.randn(2), torch.randn(2, requires_grad=True)
+    f = g2.GDR2ScalarFunction.apply
+    assert not f(*[plain] * 5)[0].requires_grad and not f(*[plain] * 6, None)[0].requires_grad
+    with torch.no_grad():
+        assert not f(*[wants] * 5)[0].requires_grad
+    with torch.inference_mode():
+        f(*[wants] * 5)
+    assert saved == [False] * 4
+    assert f(wants, *[plain] * 4)[0].requires_grad and f(*[plain] * 5, wants)[0].requires_grad
+    assert saved[4:] == [True] * 2
+
+
 def test_a_captured_backward_with_a_foreign_graph_is_refused(monkeypatch):
     # the check alone, on the CPU: the GPU calls are stand-ins, the stream a number
     import types
