@@ -136,8 +136,8 @@ struct ScChainLds {  // one operand buffer, and the exchange
     static constexpr int XS = 0;                      // state: NS x NKB fragments
     static constexpr int XX = XS + NS * NKB * F;      // X or dDelta: NS x 2
     static constexpr int XD = XX + NS * 2 * F;        // tail Delta or -beta e^gam dY: NS x 2
-    static constexpr int XO = XD + NS * 2 * F;        // Delta or dY, one part: 2
-    static constexpr int XP = XO + 2 * F;             // backward: Q^T (e^gam dO), fp32 accumulator tiles
+    static constexpr int XO = XD + NS * 2 * F;        // Delta: NS x 2; dY, one part: 2
+    static constexpr int XP = XO + (BWD ? 1 : NS) * 2 * F;  // backward: Q^T (e^gam dO), fp32 accumulator tiles
     static constexpr int XT = XP + (BWD ? DK / 16 * 1024 : 0);
     static constexpr int XBYTES = NC * XT;
     static_assert(2 * BYTES + XBYTES + 256 <= 160 * 1024, "two operand buffers fit");
@@ -403,7 +403,7 @@ __device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk& w, in
 #pragma unroll
             for (int i = 0; i < 4; ++i) D[1][i] = t4[i] * D[0][i];
             put_split<OT>(xc + B::XD + (wv >> 1) * F, 2 * F, wv & 1, D[1]);
-            put_one<OT>(xc + B::XO + (wv >> 1) * F, wv & 1, D[0]);
+            put_split<OT>(xc + B::XO + (wv >> 1) * F, 2 * F, wv & 1, D[0]);
         }
         sync_lds();  // C: Delta is published
         // the next T: from here to A the memory path is least busy, and a wave waits where it issues a load
@@ -471,10 +471,13 @@ struct Slice {
     }
 };
 
-// Side waves: what a step gives away -- O, and for training the chunk's start state and Delta. In bf16 O takes
-// the first parts of S and Delta, and M in one part: nothing is carried on from it, and it is rounded to bf16
-// itself. It is off by 2.4e-3 (its own rounding 1.7e-3). With both parts of all three it was off by 1.65e-3, and
-// a prompt of 16384 tokens took 357 us instead of 322, a training step of 2 x 4096 345 instead of 331.
+// Side waves: what a step gives away -- O, and for training the chunk's start state and Delta. In bf16 each of
+// O's terms is off by one rounding, S's first part in one and M in the other, and O by its own: 2.4e-3 together
+// (its own alone 1.7e-3). Delta has both parts: with one it was 2.9e-3. With both parts of S and M too it was
+// 1.65e-3, and a prompt of 16384 tokens took 357 us instead of 322, a training step of 2 x 4096 345 instead of
+// 331. M Delta is added, and O stored, behind the next chunk's barrier A, where nothing waits for these waves: in
+// the step itself the prompt took 335 us. In training, where the chunk's state is stored there, it is the other
+// way round: 346 us behind A, 334 in the step.
 template <class OT, int DK, int DV, int NC, bool TRAIN, bool OUT, bool SUM>
 __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, int wv, const lds_char* b0,
                                             const lds_char* b1, const lds_char* xs) {
@@ -485,7 +488,7 @@ __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, in
     }
     using B = ScChainLds<OT, DK, NC, false>;
     using FT = typename Frag<OT>::type;
-    constexpr int NKB = B::NKB, F = B::F;
+    constexpr int NS = B::NS, NKB = B::NKB, F = B::F;
     const int l = lane_id(), li = l & 15, lq = l >> 4;
     const OT* mp = (const OT*)(a.ws + a.L.o_m) + ((size_t)w.q.slot0 * a.Hv + w.h) * a.L.m;
     const size_t mstep = (size_t)a.Hv * a.L.m;
@@ -497,11 +500,34 @@ __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, in
 #pragma unroll
         for (int ch = 0; ch < NC; ++ch) S[ch].write(p + (size_t)(NC * w.j + ch) * DK * 16, wv);
     };
+    f32x4 O[NC];  // O^T (rows: value columns, columns: this wave's tokens)
+    auto finish = [&](int n) {  // chunk n's M Delta, and its rows of O
+#pragma unroll
+        for (int ch = 0; ch < NC; ++ch)
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int p = 0; p < NS; ++p)
+                    mma(O[ch], get_x<OT>(xs + ch * B::XT + B::XO + (2 * p + kb) * F), M.f[0][kb]);
+        if (n + 1 < w.q.nt) mp += mstep;
+        M.load(mp, wv);
+        const int row = 16 * wv + li;
+        if (CH * n + row < w.q.len) {
+            OT* o = (OT*)a.o + ((size_t)(w.q.tok0 + 64LL * n + row) * a.Hv + w.h) * DV + 16 * NC * w.j + 4 * lq;
+#pragma unroll
+            for (int ch = 0; ch < NC; ++ch) {
+                const float ov[4] = {O[ch][0], O[ch][1], O[ch][2], O[ch][3]};
+                st4(o + 16 * ch, ov);
+            }
+        }
+    };
+    constexpr bool LATE = OUT && !TRAIN;
 #pragma unroll 1
     for (int n = 0; n < w.q.nt; ++n) {
         const lds_char* buf = (n & 1) ? b1 : b0;
         const size_t id = (size_t)(w.q.slot0 + n) * a.Hv + w.h;
         sync_lds();  // A
+        if (LATE && n > 0) finish(n - 1);  // (until the next barrier the exchange still holds its Delta)
         if (TRAIN && n > 0) store_state(n - 1);
         FT Q[NKB];
         if (OUT) {
@@ -510,9 +536,7 @@ __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, in
             for (int kb = 0; kb < NKB; ++kb) Q[kb] = lfrag_rowk8<OT>(vQ, 16 * wv, 32 * kb);
         }
         sync_lds();  // B: from here to C the compute waves leave LDS mostly idle
-        // O^T (rows: value columns, columns: this wave's tokens), the state's part
-        f32x4 O[NC];
-        if (OUT) {
+        if (OUT) {  // O, the state's part
 #pragma unroll
             for (int ch = 0; ch < NC; ++ch) O[ch] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -528,23 +552,7 @@ __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, in
             for (int ch = 0; ch < NC; ++ch) S[ch].read(xs + ch * B::XT + B::XS, wv);
         }
         sync_lds();  // C
-        if (OUT) {
-#pragma unroll
-            for (int ch = 0; ch < NC; ++ch)
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) mma(O[ch], get_x<OT>(xs + ch * B::XT + B::XO + kb * F), M.f[0][kb]);
-            if (n + 1 < w.q.nt) mp += mstep;
-            M.load(mp, wv);
-            const int row = 16 * wv + li;
-            if (CH * n + row < w.q.len) {
-                OT* o = (OT*)a.o + ((size_t)(w.q.tok0 + 64LL * n + row) * a.Hv + w.h) * DV + 16 * NC * w.j + 4 * lq;
-#pragma unroll
-                for (int ch = 0; ch < NC; ++ch) {
-                    const float ov[4] = {O[ch][0], O[ch][1], O[ch][2], O[ch][3]};
-                    st4(o + 16 * ch, ov);
-                }
-            }
-        }
+        if (OUT && !LATE) finish(n);
         if (TRAIN) {
             OT* p = (OT*)(a.ws + a.L.o_delta) + id * a.L.d;
 #pragma unroll
@@ -555,6 +563,7 @@ __device__ __forceinline__ void sc_fwd_side(const ScArgs& a, const ScWalk& w, in
             }
         }
     }
+    if (LATE && w.q.nt > 0) finish(w.q.nt - 1);
     if (TRAIN && w.q.nt > 0) store_state(w.q.nt - 1);
 }
 

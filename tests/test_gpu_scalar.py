@@ -188,6 +188,24 @@ def test_write_strengths_next_to_nothing(dtype, beta):
     check(train(x, cu), x, cu, dtype)
 
 
+@pytest.mark.parametrize("case", [([64] * 8, False, 4, 4, 128, 128), ([200, 57, 130], True, 2, 4, 64, 128),
+                                  ([300, 300], False, 2, 2, 128, 64)])
+@pytest.mark.parametrize("g_scale", [0.02, 0.5])
+def test_output_is_off_by_two_roundings(case, g_scale):
+    # bf16: a term of O is rounded once (S's in one operand, M Delta's in the other), and O itself. A rounding is
+    # uniform over a step, 2^-8 / sqrt(3) of the step's lower end in the mean square, and over the numbers of a
+    # binade, evenly spread in their logarithm, sqrt(3 / (8 ln 2)) of that: 1.66e-3. Two are sqrt(2) of it (three
+    # sqrt(3)); a tenth more for what spread the numbers really have.
+    lens, packed, hk, hv, dk, dv = case
+    x, cu = inputs(lens, packed, hk, hv, dk, dv, BF, g_scale=g_scale, seed=44)
+    want = ref.run_recurrence(x, cu)
+    w = torch.cat([t.reshape(-1, hv, dv) for t in want["o"]])
+    once = 2.0 ** -8 / 3 ** 0.5 * (3 / 8 / 0.6931471805599453) ** 0.5
+    for o in (train(x, cu)["o"], g2.gdr2_scalar_fwd(*[x[n] for n in ("q", "k", "v", "g", "beta", "h0")],
+                                                    cu_seqlens=device_cu(cu))[0]):
+        assert ref.normwise(o.reshape(w.shape), w) <= 1.1 * 2 ** 0.5 * once
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_inference_forward_recompute_and_repeats(dtype):
     x, cu = inputs([100, 64, 7], True, 2, 4, 64, 64, dtype, seed=9)
