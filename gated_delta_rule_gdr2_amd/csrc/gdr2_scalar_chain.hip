@@ -436,7 +436,7 @@ __device__ __forceinline__ void sc_fwd_walk(const ScArgs& a, const ScWalk& w, in
 // The 16-column slice [rows][16] of an exchanged matrix of 16 RT rows (its fragments' first parts, from
 // frag on) to the workspace, by the four side waves: read while the exchange holds it, stored later, since
 // a wave waits where it issues a store and the others then wait for it at the next barrier. What is saved for
-// the gradients (S, dS', Delta, dY) is one bf16 each: the gradients end in bf16, off by 2 to 3e-3, and a second
+// the gradients (S, dS', Delta, dY) is one bf16 each: the gradients end in bf16, off by 2.3 to 2.9e-3, and a second
 // part would add half as much again to the 208 KB a chunk and head that their kernel waits for. The chains
 // themselves carry both parts on.
 template <class OT, int RT>

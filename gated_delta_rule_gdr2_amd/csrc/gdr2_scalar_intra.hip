@@ -281,7 +281,7 @@ __global__ __launch_bounds__(256, 4) void k_sc_prep(ScArgs a) {
 // ============================================================================ gradients
 template <class OT, int DK, int DV, bool MULTI>
 struct ScGradLds {
-    static constexpr int ES = sizeof(OT);
+    static constexpr int ES = sizeof(OT), NS = Split<OT>::NS;
     static constexpr int NW = 8;               // waves
     static constexpr int KW = DK / 16;         // 16-row tiles of key channels, one a wave;
     static constexpr int TPW = 4 * KW / NW;    // token tiles of a wave: all four, or half of them where KW = 4
@@ -293,13 +293,14 @@ struct ScGradLds {
     static constexpr int DO = 0;            // dO rows, swizzled
     static constexpr int DEL = DO + TV;     // Delta, dY: slices [DV / 16][64][16]
     static constexpr int DY = DEL + TV;
-    static constexpr int P = DO;            // after the pair products: P, R / beta, R [64][64]
+    static constexpr int P = DO;            // after the pair products: P, R / beta, R, P's second part [64][64]
     static constexpr int RP = P + SQ;
     static constexpr int R = RP + SQ;
-    static constexpr int QL = R + SQ;       // and raw q rows: one head
+    static constexpr int PL = R + SQ;       // (bf16)
+    static constexpr int QL = PL + (NS == 2 ? SQ : 0);  // and raw q rows: one head
     static constexpr int ODQ = DO;          // at the end: dq and dk rows on their way out
     static constexpr int ODK = ODQ + TK;
-    static constexpr int AFTER = MULTI ? 3 * SQ : 3 * SQ + TK;
+    static constexpr int AFTER = MULTI ? QL : QL + TK;
     static constexpr int MX = 3 * TV > AFTER ? 3 * TV : AFTER;
     static constexpr int VEC = MX > 2 * TK ? MX : 2 * TK;  // the row factors (copied by two waves, 1 KB each)
     static constexpr int REGION = VEC + 2048;
@@ -344,8 +345,10 @@ __device__ __forceinline__ bool sc_dbeta_by_delta(float beta) { return fabsf(bet
 //   dq = dq_s + P K,  G = dx_s + (R / beta) K,  dk = P^T Q + R^T K + beta G + dk_s
 //   dv = beta dY,  dbeta = dY.Delta / beta, or dY.v + k.G where beta is next to nothing (sc_dbeta_by_delta)
 //   dg_t = sum_{r >= t} (row_r - col_r of N + q.dq_s + beta k.dx_s) + sum_{i < t} k.dk_s + e^gamC <dS', S>
-// (P, R and R / beta are rounded to bf16 as the operands of the last products, as q, k and the saved arrays are;
-// N and all sums stay in 32 bits.)
+// In bf16 P enters the last products in two parts, a value and what its rounding left over: dq and dk are off by
+// 2.4e-3 (2.9e-3 with one, and 329 us instead of 330 for the whole step of 2 x 4096 tokens, 407 instead of 411
+// for the packed one), of which 1.7e-3 are their own rounding. R and R / beta take one part, the smaller terms
+// beside what the saved arrays' roundings leave. N and all sums stay in 32 bits.
 // The last line sums only terms that carry the decay across t: the diagonal of N, which does not
 // depend on the decay, is left out, so that a strong decay leaves a small dg and no cancellation.
 //
@@ -444,7 +447,7 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
         const LSwz<OT, DK> vQ{MULTI ? sm + LS::Q : hd + LS::QL};
         const LSwz<OT, DV> vO{hd + LS::DO};
         const LSlice<OT, CH> vDel{hd + LS::DEL}, vDy{hd + LS::DY};
-        const LSwz<OT, CH> vP{hd + LS::P}, vRp{hd + LS::RP}, vR{hd + LS::R};
+        const LSwz<OT, CH> vP{hd + LS::P}, vPl{hd + LS::PL}, vRp{hd + LS::RP}, vR{hd + LS::R};
         Lane ln = fresh_lane();
         const int li = ln.li, lq = ln.lq, l = li + 16 * lq, tid = 64 * wv + l;
         const bool more = MULTI && hh + 1 < a.R;
@@ -609,6 +612,12 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
                 const float y[4] = {fRp[n][0], fRp[n][1], fRp[n][2], fRp[n][3]};
                 const float z[4] = {br * y[0], br * y[1], br * y[2], br * y[3]};
                 lds_put4<OT>(hd + LS::P + o, x);
+                if constexpr (LS::NS == 2) {
+                    float w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = x[i] - to_f(to_ot<OT>(x[i]));
+                    lds_put4<OT>(hd + LS::PL + o, w);
+                }
                 lds_put4<OT>(hd + LS::RP + o, y);
                 lds_put4<OT>(hd + LS::R + o, z);
             }
@@ -619,6 +628,7 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             const int o = swz<OT, CH>(16 * R + ln.li, 16 * I + 4 * ln.lq) * ES;
             const float z[4] = {0.f, 0.f, 0.f, 0.f};
             lds_put4<OT>(hd + LS::P + o, z);
+            if constexpr (LS::NS == 2) lds_put4<OT>(hd + LS::PL + o, z);
             lds_put4<OT>(hd + LS::RP + o, z);
             lds_put4<OT>(hd + LS::R + o, z);
         }
@@ -640,10 +650,12 @@ __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_g
             for (int kb = 0; kb < 2; ++kb) {
                 if (kb == 0 || tt >= 2) {  // rows of token tile t: columns up to it
                     mma(dq[t], fK[kb], frag_rows<OT>(ln, vP, 16 * tt, 32 * kb));
+                    if constexpr (LS::NS == 2) mma(dq[t], fK[kb], frag_rows<OT>(ln, vPl, 16 * tt, 32 * kb));
                     mma(G[t], fK[kb], frag_rows<OT>(ln, vRp, 16 * tt, 32 * kb));
                 }
                 if (kb == 1 || tt < 2) {   // columns of token tile t: rows from it on
                     mma(dk[t], fQ[kb], frag_cols<OT>(ln, vP, 16 * tt, 32 * kb));
+                    if constexpr (LS::NS == 2) mma(dk[t], fQ[kb], frag_cols<OT>(ln, vPl, 16 * tt, 32 * kb));
                     mma(dk[t], fK[kb], frag_cols<OT>(ln, vR, 16 * tt, 32 * kb));
                 }
             }

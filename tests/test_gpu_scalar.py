@@ -206,6 +206,18 @@ def test_output_is_off_by_two_roundings(case, g_scale):
         assert ref.normwise(o.reshape(w.shape), w) <= 1.1 * 2 ** 0.5 * once
 
 
+@pytest.mark.parametrize("case", [([130] * 4, False, 2, 4, 128, 128), ([200, 57, 130], True, 4, 4, 64, 128),
+                                  ([300, 300], False, 2, 2, 128, 64)])
+def test_query_gradient_is_off_by_two_roundings(case):
+    # bf16: as the output. dq's terms are rounded once each, in S and in Delta (P is held in two parts), then dq
+    lens, packed, hk, hv, dk, dv = case
+    x, cu = inputs(lens, packed, hk, hv, dk, dv, BF, g_scale=0.5, seed=45)
+    want = ref.run_recurrence(x, cu, grads=True)
+    w = torch.cat([t.reshape(-1, hk, dk) for t in want["dq"]])
+    once = 2.0 ** -8 / 3 ** 0.5 * (3 / 8 / 0.6931471805599453) ** 0.5
+    assert ref.normwise(train(x, cu)["dq"].reshape(w.shape), w) <= 1.1 * 2 ** 0.5 * once
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_inference_forward_recompute_and_repeats(dtype):
     x, cu = inputs([100, 64, 7], True, 2, 4, 64, 64, dtype, seed=9)
