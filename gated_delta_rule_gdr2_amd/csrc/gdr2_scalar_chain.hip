@@ -31,7 +31,7 @@
 // there. (With 64 walks and more the first segment is walked in full at once: ScArgs::lead.)
 //
 // Bound by the latency of a step: 256 walks of 64 steps (2 x 4096 tokens, 16 heads, d = 128, one walk on each
-// compute unit) take 93 us forward with what training saves and 100 us backward, 1.5 us a step; 128 walks
+// compute unit) take 96 us forward with what training saves and 101 us backward, 1.5 us a step; 128 walks
 // of 256 steps (one prompt of 16384 tokens, walked whole) 283 us, 1.1 us or 2700 cycles a step, of which the three
 // barriers with the exchange behind each are most. Measured and not taken: T through LDS like the rest
 // (forward 104 -> 111 us at the time), q straight to the side waves' registers (104 -> 113), the keys of K S

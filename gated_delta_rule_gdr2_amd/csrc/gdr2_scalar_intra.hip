@@ -357,8 +357,8 @@ __device__ __forceinline__ bool sc_dbeta_by_delta(float beta) { return fabsf(bet
 // is what the LDS layout (q enters LDS only when dO, Delta and dY have left it) and the register bound
 // are for. MULTI, more than one: around a loop over heads the registers are not enough for two workgroups
 // (84 spilled), so one has the compute unit, keeps q in LDS and loads the next head while this one is
-// worked on. Measured, d = 128, bf16: 98 us at 2 x 4096 tokens, 16 heads (4.5 TB/s); 129 us at 8859 packed
-// tokens, 8 key heads with 2 value heads each (3.1 TB/s, five rounds of workgroups of which the last is half
+// worked on. Measured, d = 128, bf16: 100 us at 2 x 4096 tokens, 16 heads (4.4 TB/s); 135 us at 8859 packed
+// tokens, 8 key heads with 2 value heads each (3.0 TB/s, five rounds of workgroups of which the last is half
 // empty; without the loads ahead 144 us).
 template <class OT, int DK, int DV, bool MULTI>
 __global__ __launch_bounds__(512, sizeof(OT) == 2 && !MULTI ? 4 : 2) void k_sc_grad(ScArgs a) {

@@ -49,7 +49,8 @@ __global__ __launch_bounds__(128) void k_sc_step(ScStepArgs a) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) S[i] = *(const f32x4*)(hs + (size_t)(rg + 8 * i) * DV);
     // Rows that name the same state are one sequence, in the order of the rows: the first of them
-    // does the work of all.
+    // does the work of all. Every workgroup looks through all slots: 1 us of 214 for 512 rows of 16 heads of
+    // 128, 43 of 150 for 4096 rows of 4 heads of 64, 208 of 314 for 16384 rows of one.
     int more = 0;
     if (a.slots) {
         int seen = 0;  // 1: an earlier row has this state; 2: a later one
