@@ -55,17 +55,17 @@ int sc_shape(int N, int T, int Hk, int Hv, int dk, int dv, int dtype, bool packe
     return GDR2_OK;
 }
 
+bool sc_no_tokens(int N, int T, int Hv) { return N == 0 || T == 0 || Hv == 0; }
+
 // ... and for the chunkwise kernels: preparation, gradients and chains (of many walks, two column tiles each)
 int sc_chunk_shape(int N, int T, int Hk, int Hv, int dk, int dv, int dtype, bool packed) {
     const int st = sc_shape(N, T, Hk, Hv, dk, dv, dtype, packed);
-    if (st != GDR2_OK) return st;
+    if (st != GDR2_OK || sc_no_tokens(N, T, Hv)) return st;
     const long long slots = sc_slots(N, T, packed);
-    return slots * Hv <= 0x7fffffffLL && grid_fits(slots * Hv, 256) && grid_fits(slots * Hk, 512) &&
+    return grid_fits(slots * Hv, 256) && grid_fits(slots * Hk, 512) &&
                    grid_fits((long long)N * Hv * (dv / 32), gdr2::SC_CHAIN_THREADS)
                ? GDR2_OK : GDR2_ERR_SHAPE;
 }
-
-bool sc_no_tokens(int N, int T, int Hv) { return N == 0 || T == 0 || Hv == 0; }
 
 gdr2::ScLayout sc_layout_for(int N, int T, int Hv, int dk, int dv, int dtype, bool packed) {
     int nseg, seglen, lead;
@@ -203,9 +203,9 @@ int gdr2_scalar_step(const void* q, const void* k, const void* v, const void* g,
                      void* stream) {
     const int st = sc_shape(B, T, Hk, Hv, dk, dv, dtype, false);
     if (st != GDR2_OK) return st;
-    if (!grid_fits((long long)B * Hv * (dv / 64), 128)) return GDR2_ERR_SHAPE;
     if (n_states < 0 || (!slots && n_states < B)) return GDR2_ERR_SHAPE;
     const bool none = sc_no_tokens(B, T, Hv);
+    if (!none && !grid_fits((long long)B * Hv * (dv / 64), 128)) return GDR2_ERR_SHAPE;
     if (!none && (!q || !k || !v || !g || !beta || !o)) return GDR2_ERR_NULL;
     if (!none && n_states > 0 && !state) return GDR2_ERR_NULL;
     const void* const ptrs[] = {q, k, v, state, o};

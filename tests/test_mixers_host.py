@@ -226,6 +226,13 @@ def test_marks_of_leaves_live_as_long_as_their_graphs():
         assert marks() == []
 
 
+def test_calls_without_tokens_have_no_launch_to_fit(lib):
+    for bwd in (False, True):
+        n = 14 if bwd else 8
+        assert scalar(lib, bwd, [0] * n, N=1 << 22, T=0, dk=128, dv=128, ws=0) == OK
+    assert step(lib, [0] * 7, B=1 << 25, T=0, states=1) == OK
+
+
 def test_nothing_is_saved_where_no_gradient_is_wanted(monkeypatch):
     import types
 
