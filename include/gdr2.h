@@ -65,7 +65,8 @@ enum gdr2_dtype { GDR2_DTYPE_F32 = 0, GDR2_DTYPE_BF16 = 1 };
 enum gdr2_status {
     GDR2_OK = 0,
     GDR2_ERR_NULL = -1,        /* a required pointer is NULL */
-    GDR2_ERR_SHAPE = -2,       /* B, T or H negative, heads that do not divide, or sizes overflow */
+    GDR2_ERR_SHAPE = -2,       /* B, T or H negative, heads that do not divide, or sizes overflow
+                                  (scalar gates and cache: launches of 2^32 threads among them) */
     GDR2_ERR_UNSUPPORTED = -3, /* dk/dv/chunk/dtype combination not built */
     GDR2_ERR_ALIGN = -4,       /* a pointer is not 16-byte aligned */
     GDR2_ERR_WORKSPACE = -5,   /* workspace NULL or smaller than required */
