@@ -9,8 +9,10 @@ Attention", anthology record LIT-802, takeaway 1; paper Sec. 3.1 Eqs. 8-10)
 runs entirely in the HIP kernels of ``libgdr2.so`` (built from ``csrc/`` by
 ``python -m gated_delta_rule_gdr2_amd.build``); see ``include/gdr2.h`` for the
 C ABI. So do the same recurrence with scalar gates (``gdr2_scalar_*``) and, for
-the other layers of a hybrid decoder, attention over a paged key-value cache
-(``gdr2_attn_step``) and the cache's writer (``gdr2_kv_append``). This module
+the other layers of a hybrid decoder, attention over whole sequences with its
+gradients (``gdr2_attn_fwd``, ``gdr2_attn_bwd``), over a paged key-value cache, of
+one token (``gdr2_attn_step``) or of drafted ones (``gdr2_attn_tree``), and what
+keeps the cache (``gdr2_kv_append``, ``gdr2_kv_keep``, ``gdr2_kv_pages``). This module
 only marshals torch tensors (device memory and the current HIP stream) into
 those calls. There is no fallback: if the library is missing every call raises.
 """
@@ -28,6 +30,8 @@ __all__ = ["gdr2_fwd", "gdr2_bwd", "gdr2_step", "gdr2_fwd_logits", "gdr2_bwd_log
            "gdr2_bwd_workspace_bytes", "gdr2_seg_workspace_bytes", "gdr2_strerror", "gdr2_version", "GDR2Function",
            "gdr2_scalar_fwd", "gdr2_scalar_bwd", "gdr2_scalar_step", "gdr2_scalar_workspace_bytes",
            "GDR2ScalarFunction", "gdr2_attn_step", "gdr2_attn_workspace_bytes", "gdr2_kv_append",
+           "gdr2_attn_fwd", "gdr2_attn_bwd", "gdr2_attn_bwd_workspace_bytes", "GDR2AttnFunction", "gdr2_attn_tree",
+           "gdr2_attn_tree_workspace_bytes", "gdr2_kv_keep", "gdr2_kv_pages",
            "library_path", "load_library"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,7 +45,9 @@ EXPORTED = ["gdr2_fwd", "gdr2_bwd", "gdr2_step", "gdr2_fwd_logits", "gdr2_bwd_lo
             "gdr2_fwd_seg", "gdr2_bwd_seg", "gdr2_fwd_noalloc", "gdr2_fwd_workspace_bytes",
             "gdr2_bwd_workspace_bytes", "gdr2_seg_workspace_bytes", "gdr2_strerror", "gdr2_version",
             "gdr2_scalar_fwd", "gdr2_scalar_bwd", "gdr2_scalar_step", "gdr2_scalar_workspace_bytes",
-            "gdr2_attn_step", "gdr2_attn_workspace_bytes", "gdr2_kv_append"]
+            "gdr2_attn_step", "gdr2_attn_workspace_bytes", "gdr2_kv_append", "gdr2_attn_fwd", "gdr2_attn_bwd",
+            "gdr2_attn_bwd_workspace_bytes", "gdr2_attn_tree", "gdr2_attn_tree_workspace_bytes", "gdr2_kv_keep",
+            "gdr2_kv_pages"]
 NOALLOC_SCRATCH_BYTES = 64 << 20  # GDR2_NOALLOC_SCRATCH_BYTES in include/gdr2.h
 
 
@@ -98,6 +104,20 @@ def load_library():
     lib.gdr2_attn_step.restype = i
     lib.gdr2_kv_append.argtypes = [vp] * 8 + [i] * 8 + [vp]
     lib.gdr2_kv_append.restype = i
+    lib.gdr2_attn_fwd.argtypes = [vp] * 8 + [i] * 5 + [f] + [i] * 3 + [vp]
+    lib.gdr2_attn_fwd.restype = i
+    lib.gdr2_attn_bwd_workspace_bytes.argtypes = [i] * 7
+    lib.gdr2_attn_bwd_workspace_bytes.restype = sz
+    lib.gdr2_attn_bwd.argtypes = [vp] * 12 + [i] * 5 + [f] + [i] * 3 + [vp, sz, vp]
+    lib.gdr2_attn_bwd.restype = i
+    lib.gdr2_attn_tree_workspace_bytes.argtypes = [i] * 6
+    lib.gdr2_attn_tree_workspace_bytes.restype = sz
+    lib.gdr2_attn_tree.argtypes = [vp] * 9 + [i] * 8 + [f] + [i] * 2 + [vp, sz, vp]
+    lib.gdr2_attn_tree.restype = i
+    lib.gdr2_kv_keep.argtypes = [vp] * 7 + [i] * 8 + [vp]
+    lib.gdr2_kv_keep.restype = i
+    lib.gdr2_kv_pages.argtypes = [vp] * 8 + [i] * 5 + [vp]
+    lib.gdr2_kv_pages.restype = i
     lib.gdr2_strerror.argtypes = [i]
     lib.gdr2_strerror.restype = ctypes.c_char_p
     lib.gdr2_version.argtypes = []
@@ -755,3 +775,287 @@ def gdr2_kv_append(k, v, k_cache, v_cache, block_table, starts, *, cu_seqlens=No
                  strides, block_table.data_ptr(), starts.data_ptr(), _adr(cu_seqlens), B, tokens, Hkv, D, pages, page,
                  max_pages, _DT[k.dtype])
     _raise(st, "gdr2_kv_append")
+
+
+def gdr2_attn_tree(q, parents, k_cache, v_cache, block_table, starts, *, scale=None, window=0, o=None, lse=None,
+                   return_lse=False, ws=None, stream=None):
+    """Attention of a tree of drafted tokens over a paged key-value cache (see include/gdr2.h). q: [B,T,Hq,D],
+    T at most 64; parents: int32 [B,T], the draft that each one continues, -1 where it continues the
+    sequence itself (any other value: padding); cache and block_table as gdr2_attn_step; starts: int32 [B],
+    tokens held before the drafts, which stand in the cache behind them (gdr2_kv_append with the same
+    starts). Returns o, or (o, lse) with return_lse or an ``lse`` tensor (fp32 [B,T,Hq]). ``ws``: a uint8
+    workspace of gdr2_attn_tree_workspace_bytes."""
+    lib = load_library()
+    if q.dim() != 4:
+        raise ValueError("q must have four dimensions [B,T,Hq,D]")
+    B, T, Hq, D = q.shape
+    if q.dtype not in _DT:
+        raise ValueError("unsupported dtype %s" % q.dtype)
+    dt, dev = _DT[q.dtype], _device_of(q, "q")
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    strides, pages, page, Hkv = _cache_strides(k_cache, v_cache, block_table, q.dtype, D, dev)
+    max_pages = block_table.shape[1]
+    _want(parents, "parents", torch.int32, (B, T), dev)
+    _want(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    _want(starts, "starts", torch.int32, (B,), dev)
+    new = []
+    if o is None:
+        o = torch.empty_like(q)
+        new.append(o)
+    else:
+        _want(o, "o", q.dtype, (B, T, Hq, D), dev)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, (B, T, Hq), dev)
+    elif return_lse:
+        lse = torch.empty(B, T, Hq, dtype=torch.float32, device=q.device)
+        new.append(lse)
+    if ws is None:
+        ws = torch.empty(gdr2_attn_tree_workspace_bytes(B, T, Hq, Hkv, D, dt), dtype=torch.uint8, device=q.device)
+        new.append(ws)
+    else:
+        _want(ws, "ws", torch.uint8, ws.shape, dev)
+    _keep_for(stream, *new)
+    st = _launch(lib.gdr2_attn_tree, dev, stream, q.data_ptr(), parents.data_ptr(), k_cache.data_ptr(),
+                 v_cache.data_ptr(), strides, block_table.data_ptr(), starts.data_ptr(), o.data_ptr(), _adr(lse), B, T,
+                 Hq, Hkv, D, pages, page, max_pages, D ** -0.5 if scale is None else scale,
+                 max(-1, min(window, 0x7fffffff)), dt, ws.data_ptr(), ws.numel())
+    _raise(st, "gdr2_attn_tree")
+    return o if lse is None else (o, lse)
+
+
+def gdr2_kv_keep(k_cache, v_cache, block_table, starts, path, *, lengths=None, stream=None):
+    """Keeps an accepted path of a tree of drafts: of each sequence the token at starts[b] + path[b][j] of
+    the cache goes to starts[b] + j, for the entries of path (int32 [B,P], P at most 64) before its first
+    negative one. Returns the tokens that each sequence then holds (int32 [B], in ``lengths`` if given)."""
+    lib = load_library()
+    if path.dim() != 2:
+        raise ValueError("path must have two dimensions [B,P]")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must have four dimensions [pages,page_size,Hkv,D]")
+    if k_cache.dtype not in _DT:
+        raise ValueError("unsupported dtype %s" % k_cache.dtype)
+    dev, D = _device_of(k_cache, "k_cache"), k_cache.shape[3]
+    strides, pages, page, Hkv = _cache_strides(k_cache, v_cache, block_table, k_cache.dtype, D, dev)
+    B, max_pages = block_table.shape
+    P = path.shape[1]
+    _want(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    _want(starts, "starts", torch.int32, (B,), dev)
+    _want(path, "path", torch.int32, (B, P), dev)
+    if lengths is None:
+        lengths = torch.empty_like(starts)
+        _keep_for(stream, lengths)
+    else:
+        _want(lengths, "lengths", torch.int32, (B,), dev)
+    st = _launch(lib.gdr2_kv_keep, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), strides, block_table.data_ptr(),
+                 starts.data_ptr(), path.data_ptr(), lengths.data_ptr(), B, P, Hkv, D, pages, page, max_pages,
+                 _DT[k_cache.dtype])
+    _raise(st, "gdr2_kv_keep")
+    return lengths
+
+
+def gdr2_kv_pages(lengths, counts, block_table, free_pages, num_free, *, page_size, max_tokens, new_lengths=None,
+                  cu_seqlens=None, slots=None, stream=None):
+    """Pages for the tokens to come (see include/gdr2.h). lengths, counts: int32 [B], the tokens that each
+    request holds and how many come to it, negative where it ends; block_table: int32 [B,max_pages],
+    free_pages: int32 [pages], a stack of which the first num_free (int32 [1]) entries are free: all three
+    are updated. Returns (new_lengths int32 [B], cu_seqlens int32 [B+1], slots int64 [max_tokens]), in the
+    tensors passed in if there are any."""
+    lib = load_library()
+    if block_table.dim() != 2:
+        raise ValueError("block_table must have two dimensions [B,max_pages]")
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must have one dimension")
+    B, max_pages = block_table.shape
+    pages, i32, dev = free_pages.shape[0], torch.int32, _device_of(block_table, "block_table")
+    if not (max_pages <= 0x7fffffff and pages <= 0x7fffffff and 0 <= max_tokens <= 0x7fffffff):
+        raise ValueError("block_table, free_pages or max_tokens out of range")
+    _want(lengths, "lengths", i32, (B,), dev)
+    _want(counts, "counts", i32, (B,), dev)
+    _want(block_table, "block_table", i32, (B, max_pages), dev)
+    _want(free_pages, "free_pages", i32, (pages,), dev)
+    _want(num_free, "num_free", i32, (1,), dev)
+    new = []
+    if new_lengths is None:
+        new_lengths = torch.empty_like(lengths)
+        new.append(new_lengths)
+    else:
+        _want(new_lengths, "new_lengths", i32, (B,), dev)
+    if cu_seqlens is None:
+        cu_seqlens = torch.empty(B + 1, dtype=i32, device=lengths.device)
+        new.append(cu_seqlens)
+    else:
+        _want(cu_seqlens, "cu_seqlens", i32, (B + 1,), dev)
+    if slots is None:
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=lengths.device)
+        new.append(slots)
+    else:
+        _want(slots, "slots", torch.int64, (max_tokens,), dev)
+    _keep_for(stream, *new)
+    st = _launch(lib.gdr2_kv_pages, dev, stream, lengths.data_ptr(), counts.data_ptr(), block_table.data_ptr(),
+                 free_pages.data_ptr(), num_free.data_ptr(), new_lengths.data_ptr(), cu_seqlens.data_ptr(),
+                 slots.data_ptr(), B, max_tokens, pages, max(-1, min(page_size, 0x7fffffff)), max_pages)
+    _raise(st, "gdr2_kv_pages")
+    return new_lengths, cu_seqlens, slots
+
+
+@functools.lru_cache(maxsize=256)
+def gdr2_attn_tree_workspace_bytes(B, T, Hq, Hkv, D, dtype=DTYPE_BF16) -> int:
+    return int(load_library().gdr2_attn_tree_workspace_bytes(B, T, Hq, Hkv, D, dtype))
+
+
+# ---------------------------------------------------------------- attention over whole sequences
+
+
+@functools.lru_cache(maxsize=256)
+def gdr2_attn_bwd_workspace_bytes(N, T, Hq, Hkv, D, packed=False, dtype=DTYPE_BF16) -> int:
+    return int(load_library().gdr2_attn_bwd_workspace_bytes(N, T, Hq, Hkv, D, int(bool(packed)), dtype))
+
+
+def _attn_input(t, name, dtype, shape, dev):
+    """Checks q, k or v of [B,T,H,D], which may be a part of a larger tensor's rows. Returns its token and head
+    strides."""
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError("%s must be on the GPU of the other tensors" % name)
+    if t.dtype is not dtype:
+        raise ValueError("%s must have dtype %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    B, T, H, D = shape
+    sb, st, sh, sd = t.stride()
+    if t.is_contiguous():
+        return H * D, D
+    if sd != 1 or (B > 1 and T > 0 and sb != T * st):
+        raise ValueError("the channels of %s must be contiguous, and its sequences T token strides apart" % name)
+    return st, sh
+
+
+def _attn_dims(q, k, v, cu_seqlens):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must have four dimensions [B,T,H,D]")
+    if q.dtype not in _DT:
+        raise ValueError("unsupported dtype %s" % q.dtype)
+    B, T, Hq, D = q.shape
+    Hkv, dev, t = k.shape[2], _device_of(q, "q"), q.dtype
+    strides = None
+    if not (k.shape == v.shape == (B, T, Hkv, D) and k.dtype is t and v.dtype is t and k.get_device() == dev
+            and v.get_device() == dev and q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        qs, ks, vs = (_attn_input(x, n, t, (B, T, h, D), dev) for x, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)))
+        strides = _strides((*qs, ks[0]), (ks[1], *vs))
+    N = B
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("packed sequences need B = 1, got B = %d" % B)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must have one dimension and at least one entry")
+        _want(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, dev)
+        N = cu_seqlens.numel() - 1
+    return N, T, Hq, Hkv, D, _DT[t], dev, strides
+
+
+def gdr2_attn_fwd(q, k, v, *, cu_seqlens=None, scale=None, window=0, o=None, lse=None, return_lse=False,
+                  save_for_bwd=False, stream=None):
+    """Causal attention over whole sequences (see include/gdr2.h). q: [B,T,Hq,D]; k, v: [B,T,Hkv,D], one dtype (bf16
+    or fp32); they may be parts of the rows of a larger tensor. cu_seqlens: None (B sequences of T tokens) or
+    int32 [N+1] on the device, the bounds of N sequences packed along T with B = 1. scale: D ** -0.5 unless
+    given; window: only the last ``window`` tokens (0: all). Returns o, or (o, lse) with return_lse or an
+    ``lse`` tensor (fp32 [B,T,Hq]), or with save_for_bwd (o, lse, rest) for gdr2_attn_bwd, rest (bf16; None
+    for fp32) being what o's rounding left over. Rows of no sequence are zero, or left as they were in an
+    ``o`` that is passed in."""
+    lib = load_library()
+    N, T, Hq, Hkv, D, dt, dev, strides = _attn_dims(q, k, v, cu_seqlens)
+    new, own_o, rest = [], o is None, None
+    if own_o:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        new.append(o)
+    else:
+        _want(o, "o", q.dtype, q.shape, dev)
+    if lse is not None:
+        _want(lse, "lse", torch.float32, q.shape[:3], dev)
+    elif return_lse or save_for_bwd:
+        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        new.append(lse)
+    if save_for_bwd and dt == DTYPE_BF16:
+        rest = torch.empty_like(o)
+        new.append(rest)
+    _keep_for(stream, *new)
+    if own_o and N == 0:
+        _zero(stream, *new)  # no sequence, and no kernel
+    st = _launch(lib.gdr2_attn_fwd, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _adr(cu_seqlens),
+                 o.data_ptr(), _adr(lse), _adr(rest), N, T, Hq, Hkv, D, D ** -0.5 if scale is None else scale,
+                 max(-1, min(window, 0x7fffffff)), dt, int(own_o))
+    _raise(st, "gdr2_attn_fwd")
+    return (o, lse, rest) if save_for_bwd else o if lse is None else (o, lse)
+
+
+def gdr2_attn_bwd(q, k, v, o, lse, dout, *, rest=None, cu_seqlens=None, scale=None, window=0, grads=None, ws=None,
+                  stream=None):
+    """Backward of gdr2_attn_fwd, with its o, lse and (bf16) rest for the same arguments. Returns a dict with dq, dk
+    and dv (contiguous), written into ``grads`` if given. ``ws``: a uint8 workspace of
+    gdr2_attn_bwd_workspace_bytes."""
+    lib = load_library()
+    N, T, Hq, Hkv, D, dt, dev, strides = _attn_dims(q, k, v, cu_seqlens)
+    _want(o, "o", q.dtype, q.shape, dev)
+    _want(lse, "lse", torch.float32, q.shape[:3], dev)
+    _want(dout, "dout", q.dtype, q.shape, dev)
+    if rest is not None:
+        _want(rest, "rest", q.dtype, q.shape, dev)
+    new, own = [], grads is None
+    if own:
+        grads = {n: torch.empty(x.shape, dtype=x.dtype, device=x.device) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+        new += list(grads.values())
+    else:
+        for n, x in (("dq", q), ("dk", k), ("dv", v)):
+            if grads.get(n) is None:
+                raise ValueError("grads must hold %s" % n)
+            _want(grads[n], n, q.dtype, x.shape, dev)
+    if ws is None:
+        n = gdr2_attn_bwd_workspace_bytes(N, T, Hq, Hkv, D, cu_seqlens is not None, dt)
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+        new.append(ws)
+    else:
+        _want(ws, "ws", torch.uint8, ws.shape, dev)
+    _keep_for(stream, *new)
+    if own and N == 0:
+        _zero(stream, *grads.values())
+    st = _launch(lib.gdr2_attn_bwd, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, o.data_ptr(),
+                 lse.data_ptr(), _adr(rest), dout.data_ptr(), _adr(cu_seqlens), grads["dq"].data_ptr(),
+                 grads["dk"].data_ptr(), grads["dv"].data_ptr(), N, T, Hq, Hkv, D, D ** -0.5 if scale is None else scale,
+                 max(-1, min(window, 0x7fffffff)), dt, int(own), ws.data_ptr(), ws.numel())
+    _raise(st, "gdr2_attn_bwd")
+    return grads
+
+
+class GDR2AttnFunction(torch.autograd.Function):
+    """Autograd wrapper of gdr2_attn_fwd and gdr2_attn_bwd; apply(q, k, v, cu_seqlens, scale, window) returns o. Where no
+    gradient is wanted it is gdr2_attn_fwd and saves nothing. Capturing forward and backward into a graph: as
+    GDR2ScalarFunction."""
+
+    @classmethod
+    def apply(cls, q, k, v, cu_seqlens=None, scale=None, window=0):
+        if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v)):
+            return super().apply(q, k, v, cu_seqlens, scale, window)
+        return gdr2_attn_fwd(q, k, v, cu_seqlens=cu_seqlens, scale=scale, window=window)
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_seqlens=None, scale=None, window=0):
+        here = torch.cuda.current_stream(q.device).cuda_stream
+        for m in _accumulation_streams((q, k, v)):
+            m.setdefault("gdr2_stream", here)
+        o, lse, rest = gdr2_attn_fwd(q, k, v, cu_seqlens=cu_seqlens, scale=scale, window=window, save_for_bwd=True)
+        ctx.save_for_backward(q, k, v, o, lse, rest, cu_seqlens)
+        ctx.scale, ctx.window = scale, window
+        return o
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, do):
+        q, k, v, o, lse, rest, cu_seqlens = ctx.saved_tensors
+        if torch.cuda.is_current_stream_capturing():
+            here = torch.cuda.current_stream(q.device).cuda_stream
+            if any(m.get("gdr2_stream", here) != here for m in _accumulation_streams((q, k, v))):
+                raise RuntimeError("cannot capture this backward: a graph of the same leaves from another stream is "
+                                   "still alive (drop its outputs first, or capture gdr2_attn_bwd)")
+        gr = gdr2_attn_bwd(q, k, v, o, lse, do.contiguous(), rest=rest, cu_seqlens=cu_seqlens, scale=ctx.scale,
+                           window=ctx.window)
+        return gr["dq"], gr["dk"], gr["dv"], None, None, None

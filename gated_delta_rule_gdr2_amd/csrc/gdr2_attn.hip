@@ -27,14 +27,10 @@
 // with the join, 5.15 TB/s, and 4096 of 300 tokens (5 GB) 1.10 ms, 4.6 TB/s; 24 windows of up to 2048 tokens, 16 heads of 64, fp32 (134 MB)
 // 38 us a pass, 3.5 TB/s, of which about 12 us are what even short rows take on the line (two launches,
 // the line, the join).
-#include "gdr2_attn.hpp"
-#include "gdr2_device.hpp"
+#include "gdr2_attn_device.hpp"
 
 namespace gdr2 {
 
-template <class OT>
-constexpr int attn_unit() { return attn_unit_tokens(sizeof(OT) == 2); }
-constexpr int AW = 8;           // waves of a workgroup
 constexpr int ATTN_MIN = 14;    // places of the line a workgroup takes at least (ATTN_COST + a unit for each wave)
 
 // The visible tokens of sequence b and its units (at least one, so that every row is written).
@@ -105,57 +101,11 @@ __device__ __forceinline__ AttnAt attn_find(const AttnArgs& a, const AttnLine& l
     return f;
 }
 
-// One unit's keys and values in registers, as loaded.
-template <class OT, int D>
-struct AttnTile;
-template <int D>
-struct AttnTile<bf16, D> {
-    static constexpr int EV = D / 16;
-    typedef bf16 VT __attribute__((ext_vector_type(EV)));
-    bf16x8 k[2][D / 32];  // [token tile][channel block]
-    VT v[8];              // token 16 (e / 4) + 4 lq + e % 4, channels EV li ..
-    int ok;               // bit s: token tile s lies on a valid page
-};
-template <int D>
-struct AttnTile<float, D> {
-    static constexpr int EV = D / 16;
-    f32x4 k[D / 16];      // channels 16 s + 4 lq ..
-    f32x4 v[4][EV / 4];   // token 4 lq + i
-    int ok;
-};
-
-// pg[s]: page of token tile s of the unit, or negative. Tiles never straddle pages (a page holds a
-// multiple of 16 tokens). Invalid tiles read page 0 and are masked.
 template <class OT, int D>
 __device__ __forceinline__ void attn_load(const AttnArgs& a, int u, int hkv, const int (&pg)[2], AttnTile<OT, D>& t) {
-    const int l = lane_id(), li = l & 15, lq = l >> 4;
-    constexpr int U = attn_unit<OT>();
-    t.ok = 0;
-#pragma unroll
-    for (int s = 0; s < U / 16; ++s) {
-        const int tok = (u * U + 16 * s) & (a.c.page - 1);
-        if (pg[s] >= 0) t.ok |= 1 << s;
-        const long long page = pg[s] >= 0 ? pg[s] : 0;
-        const OT* kp = (const OT*)a.c.k + page * a.c.ks[0] + tok * a.c.ks[1] + hkv * a.c.ks[2];
-        const OT* vp = (const OT*)a.c.v + page * a.c.vs[0] + tok * a.c.vs[1] + hkv * a.c.vs[2];
-        if constexpr (sizeof(OT) == 2) {
-            const OT* kr = kp + li * a.c.ks[1] + 8 * lq;
-#pragma unroll
-            for (int kb = 0; kb < D / 32; ++kb) t.k[s][kb] = *(const bf16x8*)(kr + 32 * kb);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                t.v[4 * s + i] = *(const typename AttnTile<OT, D>::VT*)(vp + (4 * lq + i) * a.c.vs[1] + (D / 16) * li);
-        } else {
-            const OT* kr = kp + li * a.c.ks[1] + 4 * lq;
-#pragma unroll
-            for (int kb = 0; kb < D / 16; ++kb) t.k[kb] = *(const f32x4*)(kr + 16 * kb);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j)
-                    t.v[i][j] = *(const f32x4*)(vp + (4 * lq + i) * a.c.vs[1] + (D / 16) * li + 4 * j);
-        }
-    }
+    attn_ok<OT, D>(pg, t);
+    attn_load_k<OT, D>(a.c, u, hkv, pg, t);
+    attn_load_v<OT, D>(a.c, u, hkv, pg, t);
 }
 
 // Running softmax of a wave: lane (li, lq) holds head li; l is its own tokens' share of the weight.
@@ -273,17 +223,7 @@ __device__ __forceinline__ void attn_run(const AttnArgs& a, int b, int hr, const
     const int heads = min(a.gh, a.G - (hr % a.NG) * a.gh);
     const int u0 = sp.u0 + i0;
     const int work = sp.hi > sp.lo ? n : 0;  // a row with nothing to see has a unit, but no page to read
-    auto pages = [&](int i, int (&pg)[2]) {  // pages of unit i of the run
-#pragma unroll
-        for (int s = 0; s < U / 16; ++s) {
-            const int tok = (u0 + i) * U + 16 * s;
-            pg[s] = -1;
-            if (i < work && tok < sp.hi) {
-                const int p = a.c.table[(size_t)b * a.c.max_pages + (tok >> a.c.shift)];
-                pg[s] = (unsigned)p < (unsigned)a.c.pages ? p : -1;
-            }
-        }
-    };
+    auto pages = [&](int i, int (&pg)[2]) { attn_pages<OT>(a.c, b, u0 + i, sp.hi, i < work, pg); };  // of unit i of the run
     int pg[2] = {-1, -1};
     pages(wv, pg);
     QT q[NQ];

@@ -1,4 +1,4 @@
-// C ABI of libgdr2: the gated delta rule with scalar gates and attention over a paged cache --
+// C ABI of libgdr2: the gated delta rule with scalar gates, attention over a paged cache and over whole sequences --
 // argument validation (host only, before any HIP call), workspace sizing and dispatch. See
 // include/gdr2.h for the contract.
 #include "../../include/gdr2.h"
@@ -9,7 +9,10 @@
 
 #include "gdr2_attn.hpp"
 #include "gdr2_kernels.hpp"
+#include "gdr2_pages.hpp"
+#include "gdr2_prompt.hpp"
 #include "gdr2_scalar.hpp"
+#include "gdr2_tree.hpp"
 
 namespace {
 
@@ -134,6 +137,49 @@ int attn_shape(int B, int Hq, int Hkv, int D, int dtype) {
 
 // heads of a head group: the matrix cores' 16 columns at most
 int group_heads(int Hq, int Hkv) { return Hq / Hkv < 16 ? Hq / Hkv : 16; }
+
+// Attention over whole sequences: tokens below 2^31 - 1024 (a tile's last row still fits in 32 bits), and launches of
+// fewer than 2^32 threads at the smallest tile.
+int prompt_shape(int N, int T, int Hq, int Hkv, int D, int dtype, bool packed) {
+    if (N < 0 || T < 0) return GDR2_ERR_SHAPE;
+    const int st = attn_shape(1, Hq, Hkv, D, dtype);
+    if (st != GDR2_OK) return st;
+    const long long tokens = packed ? T : (long long)N * T;
+    if (tokens > 0x7fffffffLL - 1024 || tokens * Hq > (1LL << 40)) return GDR2_ERR_SHAPE;
+    if (N > 0 && T > 0 && gdr2::prompt_slots(N, T, packed, 32) * Hq >= (1LL << 32) / 256) return GDR2_ERR_SHAPE;
+    return GDR2_OK;
+}
+bool prompt_none(int N, int T, int Hq) { return N == 0 || T == 0 || Hq == 0; }
+
+int prompt_fill(gdr2::PromptArgs& a, const long long* strides, const int* cu, int N, int T, int Hq, int Hkv, int D,
+                float scale, int window, int dtype, int zero_rest) {
+    if (!isfinite(scale) || window < 0) return GDR2_ERR_VALUE;
+    const long long heads[3] = {Hq, Hkv, Hkv};
+    long long* const to[3] = {a.qs, a.ks, a.vs};
+    for (int i = 0; i < 3; ++i) {
+        to[i][0] = strides ? strides[2 * i] : heads[i] * D;
+        to[i][1] = strides ? strides[2 * i + 1] : D;
+        for (int j = 0; j < 2; ++j)
+            if (to[i][j] < 0 || to[i][j] % (16 / esize(dtype)) != 0) return GDR2_ERR_ALIGN;
+    }
+    a.cu = cu;
+    a.N = N; a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.D = D;
+    a.window = window > 0 && window < T ? window : T;
+    a.zero_rest = zero_rest;
+    a.neg = scale < 0.f;
+    // a scale of zero weighs all that is seen alike, and so does one too small to matter, which leaves -inf what it is
+    a.scale = fabsf(scale);
+    a.scale2 = fmaxf((float)(fabs((double)scale) * 1.4426950408889634), 1e-30f);
+    return GDR2_OK;
+}
+
+int tree_shape(int B, int T, int Hq, int Hkv, int D, int dtype) {
+    if (T < 0) return GDR2_ERR_SHAPE;
+    const int st = attn_shape(B, Hq, Hkv, D, dtype);
+    if (st != GDR2_OK) return st;
+    if (T > gdr2::TREE_MAX || (long long)B * T * Hq > 0x7fffffffLL) return GDR2_ERR_SHAPE;
+    return GDR2_OK;
+}
 
 }  // namespace
 
@@ -280,6 +326,134 @@ int gdr2_kv_append(const void* k, const void* v, void* k_cache, void* v_cache, c
     a.B = B; a.tokens = tokens; a.Hkv = Hkv; a.D = D;
     return gdr2::launch_append(a, dtype == GDR2_DTYPE_BF16, (hipStream_t)stream) == hipSuccess ? GDR2_OK
                                                                                                 : GDR2_ERR_HIP;
+}
+
+int gdr2_attn_fwd(const void* q, const void* k, const void* v, const long long* strides, const int* cu_seqlens, void* o,
+                  float* lse, void* rest, int N, int T, int Hq, int Hkv, int D, float scale, int window, int dtype,
+                  int zero_rest, void* stream) {
+    int st = prompt_shape(N, T, Hq, Hkv, D, dtype, cu_seqlens != nullptr);
+    if (st != GDR2_OK) return st;
+    if (prompt_none(N, T, Hq)) return GDR2_OK;
+    if (!q || !k || !v || !o) return GDR2_ERR_NULL;
+    gdr2::PromptArgs a = {};
+    st = prompt_fill(a, strides, cu_seqlens, N, T, Hq, Hkv, D, scale, window, dtype, zero_rest);
+    if (st != GDR2_OK) return st;
+    const void* const ptrs[] = {q, k, v, o, rest};
+    const void* const floats[] = {lse};
+    if (!all_aligned(ptrs) || !gates_aligned(floats, 4)) return GDR2_ERR_ALIGN;
+    a.q = q; a.k = k; a.v = v; a.o = o; a.lse = lse;
+    a.rest = dtype == GDR2_DTYPE_BF16 ? rest : nullptr;
+    return gdr2::launch_prompt_fwd(a, dtype == GDR2_DTYPE_BF16, (hipStream_t)stream) == hipSuccess ? GDR2_OK
+                                                                                                    : GDR2_ERR_HIP;
+}
+
+size_t gdr2_attn_bwd_workspace_bytes(int N, int T, int Hq, int Hkv, int D, int packed, int dtype) {
+    if (prompt_shape(N, T, Hq, Hkv, D, dtype, packed != 0) != GDR2_OK || prompt_none(N, T, Hq)) return 0;
+    return 2 * (size_t)(packed ? T : (long long)N * T) * Hq * sizeof(float);
+}
+
+int gdr2_attn_bwd(const void* q, const void* k, const void* v, const long long* strides, const void* o, const float* lse,
+                  const void* rest, const void* dout, const int* cu_seqlens, void* dq, void* dk_, void* dv_, int N, int T,
+                  int Hq, int Hkv, int D, float scale, int window, int dtype, int zero_rest, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+    const bool packed = cu_seqlens != nullptr;
+    int st = prompt_shape(N, T, Hq, Hkv, D, dtype, packed);
+    if (st != GDR2_OK) return st;
+    if (prompt_none(N, T, Hq)) return GDR2_OK;
+    if (!q || !k || !v || !o || !lse || !dout || !dq || !dk_ || !dv_) return GDR2_ERR_NULL;
+    gdr2::PromptArgs a = {};
+    st = prompt_fill(a, strides, cu_seqlens, N, T, Hq, Hkv, D, scale, window, dtype, zero_rest);
+    if (st != GDR2_OK) return st;
+    const void* const ptrs[] = {q, k, v, o, rest, dout, dq, dk_, dv_, workspace};
+    const void* const floats[] = {lse};
+    if (!all_aligned(ptrs) || !gates_aligned(floats, 4)) return GDR2_ERR_ALIGN;
+    if (!workspace || workspace_bytes < gdr2_attn_bwd_workspace_bytes(N, T, Hq, Hkv, D, packed, dtype))
+        return GDR2_ERR_WORKSPACE;
+    a.q = q; a.k = k; a.v = v; a.o = (void*)o; a.lse = (float*)lse;
+    a.rest = dtype == GDR2_DTYPE_BF16 ? (void*)rest : nullptr;
+    a.dout = dout; a.dq = dq; a.dk = dk_; a.dv = dv_;
+    a.lse2 = (float*)workspace;
+    a.delta = a.lse2 + (size_t)(packed ? T : (long long)N * T) * Hq;
+    return gdr2::launch_prompt_bwd(a, dtype == GDR2_DTYPE_BF16, (hipStream_t)stream) == hipSuccess ? GDR2_OK
+                                                                                                    : GDR2_ERR_HIP;
+}
+
+size_t gdr2_attn_tree_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int dtype) {
+    if (tree_shape(B, T, Hq, Hkv, D, dtype) != GDR2_OK || B == 0 || T == 0 || Hq == 0) return 0;
+    gdr2::TreeArgs a = {};
+    a.T = T; a.G = Hq / Hkv; a.D = D;
+    gdr2::tree_rows(a);
+    return 2 * (size_t)a.wgs * gdr2::tree_part_floats(a) * sizeof(float);
+}
+
+int gdr2_attn_tree(const void* q, const int* parents, const void* k_cache, const void* v_cache,
+                   const long long* cache_strides, const int* block_table, const int* starts, void* o, float* lse, int B,
+                   int T, int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, float scale, int window,
+                   int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = tree_shape(B, T, Hq, Hkv, D, dtype);
+    if (st != GDR2_OK) return st;
+    if (B == 0 || T == 0 || Hq == 0) return GDR2_OK;
+    st = cache_check(k_cache, v_cache, cache_strides, block_table, B, num_pages, page_size, max_pages, esize(dtype));
+    if (st != GDR2_OK) return st;
+    if (!q || !o || !parents || !starts) return GDR2_ERR_NULL;
+    if (!isfinite(scale) || window < 0) return GDR2_ERR_VALUE;
+    if ((long long)max_pages * page_size > 0x7fffffffLL - 128) return GDR2_ERR_SHAPE;
+    gdr2::TreeArgs a = {};
+    a.q = q; a.parents = parents; a.starts = starts; a.o = o; a.lse = lse;
+    a.part = (float*)workspace;
+    fill_cache(a.c, k_cache, v_cache, cache_strides, block_table, num_pages, page_size, num_pages > 0 ? max_pages : 0);
+    a.B = B; a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.G = Hq / Hkv;
+    a.window = window;
+    a.scale2 = (float)((double)scale * 1.4426950408889634);
+    gdr2::tree_rows(a);
+    if (gdr2::tree_line_places(a, gdr2::attn_unit_tokens(dtype == GDR2_DTYPE_BF16)) > 0x7fffffffLL) return GDR2_ERR_SHAPE;
+    const void* const ptrs[] = {q, k_cache, v_cache, o, workspace};
+    const void* const words[] = {parents, starts, block_table, lse};
+    if (!all_aligned(ptrs) || !gates_aligned(words, 4)) return GDR2_ERR_ALIGN;
+    if (!workspace || workspace_bytes < gdr2_attn_tree_workspace_bytes(B, T, Hq, Hkv, D, dtype)) return GDR2_ERR_WORKSPACE;
+    return gdr2::launch_tree(a, dtype == GDR2_DTYPE_BF16, (hipStream_t)stream) == hipSuccess ? GDR2_OK : GDR2_ERR_HIP;
+}
+
+int gdr2_kv_keep(void* k_cache, void* v_cache, const long long* cache_strides, const int* block_table, const int* starts,
+                 const int* path, int* lengths, int B, int P, int Hkv, int D, int num_pages, int page_size, int max_pages,
+                 int dtype, void* stream) {
+    int st = attn_shape(B, Hkv, Hkv, D, dtype);
+    if (st != GDR2_OK) return st;
+    if (P < 0 || P > gdr2::TREE_MAX) return GDR2_ERR_SHAPE;
+    if (B == 0) return GDR2_OK;
+    st = cache_check(k_cache, v_cache, cache_strides, block_table, B, num_pages, page_size, max_pages, esize(dtype));
+    if (st != GDR2_OK) return st;
+    if (!starts || (P > 0 && !path)) return GDR2_ERR_NULL;
+    const void* const ptrs[] = {k_cache, v_cache};
+    const void* const words[] = {block_table, starts, path, lengths};
+    if (!all_aligned(ptrs) || !gates_aligned(words, 4)) return GDR2_ERR_ALIGN;
+    if ((long long)B * (Hkv * (long long)(D / (16 / esize(dtype))) / 16 + 1) >= (1LL << 32) / 512) return GDR2_ERR_SHAPE;
+    gdr2::KeepArgs a = {};
+    fill_cache(a.c, k_cache, v_cache, cache_strides, block_table, num_pages, page_size, num_pages > 0 ? max_pages : 0);
+    a.starts = starts; a.path = path; a.lengths = lengths;
+    a.B = B; a.P = P; a.Hkv = Hkv; a.D = D; a.es = esize(dtype);
+    return gdr2::launch_keep(a, (hipStream_t)stream) == hipSuccess ? GDR2_OK : GDR2_ERR_HIP;
+}
+
+int gdr2_kv_pages(const int* lengths, const int* counts, int* block_table, int* free_pages, int* num_free,
+                  int* new_lengths, int* cu_seqlens, long long* slots, int B, int max_tokens, int num_pages, int page_size,
+                  int max_pages, void* stream) {
+    if (B < 0 || max_tokens < 0 || num_pages < 0 || max_pages < 0) return GDR2_ERR_SHAPE;
+    if (page_size < 16 || page_size > (1 << 20) || (page_size & (page_size - 1)) != 0) return GDR2_ERR_VALUE;
+    if ((long long)max_pages * page_size > 0x7fffffffLL) return GDR2_ERR_SHAPE;
+    if (!num_free || !cu_seqlens) return GDR2_ERR_NULL;
+    if (B > 0 && (!lengths || !counts || !new_lengths || (max_pages > 0 && !block_table))) return GDR2_ERR_NULL;
+    if (num_pages > 0 && !free_pages) return GDR2_ERR_NULL;
+    const void* const words[] = {lengths, counts, block_table, free_pages, num_free, new_lengths, cu_seqlens};
+    const void* const longs[] = {slots};
+    if (!gates_aligned(words, 4) || !gates_aligned(longs, 8)) return GDR2_ERR_ALIGN;
+    gdr2::PagesArgs a = {};
+    a.lengths = lengths; a.counts = counts; a.table = block_table; a.free_pages = free_pages; a.num_free = num_free;
+    a.out = new_lengths; a.cu = cu_seqlens; a.slots = max_tokens > 0 ? slots : nullptr;
+    a.B = B; a.max_tokens = max_tokens; a.pages = num_pages; a.page = page_size;
+    a.shift = __builtin_ctz(page_size);
+    a.max_pages = max_pages;
+    return gdr2::launch_pages(a, (hipStream_t)stream) == hipSuccess ? GDR2_OK : GDR2_ERR_HIP;
 }
 
 }  // extern "C"

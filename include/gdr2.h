@@ -314,6 +314,93 @@ int gdr2_kv_append(const void* k, const void* v, void* k_cache, void* v_cache, c
                    const int* block_table, const int* starts, const int* cu_seqlens, int B, int tokens, int Hkv, int D,
                    int num_pages, int page_size, int max_pages, int dtype, void* stream);
 
+/* Causal attention over whole sequences, for prompts and for training:
+ *
+ *     o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j),   lse_i = log sum_j p_ij
+ *
+ * over the tokens j <= i of token i's sequence, or the last `window` of them (i included) when window > 0.
+ *   q, o, rest, dout, dq : [tokens][Hq][D] in `dtype`;   k, v, dk_, dv_ : [tokens][Hkv][D];   lse : fp32 [tokens][Hq]
+ * Hq is a multiple of Hkv, query head h reading key head h / (Hq / Hkv); dk_ and dv_ are summed over the heads that
+ * share them. Sequences, cu_seqlens and zero_rest as in gdr2_scalar_fwd (zero_rest covers lse and rest too); calls
+ * without tokens do nothing. strides (a host array, or NULL: contiguous) = { token stride, head stride } of q, then of
+ * k, then of v, in elements, multiples of 16 bytes, for inputs that are parts of one projection's output; sequences of
+ * one length follow one another at T token strides. All else is contiguous. D is 64 or 128, dtype BF16 or F32.
+ *
+ * gdr2_attn_bwd takes o and lse as gdr2_attn_fwd left them for the same inputs. `rest`, NULL or a tensor as o, bf16
+ * only (ignored for fp32), takes what o's rounding left over, o + rest being the result to 16 bits; the backward reads
+ * it, where it is given, for sum_c dout_c o_c, whose rounding error would otherwise be the largest part of dq's and dk_'s
+ * in rows that see few tokens. Scores, softmax statistics and sums are fp32; with bf16 the weights and their gradients
+ * enter the second products as one bf16 each, so that outputs carry two roundings, their own among them.
+ *
+ * A value that is infinite or NaN at a token reaches the tokens of its own sequence, also some before it; other
+ * sequences are not affected. Results repeat bit for bit. Outputs must not overlap one another or the inputs.
+ * Workspace: gdr2_attn_bwd_workspace_bytes, of no content between calls; calls that may overlap need one each.
+ * Errors as gdr2_attn_step; GDR2_ERR_SHAPE also for 2^31 - 1024 tokens or 2^24 workgroups (32 tokens of a head) and more. */
+int gdr2_attn_fwd(const void* q, const void* k, const void* v, const long long* strides, const int* cu_seqlens, void* o,
+                  float* lse, void* rest, int N, int T, int Hq, int Hkv, int D, float scale, int window, int dtype,
+                  int zero_rest, void* stream);
+
+size_t gdr2_attn_bwd_workspace_bytes(int N, int T, int Hq, int Hkv, int D, int packed, int dtype);
+
+int gdr2_attn_bwd(const void* q, const void* k, const void* v, const long long* strides, const void* o, const float* lse,
+                  const void* rest, const void* dout, const int* cu_seqlens, void* dq, void* dk_, void* dv_, int N, int T,
+                  int Hq, int Hkv, int D, float scale, int window, int dtype, int zero_rest, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Attention of a tree of T drafted tokens (at most 64) a sequence over a paged cache, as speculative decoding checks
+ * them; a chain of T new tokens is a tree too. The drafts' keys and values stand in the cache behind the starts[b]
+ * tokens that sequence b holds, draft i at position starts[b] + i (gdr2_kv_append puts them there).
+ *   q, o    : [B][T][Hq][D];   lse : fp32 [B][T][Hq], or NULL
+ *   parents : int32 [B][T] on the device: the draft that i continues, one of 0 .. i - 1, or -1 where it continues the
+ *             sequence itself. Any other value makes it padding, and with it all that continue it
+ *   starts  : int32 [B] on the device, taken as 0 .. max_pages page_size where outside
+ * Draft i sees the tokens that its sequence holds, the drafts on its way to the root, and itself; with window > 0 the
+ * last `window` of these (the place of a draft in its sequence is starts[b] + the number of drafts above it).
+ * Caches, strides, block_table, scale and results as in gdr2_attn_step; padding gets o = 0 and lse = -inf. What the
+ * cache holds where no draft of the sequence sees it does not matter; a value that some of its drafts see has to be finite.
+ * GDR2_ERR_SHAPE: T over 64, max_pages page_size over 2^31 - 129, B T Hq over 2^31 - 1, and long lines as there, a
+ * row being 128 (T Hq / Hkv of 16 and less: that many, else a power of two times 32, up to 256) of a key head's pairs
+ * of drafts and heads. Workspace: gdr2_attn_tree_workspace_bytes, of no content between calls; calls that may overlap
+ * need one each. */
+size_t gdr2_attn_tree_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int dtype);
+
+int gdr2_attn_tree(const void* q, const int* parents, const void* k_cache, const void* v_cache,
+                   const long long* cache_strides, const int* block_table, const int* starts, void* o, float* lse, int B,
+                   int T, int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, float scale, int window,
+                   int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Keeps an accepted path of a tree: the token at position starts[b] + path[b][j] goes to position starts[b] + j, for
+ * the entries of path[b] (int32 [B][P] on the device, P at most 64) before its first negative one. All are read before
+ * any is written, so entries may come in any order and more than once. lengths (int32 [B], or NULL) gets starts[b] and
+ * the number of these entries, the tokens that the sequence then holds. Tokens whose old or new position is on no page
+ * are not moved. Pages that a call writes belong to one sequence each. lengths must not overlap the inputs. */
+int gdr2_kv_keep(void* k_cache, void* v_cache, const long long* cache_strides, const int* block_table, const int* starts,
+                 const int* path, int* lengths, int B, int P, int Hkv, int D, int num_pages, int page_size, int max_pages,
+                 int dtype, void* stream);
+
+/* Pages for the tokens to come. All arrays are on the device.
+ *   lengths, counts : int32 [B]: the tokens that each request holds (taken as 0 .. max_pages page_size where outside),
+ *                     and how many come to it; a negative count ends the request
+ *   block_table     : int32 [B][max_pages], updated; entries outside 0 .. num_pages - 1 are no page
+ *   free_pages      : int32 [num_pages], updated: a stack whose first num_free[0] (int32, updated; taken as
+ *                     0 .. num_pages where outside) entries are the free pages
+ *   new_lengths     : int32 [B]: tokens held with the new ones
+ *   cu_seqlens      : int32 [B + 1]: bounds of the requests' new tokens, packed one after another; at most max_tokens
+ *   slots           : int64 [max_tokens], or NULL: page * page_size + offset for each packed token, -1 where it has none
+ * First the requests that end give back what pages they have, in the order of the requests and of their tables; their
+ * table entries become -1 and their new lengths 0. Then the requests to which tokens come take, in order, a page from
+ * the top of the stack for each place of the table from lengths / page_size on that the new tokens reach and that holds
+ * no page. A request takes all it lacks or nothing: nothing where the table is too short, where the new tokens
+ * would end behind max_tokens, or where it and those before it lack more pages than are free (also one that lacks fewer,
+ * behind one that lacked too many; those that lack none go on). Such a request's table and length stay as they were and
+ * its tokens have no slots (starts and cu_seqlens of gdr2_kv_append would still place those that fit its last page,
+ * behind what it holds). Each page has one owner: one that a table names twice is given back twice.
+ * A call with the same lengths and counts again changes nothing. new_lengths and cu_seqlens must not overlap the inputs.
+ * page_size as in gdr2_attn_step; GDR2_ERR_SHAPE for max_pages page_size over 2^31 - 1. */
+int gdr2_kv_pages(const int* lengths, const int* counts, int* block_table, int* free_pages, int* num_free,
+                  int* new_lengths, int* cu_seqlens, long long* slots, int B, int max_tokens, int num_pages, int page_size,
+                  int max_pages, void* stream);
+
 /* Static description of a status code. */
 const char* gdr2_strerror(int status);
 
