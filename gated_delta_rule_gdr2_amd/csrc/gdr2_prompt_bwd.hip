@@ -12,9 +12,13 @@ namespace gdr2 {
 
 constexpr int BT = 64;  // rows of a tile
 
+// waves a SIMD that a kernel's registers have to leave room for
+template <class OT, int D>
+constexpr int prompt_waves() { return sizeof(OT) == 4 && D == 128 ? 1 : 2; }
+
 // ---------------------------------------------------------------- dQ: as the forward, keys in tiles
 template <class OT, int D, int NW>
-__global__ __launch_bounds__(64 * NW) void k_prompt_dq(PromptArgs a) {
+__global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dq(PromptArgs a) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
     constexpr int QT = 32 * NW, TB = BT * TL::RB;
@@ -113,7 +117,7 @@ __global__ __launch_bounds__(64 * NW) void k_prompt_dq(PromptArgs a) {
 
 // ---------------------------------------------------------------- dK, dV: queries in tiles
 template <class OT, int D, int NW>
-__global__ __launch_bounds__(64 * NW) void k_prompt_dkv(PromptArgs a) {
+__global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dkv(PromptArgs a) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
     constexpr int KT = 32 * NW, TB = BT * TL::RB, BUF = 2 * TB + 2 * BT * 4;
