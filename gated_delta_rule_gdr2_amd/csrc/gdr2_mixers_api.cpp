@@ -146,7 +146,7 @@ int prompt_shape(int N, int T, int Hq, int Hkv, int D, int dtype, bool packed) {
     if (st != GDR2_OK) return st;
     const long long tokens = packed ? T : (long long)N * T;
     if (tokens > 0x7fffffffLL - 1024 || tokens * Hq > (1LL << 40)) return GDR2_ERR_SHAPE;
-    if (N > 0 && T > 0 && gdr2::prompt_slots(N, T, packed, 32) * Hq >= (1LL << 32) / 256) return GDR2_ERR_SHAPE;
+    if (N > 0 && T > 0 && gdr2::prompt_blocks(N, T, packed) * Hq >= (1LL << 32) / 512) return GDR2_ERR_SHAPE;
     return GDR2_OK;
 }
 bool prompt_none(int N, int T, int Hq) { return N == 0 || T == 0 || Hq == 0; }
@@ -349,7 +349,8 @@ int gdr2_attn_fwd(const void* q, const void* k, const void* v, const long long* 
 
 size_t gdr2_attn_bwd_workspace_bytes(int N, int T, int Hq, int Hkv, int D, int packed, int dtype) {
     if (prompt_shape(N, T, Hq, Hkv, D, dtype, packed != 0) != GDR2_OK || prompt_none(N, T, Hq)) return 0;
-    return 2 * (size_t)(packed ? T : (long long)N * T) * Hq * sizeof(float);
+    const size_t tokens = (size_t)(packed ? T : (long long)N * T), parts = gdr2::prompt_parts(N, T, Hq, Hkv, packed != 0);
+    return (2 * tokens * Hq + (parts > 1 ? 2 * parts * tokens * Hkv * D : 0)) * sizeof(float);
 }
 
 int gdr2_attn_bwd(const void* q, const void* k, const void* v, const long long* strides, const void* o, const float* lse,
@@ -373,7 +374,10 @@ int gdr2_attn_bwd(const void* q, const void* k, const void* v, const long long* 
     a.rest = dtype == GDR2_DTYPE_BF16 ? (void*)rest : nullptr;
     a.dout = dout; a.dq = dq; a.dk = dk_; a.dv = dv_;
     a.lse2 = (float*)workspace;
-    a.delta = a.lse2 + (size_t)(packed ? T : (long long)N * T) * Hq;
+    const size_t rows = (size_t)(packed ? T : (long long)N * T) * Hq;
+    a.delta = a.lse2 + rows;
+    a.part = a.delta + rows;
+    a.parts = gdr2::prompt_parts(N, T, Hq, Hkv, packed);
     return gdr2::launch_prompt_bwd(a, dtype == GDR2_DTYPE_BF16, (hipStream_t)stream) == hipSuccess ? GDR2_OK
                                                                                                     : GDR2_ERR_HIP;
 }

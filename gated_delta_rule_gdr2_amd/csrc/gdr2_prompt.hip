@@ -12,13 +12,13 @@
 
 namespace gdr2 {
 
-constexpr int PKT = 64;  // keys of a tile
-
-template <class OT, int D, int NW>
-__global__ __launch_bounds__(64 * NW) void k_prompt_fwd(PromptArgs a) {
+// RW x 32 queries a workgroup, S waves for each 32 of them, which share the keys
+template <class OT, int D, int RW, int S>
+__global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt_fwd(PromptArgs a) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
-    constexpr int QT = 32 * NW, TB = PKT * TL::RB;
+    constexpr int NW = RW * S, QT = 32 * RW, KT = tile_rows(S), TB = KT * TL::RB, NB = KT / 32 / S;
+    constexpr int ACC = D / 32 * 4096;  // bytes of a wave's accumulators
     extern __shared__ __align__(16) char smem[];
     lds_char* lds = (lds_char*)smem;
     poison_lds(lds, 4 * TB);
@@ -34,84 +34,108 @@ __global__ __launch_bounds__(64 * NW) void k_prompt_fwd(PromptArgs a) {
     }
     if (!at.any) return;
     const int l = lane_id(), h = l >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rw = S == 1 ? w : w % RW, sp = S == 1 ? 0 : w / RW;
     const int q0 = at.tile * QT, last = at.len - 1;
-    const int wq0 = q0 + 32 * w, qi = wq0 + (l & 31);
+    const int wq0 = q0 + 32 * rw, qi = wq0 + (l & 31);
     const long long tok = at.tok0 + min(qi, last);
     FR qf[D / 16];
     load_own<OT, D>((const OT*)a.q + tok * a.qs[0] + hq * a.qs[1], a.neg, qf);
     const char* kb = (const char*)((const OT*)a.k + at.tok0 * a.ks[0] + hk * a.ks[1]);
     const char* vb = (const char*)((const OT*)a.v + at.tok0 * a.vs[0] + hk * a.vs[1]);
-    const long long krs = a.ks[0] * (int)sizeof(OT), vrs = a.vs[0] * (int)sizeof(OT);
+    const TileLoad<OT, D, KT, NW, true> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
     // the tiles that any of the workgroup's queries sees
-    const int t0 = max(0, q0 - a.window + 1) / PKT, t1 = min(q0 + QT - 1, last) / PKT;
+    const int t0 = max(0, q0 - a.window + 1) / KT, t1 = min(q0 + QT - 1, last) / KT;
     auto fetch = [&](int t) {
         lds_char* b = lds + (t & 1) * 2 * TB;
-        TL::template load<PKT, NW>(kb, krs, t * PKT, last, b, w);
-        TL::template load<PKT, NW>(vb, vrs, t * PKT, last, b + TB, w);
+        lk(kb, t * KT, b);
+        lv(vb, t * KT, b + TB);
     };
     fetch(t0);
     f32x16 acc[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[i] = zero16();
-    float m = -INFINITY, sum = 0.f;
+    float m = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};  // the lane's weights, in four chains
+    TL tl;
     for (int t = t0; t <= t1; ++t) {
+        tl.fresh();
         wait_vm<0>();
         __syncthreads();  // the tile has landed, and everyone is done with the one before
         if (t < t1) fetch(t + 1);
-        const int k0 = t * PKT;
-        if (k0 > wq0 + 31 || k0 + PKT - 1 <= wq0 - a.window) continue;  // nothing of it is seen by this wave
+        const int r0 = 32 * NB * sp, k0 = t * KT + r0;  // the wave's keys of the tile
+        if (k0 > wq0 + 31 || wq0 > last || k0 + 32 * NB - 1 <= wq0 - a.window) continue;  // it sees nothing of them
         const lds_char* kt = lds + (t & 1) * 2 * TB;
         const lds_char* vt = kt + TB;
-        f32x16 s[2];
+        f32x16 s[NB];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            s[n] = zero16();
+        for (int n = 0; n < NB; ++n) s[n] = zero16();
 #pragma unroll
-            for (int b = 0; b < D / 16; ++b) mma32(s[n], TL::rows(kt, 32 * n, 16 * b), qf[b]);
-        }
-        if (k0 + PKT - 1 > wq0 || k0 <= wq0 + 31 - a.window) {
+        for (int b = 0; b < D / 16; ++b)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NB; ++n) mma32(s[n], tl.rows(kt, r0 + 32 * n, 16 * b), qf[b]);
+        if constexpr (sizeof(OT) == 2) reads_ahead<D / 16 * NB, 1, 4>();
+        if (k0 + 32 * NB - 1 > wq0 || k0 <= wq0 + 31 - a.window) {
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int d = qi - (k0 + 32 * n + 8 * (r >> 2) + 4 * h + (r & 3));
                     s[n][r] = d >= 0 && d < a.window ? s[n][r] : -INFINITY;
                 }
         }
-        float mx = s[0][0];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[n][r]);
-        mx = fmaxf(mx, other_half(mx)) * a.scale2;
+        const float mx = max_halves(max_acc(s)) * a.scale2;
         // the reference moves only where it would let a weight pass 2^8: sums and weights are relative to it
         if (__any(mx > m + 8.f)) {
             const float mn = fmaxf(m, mx), al = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
             m = mn;
-            sum *= al;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum[c] *= al;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) acc[i] = acc[i] * al;
         }
         const float mu = m == -INFINITY ? 0.f : m;
-        FR pf[4];
+        FR pf[2 * NB];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < NB; ++n) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 s[n][r] = __builtin_amdgcn_exp2f(fmaf(s[n][r], a.scale2, -mu));
-                sum += s[n][r];
+                sum[r & 3] += s[n][r];
             }
             pf[2 * n] = acc_frag<OT>(s[n], 0);
             pf[2 * n + 1] = acc_frag<OT>(s[n], 1);
         }
 #pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt)
+        for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
-            for (int b = 0; b < 4; ++b) mma32(acc[dt], TL::cols(vt, 32 * dt, 16 * b), pf[b]);
+            for (int dt = 0; dt < D / 32; ++dt) mma32(acc[dt], tl.cols(vt, 32 * dt, r0 + 16 * b), pf[b]);
+        if constexpr (sizeof(OT) == 2) reads_ahead<D / 16 * NB, 2, 4>();
     }
-    sum += other_half(sum);
+    float total = sum_halves((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if constexpr (S > 1) {
+        // join the waves of the same queries, in their order
+        __syncthreads();
+        if (sp > 0) {
+            lds_char* p = lds + ((sp - 1) * RW + rw) * (ACC + 512);
+            put_acc(p, acc);
+            lds_store<float>(p + ACC + l * 4, m);
+            lds_store<float>(p + ACC + 256 + l * 4, total);
+        }
+        __syncthreads();
+        if (sp > 0) return;
+        for (int x = 0; x < S - 1; ++x) {
+            const lds_char* p = lds + (x * RW + rw) * (ACC + 512);
+            const float mo = lds_load<float>(p + ACC + l * 4), so = lds_load<float>(p + ACC + 256 + l * 4);
+            const float mn = fmaxf(m, mo), mu = mn == -INFINITY ? 0.f : mn;
+            const float fa = __builtin_amdgcn_exp2f(m - mu), fb = __builtin_amdgcn_exp2f(mo - mu);
+            m = mn;
+            total = total * fa + so * fb;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) acc[i] = acc[i] * fa;
+            add_acc(p, fb, acc);
+        }
+    }
     if (qi > last) return;
-    const float inv = 1.f / sum;
+    const float inv = 1.f / total;
     const size_t row = (size_t)(at.tok0 + qi) * a.Hq + hq;
     if (sizeof(OT) == 2 && a.rest) {
         OT *po = (OT*)a.o + row * D, *pr = (OT*)a.rest + row * D;
@@ -131,25 +155,234 @@ __global__ __launch_bounds__(64 * NW) void k_prompt_fwd(PromptArgs a) {
     } else {
         store_col<OT, D>((OT*)a.o + row * D, acc, inv);
     }
-    if (a.lse && h == 0) a.lse[row] = (m + __log2f(sum)) * 0.6931471805599453f;
+    if (a.lse && h == 0) a.lse[row] = (m + __log2f(total)) * 0.6931471805599453f;
 }
 
-template <class OT, int D, int NW>
+template <class OT, int D, int RW, int S>
 static hipError_t launch_fwd_t(const PromptArgs& a, hipStream_t stream) {
-    constexpr int LDS = 4 * PKT * D * (int)sizeof(OT);
-    const auto f = k_prompt_fwd<OT, D, NW>;
+    constexpr int TILES = 4 * tile_rows(S) * D * (int)sizeof(OT), JOIN = (S - 1) * RW * (D / 32 * 4096 + 512);
+    constexpr int LDS = TILES > JOIN ? TILES : JOIN;
+    static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
+    const auto f = k_prompt_fwd<OT, D, RW, S>;
     if (LDS > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
         if (e != hipSuccess) return e;
     }
-    const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 32 * NW) * a.Hq;
-    hipLaunchKernelGGL(f, dim3((unsigned)n), dim3(64 * NW), LDS, stream, a);
+    const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 32 * RW) * a.Hq;
+    hipLaunchKernelGGL(f, dim3((unsigned)n), dim3(64 * RW * S), LDS, stream, a);
     return hipGetLastError();
 }
 
+// Long sequences: 256 queries a workgroup, two waves a SIMD that take turns. A wave's tile is a phase of matrix products
+// (the weights of the tile before with its values, then this tile's scores) and one of vector work (its softmax), which
+// take about as long; the waves 4 .. 7 are a phase behind the waves 0 .. 3, with a barrier between phases, so that on
+// each SIMD one wave multiplies while the other is in its softmax. Phase 2 i is the products of tile i (first half), phase
+// 2 i + 1 its softmax.
+//
+// Tiles are three deep in LDS. A load is held at its issue while the compute unit moves what was asked for before, some
+// 400 clocks for a wave's share of a tile, so each half sends for its share in its softmax phase: keys of tile i + 2 and
+// values of tile i + 1 from phase 2 i on, when what they replace has been read, for phase 2 i + 4.
+template <class OT, int D>
+__global__ __launch_bounds__(512, 2) void k_prompt_fwd2(PromptArgs a) {
+    using FR = typename Frag<OT>::type;
+    using TL = Tile32<OT, D>;
+    constexpr int NW = 8, QT = 32 * NW, KT = 64, TB = KT * TL::RB;
+    extern __shared__ __align__(16) char smem[];
+    lds_char* lds = (lds_char*)smem;
+    poison_lds(lds, 6 * TB);
+    poison_lds_done();
+    PromptAt at;
+    int slot;
+    const int hp = prompt_at(a, blockIdx.x, QT, a.Hq, true, at, slot);
+    const int hk = hp % a.Hkv, hq = hk * a.G + hp / a.Hkv;
+    if (a.cu && a.zero_rest) {
+        prompt_zero(a, slot, QT, (OT*)a.o, a.Hq, hq, D);
+        if (a.rest) prompt_zero(a, slot, QT, (OT*)a.rest, a.Hq, hq, D);
+        if (a.lse) prompt_zero(a, slot, QT, a.lse, a.Hq, hq, 1);
+    }
+    if (!at.any) return;
+    const int l = lane_id(), h = l >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q0 = at.tile * QT, last = at.len - 1;
+    const int wq0 = q0 + 32 * w, qi = wq0 + (l & 31);
+    const long long tok = at.tok0 + min(qi, last);
+    FR qf[D / 16];
+    load_own<OT, D>((const OT*)a.q + tok * a.qs[0] + hq * a.qs[1], a.neg, qf);
+    const char* kb = (const char*)((const OT*)a.k + at.tok0 * a.ks[0] + hk * a.ks[1]);
+    const char* vb = (const char*)((const OT*)a.v + at.tok0 * a.vs[0] + hk * a.vs[1]);
+    const TileLoad<OT, D, KT, NW, true> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
+    constexpr int LOADS = 2 * decltype(lk)::N;  // of a wave, a tile's keys and values
+    const int t0 = max(0, q0 - a.window + 1) / KT, n = min(q0 + QT - 1, last) / KT - t0 + 1;
+    TL tl;
+    tl.fresh();
+    // (past the last tile the last one is sent for again, so that as many loads are under way at every wait)
+    auto send_k = [&](int i, int buf) __attribute__((always_inline)) { lk(kb, (t0 + min(i, n - 1)) * KT, lds + buf * TB); };
+    auto send_v = [&](int i, int buf) __attribute__((always_inline)) { lv(vb, (t0 + min(i, n - 1)) * KT, lds + (3 + buf) * TB); };
+    send_k(0, 0);
+    send_k(1, 1);
+    send_v(0, 0);
+    f32x16 acc[D / 32], s[2];
+    FR pf[4];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = zero16();
+    float m = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};  // the lane's weights, in four chains
+    // tile i is seen by the wave
+    auto sees = [&](int i) __attribute__((always_inline)) {
+        const int k0 = (t0 + i) * KT;
+        return k0 <= wq0 + 31 && wq0 <= last && k0 + KT - 1 > wq0 - a.window;
+    };
+    // b0: i mod 3, b1 and b2 the two buffers after it (the second is also the one before it)
+    auto products = [&](int i, int b0, int b2) __attribute__((always_inline)) {
+        const lds_char *kt = lds + b0 * TB, *vt = lds + (3 + b2) * TB;
+        __builtin_amdgcn_s_setprio(1);
+        if (i > 0 && sees(i - 1)) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+                for (int dt = 0; dt < D / 32; ++dt) mma32(acc[dt], tl.cols(vt, 32 * dt, 16 * b), pf[b]);
+            reads_ahead<D / 8, 2, 4>();
+        }
+        if (i < n && sees(i)) {
+            s[0] = s[1] = zero16();
+#pragma unroll
+            for (int b = 0; b < D / 16; ++b)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) mma32(s[x], tl.rows(kt, 32 * x, 16 * b), qf[b]);
+            reads_ahead<D / 8, 1, 4>();
+        }
+        __builtin_amdgcn_s_setprio(0);
+    };
+    auto softmax = [&](int i) __attribute__((always_inline)) {
+        if (!sees(i)) return;
+        const int k0 = (t0 + i) * KT;
+        if (k0 + KT - 1 > wq0 || k0 <= wq0 + 31 - a.window) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int d = qi - (k0 + 32 * x + 8 * (r >> 2) + 4 * h + (r & 3));
+                    s[x][r] = d >= 0 && d < a.window ? s[x][r] : -INFINITY;
+                }
+        }
+        const float mx = max_halves(max_acc(s)) * a.scale2;
+        // the reference moves only where it would let a weight pass 2^8: sums and weights are relative to it
+        if (__any(mx > m + 8.f)) {
+            const float mn = fmaxf(m, mx), al = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.f : mn));
+            m = mn;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) sum[c] *= al;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) acc[j] = acc[j] * al;
+        }
+        const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                s[x][r] = __builtin_amdgcn_exp2f(fmaf(s[x][r], a.scale2, -mu));
+                sum[r & 3] += s[x][r];
+            }
+            pf[2 * x] = acc_frag<OT>(s[x], 0);
+            pf[2 * x + 1] = acc_frag<OT>(s[x], 1);
+        }
+    };
+    wait_vm<LOADS>();
+    sync_lds();
+    int b0 = 0, b1 = 1, b2 = 2;
+    auto turn = [&]() __attribute__((always_inline)) {
+        const int x = b0;
+        b0 = b1;
+        b1 = b2;
+        b2 = x;
+    };
+    if (w < 4) {
+        for (int i = 0; i <= n; ++i) {
+            products(i, b0, b2);
+            sync_lds();
+            send_k(i + 2, b2);
+            send_v(i + 1, b1);
+            if (i < n) softmax(i);
+            wait_vm<LOADS>();
+            sync_lds();
+            turn();
+        }
+    } else {
+        send_k(2, 2);
+        send_v(1, 1);
+        sync_lds();
+        for (int i = 0; i <= n; ++i) {
+            products(i, b0, b2);
+            wait_vm<LOADS>();
+            sync_lds();
+            turn();
+            if (i == n) break;
+            send_k(i + 3, b2);
+            send_v(i + 2, b1);
+            softmax(i);
+            sync_lds();
+        }
+    }
+    wait_vm<0>();  // no load outlives the workgroup's LDS
+    float total = sum_halves((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (qi > last) return;
+    const float inv = 1.f / total;
+    const size_t row = (size_t)(at.tok0 + qi) * a.Hq + hq;
+    if (sizeof(OT) == 2 && a.rest) {
+        OT *po = (OT*)a.o + row * D, *pr = (OT*)a.rest + row * D;
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float x[4], y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = acc[dt][4 * j + i] * inv;
+                    y[i] = x[i] - to_f(to_ot<OT>(x[i]));
+                }
+                st4(po + 32 * dt + 8 * j + 4 * h, x);
+                st4(pr + 32 * dt + 8 * j + 4 * h, y);
+            }
+    } else {
+        store_col<OT, D>((OT*)a.o + row * D, acc, inv);
+    }
+    if (a.lse && h == 0) a.lse[row] = (m + __log2f(total)) * 0.6931471805599453f;
+}
+
+template <class OT, int D>
+static hipError_t launch_fwd2_t(const PromptArgs& a, hipStream_t stream) {
+    const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 256) * a.Hq;
+    constexpr int LDS = 6 * 64 * D * (int)sizeof(OT);
+    const auto f = k_prompt_fwd2<OT, D>;
+    if (LDS > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(f, dim3((unsigned)n), dim3(512), LDS, stream, a);
+    return hipGetLastError();
+}
+
+template <class OT, int D>
+static hipError_t launch_fwd_d(const PromptArgs& a, hipStream_t stream) {
+    const long long blocks = prompt_blocks(a.N, a.T, a.cu != nullptr), tasks = blocks * a.Hq;
+    const int S = prompt_sharing(a, tasks, 1);
+    if constexpr (sizeof(OT) == 2) {
+        // the turns of k_prompt_fwd2 from two rounds of its workgroups on (us against those of four waves: 2 x 4096
+        // tokens, 16 heads 143 and 165; 16384 tokens 984 and 1048; 8 x 1024 58 and 58; with 64 channels, whose products
+        // are half as long as their softmax, 79 and 56)
+        if (D == 128 && S == 1 && tasks >= 4096 && prompt_length(a.N, a.T, a.cu != nullptr) >= 1024)
+            return launch_fwd2_t<OT, D>(a, stream);
+        if (S == 1) return launch_fwd_t<OT, D, 4, 1>(a, stream);
+        if (S == 2) return launch_fwd_t<OT, D, 4, 2>(a, stream);
+        return tasks <= 256 ? launch_fwd_t<OT, D, 1, 4>(a, stream) : launch_fwd_t<OT, D, 2, 4>(a, stream);
+    } else {
+        if (S == 1) return launch_fwd_t<OT, D, 4, 1>(a, stream);
+        if constexpr (D == 64)  // (128 rows of 128 channels do not fit in LDS)
+            if (S == 4) return launch_fwd_t<OT, D, 1, 4>(a, stream);
+        return launch_fwd_t<OT, D, 2, 2>(a, stream);
+    }
+}
 hipError_t launch_prompt_fwd(const PromptArgs& a, bool bf, hipStream_t stream) {
-    if (bf) return a.D == 64 ? launch_fwd_t<bf16, 64, 8>(a, stream) : launch_fwd_t<bf16, 128, 8>(a, stream);
-    return a.D == 64 ? launch_fwd_t<float, 64, 4>(a, stream) : launch_fwd_t<float, 128, 4>(a, stream);
+    if (bf) return a.D == 64 ? launch_fwd_d<bf16, 64>(a, stream) : launch_fwd_d<bf16, 128>(a, stream);
+    return a.D == 64 ? launch_fwd_d<float, 64>(a, stream) : launch_fwd_d<float, 128>(a, stream);
 }
 
 }  // namespace gdr2

@@ -14,6 +14,8 @@ struct PromptArgs {
     const void* dout;                    // [tokens][Hq][D]
     void *dq, *dk, *dv;                  // [tokens][Hq][D], [tokens][Hkv][D]
     float *lse2, *delta;                 // workspace of the backward, [tokens][Hq] each
+    float* part;                         // workspace: parts of dk, then of dv, [parts][tokens][Hkv][D] each
+    int parts;                           // parts that a key head's query heads are cut in (dk, dv)
     const int* cu;                       // packed: [N + 1] on the device, else null
     int N, T;                            // sequences; tokens of each (packed: tokens in all)
     int Hq, Hkv, G, D;                   // G = Hq / Hkv query heads share a key head
@@ -27,6 +29,34 @@ struct PromptArgs {
 // they have tiles fit before the next one's first.
 inline long long prompt_slots(int N, int T, bool packed, int tile) {
     return packed ? (long long)T / tile + N : (long long)N * (((long long)T + tile - 1) / tile);
+}
+
+// Blocks of 32 rows, a wave's, of all sequences and one head; packed ones may be spare.
+inline long long prompt_blocks(int N, int T, bool packed) { return prompt_slots(N, T, packed, 32); }
+// Tokens of a sequence: of packed ones the mean, the lengths being the device's to know.
+inline long long prompt_length(int N, int T, bool packed) { return packed ? ((long long)T + N - 1) / (N > 0 ? N : 1) : T; }
+
+// Waves that share a block's other axis: none share where the longest walk is at most half of what each of the 1024
+// SIMDs has to do anyway, or where two short walks for each are there to hide one another's latency, two where it is no
+// longer than that, else four. `tasks`: walks of one head each; `heads`: heads that a walk goes through one after another. Measured, bf16, 128 channels, us (S = 1, 2, 4; the tile that is best):
+//   forward   2 x 4096 tokens, 16 heads 143, 189, 233   1 x 8192, 8 heads 184, 165, 201   1 x 2048, 16 heads 47, 42, 39
+//             1 x 512, 16 heads 16, 15, 12              24 packed, 17 - 700 tokens, 16 heads 30, 35, 62
+//   dK, dV    2 x 4096 tokens, 16 heads 282, 321, 383   1 x 8192, 8 heads over 1 453, 304, 374
+//             1 x 2048, 16 heads 112, 74, 66            1 x 512, 16 heads over 4 41, 29, 24
+inline int prompt_sharing(const PromptArgs& a, long long tasks, int heads) {
+    const long long len = prompt_length(a.N, a.T, a.cu != nullptr), seen = len < a.window ? len : a.window;
+    const long long walk = (seen + 63) / 64 * heads;  // tiles of the longest walk
+    const double each = (double)tasks * walk * (seen < len ? 1.0 : 0.5) / 1024.0;
+    return 2.0 * walk <= each || (tasks >= 2048 && walk <= 8) ? 1 : walk <= each ? 2 : 4;
+}
+
+// Parts that the query heads of a key head are cut in for dK and dV, each walked by itself and added up by a further
+// kernel: as many as make 4096 walks. Measured, us, for 1 .. G parts: 1 x 4096 tokens, 32 heads over 8 380, 316, 301;
+// 1 x 8192, 8 over 1 1222, 640, 363, 304; 9 packed documents, 16 over 4 of 64 channels 134, 119, 110.
+inline int prompt_parts(int N, int T, int Hq, int Hkv, bool packed) {
+    const long long walks = prompt_blocks(N, T, packed) * Hkv, G = Hq / Hkv;
+    const long long p = walks > 0 ? (4096 + walks - 1) / walks : 1;
+    return (int)(p < G ? p : G);
 }
 
 hipError_t launch_prompt_fwd(const PromptArgs& a, bool bf16, hipStream_t stream);

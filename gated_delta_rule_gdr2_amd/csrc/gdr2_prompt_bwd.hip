@@ -10,18 +10,15 @@
 
 namespace gdr2 {
 
-constexpr int BT = 64;  // rows of a tile
-
-// waves a SIMD that a kernel's registers have to leave room for
-template <class OT, int D>
-constexpr int prompt_waves() { return sizeof(OT) == 4 && D == 128 ? 1 : 2; }
 
 // ---------------------------------------------------------------- dQ: as the forward, keys in tiles
-template <class OT, int D, int NW>
-__global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dq(PromptArgs a) {
+// (RW x 32 queries a workgroup, S waves for each 32 of them, which share the keys)
+template <class OT, int D, int RW, int S>
+__global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt_dq(PromptArgs a) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
-    constexpr int QT = 32 * NW, TB = BT * TL::RB;
+    constexpr int NW = RW * S, QT = 32 * RW, BT = tile_rows(S), TB = BT * TL::RB, NB = BT / 32 / S;
+    constexpr int ACC = D / 32 * 4096;
     extern __shared__ __align__(16) char smem[];
     lds_char* lds = (lds_char*)smem;
     poison_lds(lds, 4 * TB);
@@ -33,8 +30,9 @@ __global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dq(
     if (a.cu && a.zero_rest) prompt_zero(a, slot, QT, (OT*)a.dq, a.Hq, hq, D);
     if (!at.any) return;
     const int l = lane_id(), h = l >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rw = S == 1 ? w : w % RW, sp = S == 1 ? 0 : w / RW;
     const int q0 = at.tile * QT, last = at.len - 1;
-    const int wq0 = q0 + 32 * w, qi = wq0 + (l & 31);
+    const int wq0 = q0 + 32 * rw, qi = wq0 + (l & 31);
     const long long tok = at.tok0 + min(qi, last);
     const size_t row = (size_t)tok * a.Hq + hq;
     FR qf[D / 16], df[D / 16];
@@ -42,12 +40,12 @@ __global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dq(
     load_own<OT, D>((const OT*)a.dout + row * D, false, df);
     const char* kb = (const char*)((const OT*)a.k + at.tok0 * a.ks[0] + hk * a.ks[1]);
     const char* vb = (const char*)((const OT*)a.v + at.tok0 * a.vs[0] + hk * a.vs[1]);
-    const long long krs = a.ks[0] * (int)sizeof(OT), vrs = a.vs[0] * (int)sizeof(OT);
+    const TileLoad<OT, D, BT, NW, true> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
     const int t0 = max(0, q0 - a.window + 1) / BT, t1 = min(q0 + QT - 1, last) / BT;
     auto fetch = [&](int t) {
         lds_char* b = lds + (t & 1) * 2 * TB;
-        TL::template load<BT, NW>(kb, krs, t * BT, last, b, w);
-        TL::template load<BT, NW>(vb, vrs, t * BT, last, b + TB, w);
+        lk(kb, t * BT, b);
+        lv(vb, t * BT, b + TB);
     };
     fetch(t0);
     // delta from o and what its rounding left over: of a row that sees few keys dP - delta is a small difference
@@ -66,32 +64,35 @@ __global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dq(
                 for (int e = 0; e < 8; ++e) delta = fmaf(to_f(y[e]), to_f(df[b][e]), delta);
             }
         }
-        delta += other_half(delta);
+        delta = sum_halves(delta);
     }
     const float lse2 = a.lse[row] * 1.4426950408889634f;
-    if (qi <= last && h == 0) {
+    if (qi <= last && h == 0 && sp == 0) {
         a.lse2[row] = lse2;
         a.delta[row] = delta;
     }
     f32x16 acc[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[i] = zero16();
+    TL tl;
     for (int t = t0; t <= t1; ++t) {
+        tl.fresh();
         wait_vm<0>();
         __syncthreads();
         if (t < t1) fetch(t + 1);
-        const int k0 = t * BT;
-        if (k0 > wq0 + 31 || k0 + BT - 1 <= wq0 - a.window) continue;
+        const int b0 = 32 * NB * sp, k0 = t * BT + b0;
+        if (k0 > wq0 + 31 || wq0 > last || k0 + 32 * NB - 1 <= wq0 - a.window) continue;
         const lds_char* kt = lds + (t & 1) * 2 * TB;
         const lds_char* vt = kt + TB;
-        const bool part = k0 + BT - 1 > wq0 || k0 <= wq0 + 31 - a.window;
+        const bool part = k0 + 32 * NB - 1 > wq0 || k0 <= wq0 + 31 - a.window;
 #pragma unroll
-        for (int n = 0; n < BT / 32; ++n) {
+        for (int n = 0; n < NB; ++n) {
             f32x16 s = zero16(), dp = zero16();
 #pragma unroll
-            for (int b = 0; b < D / 16; ++b) mma32(s, TL::rows(kt, 32 * n, 16 * b), qf[b]);
+            for (int b = 0; b < D / 16; ++b) mma32(s, tl.rows(kt, b0 + 32 * n, 16 * b), qf[b]);
 #pragma unroll
-            for (int b = 0; b < D / 16; ++b) mma32(dp, TL::rows(vt, 32 * n, 16 * b), df[b]);
+            for (int b = 0; b < D / 16; ++b) mma32(dp, tl.rows(vt, b0 + 32 * n, 16 * b), df[b]);
+            if constexpr (sizeof(OT) == 2) reads_ahead<D / 8, 1, 4>();
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, -lse2));
@@ -108,57 +109,77 @@ __global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dq(
             for (int b = 0; b < 2; ++b) {
                 const FR f = acc_frag<OT>(s, b);
 #pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) mma32(acc[dt], TL::cols(kt, 32 * dt, 32 * n + 16 * b), f);
+                for (int dt = 0; dt < D / 32; ++dt) mma32(acc[dt], tl.cols(kt, 32 * dt, b0 + 32 * n + 16 * b), f);
             }
+            if constexpr (sizeof(OT) == 2) reads_ahead<D / 16, 2, 4>();
         }
+    }
+    if constexpr (S > 1) {
+        __syncthreads();
+        if (sp > 0) put_acc(lds + ((sp - 1) * RW + rw) * ACC, acc);
+        __syncthreads();
+        if (sp > 0) return;
+        for (int x = 0; x < S - 1; ++x) add_acc(lds + (x * RW + rw) * ACC, 1.f, acc);
     }
     if (qi <= last) store_col<OT, D>((OT*)a.dq + row * D, acc, a.neg ? -a.scale : a.scale);
 }
 
 // ---------------------------------------------------------------- dK, dV: queries in tiles
-template <class OT, int D, int NW>
-__global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dkv(PromptArgs a) {
+// (RW x 32 keys a workgroup, S waves for each 32 of them, which share the queries)
+template <class OT, int D, int RW, int S>
+__global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt_dkv(PromptArgs a) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
-    constexpr int KT = 32 * NW, TB = BT * TL::RB, BUF = 2 * TB + 2 * BT * 4;
+    constexpr int NW = RW * S, KT = 32 * RW, BT = tile_rows(S), TB = BT * TL::RB, BUF = 2 * TB + 2 * BT * 4, NB = BT / 32 / S;
+    constexpr int ACC = D / 32 * 4096;
     extern __shared__ __align__(16) char smem[];
     lds_char* lds = (lds_char*)smem;
     poison_lds(lds, 2 * BUF);
     poison_lds_done();
     PromptAt at;
     int slot;
-    const int hk = prompt_at(a, blockIdx.x, KT, a.Hkv, false, at, slot);
-    if (a.cu && a.zero_rest) {
+    const int hp = prompt_at(a, blockIdx.x, KT, a.Hkv * a.parts, false, at, slot);
+    const int hk = hp % a.Hkv, part = hp / a.Hkv;
+    const int g0 = a.G * part / a.parts, g1 = a.G * (part + 1) / a.parts;  // its query heads
+    if (a.cu && a.zero_rest && a.parts == 1) {
         prompt_zero(a, slot, KT, (OT*)a.dk, a.Hkv, hk, D);
         prompt_zero(a, slot, KT, (OT*)a.dv, a.Hkv, hk, D);
     }
     if (!at.any) return;
     const int l = lane_id(), h = l >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rw = S == 1 ? w : w % RW, sp = S == 1 ? 0 : w / RW;
     const int k0 = at.tile * KT, last = at.len - 1;
-    const int wk0 = k0 + 32 * w, ki = wk0 + (l & 31);
+    const int wk0 = k0 + 32 * rw, ki = wk0 + (l & 31);
     const long long tok = at.tok0 + min(ki, last);
     FR kf[D / 16], vf[D / 16];
     load_own<OT, D>((const OT*)a.k + tok * a.ks[0] + hk * a.ks[1], a.neg, kf);
     load_own<OT, D>((const OT*)a.v + tok * a.vs[0] + hk * a.vs[1], false, vf);
     // the query tiles that see any of the workgroup's keys, for each head in turn
     const int t0 = k0 / BT, t1 = (int)min((long long)last, (long long)k0 + KT - 2 + a.window) / BT, nt = t1 - t0 + 1;
-    const long long qrs = a.qs[0] * (int)sizeof(OT), drs = (long long)a.Hq * TL::RB;
+    const TileLoad<OT, D, BT, NW, false> lq(a.qs[0] * (int)sizeof(OT), last, w), ld((long long)a.Hq * TL::RB, last, w);
     auto fetch = [&](int i) {
-        const int hq = hk * a.G + i / nt, r0 = (t0 + i % nt) * BT;
+        const int hq = hk * a.G + g0 + i / nt, r0 = (t0 + i % nt) * BT;
         lds_char* b = lds + (i & 1) * BUF;
-        TL::template load<BT, NW>((const char*)((const OT*)a.q + at.tok0 * a.qs[0] + hq * a.qs[1]), qrs, r0, last, b, w);
-        TL::template load<BT, NW>((const char*)((const OT*)a.dout + (at.tok0 * a.Hq + hq) * D), drs, r0, last, b + TB, w);
-        if (w < 2) {
-            const float* src = (w ? a.delta : a.lse2) + (at.tok0 + min(r0 + l, last)) * a.Hq + hq;
-            __builtin_amdgcn_global_load_lds(src, (lds_void*)(b + 2 * TB + w * BT * 4), 4, 0, 0);
+        lq((const char*)((const OT*)a.q + at.tok0 * a.qs[0] + hq * a.qs[1]), r0, b);
+        ld((const char*)((const OT*)a.dout + (at.tok0 * a.Hq + hq) * D), r0, b + TB);
+#pragma unroll
+        for (int x = 0; x < (2 * BT / 64 + NW - 1) / NW; ++x) {
+            const int y = x * NW + w;  // which 64 of the 2 BT numbers
+            if (y < 2 * BT / 64) {
+                const int r = y % (BT / 64) * 64 + l;
+                const float* src = (y / (BT / 64) ? a.delta : a.lse2) + (at.tok0 + min(r0 + r, last)) * a.Hq + hq;
+                __builtin_amdgcn_global_load_lds(src, (lds_void*)(b + 2 * TB + y * 256), 4, 0, 0);
+            }
         }
     };
     fetch(0);
     f32x16 ak[D / 32], av[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) ak[i] = av[i] = zero16();
-    const int all = nt * a.G;
+    const int all = nt * (g1 - g0);
+    TL tl;
     for (int i = 0; i < all; ++i) {
+        tl.fresh();
         wait_vm<0>();
         __syncthreads();
         if (i + 1 < all) fetch(i + 1);
@@ -166,15 +187,16 @@ __global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dkv
         const lds_char* dt_ = qt + TB;
         const lds_char* st = qt + 2 * TB;
 #pragma unroll
-        for (int n = 0; n < BT / 32; ++n) {
-            const int r0 = (t0 + i % nt) * BT + 32 * n;
+        for (int n_ = 0; n_ < NB; ++n_) {
+            const int n = NB * sp + n_, r0 = (t0 + i % nt) * BT + 32 * n;
             if (r0 + 31 < wk0 || r0 > last || r0 - wk0 - 31 >= a.window) continue;
             f32x16 s = zero16(), dp = zero16();
 #pragma unroll
-            for (int b = 0; b < D / 16; ++b) mma32(s, TL::rows(qt, 32 * n, 16 * b), kf[b]);
+            for (int b = 0; b < D / 16; ++b) mma32(s, tl.rows(qt, 32 * n, 16 * b), kf[b]);
 #pragma unroll
-            for (int b = 0; b < D / 16; ++b) mma32(dp, TL::rows(dt_, 32 * n, 16 * b), vf[b]);
-            const bool part = r0 < wk0 + 31 || r0 + 31 > last || r0 + 31 - wk0 >= a.window;
+            for (int b = 0; b < D / 16; ++b) mma32(dp, tl.rows(dt_, 32 * n, 16 * b), vf[b]);
+            if constexpr (sizeof(OT) == 2) reads_ahead<D / 8, 1, 2>();
+            const bool mask = r0 < wk0 + 31 || r0 + 31 > last || r0 + 31 - wk0 >= a.window;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const f32x4 ls = lds_load<f32x4>(st + (32 * n + 8 * j + 4 * h) * 4);
@@ -183,7 +205,7 @@ __global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dkv
                 for (int x = 0; x < 4; ++x) {
                     float p = __builtin_amdgcn_exp2f(fmaf(s[4 * j + x], a.scale2, -ls[x]));
                     float g = p * (dp[4 * j + x] - de[x]);
-                    if (part) {
+                    if (mask) {
                         const int r = r0 + 8 * j + 4 * h + x, d = r - ki;
                         const bool see = d >= 0 && d < a.window && r <= last;
                         p = see ? p : 0.f;
@@ -198,40 +220,134 @@ __global__ __launch_bounds__(64 * NW, (prompt_waves<OT, D>())) void k_prompt_dkv
                 const FR pf = acc_frag<OT>(s, b), gf = acc_frag<OT>(dp, b);
 #pragma unroll
                 for (int dt = 0; dt < D / 32; ++dt) {
-                    mma32(av[dt], TL::cols(dt_, 32 * dt, 32 * n + 16 * b), pf);
-                    mma32(ak[dt], TL::cols(qt, 32 * dt, 32 * n + 16 * b), gf);
+                    mma32(av[dt], tl.cols(dt_, 32 * dt, 32 * n + 16 * b), pf);
+                    mma32(ak[dt], tl.cols(qt, 32 * dt, 32 * n + 16 * b), gf);
                 }
             }
+            if constexpr (sizeof(OT) == 2) reads_ahead<D / 8, 2, 1>();  // (as far as the registers go)
         }
+    }
+    if constexpr (S > 1) {
+        // one of the two at a time: both together pass the LDS
+        __syncthreads();
+        if (sp > 0) put_acc(lds + ((sp - 1) * RW + rw) * ACC, ak);
+        __syncthreads();
+        if (sp == 0)
+            for (int x = 0; x < S - 1; ++x) add_acc(lds + (x * RW + rw) * ACC, 1.f, ak);
+        __syncthreads();
+        if (sp > 0) put_acc(lds + ((sp - 1) * RW + rw) * ACC, av);
+        __syncthreads();
+        if (sp > 0) return;
+        for (int x = 0; x < S - 1; ++x) add_acc(lds + (x * RW + rw) * ACC, 1.f, av);
     }
     if (ki > last) return;
     const size_t row = (size_t)(at.tok0 + ki) * a.Hkv + hk;
+    if (a.parts > 1) {
+        const size_t tokens = a.cu ? (size_t)a.T : (size_t)a.N * a.T;
+        float* pk = a.part + ((size_t)part * tokens * a.Hkv + row) * D;
+        store_col<float, D>(pk, ak, 1.f);
+        store_col<float, D>(pk + (size_t)a.parts * tokens * a.Hkv * D, av, 1.f);
+        return;
+    }
     // the sign of a negative scale went into k for the scores; q itself entered dK
     store_col<OT, D>((OT*)a.dk + row * D, ak, a.neg ? -a.scale : a.scale);
     store_col<OT, D>((OT*)a.dv + row * D, av, 1.f);
 }
 
-template <class OT, int D, int NW>
-static hipError_t launch_bwd_t(const PromptArgs& a, hipStream_t stream) {
-    constexpr int TB = BT * D * (int)sizeof(OT), LQ = 4 * TB, LK = 4 * TB + 4 * BT * 4;
-    const auto fq = k_prompt_dq<OT, D, NW>;
-    const auto fk = k_prompt_dkv<OT, D, NW>;
-    if (LK > 65536) {
-        hipError_t e = hipFuncSetAttribute((const void*)fq, hipFuncAttributeMaxDynamicSharedMemorySize, LQ);
-        if (e == hipSuccess) e = hipFuncSetAttribute((const void*)fk, hipFuncAttributeMaxDynamicSharedMemorySize, LK);
-        if (e != hipSuccess) return e;
+// dK and dV from their parts, in order
+template <class OT>
+__global__ __launch_bounds__(256) void k_prompt_sum(PromptArgs a) {
+    const size_t tokens = a.cu ? (size_t)a.T : (size_t)a.N * a.T, all = tokens * a.Hkv * a.D;
+    const size_t e = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (e >= all) return;
+    bool rest = false;
+    if (a.cu) {
+        const int r = (int)(e / ((size_t)a.Hkv * a.D)), b = clamp_int(a.cu[0], 0, a.T);
+        rest = r < b || r >= clamp_int(a.cu[a.N], b, a.T);
+        if (rest && !a.zero_rest) return;
     }
-    const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 32 * NW);
-    hipLaunchKernelGGL(fq, dim3((unsigned)(n * a.Hq)), dim3(64 * NW), LQ, stream, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(fk, dim3((unsigned)(n * a.Hkv)), dim3(64 * NW), LK, stream, a);
-    return hipGetLastError();
+    f32x4 k = {0.f, 0.f, 0.f, 0.f}, v = k;
+    if (!rest)
+        for (int p = 0; p < a.parts; ++p) {
+            k += *(const f32x4*)(a.part + p * all + e);
+            v += *(const f32x4*)(a.part + (a.parts + p) * all + e);
+        }
+    const float f = a.neg ? -a.scale : a.scale;
+    const float x[4] = {k[0] * f, k[1] * f, k[2] * f, k[3] * f}, y[4] = {v[0], v[1], v[2], v[3]};
+    st4((OT*)a.dk + e, x);
+    st4((OT*)a.dv + e, y);
 }
 
+template <class F>
+static hipError_t launch_one(F f, long long groups, int threads, int lds, const PromptArgs& a, hipStream_t stream) {
+    if (lds > 65536) {
+        const hipError_t e = hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(f, dim3((unsigned)groups), dim3((unsigned)threads), lds, stream, a);
+    return hipGetLastError();
+}
+template <class OT, int D, int RW, int S>
+static hipError_t launch_dq_t(const PromptArgs& a, hipStream_t stream) {
+    constexpr int TILES = 4 * tile_rows(S) * D * (int)sizeof(OT), JOIN = (S - 1) * RW * (D / 32 * 4096);
+    constexpr int LDS = TILES > JOIN ? TILES : JOIN;
+    static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
+    const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 32 * RW) * a.Hq;
+    return launch_one(k_prompt_dq<OT, D, RW, S>, n, 64 * RW * S, LDS, a, stream);
+}
+template <class OT, int D, int RW, int S>
+static hipError_t launch_dkv_t(const PromptArgs& a, hipStream_t stream) {
+    constexpr int TILES = 4 * tile_rows(S) * (D * (int)sizeof(OT) + 4), JOIN = (S - 1) * RW * (D / 32 * 4096);
+    constexpr int LDS = TILES > JOIN ? TILES : JOIN;
+    static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
+    const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 32 * RW) * a.Hkv * a.parts;
+    const hipError_t e = launch_one(k_prompt_dkv<OT, D, RW, S>, n, 64 * RW * S, LDS, a, stream);
+    if (e != hipSuccess || a.parts == 1) return e;
+    const long long all = (a.cu ? (long long)a.T : (long long)a.N * a.T) * a.Hkv * D;
+    return launch_one(k_prompt_sum<OT>, (all / 4 + 255) / 256, 256, 0, a, stream);
+}
+
+template <class OT, int D>
+static hipError_t launch_dq_d(const PromptArgs& a, hipStream_t stream) {
+    const long long tasks = prompt_blocks(a.N, a.T, a.cu != nullptr) * a.Hq;
+    const int S = prompt_sharing(a, tasks, 1);
+    if constexpr (sizeof(OT) == 2) {
+        // 256 queries a workgroup from two rounds of them on (2 x 4096 tokens, 16 heads 200 us, with 128 queries 214;
+        // 64 channels, 9 packed documents, 92 and 73)
+        if (D == 128 && S == 1 && tasks >= 4096 && prompt_length(a.N, a.T, a.cu != nullptr) >= 1024)
+            return launch_dq_t<OT, D, 8, 1>(a, stream);
+        if (S == 1) return launch_dq_t<OT, D, 4, 1>(a, stream);
+        if (S == 2) return launch_dq_t<OT, D, 4, 2>(a, stream);
+        return tasks <= 256 ? launch_dq_t<OT, D, 1, 4>(a, stream) : launch_dq_t<OT, D, 2, 4>(a, stream);
+    } else {
+        if (S == 1) return launch_dq_t<OT, D, 4, 1>(a, stream);
+        if constexpr (D == 64)
+            if (S == 4) return launch_dq_t<OT, D, 1, 4>(a, stream);
+        return launch_dq_t<OT, D, 2, 2>(a, stream);
+    }
+}
+template <class OT, int D>
+static hipError_t launch_dkv_d(const PromptArgs& a, hipStream_t stream) {
+    const long long tasks = prompt_blocks(a.N, a.T, a.cu != nullptr) * a.Hkv * a.parts;
+    const int S = prompt_sharing(a, tasks, (a.G + a.parts - 1) / a.parts);
+    if (S == 1) return launch_dkv_t<OT, D, 4, 1>(a, stream);
+    if constexpr (sizeof(OT) == 2) {
+        if (S == 2) return launch_dkv_t<OT, D, 2, 2>(a, stream);
+        return tasks <= 256 ? launch_dkv_t<OT, D, 1, 4>(a, stream) : launch_dkv_t<OT, D, 2, 4>(a, stream);
+    } else {
+        if constexpr (D == 64)
+            if (S == 4) return launch_dkv_t<OT, D, 1, 4>(a, stream);
+        return launch_dkv_t<OT, D, 2, 2>(a, stream);
+    }
+}
+template <class OT, int D>
+static hipError_t launch_bwd_d(const PromptArgs& a, hipStream_t stream) {
+    const hipError_t e = launch_dq_d<OT, D>(a, stream);
+    return e == hipSuccess ? launch_dkv_d<OT, D>(a, stream) : e;
+}
 hipError_t launch_prompt_bwd(const PromptArgs& a, bool bf, hipStream_t stream) {
-    if (bf) return a.D == 64 ? launch_bwd_t<bf16, 64, 4>(a, stream) : launch_bwd_t<bf16, 128, 4>(a, stream);
-    return a.D == 64 ? launch_bwd_t<float, 64, 4>(a, stream) : launch_bwd_t<float, 128, 4>(a, stream);
+    if (bf) return a.D == 64 ? launch_bwd_d<bf16, 64>(a, stream) : launch_bwd_d<bf16, 128>(a, stream);
+    return a.D == 64 ? launch_bwd_d<float, 64>(a, stream) : launch_bwd_d<float, 128>(a, stream);
 }
 
 }  // namespace gdr2

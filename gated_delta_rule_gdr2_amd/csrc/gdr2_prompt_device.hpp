@@ -42,57 +42,100 @@ __device__ __forceinline__ int tile_f(int r) {
     static_assert(NCH == 8 || NCH == 16 || NCH == 32, "tiles have 8, 16 or 32 chunks a row");
     return NCH == 8 ? 4 * ((r >> 1) & 1) + ((r >> 2) & 3) : 4 * (r & 3) + ((r >> 2) & 3);
 }
+// A lane's addresses are an XOR of a part that belongs to the lane and one that belongs to the operand: left to itself
+// the compiler keeps one address for each operand over the whole loop, some thirty registers; from lane parts that it
+// cannot trace back to the thread index (fresh) it forms them where they are used, one instruction each.
 template <class OT, int D>
 struct Tile32 {
     static constexpr int ES = (int)sizeof(OT), EPC = 16 / ES, NCH = D / EPC, RB = D * ES;  // row bytes
-    static __device__ __forceinline__ int off(int r, int c) {
-        return r * RB + (((c / EPC) ^ tile_f<NCH>(r)) * 16) + (c % EPC) * ES;
-    }
-    // A operand of the K block k0 .. k0 + 15, rows r0 + li, contiguous K order
-    static __device__ __forceinline__ typename Frag<OT>::type rows(const lds_char* t, int r0, int k0) {
-        const int l = lane_id(), r = r0 + (l & 31), c = k0 + 8 * (l >> 5);
+    int rb, cb;  // lane parts of row and transposed reads
+
+    __device__ __forceinline__ void fresh() {
+        int l = lane_id();
+        asm volatile("" : "+v"(l));
+        const int li = l & 31, h = l >> 5;
         if constexpr (ES == 2) {
-            return lds_load<bf16x8>(t + off(r, c));
+            const int r4 = (l & 15) >> 2;  // row of four
+            rb = li * RB + ((h ^ tile_f<NCH>(li)) * 16);
+            cb = (4 * h + r4) * RB + (((2 * ((l >> 4) & 1) + ((l & 3) >> 1)) ^ tile_f<NCH>(4 * h + r4)) * 16) + 8 * (l & 1);
         } else {
-            const f32x4 x0 = lds_load<f32x4>(t + off(r, c)), x1 = lds_load<f32x4>(t + off(r, c + 4));
+            rb = li * RB + (((2 * h) ^ tile_f<NCH>(li)) * 16);
+            cb = 4 * h * RB + (((li >> 2) ^ h) * 16) + (li & 3) * 4;
+        }
+    }
+    // A operand of the K block k0 .. k0 + 15, rows r0 + li (r0 a multiple of 32), contiguous K order
+    __device__ __forceinline__ typename Frag<OT>::type rows(const lds_char* t, int r0, int k0) const {
+        const lds_char* p = t + r0 * RB;
+        if constexpr (ES == 2) {
+            return lds_load<bf16x8>(p + (rb ^ (k0 * ES)));
+        } else {
+            const f32x4 x0 = lds_load<f32x4>(p + (rb ^ (k0 * ES))), x1 = lds_load<f32x4>(p + (rb ^ (k0 * ES + 16)));
             return __builtin_shufflevector(x0, x1, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
-    // A operand of the transposed tile: rows are the tile's columns c0 + li, the K block its rows k0 .. k0 + 15 in
-    // the accumulator's order
-    static __device__ __forceinline__ typename Frag<OT>::type cols(const lds_char* t, int c0, int k0) {
-        const int l = lane_id(), h = l >> 5;
+    // A operand of the transposed tile: rows are the tile's columns c0 + li (c0 a multiple of 32), the K block its rows
+    // k0 .. k0 + 15 in the accumulator's order
+    __device__ __forceinline__ typename Frag<OT>::type cols(const lds_char* t, int c0, int k0) const {
+        const lds_char* p = t + k0 * RB;
         if constexpr (ES == 2) {
-            const int r = k0 + 4 * h + ((l & 15) >> 2), c = c0 + 16 * ((l >> 4) & 1) + 4 * (l & 3);
-            const bf16x4 v0 = lds_read_tr16(t + off(r, c)), v1 = lds_read_tr16(t + off(r + 8, c));
+            const bf16x4 v0 = lds_read_tr16(p + (cb ^ (c0 * ES))), v1 = lds_read_tr16(p + (cb ^ (c0 * ES + 32)) + 8 * RB);
             return __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
             typename Frag<OT>::type f;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                f[e] = lds_load<float>(t + off(k0 + 8 * (e >> 2) + 4 * h + (e & 3), c0 + (l & 31)));
+                f[e] = lds_load<float>(p + (cb ^ (c0 * ES) ^ ((4 * (e & 3) + 2 * (e >> 2)) * 16)) + (8 * (e >> 2) + (e & 3)) * RB);
             return f;
         }
     }
-    // Rows row0 .. row0 + R - 1 (held in 0 .. last) of a matrix with row stride rs (bytes) into LDS, 1 KB a wave
-    // instruction, wave w of NW
-    template <int R, int NW>
-    static __device__ __forceinline__ void load(const char* base, long long rs, int row0, int last, lds_char* t, int w) {
-        constexpr int N = R * RB / 1024, RPI = 64 / NCH > 0 ? 64 / NCH : 1;
-        const int l = lane_id();
-        static_assert(NCH <= 64 && R * RB % 1024 == 0, "whole rows an instruction");
+};
+
+// Rows of a matrix (row stride rs bytes, rows 0 .. last) in tiles of R into LDS by NW waves, this one being wave w. The
+// lane's offsets inside a tile are formed once (KEEP), or, where registers are short, at each tile; a tile that reaches
+// past the last row forms others.
+template <class OT, int D, int R, int NW, bool KEEP>
+struct TileLoad {
+    using TL = Tile32<OT, D>;
+    static constexpr int ALL = R * TL::RB / 1024, N = (ALL + NW - 1) / NW, RPI = 64 / TL::NCH;  // 1 KB an instruction
+    static_assert(R * TL::RB % 1024 == 0, "whole rows an instruction");
+    long long rs;
+    int last, w;
+    unsigned off[KEEP ? N : 1];
+
+    __device__ __forceinline__ int row(int l, int i) const { return (i * NW + w) * RPI + l / TL::NCH; }
+    __device__ __forceinline__ unsigned piece(int l, int i) const { return ((l % TL::NCH) ^ tile_f<TL::NCH>(row(l, i))) * 16; }
+    __device__ __forceinline__ TileLoad(long long rs_, int last_, int w_) : rs(rs_), last(last_), w(w_) {
+        if constexpr (KEEP)
 #pragma unroll
-        for (int i = 0; i < (N + NW - 1) / NW; ++i) {
-            const int n = i * NW + w;
-            if (N % NW == 0 || n < N) {
-                const int r = n * RPI + l / NCH;
-                const int row = max(0, min(row0 + r, last));
-                const char* src = base + (long long)row * rs + (((l % NCH) ^ tile_f<NCH>(r)) * 16);
-                __builtin_amdgcn_global_load_lds(src, (lds_void*)(t + n * 1024), 16, 0, 0);
-            }
+            for (int i = 0; i < N; ++i) off[i] = row(lane_id(), i) * (unsigned)rs + piece(lane_id(), i);
+    }
+    __device__ __forceinline__ void operator()(const char* base, int row0, lds_char* t) const {
+        const char* b = base + (long long)row0 * rs;
+        const bool whole = row0 + R - 1 <= last;
+        int l = lane_id();
+        if constexpr (!KEEP) asm volatile("" : "+v"(l));
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (ALL % NW != 0 && i * NW + w >= ALL) break;
+            const char* src = b + (KEEP ? off[KEEP ? i : 0] : row(l, i) * (unsigned)rs + piece(l, i));
+            if (!whole) src = base + (long long)max(0, min(row0 + row(l, i), last)) * rs + piece(l, i);
+            __builtin_amdgcn_global_load_lds(src, (lds_void*)(t + (i * NW + w) * 1024), 16, 0, 0);
         }
     }
 };
+
+// Order of a block of STEPS matrix products with R LDS reads each: the reads run AHEAD products before their use. Left
+// to itself the compiler reads each operand just before its product and waits for it.
+template <int STEPS, int R, int AHEAD>
+__device__ __forceinline__ void reads_ahead() {
+    __builtin_amdgcn_sched_group_barrier(0x100, R * AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < STEPS - AHEAD; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
+}
 
 // B operands of a wave's own 32 rows, all K blocks, straight from memory: row p (this lane's), contiguous K order.
 template <class OT, int D>
@@ -124,8 +167,64 @@ __device__ __forceinline__ void store_col(OT* p, const f32x16 (&acc)[D / 32], fl
             st4(p + 32 * dt + 8 * j + 4 * h, x);
         }
 }
-// the other half wave's value of this column
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32); }
+// waves a SIMD that a kernel's registers have to leave room for
+template <class OT, int D>
+constexpr int prompt_waves() { return sizeof(OT) == 4 && D == 128 ? 1 : 2; }
+
+// Waves side by side (S of them) on the same rows, each with its part of the other axis: their sums come together
+// through LDS, which everyone is done with. A wave's accumulators as 16 bytes a lane, one after another.
+template <int N>
+__device__ __forceinline__ void put_acc(lds_char* p, const f32x16 (&acc)[N]) {
+    const int l = lane_id();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            lds_store<f32x4>(p + (4 * i + j) * 1024 + l * 16,
+                             f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]});
+}
+template <int N>
+__device__ __forceinline__ void add_acc(const lds_char* p, float f, f32x16 (&acc)[N]) {
+    const int l = lane_id();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f32x4 x = lds_load<f32x4>(p + (4 * i + j) * 1024 + l * 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][4 * j + e] += x[e] * f;
+        }
+}
+// rows of a tile of the other axis: two blocks of 32 for a wave alone, one or two for each of several
+constexpr int tile_rows(int S) { return S == 4 ? 128 : 64; }
+// the larger, or the sum, of this lane's value and the other half wave's of the same column, by an exchange of half waves
+// in the vector unit
+__device__ __forceinline__ float max_halves(float x) {
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+    typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// largest value of accumulators, in four chains: one chain of dependent instructions would take twice as long
+template <int N>
+__device__ __forceinline__ float max_acc(const f32x16 (&s)[N]) {
+    float m[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        m[c] = fmaxf(s[0][c], s[0][4 + c]);
+        m[c] = fmaxf(fmaxf(m[c], s[0][8 + c]), s[0][12 + c]);
+#pragma unroll
+        for (int n = 1; n < N; ++n) {
+            m[c] = fmaxf(fmaxf(m[c], s[n][c]), s[n][4 + c]);
+            m[c] = fmaxf(fmaxf(m[c], s[n][8 + c]), s[n][12 + c]);
+        }
+    }
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
 
 // The sequence tile a workgroup works on.
 struct PromptAt {
@@ -134,22 +233,64 @@ struct PromptAt {
     bool any;        // false: a spare slot
 };
 __device__ __forceinline__ int clamp_int(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
-// Packed: the sequence whose tile a slot holds. cu is data of the caller's that no host check can see, so its entries
+// Packed sequence s: its first token and tokens. cu is data of the caller's that no host check can see, so its entries
 // are held inside the tensors here.
-__device__ __forceinline__ PromptAt prompt_packed(const PromptArgs& a, int slot, int tile) {
-    int lo = 0, hi = a.N - 1;  // the last sequence whose first slot is not behind it
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (clamp_int(a.cu[mid], 0, a.T) / tile + mid <= slot) lo = mid;
-        else hi = mid - 1;
+__device__ __forceinline__ void prompt_seq(const PromptArgs& a, int s, int& tok0, int& len) {
+    tok0 = clamp_int(a.cu[s], 0, a.T);
+    len = clamp_int(a.cu[s + 1], tok0, a.T) - tok0;
+}
+// Packed, more sequences than lanes: the sequence whose tile a slot holds, the last one whose first slot is not behind
+// it, found by 64 probes at a time.
+__device__ __forceinline__ void prompt_slot(const PromptArgs& a, int slot, int tile, PromptAt& p) {
+    int lo = 0, hi = a.N;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64, s = lo + lane_id() * step;
+        const bool in = s < hi && clamp_int(a.cu[s < hi ? s : lo], 0, a.T) / tile + s <= slot;
+        const int n = __builtin_ctzll(~__ballot(in) | (1ull << 63));
+        lo += max(n - 1, 0) * step;
+        hi = min(hi, lo + step);
     }
-    const int b = clamp_int(a.cu[lo], 0, a.T), e = clamp_int(a.cu[lo + 1], b, a.T);
-    PromptAt p;
-    p.tok0 = b;
-    p.len = e - b;
-    p.tile = slot - (b / tile + lo);
+    int tok0;
+    prompt_seq(a, lo, tok0, p.len);
+    p.tok0 = tok0;
+    p.tile = slot - (tok0 / tile + lo);
     p.any = p.tile >= 0 && (long long)p.tile * tile < p.len;
-    return p;
+}
+// sum over the wave, by moves between lanes in the vector unit
+__device__ __forceinline__ int wave_sum(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);  // lane 15 of a row: the row's sum
+    return __builtin_amdgcn_readlane(x, 15) + __builtin_amdgcn_readlane(x, 31) + __builtin_amdgcn_readlane(x, 47) +
+           __builtin_amdgcn_readlane(x, 63);
+}
+// Packed, a sequence to a lane: the r-th tile of all in the order of their distance from the sequence's other end,
+// longest first, so that no long tile begins late. `last_first`: that distance is the tile's number (it sees all tiles
+// before it), else the tiles behind it (which see it).
+__device__ __forceinline__ void prompt_rank(const PromptArgs& a, int r, int tile, bool last_first, PromptAt& p) {
+    const int l = lane_id();
+    int tok0 = 0, len = 0;
+    if (l < a.N) prompt_seq(a, l, tok0, len);
+    const int nt = (len + tile - 1) / tile;
+    // tiles with more than L tiles on their side
+    auto above = [&](int L) {
+        return wave_sum(max(nt - 1 - L, 0));
+    };
+    p.any = r < above(-1);
+    if (!p.any) return;
+    int lo = 0, hi = (a.T + tile - 1) / tile;  // the smallest L with above(L) <= r
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (above(mid) <= r) hi = mid;
+        else lo = mid + 1;
+    }
+    unsigned long long who = __ballot(nt > lo);
+    for (int n = r - above(lo); n > 0; --n) who &= who - 1;
+    const int s = __builtin_ctzll(who);
+    p.tok0 = __builtin_amdgcn_readlane(tok0, s);
+    p.len = __builtin_amdgcn_readlane(len, s);
+    p.tile = last_first ? lo : __builtin_amdgcn_readlane(nt, s) - 1 - lo;
 }
 // Tiles in the order of the launch: the last tile of every sequence first (`last_first`), which sees the most keys, or
 // the first one first, which is seen most. `heads` workgroups a tile; heads that share keys lie a multiple of the
@@ -157,9 +298,9 @@ __device__ __forceinline__ PromptAt prompt_packed(const PromptArgs& a, int slot,
 __device__ __forceinline__ int prompt_at(const PromptArgs& a, int bid, int tile, int heads, bool last_first, PromptAt& p,
                                          int& slot) {
     if (a.cu) {
-        const int ns = a.T / tile + a.N, s = bid / heads;
-        slot = last_first ? ns - 1 - s : s;
-        p = prompt_packed(a, slot, tile);
+        slot = bid / heads;
+        if (a.N <= 64) prompt_rank(a, slot, tile, last_first, p);
+        else prompt_slot(a, slot, tile, p);
         return bid % heads;
     }
     const int nt = (a.T + tile - 1) / tile, cols = a.N * heads, t = bid / cols, c = bid % cols;

@@ -333,9 +333,10 @@ int gdr2_kv_append(const void* k, const void* v, void* k_cache, void* v_cache, c
  * enter the second products as one bf16 each, so that outputs carry two roundings, their own among them.
  *
  * A value that is infinite or NaN at a token reaches the tokens of its own sequence, also some before it; other
- * sequences are not affected. Results repeat bit for bit. Outputs must not overlap one another or the inputs.
+ * sequences are not affected. Results repeat bit for bit; how waves share the work goes by the sizes of the call, so that
+ * last bits differ between calls of other sizes. Outputs must not overlap one another or the inputs.
  * Workspace: gdr2_attn_bwd_workspace_bytes, of no content between calls; calls that may overlap need one each.
- * Errors as gdr2_attn_step; GDR2_ERR_SHAPE also for 2^31 - 1024 tokens or 2^24 workgroups (32 tokens of a head) and more. */
+ * Errors as gdr2_attn_step; GDR2_ERR_SHAPE also for 2^31 - 1024 tokens, or 2^23 pieces of 32 tokens of a head, and more. */
 int gdr2_attn_fwd(const void* q, const void* k, const void* v, const long long* strides, const int* cu_seqlens, void* o,
                   float* lse, void* rest, int N, int T, int Hq, int Hkv, int D, float scale, int window, int dtype,
                   int zero_rest, void* stream);

@@ -374,8 +374,9 @@ def test_offsets_past_32_bits():
     c = ints(cu)
     o, lse, rest = g2.gdr2_attn_fwd(q, k, v, cu_seqlens=c, save_for_bwd=True)
     gr = g2.gdr2_attn_bwd(q, k, v, o, lse, do, rest=rest, cu_seqlens=c)
+    # (how waves share the work goes by the call's sizes, and with it the order of sums: two results within 2^-7 each)
     for a, b in ((o, want[0]), (lse, want[1]), *((gr[x], want[3][x]) for x in gr)):
-        assert torch.equal(a[:, cu[0]:cu[-1]], b)
+        assert normwise(a[:, cu[0]:cu[-1]].double(), b.double()) <= 2.0 ** -6
         assert not a[:, :cu[0]].any() and not a[:, cu[-1]:].any()
 
 

@@ -75,7 +75,7 @@ def test_prompt_refusals(lib, call):
     assert call(lib, Hq=3, Hkv=0) == SHAPE
     assert call(lib, D=96) == UNSUP and call(lib, dtype=9) == UNSUP
     assert call(lib, T=2 ** 31 - 1) == SHAPE and call(lib, N=1 << 12, T=1 << 20) == SHAPE
-    assert call(lib, N=1 << 20, T=1, Hq=64) == SHAPE  # 2^26 workgroups
+    assert call(lib, N=1 << 20, T=1, Hq=8) == SHAPE  # 2^23 workgroups
     for s in (math.inf, math.nan, -math.inf):
         assert call(lib, scale=s) == VALUE
     assert call(lib, window=-1) == VALUE
@@ -85,7 +85,9 @@ def test_prompt_refusals(lib, call):
 
 def test_prompt_workspace_sizes(lib):
     f = g2.gdr2_attn_bwd_workspace_bytes
-    assert f(2, 100, 4, 2, 64) == f(1, 200, 4, 2, 64) == f(7, 200, 4, 2, 64, packed=True) == 200 * 4 * 8
+    assert f(2, 100, 4, 4, 64) == f(1, 200, 4, 4, 64) == f(7, 200, 4, 4, 64, packed=True) == 200 * 4 * 8
+    assert f(1, 200, 8, 2, 64) == 200 * 8 * 8 + 4 * 200 * 2 * 64 * 8    # parts of dK and dV, a query head each
+    assert f(8, 4096, 64, 32, 64) == 8 * 4096 * 64 * 8                  # enough walks without
     assert f(1, 0, 4, 2, 64) == 0 and f(1, 64, 3, 2, 64) == 0 and f(1, 64, 2, 2, 96) == 0
     n = f(1, 64, 2, 1, 64)
     assert bwd(lib, ws_bytes=n - 1) == WS
