@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libgdr2.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["gdr2_api.cpp", "gdr2_fwd.hip", "gdr2_bwd.hip", "gdr2_chain.hip", "gdr2_step.hip", "gdr2_noalloc.hip",
            "gdr2_mixers_api.cpp", "gdr2_scalar_intra.hip", "gdr2_scalar_chain.hip", "gdr2_scalar_step.hip", "gdr2_attn.hip",
-           "gdr2_prompt.hip", "gdr2_prompt_bwd.hip", "gdr2_tree.hip", "gdr2_pages.hip"]
+           "gdr2_prompt.hip", "gdr2_prompt_bwd.hip", "gdr2_tree.hip", "gdr2_tree_wide.hip", "gdr2_pages.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

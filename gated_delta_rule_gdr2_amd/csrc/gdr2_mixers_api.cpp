@@ -386,8 +386,8 @@ size_t gdr2_attn_tree_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int 
     if (tree_shape(B, T, Hq, Hkv, D, dtype) != GDR2_OK || B == 0 || T == 0 || Hq == 0) return 0;
     gdr2::TreeArgs a = {};
     a.T = T; a.G = Hq / Hkv; a.D = D;
-    gdr2::tree_rows(a);
-    return 2 * (size_t)a.wgs * gdr2::tree_part_floats(a) * sizeof(float);
+    gdr2::tree_rows(a, dtype == GDR2_DTYPE_BF16);
+    return gdr2::tree_workspace(a);
 }
 
 int gdr2_attn_tree(const void* q, const int* parents, const void* k_cache, const void* v_cache,
@@ -409,8 +409,10 @@ int gdr2_attn_tree(const void* q, const int* parents, const void* k_cache, const
     a.B = B; a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.G = Hq / Hkv;
     a.window = window;
     a.scale2 = (float)((double)scale * 1.4426950408889634);
-    gdr2::tree_rows(a);
-    if (gdr2::tree_line_places(a, gdr2::attn_unit_tokens(dtype == GDR2_DTYPE_BF16)) > 0x7fffffffLL) return GDR2_ERR_SHAPE;
+    gdr2::tree_rows(a, dtype == GDR2_DTYPE_BF16);
+    a.neg = a.wide && scale < 0.f;
+    if (a.wide) a.scale2 = fmaxf(fabsf(a.scale2), 1e-30f);  // as for whole sequences
+    if (gdr2::tree_line_places(a) > 0x7fffffffLL) return GDR2_ERR_SHAPE;
     const void* const ptrs[] = {q, k_cache, v_cache, o, workspace};
     const void* const words[] = {parents, starts, block_table, lse};
     if (!all_aligned(ptrs) || !gates_aligned(words, 4)) return GDR2_ERR_ALIGN;

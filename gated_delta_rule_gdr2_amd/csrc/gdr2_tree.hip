@@ -12,108 +12,9 @@
 // from the parents (each round of lane exchanges doubles the way up that is known); only units that reach into the
 // drafts, or a window's edge, look at it. Rows are split over workgroups as in gdr2_attn.hip.
 #include "gdr2_attn_device.hpp"
-#include "gdr2_tree.hpp"
+#include "gdr2_tree_device.hpp"
 
 namespace gdr2 {
-
-struct TreeSpan {
-    int start, lo, hi, u0, units;  // context tokens; first and last token that any draft may see; units
-};
-template <class OT>
-__device__ __forceinline__ TreeSpan tree_span(const TreeArgs& a, int b) {
-    constexpr int U = attn_unit<OT>();
-    const long long cap = (long long)a.c.max_pages << a.c.shift;
-    const int st = a.starts[b];
-    TreeSpan s;
-    s.start = st < 0 ? 0 : (long long)st < cap ? st : (int)cap;
-    s.hi = (int)min((long long)s.start + a.T, cap);
-    s.lo = a.window > 0 && s.start >= a.window ? s.start + 1 - a.window : 0;
-    s.u0 = s.lo / U;
-    s.units = max(1, (s.hi + U - 1) / U - s.u0);
-    return s;
-}
-
-// The line of all rows (gdr2_attn.hip): lane t holds the place before its run of `per` sequences.
-struct TreeLine {
-    unsigned before, total, share;
-    int per;
-};
-template <class OT>
-__device__ __forceinline__ TreeLine tree_line(const TreeArgs& a) {
-    const int l = lane_id(), HR = a.Hkv * a.nb;
-    TreeLine p;
-    p.per = (a.B + 63) / 64;
-    unsigned own = 0;
-    for (int i = 0; i < p.per; ++i) {
-        const int b = l * p.per + i;
-        if (b < a.B) own += (tree_span<OT>(a, b).units + ATTN_COST) * HR;
-    }
-    unsigned x = own;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const unsigned y = __shfl_up(x, o);
-        if (l >= o) x += y;
-    }
-    p.before = x - own;
-    p.total = __builtin_amdgcn_readlane(x, 63);
-    p.share = max((p.total + a.wgs - 1) / a.wgs, (unsigned)a.share_min);
-    return p;
-}
-struct TreeAt {
-    int b;
-    unsigned at;
-    TreeSpan sp;
-};
-template <class OT>
-__device__ __forceinline__ TreeAt tree_find(const TreeArgs& a, const TreeLine& line, unsigned t) {
-    const int HR = a.Hkv * a.nb;
-    const int ln = __popcll(__ballot(line.before <= t && lane_id() * line.per < a.B)) - 1;
-    TreeAt f;
-    f.b = ln * line.per;
-    f.at = __builtin_amdgcn_readlane(line.before, ln);
-    f.sp = tree_span<OT>(a, f.b);
-    while (t >= f.at + (f.sp.units + ATTN_COST) * HR) {
-        f.at += (f.sp.units + ATTN_COST) * HR;
-        f.sp = tree_span<OT>(a, ++f.b);
-    }
-    return f;
-}
-
-// The tree of sequence b, draft i in lane i: the drafts that it sees (itself and those above it, within the window),
-// how many lie above it, and whether it is one (a chain of parents that ends at -1) or padding.
-struct TreeLane {
-    unsigned long long sees, all;  // all: the drafts of the tree
-    int depth;
-};
-__device__ __forceinline__ TreeLane tree_lane(const TreeArgs& a, int b) {
-    const int i = lane_id();
-    const int p = i < a.T ? a.parents[(size_t)b * a.T + i] : -2;
-    int ok = p >= -1 && p < i;
-    const int up = ok && p >= 0 ? p : i;
-    TreeLane t;
-    t.depth = up != i;
-    t.sees = 1ull << i;
-    int hop = up;
-    ok &= __shfl(ok, up);
-    for (int n = 1; n < a.T; n *= 2) {
-        t.sees |= __shfl(t.sees, hop);
-        t.depth += __shfl(t.depth, hop);
-        ok &= __shfl(ok, hop);
-        hop = __shfl(hop, hop);
-    }
-    if (a.window > 0 && a.window < a.T) {  // the nearest ones only
-        unsigned long long m = 0;
-        int x = i;
-        for (int n = 0; n < a.window; ++n) {
-            m |= 1ull << x;
-            x = __shfl(up, x);
-        }
-        t.sees = m;
-    }
-    t.all = __ballot(ok);
-    if (!ok) t.sees = 0;
-    return t;
-}
 
 // Running softmax of a wave's columns: lane (li, lq) holds column 16 n + li; l is its own tokens' share of the weight.
 // acc[n][j]: channels (D / 16) (4 lq + i) + j. lo, sees: the column's mask.
@@ -354,24 +255,24 @@ __global__ __launch_bounds__(64 * AW) void k_tree(TreeArgs a) {
     const int HR = a.Hkv * a.nb;
     if constexpr (!SPLIT) {
         const int b = blockIdx.x / HR, hr = blockIdx.x % HR;
-        const TreeSpan sp = tree_span<OT>(a, b);
+        const TreeSpan sp = tree_span<attn_unit<OT>()>(a, b);
         tree_run<OT, D, NC>(a, b, hr, sp, 0, sp.units, true, nullptr, sml, so);
         return;
     }
-    const TreeLine line = tree_line<OT>(a);
+    const TreeLine line = tree_line<attn_unit<OT>()>(a);
     unsigned t = blockIdx.x * line.share;
     if (t >= line.total) return;
     const unsigned tend = min(t + line.share, line.total);
-    TreeAt f = tree_find<OT>(a, line, t);
+    TreeAt f = tree_find<attn_unit<OT>()>(a, line, t);
     int b = f.b;
     unsigned at = f.at;
     TreeSpan sp = f.sp;
     while (t < tend) {
-        const int len = sp.units + ATTN_COST;
+        const int len = sp.units + a.cost;
         const int hr = (t - at) / len;
         const unsigned r0 = at + (unsigned)hr * len;
         const unsigned r1 = min(r0 + len, tend);
-        const int i0 = max(0, (int)(t - r0) - ATTN_COST), i1 = max(0, (int)(r1 - r0) - ATTN_COST);
+        const int i0 = max(0, (int)(t - r0) - a.cost), i1 = max(0, (int)(r1 - r0) - a.cost);
         if (i1 > i0) {
             const bool whole = i1 - i0 == sp.units;
             float* part = a.part + (size_t)(2 * blockIdx.x + (i0 > 0 ? 0 : 1)) * ((size_t)16 * NC * a.rg * (D + 4));
@@ -381,7 +282,7 @@ __global__ __launch_bounds__(64 * AW) void k_tree(TreeArgs a) {
         t = r1;
         if (t < tend && t == at + (unsigned)len * HR) {
             at = t;
-            sp = tree_span<OT>(a, ++b);
+            sp = tree_span<attn_unit<OT>()>(a, ++b);
         }
     }
 }
@@ -399,12 +300,12 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
     poison_lds_done();
     const int tid = threadIdx.x;
     const unsigned w0 = blockIdx.x;
-    const TreeLine line = tree_line<OT>(a);
+    const TreeLine line = tree_line<attn_unit<OT>()>(a);
     const unsigned t = (w0 + 1) * line.share;  // the first place behind the run
     if (t >= line.total) return;
-    const TreeAt f = tree_find<OT>(a, line, t);
-    const int len = f.sp.units + ATTN_COST, hr = (t - f.at) / len;
-    const unsigned r0 = f.at + (unsigned)hr * len + ATTN_COST;  // the place of the row's unit 0
+    const TreeAt f = tree_find<attn_unit<OT>()>(a, line, t);
+    const int len = f.sp.units + a.cost, hr = (t - f.at) / len;
+    const unsigned r0 = f.at + (unsigned)hr * len + a.cost;  // the place of the row's unit 0
     if (r0 >= t || r0 / line.share != w0) return;
     const unsigned w1 = (r0 + f.sp.units - 1) / line.share;
     const int hkv = hr / a.nb, per = 16 * a.nc * a.rg, c0 = hr % a.nb * per;
@@ -453,16 +354,16 @@ __global__ __launch_bounds__(256) void k_tree_join(TreeArgs a) {
 }
 
 // One row a workgroup, without a second kernel, where no row can pass four units a wave (as gdr2_attn.hip).
-inline bool tree_rows_mode(const TreeArgs& a, int unit) {
+inline bool tree_rows_mode(const TreeArgs& a) {
     const long long rows = (long long)a.B * a.Hkv * a.nb;
-    return tree_max_units(a, unit) <= 4 * (AW / a.rg) && rows < (1LL << 32) / (64 * AW);
+    return tree_max_units(a) <= 4 * (AW / a.rg) && rows < (1LL << 32) / (64 * AW);
 }
 
 template <class OT, int D, int NC>
 static hipError_t launch_tree_t(const TreeArgs& a, hipStream_t stream) {
     constexpr int LDS = AW * 16 * NC * (D + 4) * 4;
     const auto one = k_tree<OT, D, NC, false>, line = k_tree<OT, D, NC, true>;
-    const bool rows = tree_rows_mode(a, attn_unit<OT>());
+    const bool rows = tree_rows_mode(a);
     if (LDS > 65536 - 4096) {
         const hipError_t e = hipFuncSetAttribute(rows ? (const void*)one : (const void*)line,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
@@ -484,6 +385,7 @@ static hipError_t launch_tree_d(const TreeArgs& a, hipStream_t stream) {
     return a.nc == 1 ? launch_tree_t<OT, D, 1>(a, stream) : launch_tree_t<OT, D, 2>(a, stream);
 }
 hipError_t launch_tree(const TreeArgs& a, bool bf16_, hipStream_t stream) {
+    if (a.wide) return launch_tree_wide(a, stream);
     if (bf16_) return a.D == 64 ? launch_tree_d<bf16, 64>(a, stream) : launch_tree_d<bf16, 128>(a, stream);
     return a.D == 64 ? launch_tree_d<float, 64>(a, stream) : launch_tree_d<float, 128>(a, stream);
 }

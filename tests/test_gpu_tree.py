@@ -183,8 +183,8 @@ def test_one_draft_is_a_step(dtype):
 
 
 def test_large_scores_and_scales():
-    for scale in (20.0, -0.2, 0.0):
-        q, parents, kc, vc, table, starts = make([257, 40], 9, 4, 4, 64, 32, BF, seed=12)
+    for scale, hkv in ((20.0, 4), (-0.2, 4), (0.0, 4), (20.0, 1), (-0.2, 1), (0.0, 1)):
+        q, parents, kc, vc, table, starts = make([257, 40], 9, 4, hkv, 64, 32, BF, seed=12)
         o, lse = g2.gdr2_attn_tree(q, ints(parents), kc, vc, ints(table), ints(starts), scale=scale, return_lse=True)
         wo, wl = ref.tree(q, parents, kc, vc, table, starts, scale)
         tol = TOL[BF] + 2.0 ** -22 * float(wl.abs().max())
