@@ -930,6 +930,11 @@ def _attn_input(t, name, dtype, shape, dev):
     return st, sh
 
 
+def _like(x, contiguous):
+    """A contiguous tensor of x's shape (empty_like is the quicker call, and keeps the strides of a dense x)."""
+    return torch.empty_like(x) if contiguous else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def _attn_dims(q, k, v, cu_seqlens):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k and v must have four dimensions [B,T,H,D]")
@@ -966,14 +971,14 @@ def gdr2_attn_fwd(q, k, v, *, cu_seqlens=None, scale=None, window=0, o=None, lse
     N, T, Hq, Hkv, D, dt, dev, strides = _attn_dims(q, k, v, cu_seqlens)
     new, own_o, rest = [], o is None, None
     if own_o:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        o = _like(q, strides is None)
         new.append(o)
     else:
         _want(o, "o", q.dtype, q.shape, dev)
     if lse is not None:
         _want(lse, "lse", torch.float32, q.shape[:3], dev)
     elif return_lse or save_for_bwd:
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[0], T, Hq, dtype=torch.float32, device=q.device)
         new.append(lse)
     if save_for_bwd and dt == DTYPE_BF16:
         rest = torch.empty_like(o)
@@ -1002,7 +1007,7 @@ def gdr2_attn_bwd(q, k, v, o, lse, dout, *, rest=None, cu_seqlens=None, scale=No
         _want(rest, "rest", q.dtype, q.shape, dev)
     new, own = [], grads is None
     if own:
-        grads = {n: torch.empty(x.shape, dtype=x.dtype, device=x.device) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+        grads = {n: _like(x, strides is None) for n, x in (("dq", q), ("dk", k), ("dv", v))}
         new += list(grads.values())
     else:
         for n, x in (("dq", q), ("dk", k), ("dv", v)):
