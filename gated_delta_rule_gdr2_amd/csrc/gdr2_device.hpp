@@ -406,6 +406,10 @@ __device__ __forceinline__ bf16x4 lds_read_tr16(const lds_char* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4bf16((T4*)p);
 }
 
+// The same in a kernel that orders its copies to LDS itself. Left to itself the compiler takes a transposing read for one
+// that may meet any copy in flight and waits for all of them; of a pointer that nothing else in the function uses it does not.
+__device__ __forceinline__ bf16x4 lds_read_tr16_now(const lds_char* __restrict p) { return lds_read_tr16(p); }
+
 // ----------------------------------------------------------------------------- LDS fragment reads
 // Views of a matrix held in LDS: element (r, c) lives at byte offset off(r, c).
 template <class XT>

@@ -42,7 +42,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     load_own<OT, D>((const OT*)a.q + tok * a.qs[0] + hq * a.qs[1], a.neg, qf);
     const char* kb = (const char*)((const OT*)a.k + at.tok0 * a.ks[0] + hk * a.ks[1]);
     const char* vb = (const char*)((const OT*)a.v + at.tok0 * a.vs[0] + hk * a.vs[1]);
-    const TileLoad<OT, D, KT, NW, true> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
+    const TileLoad<OT, D, KT, NW> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
     // the tiles that any of the workgroup's queries sees
     const int t0 = max(0, q0 - a.window + 1) / KT, t1 = min(q0 + QT - 1, last) / KT;
     auto fetch = [&](int t) {
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(512, 2) void k_prompt_fwd2(PromptArgs a) {
     load_own<OT, D>((const OT*)a.q + tok * a.qs[0] + hq * a.qs[1], a.neg, qf);
     const char* kb = (const char*)((const OT*)a.k + at.tok0 * a.ks[0] + hk * a.ks[1]);
     const char* vb = (const char*)((const OT*)a.v + at.tok0 * a.vs[0] + hk * a.vs[1]);
-    const TileLoad<OT, D, KT, NW, true> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
+    const TileLoad<OT, D, KT, NW> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
     constexpr int LOADS = 2 * decltype(lk)::N;  // of a wave, a tile's keys and values
     const int t0 = max(0, q0 - a.window + 1) / KT, n = min(q0 + QT - 1, last) / KT - t0 + 1;
     TL tl;

@@ -5,11 +5,14 @@
 // dK and dV summed over the query heads that share a key head. Two kernels, one for dQ (a wave owns 32 queries and
 // walks their keys) and one for dK and dV (a wave owns 32 keys and walks the queries of all heads that see them), each
 // with its sums in registers: every result is added up by one wave in a fixed order, without atomics, for the price of
-// forming the scores twice. The first one leaves lse log2(e) and delta for the second.
+// forming the scores twice. The first one leaves lse log2(e) and -delta for the second.
+//
+// Matrix products bound both (seven of them where a single walk with atomics has five): 2 x 4096 tokens, 16 heads of 128
+// channels, 467 us together, 1030 TFLOP/s counted as seven products, where a large product alone reaches 1198. Packed
+// documents of 64 channels (9 of them, 16 query heads over 4, 2048-token window) 172 us with the sum of the parts.
 #include "gdr2_prompt_device.hpp"
 
 namespace gdr2 {
-
 
 // ---------------------------------------------------------------- dQ: as the forward, keys in tiles
 // (RW x 32 queries a workgroup, S waves for each 32 of them, which share the keys)
@@ -40,7 +43,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     load_own<OT, D>((const OT*)a.dout + row * D, false, df);
     const char* kb = (const char*)((const OT*)a.k + at.tok0 * a.ks[0] + hk * a.ks[1]);
     const char* vb = (const char*)((const OT*)a.v + at.tok0 * a.vs[0] + hk * a.vs[1]);
-    const TileLoad<OT, D, BT, NW, true> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
+    const TileLoad<OT, D, BT, NW> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
     const int t0 = max(0, q0 - a.window + 1) / BT, t1 = min(q0 + QT - 1, last) / BT;
     auto fetch = [&](int t) {
         lds_char* b = lds + (t & 1) * 2 * TB;
@@ -69,7 +72,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     const float lse2 = a.lse[row] * 1.4426950408889634f;
     if (qi <= last && h == 0 && sp == 0) {
         a.lse2[row] = lse2;
-        a.delta[row] = delta;
+        a.delta[row] = -delta;
     }
     f32x16 acc[D / 32];
 #pragma unroll
@@ -126,8 +129,13 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
 
 // ---------------------------------------------------------------- dK, dV: queries in tiles
 // (RW x 32 keys a workgroup, S waves for each 32 of them, which share the queries)
+// Registers leave room for two waves a SIMD at 128 channels, 192 of a lane's 256 being sums and own rows, and for three
+// at 64 (packed documents: the backward 181 us with two, 172 with three). The scheduling barriers keep the compiler from
+// drawing one phase's operands into the one before, which spilled 24 registers.
+template <class OT, int D>
+constexpr int dkv_waves() { return sizeof(OT) == 2 && D == 64 ? 3 : prompt_waves<OT, D>(); }
 template <class OT, int D, int RW, int S>
-__global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt_dkv(PromptArgs a) {
+__global__ __launch_bounds__(64 * RW * S, (dkv_waves<OT, D>())) void k_prompt_dkv(PromptArgs a) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
     constexpr int NW = RW * S, KT = 32 * RW, BT = tile_rows(S), TB = BT * TL::RB, BUF = 2 * TB + 2 * BT * 4, NB = BT / 32 / S;
@@ -156,9 +164,11 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     load_own<OT, D>((const OT*)a.v + tok * a.vs[0] + hk * a.vs[1], false, vf);
     // the query tiles that see any of the workgroup's keys, for each head in turn
     const int t0 = k0 / BT, t1 = (int)min((long long)last, (long long)k0 + KT - 2 + a.window) / BT, nt = t1 - t0 + 1;
-    const TileLoad<OT, D, BT, NW, false> lq(a.qs[0] * (int)sizeof(OT), last, w), ld((long long)a.Hq * TL::RB, last, w);
+    const TileLoad<OT, D, BT, NW> lq(a.qs[0] * (int)sizeof(OT), last, w), ld((long long)a.Hq * TL::RB, last, w);
+    int fh = hk * a.G + g0, ft = t0;  // what is read next: head and tile
     auto fetch = [&](int i) {
-        const int hq = hk * a.G + g0 + i / nt, r0 = (t0 + i % nt) * BT;
+        const int hq = fh, r0 = ft * BT;
+        if (++ft > t1) ft = t0, ++fh;
         lds_char* b = lds + (i & 1) * BUF;
         lq((const char*)((const OT*)a.q + at.tok0 * a.qs[0] + hq * a.qs[1]), r0, b);
         ld((const char*)((const OT*)a.dout + (at.tok0 * a.Hq + hq) * D), r0, b + TB);
@@ -167,8 +177,8 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
             const int y = x * NW + w;  // which 64 of the 2 BT numbers
             if (y < 2 * BT / 64) {
                 const int r = y % (BT / 64) * 64 + l;
-                const float* src = (y / (BT / 64) ? a.delta : a.lse2) + (at.tok0 + min(r0 + r, last)) * a.Hq + hq;
-                __builtin_amdgcn_global_load_lds(src, (lds_void*)(b + 2 * TB + y * 256), 4, 0, 0);
+                const float* src = (y / (BT / 64) ? a.delta : a.lse2) + (at.tok0 + r0) * a.Hq + hq;
+                __builtin_amdgcn_global_load_lds(src + (unsigned)(min(r, last - r0) * a.Hq), (lds_void*)(b + 2 * TB + y * 256), 4, 0, 0);
             }
         }
     };
@@ -178,7 +188,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     for (int i = 0; i < D / 32; ++i) ak[i] = av[i] = zero16();
     const int all = nt * (g1 - g0);
     TL tl;
-    for (int i = 0; i < all; ++i) {
+    for (int i = 0, t = t0; i < all; ++i, t = t == t1 ? t0 : t + 1) {
         tl.fresh();
         wait_vm<0>();
         __syncthreads();
@@ -188,31 +198,40 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
         const lds_char* st = qt + 2 * TB;
 #pragma unroll
         for (int n_ = 0; n_ < NB; ++n_) {
-            const int n = NB * sp + n_, r0 = (t0 + i % nt) * BT + 32 * n;
+            const int n = NB * sp + n_, r0 = t * BT + 32 * n;
             if (r0 + 31 < wk0 || r0 > last || r0 - wk0 - 31 >= a.window) continue;
-            f32x16 s = zero16(), dp = zero16();
+            asm volatile("" : "+v"(tl.rb), "+v"(tl.cb));  // (addresses formed anew: registers)
+            f32x16 s = zero16(), dp;  // dP - delta from the start
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const f32x4 de = lds_load<f32x4>(st + (BT + 32 * n + 8 * j + 4 * h) * 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) dp[4 * j + x] = de[x];
+            }
 #pragma unroll
             for (int b = 0; b < D / 16; ++b) mma32(s, tl.rows(qt, 32 * n, 16 * b), kf[b]);
 #pragma unroll
             for (int b = 0; b < D / 16; ++b) mma32(dp, tl.rows(dt_, 32 * n, 16 * b), vf[b]);
             if constexpr (sizeof(OT) == 2) reads_ahead<D / 8, 1, 2>();
+            __builtin_amdgcn_sched_barrier(0);
             const bool mask = r0 < wk0 + 31 || r0 + 31 > last || r0 + 31 - wk0 >= a.window;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const f32x4 ls = lds_load<f32x4>(st + (32 * n + 8 * j + 4 * h) * 4);
-                const f32x4 de = lds_load<f32x4>(st + (BT + 32 * n + 8 * j + 4 * h) * 4);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    float p = __builtin_amdgcn_exp2f(fmaf(s[4 * j + x], a.scale2, -ls[x]));
-                    float g = p * (dp[4 * j + x] - de[x]);
-                    if (mask) {
-                        const int r = r0 + 8 * j + 4 * h + x, d = r - ki;
-                        const bool see = d >= 0 && d < a.window && r <= last;
-                        p = see ? p : 0.f;
-                        g = see ? g : 0.f;
-                    }
-                    s[4 * j + x] = p;
-                    dp[4 * j + x] = g;
+                    s[4 * j + x] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + x], a.scale2, -ls[x]));
+                    dp[4 * j + x] *= s[4 * j + x];
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            if (mask) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int q = r0 + 8 * (r >> 2) + 4 * h + (r & 3), d = q - ki;
+                    const bool see = d >= 0 && d < a.window && q <= last;
+                    s[r] = see ? s[r] : 0.f;
+                    dp[r] = see ? dp[r] : 0.f;
                 }
             }
 #pragma unroll
@@ -225,6 +244,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
                 }
             }
             if constexpr (sizeof(OT) == 2) reads_ahead<D / 8, 2, 1>();  // (as far as the registers go)
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if constexpr (S > 1) {

@@ -78,7 +78,7 @@ struct Tile32 {
     __device__ __forceinline__ typename Frag<OT>::type cols(const lds_char* t, int c0, int k0) const {
         const lds_char* p = t + k0 * RB;
         if constexpr (ES == 2) {
-            const bf16x4 v0 = lds_read_tr16(p + (cb ^ (c0 * ES))), v1 = lds_read_tr16(p + (cb ^ (c0 * ES + 32)) + 8 * RB);
+            const bf16x4 v0 = lds_read_tr16_now(p + (cb ^ (c0 * ES))), v1 = lds_read_tr16_now(p + (cb ^ (c0 * ES + 32)) + 8 * RB);
             return __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
         } else {
             typename Frag<OT>::type f;
@@ -90,51 +90,57 @@ struct Tile32 {
     }
 };
 
-// Rows of a matrix (row stride rs bytes, rows 0 .. last) in tiles of R into LDS by NW waves, this one being wave w. The
-// lane's offsets inside a tile are formed once (KEEP), or, where registers are short, at each tile; a tile that reaches
-// past the last row forms others.
-template <class OT, int D, int R, int NW, bool KEEP>
+// Rows of a matrix (row stride rs bytes, rows 0 .. last) in tiles of R into LDS by NW waves, this one being wave w: 1 KB an
+// instruction. An instruction's first row is the wave's to know, and the permutation of its chunks repeats after PER
+// instructions: the lane's share of the address is formed once. (Formed at each instruction, a 64-row tile of queries and
+// of their gradients kept each wave of the backward 1280 clocks.) A tile that reaches past the last row forms all anew.
+template <class OT, int D, int R, int NW>
 struct TileLoad {
     using TL = Tile32<OT, D>;
-    static constexpr int ALL = R * TL::RB / 1024, N = (ALL + NW - 1) / NW, RPI = 64 / TL::NCH;  // 1 KB an instruction
-    static_assert(R * TL::RB % 1024 == 0, "whole rows an instruction");
+    static constexpr int ALL = R * TL::RB / 1024, N = (ALL + NW - 1) / NW, RPI = 64 / TL::NCH;
+    static constexpr int PER = NW * RPI % 16 == 0 ? 1 : 2;  // tile_f goes by the row modulo 16
+    static_assert(R * TL::RB % 1024 == 0 && 2 * NW * RPI % 16 == 0, "whole rows an instruction");
     long long rs;
     int last, w;
-    unsigned off[KEEP ? N : 1];
+    unsigned off[PER];
 
     __device__ __forceinline__ int row(int l, int i) const { return (i * NW + w) * RPI + l / TL::NCH; }
     __device__ __forceinline__ unsigned piece(int l, int i) const { return ((l % TL::NCH) ^ tile_f<TL::NCH>(row(l, i))) * 16; }
     __device__ __forceinline__ TileLoad(long long rs_, int last_, int w_) : rs(rs_), last(last_), w(w_) {
-        if constexpr (KEEP)
 #pragma unroll
-            for (int i = 0; i < N; ++i) off[i] = row(lane_id(), i) * (unsigned)rs + piece(lane_id(), i);
+        for (int i = 0; i < PER; ++i) off[i] = lane_id() / TL::NCH * (unsigned)rs + piece(lane_id(), i);
     }
     __device__ __forceinline__ void operator()(const char* base, int row0, lds_char* t) const {
-        const char* b = base + (long long)row0 * rs;
-        const bool whole = row0 + R - 1 <= last;
-        int l = lane_id();
-        if constexpr (!KEEP) asm volatile("" : "+v"(l));
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (ALL % NW != 0 && i * NW + w >= ALL) break;
-            const char* src = b + (KEEP ? off[KEEP ? i : 0] : row(l, i) * (unsigned)rs + piece(l, i));
-            if (!whole) src = base + (long long)max(0, min(row0 + row(l, i), last)) * rs + piece(l, i);
+        auto send = [&](const char* src, int i) __attribute__((always_inline)) {
             __builtin_amdgcn_global_load_lds(src, (lds_void*)(t + (i * NW + w) * 1024), 16, 0, 0);
+        };
+        if (row0 + R - 1 <= last) {
+            const char* b = base + ((long long)row0 + w * RPI) * rs;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (ALL % NW == 0 || i * NW + w < ALL) send(b + (long long)(i * NW * RPI) * rs + off[i % PER], i);
+        } else {
+            int l = lane_id();
+            asm volatile("" : "+v"(l));  // or these addresses take registers from the whole walk
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (ALL % NW == 0 || i * NW + w < ALL)
+                    send(base + (long long)max(0, min(row0 + row(l, i), last)) * rs + piece(l, i), i);
         }
     }
 };
 
-// Order of a block of STEPS matrix products with R LDS reads each: the reads run AHEAD products before their use. Left
-// to itself the compiler reads each operand just before its product and waits for it.
-template <int STEPS, int R, int AHEAD>
+// Order of a block of STEPS operands with R LDS reads and M matrix products each: the reads run AHEAD operands before
+// their use. Left to itself the compiler reads each operand just before its product and waits for it.
+template <int STEPS, int R, int AHEAD, int M = 1>
 __device__ __forceinline__ void reads_ahead() {
     __builtin_amdgcn_sched_group_barrier(0x100, R * AHEAD, 0);
 #pragma unroll
     for (int i = 0; i < STEPS - AHEAD; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, M * AHEAD, 0);
 }
 
 // B operands of a wave's own 32 rows, all K blocks, straight from memory: row p (this lane's), contiguous K order.

@@ -104,6 +104,20 @@ def test_window(dtype, window):
     check(*make(cu[-1], 6, 3, 64, dtype, seed=5), cu, window=window)
 
 
+@pytest.mark.parametrize("lens,heads,window", [([1024] * 4, (32, 32), 0), ([1500, 1, 2047], (40, 8), 0), ([1100, 1300], (64, 2), 300),
+                                               ([1, 3000, 130], (48, 48), 0), ([2200], (64, 64), 70)])
+def test_long_sequences_of_many_heads(lens, heads, window):
+    # enough work that waves take turns on it
+    cu = bounds(lens)
+    q, k, v, do = make(cu[-1], *heads, 128, BF, seed=30)
+    packed = check(q, k, v, do, cu, window=window)
+    again = check(q, k, v, do, cu, window=window)
+    assert all(torch.equal(a, b) for a, b in zip(packed[:3], again[:3]))
+    assert all(torch.equal(packed[3][n], again[3][n]) for n in packed[3])
+    if len(set(lens)) == 1:
+        check(*(x.view(len(lens), lens[0], -1, 128) for x in (q, k, v, do)), cu, window=window, packed=False)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_one_token_rows(dtype):
     # a token that sees itself only: o = v and lse its score, and gradients that are dO and (but for fp32's roundings
