@@ -31,6 +31,10 @@ struct TreeWide {
     static constexpr int NW = RW * S, TB = KT * TL::RB, NB = KT / 32 / S, GR = KT / 16;
     // tiles in LDS, all but one on their way: one ahead alone leaves the memory's latency longer than a tile's work
     static constexpr int NBUF = 8 * TB <= 131072 ? 4 : 2;
+    // Half of the waves send for a tile after their scores: loads are held at their issue while the memory is busy with
+    // earlier ones, and the other half multiplies meanwhile. 32 ragged trees of 32 drafts, 32 heads over 8: 126 us, 123 so;
+    // but with 64 rows a key head (64 sequences of 2000, 16 drafts) 118, and 122 so, and tiles of 64 tokens gain nothing.
+    static constexpr bool LATE = RW == 4 && KT == 128;
     static constexpr int ACC = D / 32 * 4096, TILES = NBUF * 2 * TB, JOIN = (S - 1) * RW * (ACC + 512);
     static constexpr int LDS = TILES > JOIN ? TILES : JOIN;
 
@@ -106,7 +110,8 @@ struct TreeWide {
             __syncthreads();  // the tile has landed, and everyone is done with the one before
             const int k0 = (t0 + i) * KT;
             const unsigned okp = (okq >> (8 * (i % NBUF))) & 255u;
-            if (i + NBUF - 1 < work) send(i + NBUF - 1);
+            const bool more = i + NBUF - 1 < work;
+            if (more && !(LATE && w >= NW / 2)) send(i + NBUF - 1);
             lds_char* kt = lds + i % NBUF * 2 * TB;
             lds_char* vt = kt + TB;
             const bool mask = k0 < lo_in || k0 + KT > sp.start || okp != (1u << GR) - 1;
@@ -129,6 +134,10 @@ struct TreeWide {
 #pragma unroll
                 for (int x = 0; x < NB; ++x) mma32(s[x], tf.rows(kt, r0 + 32 * x, 16 * y), qf[y]);
             reads_ahead<D / 16 * NB, 1, 4>();
+            if constexpr (LATE) {
+                __builtin_amdgcn_sched_barrier(0);
+                if (more && w >= NW / 2) send(i + NBUF - 1);
+            }
             if (mask) {
 #pragma unroll
                 for (int x = 0; x < NB; ++x) {
