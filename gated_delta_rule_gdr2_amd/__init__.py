@@ -925,6 +925,8 @@ def _attn_input(t, name, dtype, shape, dev):
     sb, st, sh, sd = t.stride()
     if t.is_contiguous():
         return H * D, D
+    if T == 1:
+        st = sb  # (the stride over tokens says nothing then)
     if sd != 1 or (B > 1 and T > 0 and sb != T * st):
         raise ValueError("the channels of %s must be contiguous, and its sequences T token strides apart" % name)
     return st, sh

@@ -93,7 +93,8 @@ struct Tile32 {
 // Rows of a matrix (row stride rs bytes, rows 0 .. last) in tiles of R into LDS by NW waves, this one being wave w: 1 KB an
 // instruction. An instruction's first row is the wave's to know, and the permutation of its chunks repeats after PER
 // instructions: the lane's share of the address is formed once. (Formed at each instruction, a 64-row tile of queries and
-// of their gradients kept each wave of the backward 1280 clocks.) A tile that reaches past the last row forms all anew.
+// of their gradients kept each wave of the backward 1280 clocks.) A tile that reaches past the last row forms all anew, and
+// so does any of rows so far apart that the lane's share would pass 32 bits.
 template <class OT, int D, int R, int NW>
 struct TileLoad {
     using TL = Tile32<OT, D>;
@@ -101,12 +102,13 @@ struct TileLoad {
     static constexpr int PER = NW * RPI % 16 == 0 ? 1 : 2;  // tile_f goes by the row modulo 16
     static_assert(R * TL::RB % 1024 == 0 && 2 * NW * RPI % 16 == 0, "whole rows an instruction");
     long long rs;
-    int last, w;
+    int last, quick, w;  // quick: the last row of tiles that are not formed anew
     unsigned off[PER];
 
     __device__ __forceinline__ int row(int l, int i) const { return (i * NW + w) * RPI + l / TL::NCH; }
     __device__ __forceinline__ unsigned piece(int l, int i) const { return ((l % TL::NCH) ^ tile_f<TL::NCH>(row(l, i))) * 16; }
     __device__ __forceinline__ TileLoad(long long rs_, int last_, int w_) : rs(rs_), last(last_), w(w_) {
+        quick = rs < (1 << 29) ? last : -1;
 #pragma unroll
         for (int i = 0; i < PER; ++i) off[i] = lane_id() / TL::NCH * (unsigned)rs + piece(lane_id(), i);
     }
@@ -114,7 +116,7 @@ struct TileLoad {
         auto send = [&](const char* src, int i) __attribute__((always_inline)) {
             __builtin_amdgcn_global_load_lds(src, (lds_void*)(t + (i * NW + w) * 1024), 16, 0, 0);
         };
-        if (row0 + R - 1 <= last) {
+        if (row0 + R - 1 <= quick) {
             const char* b = base + ((long long)row0 + w * RPI) * rs;
 #pragma unroll
             for (int i = 0; i < N; ++i)

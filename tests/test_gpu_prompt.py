@@ -394,6 +394,24 @@ def test_offsets_past_32_bits():
         assert not a[:, :cu[0]].any() and not a[:, cu[-1]:].any()
 
 
+def test_token_strides_past_32_bits():
+    T, far = 70, 5 << 26  # 640 MiB from token to token: of 8 rows, 7 strides pass 32 bits
+    q, k, v, do = make(T, 4, 2, 64, BF, seed=22)
+    want = check(q, k, v, do, [0, T])
+    room = torch.empty(T * far, dtype=BF, device="cuda").view(1, T, far)[:, :, :4 * 64].unflatten(2, (4, 64))
+    room[:, :, :2] = k
+    room[:, :, 2:] = v
+    got = check(q, room[:, :, :2], room[:, :, 2:], do, [0, T])
+    assert all(torch.equal(x, y) for x, y in zip(want[:3], got[:3])) and all(torch.equal(want[3][n], got[3][n]) for n in want[3])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_one_token_of_each_sequence(dtype):
+    q, k, v, do = (x.view(3, 50, -1, 64) for x in make(150, 4, 2, 64, dtype, seed=23))
+    one = [x[:, 7:8] for x in (q, k, v)]
+    assert torch.equal(g2.gdr2_attn_fwd(*one), g2.gdr2_attn_fwd(*(x.contiguous() for x in one)))
+
+
 def test_refusals():
     q, k, v, do = make(20, 4, 2, 64, BF, seed=21)
     f = g2.gdr2_attn_fwd
