@@ -38,11 +38,11 @@ inline long long prompt_length(int N, int T, bool packed) { return packed ? ((lo
 
 // Waves that share a block's other axis: none share where the longest walk is at most half of what each of the 1024
 // SIMDs has to do anyway, or where two short walks for each are there to hide one another's latency, two where it is no
-// longer than that, else four. `tasks`: walks of one head each; `heads`: heads that a walk goes through one after another. Measured, bf16, 128 channels, us (S = 1, 2, 4; the tile that is best):
-//   forward   2 x 4096 tokens, 16 heads 143, 189, 233   1 x 8192, 8 heads 184, 165, 201   1 x 2048, 16 heads 47, 42, 39
-//             1 x 512, 16 heads 16, 15, 12              24 packed, 17 - 700 tokens, 16 heads 30, 35, 62
-//   dK, dV    2 x 4096 tokens, 16 heads 282, 321, 383   1 x 8192, 8 heads over 1 453, 304, 374
-//             1 x 2048, 16 heads 112, 74, 66            1 x 512, 16 heads over 4 41, 29, 24
+// longer than that, else four. `tasks`: walks of one head each; `heads`: heads that a walk goes through one after
+// another. Measured with S = 1, 2, 4, bf16, 128 channels, us, forward and backward:
+//     2 x 4096 tokens, 16 heads 166, 210, 258 and 510, 566, 689     1 x 8192, 8 heads over 1 194, 169, 205 and 674, 528, 589
+//     1 x 2048, 16 heads 45, 43, 39 and 166, 120, 112               1 x 512, 16 heads 16, 17, 11 and 60, 50, 36
+//     24 packed of 17 - 700 tokens, 16 heads over 4 31, 45, 61 and 109, 132, 197
 inline int prompt_sharing(const PromptArgs& a, long long tasks, int heads) {
     const long long len = prompt_length(a.N, a.T, a.cu != nullptr), seen = len < a.window ? len : a.window;
     const long long walk = (seen + 63) / 64 * heads;  // tiles of the longest walk
@@ -51,8 +51,8 @@ inline int prompt_sharing(const PromptArgs& a, long long tasks, int heads) {
 }
 
 // Parts that the query heads of a key head are cut in for dK and dV, each walked by itself and added up by a further
-// kernel: as many as make 4096 walks. Measured, us, for 1 .. G parts: 1 x 4096 tokens, 32 heads over 8 380, 316, 301;
-// 1 x 8192, 8 over 1 1222, 640, 363, 304; 9 packed documents, 16 over 4 of 64 channels 134, 119, 110.
+// kernel: as many as make 4096 walks. The backward with 1, 2 and G parts, us: 1 x 4096 tokens, 32 heads over 8 505, 504, 492;
+// 1 x 8192, 8 over 1 1155, 716, 499; 9 packed documents, 16 over 4 of 64 channels 205, 186, 180.
 inline int prompt_parts(int N, int T, int Hq, int Hkv, bool packed) {
     const long long walks = prompt_blocks(N, T, packed) * Hkv, G = Hq / Hkv;
     const long long p = walks > 0 ? (4096 + walks - 1) / walks : 1;

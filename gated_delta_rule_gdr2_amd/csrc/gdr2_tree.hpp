@@ -31,7 +31,7 @@ struct KeepArgs {
 };
 
 // Four waves of rows side by side: tiles of 64 tokens where the tables leave a workgroup few of them, us with 64 and 128:
-// 1 sequence of 777 tokens, 12 drafts, 16 heads over 2 20.0 and 24.2; 32 of 200 to 16384, 32 drafts, 32 over 8 140 and 130.
+// 1 sequence of 777 tokens, 12 drafts, 16 heads over 2 16.6 and 19.1; 32 of 200 to 16384, 32 drafts, 32 over 8 138 and 122.
 inline int tree_tile(const TreeArgs& a) {
     const long long tiles = (((long long)a.c.max_pages << a.c.shift) + 63) / 64;
     return tiles * a.B * a.Hkv * a.nb <= 4 * a.wgs ? 64 : 128;

@@ -357,12 +357,14 @@ int gdr2_attn_bwd(const void* q, const void* k, const void* v, const long long* 
  *   starts  : int32 [B] on the device, taken as 0 .. max_pages page_size where outside
  * Draft i sees the tokens that its sequence holds, the drafts on its way to the root, and itself; with window > 0 the
  * last `window` of these (the place of a draft in its sequence is starts[b] + the number of drafts above it).
- * Caches, strides, block_table, scale and results as in gdr2_attn_step; padding gets o = 0 and lse = -inf. What the
- * cache holds where no draft of the sequence sees it does not matter; a value that some of its drafts see has to be finite.
- * GDR2_ERR_SHAPE: T over 64, max_pages page_size over 2^31 - 129, B T Hq over 2^31 - 1, and long lines as there, a
- * row being 128 (T Hq / Hkv of 16 and less: that many, else a power of two times 32, up to 256) of a key head's pairs
- * of drafts and heads. Workspace: gdr2_attn_tree_workspace_bytes, of no content between calls; calls that may overlap
- * need one each. */
+ * Caches, strides, block_table and scale as in gdr2_attn_step; padding gets o = 0 and lse = -inf. What the cache holds
+ * where no draft of the sequence sees it does not matter; a value that some of its drafts see has to be finite. Scores,
+ * weights' sums and lse are fp32; with bf16 the weights enter the second product in two bf16 parts where T Hq / Hkv is 32
+ * or less, so that o is off by its own rounding, and as one beyond, so that it carries two. Results repeat bit for bit.
+ * GDR2_ERR_SHAPE: T over 64, max_pages page_size over 2^31 - 129, B T Hq over 2^31 - 1, or more than 2^31 - 1 places of
+ * B Hkv ceil(T Hq / Hkv / 256) rows, each of which takes up to 6 and one for every 16 tokens of the table, or of the
+ * window, the drafts and 128 more where that is less. o must not overlap the inputs.
+ * Workspace: gdr2_attn_tree_workspace_bytes, of no content between calls; calls that may overlap need one each. */
 size_t gdr2_attn_tree_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int dtype);
 
 int gdr2_attn_tree(const void* q, const int* parents, const void* k_cache, const void* v_cache,
@@ -384,7 +386,7 @@ int gdr2_kv_keep(void* k_cache, void* v_cache, const long long* cache_strides, c
  *                     and how many come to it; a negative count ends the request
  *   block_table     : int32 [B][max_pages], updated; entries outside 0 .. num_pages - 1 are no page
  *   free_pages      : int32 [num_pages], updated: a stack whose first num_free[0] (int32, updated; taken as
- *                     0 .. num_pages where outside) entries are the free pages
+ *                     0 .. num_pages where outside) entries are the free pages, numbers of pages
  *   new_lengths     : int32 [B]: tokens held with the new ones
  *   cu_seqlens      : int32 [B + 1]: bounds of the requests' new tokens, packed one after another; at most max_tokens
  *   slots           : int64 [max_tokens], or NULL: page * page_size + offset for each packed token, -1 where it has none
