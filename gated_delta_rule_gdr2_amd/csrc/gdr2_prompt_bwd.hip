@@ -21,7 +21,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
     constexpr int NW = RW * S, QT = 32 * RW, BT = tile_rows(S), TB = BT * TL::RB, NB = BT / 32 / S;
-    constexpr int ACC = D / 32 * 4096;
+    constexpr int ACC = D / 32 * 4096, KB = D / 16, DT = D / 32, AHEAD = sizeof(OT) == 2 ? 4 : 1;
     extern __shared__ __align__(16) char smem[];
     lds_char* lds = (lds_char*)smem;
     poison_lds(lds, 4 * TB);
@@ -74,9 +74,11 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
         a.lse2[row] = lse2;
         a.delta[row] = -delta;
     }
-    f32x16 acc[D / 32];
+    f32x16 acc[D / 32], less;  // less: what dP starts from
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[i] = zero16();
+#pragma unroll
+    for (int r = 0; r < 16; ++r) less[r] = -delta;
     TL tl;
     for (int t = t0; t <= t1; ++t) {
         tl.fresh();
@@ -90,16 +92,25 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
         const bool part = k0 + 32 * NB - 1 > wq0 || k0 <= wq0 + 31 - a.window;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-            f32x16 s = zero16(), dp = zero16();
-#pragma unroll
-            for (int b = 0; b < D / 16; ++b) mma32(s, tl.rows(kt, b0 + 32 * n, 16 * b), qf[b]);
-#pragma unroll
-            for (int b = 0; b < D / 16; ++b) mma32(dp, tl.rows(vt, b0 + 32 * n, 16 * b), df[b]);
-            if constexpr (sizeof(OT) == 2) reads_ahead<D / 8, 1, 4>();
+            f32x16 s = zero16(), dp = less;
+            auto row = [&](int i) __attribute__((always_inline)) {
+                return i < KB ? tl.rows(kt, b0 + 32 * n, 16 * i) : tl.rows(vt, b0 + 32 * n, 16 * (i - KB));
+            };
+            Pipe<2 * KB, AHEAD, FR> scores;
+            scores.start(row);
+            scores.run(row, [&](int i, const FR& x) __attribute__((always_inline)) {
+                if (i < KB) mma32(s, x, qf[i]);
+                else mma32(dp, x, df[i - KB]);
+            });
+            auto col = [&](int i) __attribute__((always_inline)) {
+                return tl.cols(kt, 32 * (i % DT), b0 + 32 * n + 16 * (i / DT));
+            };
+            Pipe<2 * DT, AHEAD, FR> sums;
+            sums.start(col);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, -lse2));
-                s[r] = p * (dp[r] - delta);
+                s[r] = p * dp[r];
             }
             if (part) {
 #pragma unroll
@@ -108,13 +119,8 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
                     s[r] = d >= 0 && d < a.window ? s[r] : 0.f;
                 }
             }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const FR f = acc_frag<OT>(s, b);
-#pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) mma32(acc[dt], tl.cols(kt, 32 * dt, b0 + 32 * n + 16 * b), f);
-            }
-            if constexpr (sizeof(OT) == 2) reads_ahead<D / 16, 2, 4>();
+            FR f[2] = {acc_frag<OT>(s, 0), acc_frag<OT>(s, 1)};
+            sums.run(col, [&](int i, const FR& x) __attribute__((always_inline)) { mma32(acc[i % DT], x, f[i / DT]); });
         }
     }
     if constexpr (S > 1) {
@@ -129,9 +135,9 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
 
 // ---------------------------------------------------------------- dK, dV: queries in tiles
 // (RW x 32 keys a workgroup, S waves for each 32 of them, which share the queries)
-// Registers leave room for two waves a SIMD at 128 channels, 192 of a lane's 256 being sums and own rows, and for three
-// at 64 (packed documents: the backward 181 us with two, 172 with three). The scheduling barriers keep the compiler from
-// drawing one phase's operands into the one before, which spilled 24 registers.
+// Registers leave room for two waves a SIMD at 128 channels, 192 of a lane's 256 being sums and own rows (operands two
+// ahead spilled: 503 us for 480), and for three at 64 (packed documents: the backward 181 us with two, 172 with three). The
+// scheduling barriers keep the compiler from drawing one phase's operands into the one before, which spilled 24.
 template <class OT, int D>
 constexpr int dkv_waves() { return sizeof(OT) == 2 && D == 64 ? 3 : prompt_waves<OT, D>(); }
 template <class OT, int D, int RW, int S>
@@ -139,7 +145,7 @@ __global__ __launch_bounds__(64 * RW * S, (dkv_waves<OT, D>())) void k_prompt_dk
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
     constexpr int NW = RW * S, KT = 32 * RW, BT = tile_rows(S), TB = BT * TL::RB, BUF = 2 * TB + 2 * BT * 4, NB = BT / 32 / S;
-    constexpr int ACC = D / 32 * 4096;
+    constexpr int ACC = D / 32 * 4096, KB = D / 16, DT = D / 32, AHEAD = sizeof(OT) == 2 && D == 64 ? 2 : 1;
     extern __shared__ __align__(16) char smem[];
     lds_char* lds = (lds_char*)smem;
     poison_lds(lds, 2 * BUF);
@@ -208,12 +214,20 @@ __global__ __launch_bounds__(64 * RW * S, (dkv_waves<OT, D>())) void k_prompt_dk
 #pragma unroll
                 for (int x = 0; x < 4; ++x) dp[4 * j + x] = de[x];
             }
-#pragma unroll
-            for (int b = 0; b < D / 16; ++b) mma32(s, tl.rows(qt, 32 * n, 16 * b), kf[b]);
-#pragma unroll
-            for (int b = 0; b < D / 16; ++b) mma32(dp, tl.rows(dt_, 32 * n, 16 * b), vf[b]);
-            if constexpr (sizeof(OT) == 2) reads_ahead<D / 8, 1, 2>();
-            __builtin_amdgcn_sched_barrier(0);
+            auto row = [&](int i) __attribute__((always_inline)) {
+                return i < KB ? tl.rows(qt, 32 * n, 16 * i) : tl.rows(dt_, 32 * n, 16 * (i - KB));
+            };
+            Pipe<2 * KB, AHEAD, FR> scores;
+            scores.start(row);
+            scores.run(row, [&](int i, const FR& x) __attribute__((always_inline)) {
+                if (i < KB) mma32(s, x, kf[i]);
+                else mma32(dp, x, vf[i - KB]);
+            });
+            auto col = [&](int i) __attribute__((always_inline)) {
+                return tl.cols(i % 2 ? qt : dt_, 32 * (i / 2 % DT), 32 * n + 16 * (i / 2 / DT));
+            };
+            Pipe<4 * DT, AHEAD, FR> sums;
+            sums.start(col);
             const bool mask = r0 < wk0 + 31 || r0 + 31 > last || r0 + 31 - wk0 >= a.window;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -234,16 +248,12 @@ __global__ __launch_bounds__(64 * RW * S, (dkv_waves<OT, D>())) void k_prompt_dk
                     dp[r] = see ? dp[r] : 0.f;
                 }
             }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const FR pf = acc_frag<OT>(s, b), gf = acc_frag<OT>(dp, b);
-#pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) {
-                    mma32(av[dt], tl.cols(dt_, 32 * dt, 32 * n + 16 * b), pf);
-                    mma32(ak[dt], tl.cols(qt, 32 * dt, 32 * n + 16 * b), gf);
-                }
-            }
-            if constexpr (sizeof(OT) == 2) reads_ahead<D / 8, 2, 1>();  // (as far as the registers go)
+            FR pf[2] = {acc_frag<OT>(s, 0), acc_frag<OT>(s, 1)}, gf[2] = {acc_frag<OT>(dp, 0), acc_frag<OT>(dp, 1)};
+            sums.run(col, [&](int i, const FR& x) __attribute__((always_inline)) {
+                const int dt = i / 2 % DT, b = i / 2 / DT;
+                if (i % 2) mma32(ak[dt], x, gf[b]);
+                else mma32(av[dt], x, pf[b]);
+            });
             __builtin_amdgcn_sched_barrier(0);
         }
     }

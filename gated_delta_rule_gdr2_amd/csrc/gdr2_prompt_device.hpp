@@ -132,18 +132,43 @@ struct TileLoad {
     }
 };
 
-// Order of a block of STEPS operands with R LDS reads and M matrix products each: the reads run AHEAD operands before
-// their use. Left to itself the compiler reads each operand just before its product and waits for it.
-template <int STEPS, int R, int AHEAD, int M = 1>
+// Order of a block of STEPS matrix products with R LDS reads each: the reads run AHEAD products before their use. Left
+// to itself the compiler reads each operand just before its product and waits for it.
+template <int STEPS, int R, int AHEAD>
 __device__ __forceinline__ void reads_ahead() {
     __builtin_amdgcn_sched_group_barrier(0x100, R * AHEAD, 0);
 #pragma unroll
     for (int i = 0; i < STEPS - AHEAD; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, M * AHEAD, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, AHEAD, 0);
 }
+
+// STEPS matrix products whose A operands are read from LDS AHEAD of them, in the order that is written here: asked for by
+// groups of kinds alone (reads_ahead), the compiler takes the product whose operand it has just read, where there are
+// two chains of them or registers are short, and waits for it (training step's backward 487 us so, 480 in order). Vector
+// and scalar work may move across. start: the first reads, for vector work to cover.
+template <int STEPS, int AHEAD, class FR>
+struct Pipe {
+    FR x[AHEAD + 1];
+    template <class R>
+    __device__ __forceinline__ void start(R read) {
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) x[i] = read(i);
+        __builtin_amdgcn_sched_barrier(0x6);
+    }
+    template <class R, class M>
+    __device__ __forceinline__ void run(R read, M mul) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+            if (i + AHEAD < STEPS) x[(i + AHEAD) % (AHEAD + 1)] = read(i + AHEAD);
+            __builtin_amdgcn_sched_barrier(0x6);
+            mul(i, x[i % (AHEAD + 1)]);
+            __builtin_amdgcn_sched_barrier(0x6);
+        }
+    }
+};
 
 // B operands of a wave's own 32 rows, all K blocks, straight from memory: row p (this lane's), contiguous K order.
 template <class OT, int D>

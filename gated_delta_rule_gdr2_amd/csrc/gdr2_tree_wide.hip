@@ -30,7 +30,7 @@ __device__ __forceinline__ unsigned tree_mask(int k0, int start, int lo, unsigne
 template <int D, int RW, int S, int KT>
 struct TreeWide {
     using TL = Tile32<bf16, D>;
-    static constexpr int NW = RW * S, TB = KT * TL::RB, NB = KT / 32 / S, GR = KT / 16;
+    static constexpr int KB = D / 16, DT = D / 32, NW = RW * S, TB = KT * TL::RB, NB = KT / 32 / S, GR = KT / 16;
     // tiles in LDS, all but one on their way: one ahead alone leaves the memory's latency longer than a tile's work
     static constexpr int NBUF = 8 * TB <= 131072 ? 4 : 2;
     // Half of the waves send for a tile after their scores: loads are held at their issue while the memory is busy with
@@ -131,11 +131,10 @@ struct TreeWide {
             f32x16 s[NB];
 #pragma unroll
             for (int x = 0; x < NB; ++x) s[x] = zero16();
-#pragma unroll
-            for (int y = 0; y < D / 16; ++y)
-#pragma unroll
-                for (int x = 0; x < NB; ++x) mma32(s[x], tf.rows(kt, r0 + 32 * x, 16 * y), qf[y]);
-            reads_ahead<D / 16 * NB, 1, 4>();
+            auto row = [&](int i) __attribute__((always_inline)) { return tf.rows(kt, r0 + 32 * (i % NB), 16 * (i / NB)); };
+            Pipe<KB * NB, 4, bf16x8> scores;
+            scores.start(row);
+            scores.run(row, [&](int i, const bf16x8& x) __attribute__((always_inline)) { mma32(s[i % NB], x, qf[i / NB]); });
             if constexpr (LATE) {
                 __builtin_amdgcn_sched_barrier(0);
                 if (more && w >= NW / 2) send(i + NBUF - 1);
@@ -177,11 +176,10 @@ struct TreeWide {
                 pf[2 * x] = acc_frag<bf16>(s[x], 0);
                 pf[2 * x + 1] = acc_frag<bf16>(s[x], 1);
             }
-#pragma unroll
-            for (int y = 0; y < 2 * NB; ++y)
-#pragma unroll
-                for (int dt = 0; dt < D / 32; ++dt) mma32(acc[dt], tf.cols(vt, 32 * dt, r0 + 16 * y), pf[y]);
-            reads_ahead<D / 16 * NB, 2, 4>();
+            auto col = [&](int i) __attribute__((always_inline)) { return tf.cols(vt, 32 * (i % DT), r0 + 16 * (i / DT)); };
+            Pipe<2 * NB * DT, 4, bf16x8> sums;
+            sums.start(col);
+            sums.run(col, [&](int i, const bf16x8& x) __attribute__((always_inline)) { mma32(acc[i % DT], x, pf[i / DT]); });
         }
         float total = one ? sum_halves((sum[0] + sum[1]) + (sum[2] + sum[3])) : 0.f;
         if (!one) m = -INFINITY;  // padding sees nothing
