@@ -17,8 +17,8 @@
 
 namespace gdr2 {
 
-// RW x 32 queries a workgroup, S waves for each 32 of them, which share the keys
-template <class OT, int D, int RW, int S>
+// RW x 32 queries a workgroup, S waves for each 32 of them, which share the keys; EXACT: queries of few keys in two parts
+template <class OT, int D, int RW, int S, bool EXACT>
 __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt_fwd(PromptArgs a) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
@@ -109,6 +109,20 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
             pf[2 * n] = acc_frag<OT>(s[n], 0);
             pf[2 * n + 1] = acc_frag<OT>(s[n], 1);
         }
+        if constexpr (EXACT)
+            if (prompt_few(a, wq0)) {
+                FR f[2 * NB];
+#pragma unroll
+                for (int b = 0; b < 2 * NB; ++b) f[b] = rest_frag(s[b / 2], b % 2, pf[b]);
+                Pipe<2 * NB * (D / 32), 1, FR> rest;
+                auto col = [&](int i) __attribute__((always_inline)) {
+                    return tl.cols(vt, 32 * (i % (D / 32)), r0 + 16 * (i / (D / 32)));
+                };
+                rest.start(col);
+                rest.run(col, [&](int i, const FR& x) __attribute__((always_inline)) {
+                    mma32(acc[i % (D / 32)], x, f[i / (D / 32)]);
+                });
+            }
 #pragma unroll
         for (int b = 0; b < 2 * NB; ++b)
 #pragma unroll
@@ -168,7 +182,8 @@ static hipError_t launch_fwd_t(const PromptArgs& a, hipStream_t stream) {
     constexpr int TILES = 4 * tile_rows(S) * D * (int)sizeof(OT), JOIN = (S - 1) * RW * (D / 32 * 4096 + 512);
     constexpr int LDS = TILES > JOIN ? TILES : JOIN;
     static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
-    const auto f = k_prompt_fwd<OT, D, RW, S>;
+    constexpr bool BF = sizeof(OT) == 2;
+    const auto f = BF && prompt_exacts(a) ? k_prompt_fwd<OT, D, RW, S, BF> : k_prompt_fwd<OT, D, RW, S, false>;
     if (LDS > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
         if (e != hipSuccess) return e;

@@ -16,7 +16,7 @@ namespace gdr2 {
 
 // ---------------------------------------------------------------- dQ: as the forward, keys in tiles
 // (RW x 32 queries a workgroup, S waves for each 32 of them, which share the keys)
-template <class OT, int D, int RW, int S>
+template <class OT, int D, int RW, int S, bool EXACT>
 __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt_dq(PromptArgs a) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
@@ -120,6 +120,13 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
                 }
             }
             FR f[2] = {acc_frag<OT>(s, 0), acc_frag<OT>(s, 1)};
+            if constexpr (EXACT)
+                if (prompt_few(a, wq0)) {
+                    const FR y[2] = {rest_frag(s, 0, f[0]), rest_frag(s, 1, f[1])};
+                    Pipe<2 * DT, 1, FR> rest;
+                    rest.start(col);
+                    rest.run(col, [&](int i, const FR& x) __attribute__((always_inline)) { mma32(acc[i % DT], x, y[i / DT]); });
+                }
             sums.run(col, [&](int i, const FR& x) __attribute__((always_inline)) { mma32(acc[i % DT], x, f[i / DT]); });
         }
     }
@@ -140,7 +147,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
 // scheduling barriers keep the compiler from drawing one phase's operands into the one before, which spilled 24.
 template <class OT, int D>
 constexpr int dkv_waves() { return sizeof(OT) == 2 && D == 64 ? 3 : prompt_waves<OT, D>(); }
-template <class OT, int D, int RW, int S>
+template <class OT, int D, int RW, int S, bool EXACT>
 __global__ __launch_bounds__(64 * RW * S, (dkv_waves<OT, D>())) void k_prompt_dkv(PromptArgs a) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
@@ -206,55 +213,70 @@ __global__ __launch_bounds__(64 * RW * S, (dkv_waves<OT, D>())) void k_prompt_dk
         for (int n_ = 0; n_ < NB; ++n_) {
             const int n = NB * sp + n_, r0 = t * BT + 32 * n;
             if (r0 + 31 < wk0 || r0 > last || r0 - wk0 - 31 >= a.window) continue;
-            asm volatile("" : "+v"(tl.rb), "+v"(tl.cb));  // (addresses formed anew: registers)
-            f32x16 s = zero16(), dp;  // dP - delta from the start
+            // (the second parts of queries that see few keys by doing all of it again: registers)
+#pragma unroll 1
+            for (int again = EXACT && prompt_few(a, r0); again >= 0; --again) {
+                asm volatile("" : "+v"(tl.rb), "+v"(tl.cb));  // (addresses formed anew: registers)
+                f32x16 s = zero16(), dp;  // dP - delta from the start
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x4 de = lds_load<f32x4>(st + (BT + 32 * n + 8 * j + 4 * h) * 4);
+                for (int j = 0; j < 4; ++j) {
+                    const f32x4 de = lds_load<f32x4>(st + (BT + 32 * n + 8 * j + 4 * h) * 4);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) dp[4 * j + x] = de[x];
-            }
-            auto row = [&](int i) __attribute__((always_inline)) {
-                return i < KB ? tl.rows(qt, 32 * n, 16 * i) : tl.rows(dt_, 32 * n, 16 * (i - KB));
-            };
-            Pipe<2 * KB, AHEAD, FR> scores;
-            scores.start(row);
-            scores.run(row, [&](int i, const FR& x) __attribute__((always_inline)) {
-                if (i < KB) mma32(s, x, kf[i]);
-                else mma32(dp, x, vf[i - KB]);
-            });
-            auto col = [&](int i) __attribute__((always_inline)) {
-                return tl.cols(i % 2 ? qt : dt_, 32 * (i / 2 % DT), 32 * n + 16 * (i / 2 / DT));
-            };
-            Pipe<4 * DT, AHEAD, FR> sums;
-            sums.start(col);
-            const bool mask = r0 < wk0 + 31 || r0 + 31 > last || r0 + 31 - wk0 >= a.window;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const f32x4 ls = lds_load<f32x4>(st + (32 * n + 8 * j + 4 * h) * 4);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    s[4 * j + x] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + x], a.scale2, -ls[x]));
-                    dp[4 * j + x] *= s[4 * j + x];
+                    for (int x = 0; x < 4; ++x) dp[4 * j + x] = de[x];
                 }
+                auto row = [&](int i) __attribute__((always_inline)) {
+                    return i < KB ? tl.rows(qt, 32 * n, 16 * i) : tl.rows(dt_, 32 * n, 16 * (i - KB));
+                };
+                Pipe<2 * KB, AHEAD, FR> scores;
+                scores.start(row);
+                scores.run(row, [&](int i, const FR& x) __attribute__((always_inline)) {
+                    if (i < KB) mma32(s, x, kf[i]);
+                    else mma32(dp, x, vf[i - KB]);
+                });
+                auto col = [&](int i) __attribute__((always_inline)) {
+                    return tl.cols(i % 2 ? qt : dt_, 32 * (i / 2 % DT), 32 * n + 16 * (i / 2 / DT));
+                };
+                Pipe<4 * DT, AHEAD, FR> sums;
+                sums.start(col);
+                const bool mask = r0 < wk0 + 31 || r0 + 31 > last || r0 + 31 - wk0 >= a.window;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const f32x4 ls = lds_load<f32x4>(st + (32 * n + 8 * j + 4 * h) * 4);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        s[4 * j + x] = __builtin_amdgcn_exp2f(fmaf(s[4 * j + x], a.scale2, -ls[x]));
+                        dp[4 * j + x] *= s[4 * j + x];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                if (mask) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        const int q = r0 + 8 * (r >> 2) + 4 * h + (r & 3), d = q - ki;
+                        const bool see = d >= 0 && d < a.window && q <= last;
+                        s[r] = see ? s[r] : 0.f;
+                        dp[r] = see ? dp[r] : 0.f;
+                    }
+                }
+                FR pf[2], gf[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if constexpr (EXACT)
+                        if (again) {
+                            pf[b] = rest_frag(s, b, acc_frag<OT>(s, b));
+                            gf[b] = rest_frag(dp, b, acc_frag<OT>(dp, b));
+                            continue;
+                        }
+                    pf[b] = acc_frag<OT>(s, b);
+                    gf[b] = acc_frag<OT>(dp, b);
+                }
+                sums.run(col, [&](int i, const FR& x) __attribute__((always_inline)) {
+                    const int dt = i / 2 % DT, b = i / 2 / DT;
+                    if (i % 2) mma32(ak[dt], x, gf[b]);
+                    else mma32(av[dt], x, pf[b]);
+                });
                 __builtin_amdgcn_sched_barrier(0);
             }
-            if (mask) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int q = r0 + 8 * (r >> 2) + 4 * h + (r & 3), d = q - ki;
-                    const bool see = d >= 0 && d < a.window && q <= last;
-                    s[r] = see ? s[r] : 0.f;
-                    dp[r] = see ? dp[r] : 0.f;
-                }
-            }
-            FR pf[2] = {acc_frag<OT>(s, 0), acc_frag<OT>(s, 1)}, gf[2] = {acc_frag<OT>(dp, 0), acc_frag<OT>(dp, 1)};
-            sums.run(col, [&](int i, const FR& x) __attribute__((always_inline)) {
-                const int dt = i / 2 % DT, b = i / 2 / DT;
-                if (i % 2) mma32(ak[dt], x, gf[b]);
-                else mma32(av[dt], x, pf[b]);
-            });
-            __builtin_amdgcn_sched_barrier(0);
         }
     }
     if constexpr (S > 1) {
@@ -323,7 +345,8 @@ static hipError_t launch_dq_t(const PromptArgs& a, hipStream_t stream) {
     constexpr int LDS = TILES > JOIN ? TILES : JOIN;
     static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
     const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 32 * RW) * a.Hq;
-    return launch_one(k_prompt_dq<OT, D, RW, S>, n, 64 * RW * S, LDS, a, stream);
+    constexpr bool BF = sizeof(OT) == 2;
+    return launch_one(BF && prompt_exacts(a) ? k_prompt_dq<OT, D, RW, S, BF> : k_prompt_dq<OT, D, RW, S, false>, n, 64 * RW * S, LDS, a, stream);
 }
 template <class OT, int D, int RW, int S>
 static hipError_t launch_dkv_t(const PromptArgs& a, hipStream_t stream) {
@@ -331,7 +354,8 @@ static hipError_t launch_dkv_t(const PromptArgs& a, hipStream_t stream) {
     constexpr int LDS = TILES > JOIN ? TILES : JOIN;
     static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
     const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 32 * RW) * a.Hkv * a.parts;
-    const hipError_t e = launch_one(k_prompt_dkv<OT, D, RW, S>, n, 64 * RW * S, LDS, a, stream);
+    constexpr bool BF = sizeof(OT) == 2;
+    const hipError_t e = launch_one(BF && prompt_exacts(a) ? k_prompt_dkv<OT, D, RW, S, BF> : k_prompt_dkv<OT, D, RW, S, false>, n, 64 * RW * S, LDS, a, stream);
     if (e != hipSuccess || a.parts == 1) return e;
     const long long all = (a.cu ? (long long)a.T : (long long)a.N * a.T) * a.Hkv * D;
     return launch_one(k_prompt_sum<OT>, (all / 4 + 255) / 256, 256, 0, a, stream);

@@ -188,6 +188,15 @@ __device__ __forceinline__ typename Frag<OT>::type acc_frag(const f32x16& x, int
     for (int e = 0; e < 8; ++e) f[e] = to_ot<OT>(x[8 * b + e]);
     return f;
 }
+// what the rounding of f = acc_frag(x, b) left over, as an operand too
+__device__ __forceinline__ bf16x8 rest_frag(const f32x16& x, int b, const bf16x8& f) {
+    bf16x8 y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (bf16)(x[8 * b + e] - (float)f[e]);
+    return y;
+}
+// Queries of few keys (prompt_exacts).
+__device__ __forceinline__ bool prompt_few(const PromptArgs& a, int q0) { return q0 < 64 || a.window <= 64; }
 // this lane's column of D rows, held in accumulators, times f: four consecutive elements at a time
 template <class OT, int D>
 __device__ __forceinline__ void store_col(OT* p, const f32x16 (&acc)[D / 32], float f) {

@@ -118,6 +118,25 @@ def test_long_sequences_of_many_heads(lens, heads, window):
         check(*(x.view(len(lens), lens[0], -1, 128) for x in (q, k, v, do)), cu, window=window, packed=False)
 
 
+@pytest.mark.parametrize("lens,heads,D", [([2], (2, 1), 64), ([2] * 12, (2, 2), 128), ([3, 1, 4, 2, 0, 64], (3, 1), 128),
+                                          ([40], (2, 1), 64), ([63, 64], (16, 4), 64), ([10] * 30, (8, 8), 128)])
+def test_short_sequences_carry_one_rounding(lens, heads, D):
+    # Weights and their gradients enter the products in two bf16 parts, off by 2^-8 of what one part's 2^-8 left: 2^-16;
+    # delta by as much of its terms from the weights in o, and again from o and rest. Then each result is rounded once.
+    q, k, v, do = make(sum(lens), *heads, D, BF, seed=25)
+    cu, sc = bounds(lens), D ** -0.5
+    o, lse, rest = g2.gdr2_attn_fwd(q, k, v, cu_seqlens=ints(cu), save_for_bwd=True)
+    gr = g2.gdr2_attn_bwd(q, k, v, o, lse, do, rest=rest, cu_seqlens=ints(cu))
+    qf, kf, vf, df = (x.flatten(0, 1) for x in (q, k, v, do))
+    wo, _, size = ref.attention(qf, kf, vf, cu, sc, 0)
+    dq, dk, dv, sq, sk, sv, pq, pk = ref.gradients(qf, kf, vf, df, cu, sc, 0)
+    off = 2.0 ** -15 * float((df.double().abs() * size).sum(-1).max())
+    for got, want, terms, extra in ((o, wo, size, 0.0), (gr["dq"], dq, sq, off * pq), (gr["dk"], dk, sk, off * pk),
+                                    (gr["dv"], dv, sv, 0.0)):
+        room = R8 * want.abs() + (1 + R8) * ((2.0 ** -16 + FP) * terms + extra) + 1e-30
+        assert ((got.flatten(0, 1).double() - want).abs() <= room).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_one_token_rows(dtype):
     # a token that sees itself only: o = v and lse its score, and gradients that are dO and (but for fp32's roundings
