@@ -24,9 +24,10 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     using TL = Tile32<OT, D>;
     constexpr int NW = RW * S, QT = 32 * RW, KT = tile_rows(S), TB = KT * TL::RB, NB = KT / 32 / S;
     constexpr int ACC = D / 32 * 4096;  // bytes of a wave's accumulators
+    constexpr int BUFS = tile_bufs<OT, D>(S);
     extern __shared__ __align__(16) char smem[];
     lds_char* lds = (lds_char*)smem;
-    poison_lds(lds, 4 * TB);
+    poison_lds(lds, 2 * BUFS * TB);
     poison_lds_done();
     PromptAt at;
     int slot;
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     // the tiles that any of the workgroup's queries sees
     const int t0 = max(0, q0 - a.window + 1) / KT, t1 = min(q0 + QT - 1, last) / KT;
     auto fetch = [&](int t) {
-        lds_char* b = lds + (t & 1) * 2 * TB;
+        lds_char* b = lds + t % BUFS * 2 * TB;
         lk(kb, t * KT, b);
         lv(vb, t * KT, b + TB);
     };
@@ -63,12 +64,16 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     TL tl;
     for (int t = t0; t <= t1; ++t) {
         tl.fresh();
+        if (BUFS == 1 && t > t0) {
+            __syncthreads();
+            fetch(t);
+        }
         wait_vm<0>();
         __syncthreads();  // the tile has landed, and everyone is done with the one before
-        if (t < t1) fetch(t + 1);
+        if (BUFS == 2 && t < t1) fetch(t + 1);
         const int r0 = 32 * NB * sp, k0 = t * KT + r0;  // the wave's keys of the tile
         if (k0 > wq0 + 31 || wq0 > last || k0 + 32 * NB - 1 <= wq0 - a.window) continue;  // it sees nothing of them
-        const lds_char* kt = lds + (t & 1) * 2 * TB;
+        const lds_char* kt = lds + t % BUFS * 2 * TB;
         const lds_char* vt = kt + TB;
         f32x16 s[NB];
 #pragma unroll
@@ -179,7 +184,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
 
 template <class OT, int D, int RW, int S>
 static hipError_t launch_fwd_t(const PromptArgs& a, hipStream_t stream) {
-    constexpr int TILES = 4 * tile_rows(S) * D * (int)sizeof(OT), JOIN = (S - 1) * RW * (D / 32 * 4096 + 512);
+    constexpr int TILES = 2 * tile_bufs<OT, D>(S) * tile_rows(S) * D * (int)sizeof(OT), JOIN = (S - 1) * RW * (D / 32 * 4096 + 512);
     constexpr int LDS = TILES > JOIN ? TILES : JOIN;
     static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
     constexpr bool BF = sizeof(OT) == 2;
@@ -397,8 +402,7 @@ static hipError_t launch_fwd_d(const PromptArgs& a, hipStream_t stream) {
         return tasks <= 256 ? launch_fwd_t<OT, D, 1, 4>(a, stream) : launch_fwd_t<OT, D, 2, 4>(a, stream);
     } else {
         if (S == 1) return launch_fwd_t<OT, D, 4, 1>(a, stream);
-        if constexpr (D == 64)  // (128 rows of 128 channels do not fit in LDS)
-            if (S == 4) return launch_fwd_t<OT, D, 1, 4>(a, stream);
+        if (S == 4) return launch_fwd_t<OT, D, 1, 4>(a, stream);
         return launch_fwd_t<OT, D, 2, 2>(a, stream);
     }
 }

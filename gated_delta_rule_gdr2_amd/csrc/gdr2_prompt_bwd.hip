@@ -21,10 +21,11 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
     constexpr int NW = RW * S, QT = 32 * RW, BT = tile_rows(S), TB = BT * TL::RB, NB = BT / 32 / S;
+    constexpr int BUFS = tile_bufs<OT, D>(S);
     constexpr int ACC = D / 32 * 4096, KB = D / 16, DT = D / 32, AHEAD = sizeof(OT) == 2 ? 4 : 1;
     extern __shared__ __align__(16) char smem[];
     lds_char* lds = (lds_char*)smem;
-    poison_lds(lds, 4 * TB);
+    poison_lds(lds, 2 * BUFS * TB);
     poison_lds_done();
     PromptAt at;
     int slot;
@@ -46,7 +47,7 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     const TileLoad<OT, D, BT, NW> lk(a.ks[0] * (int)sizeof(OT), last, w), lv(a.vs[0] * (int)sizeof(OT), last, w);
     const int t0 = max(0, q0 - a.window + 1) / BT, t1 = min(q0 + QT - 1, last) / BT;
     auto fetch = [&](int t) {
-        lds_char* b = lds + (t & 1) * 2 * TB;
+        lds_char* b = lds + t % BUFS * 2 * TB;
         lk(kb, t * BT, b);
         lv(vb, t * BT, b + TB);
     };
@@ -82,12 +83,16 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
     TL tl;
     for (int t = t0; t <= t1; ++t) {
         tl.fresh();
+        if (BUFS == 1 && t > t0) {
+            __syncthreads();
+            fetch(t);
+        }
         wait_vm<0>();
         __syncthreads();
-        if (t < t1) fetch(t + 1);
+        if (BUFS == 2 && t < t1) fetch(t + 1);
         const int b0 = 32 * NB * sp, k0 = t * BT + b0;
         if (k0 > wq0 + 31 || wq0 > last || k0 + 32 * NB - 1 <= wq0 - a.window) continue;
-        const lds_char* kt = lds + (t & 1) * 2 * TB;
+        const lds_char* kt = lds + t % BUFS * 2 * TB;
         const lds_char* vt = kt + TB;
         const bool part = k0 + 32 * NB - 1 > wq0 || k0 <= wq0 + 31 - a.window;
 #pragma unroll
@@ -152,10 +157,11 @@ __global__ __launch_bounds__(64 * RW * S, (dkv_waves<OT, D>())) void k_prompt_dk
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
     constexpr int NW = RW * S, KT = 32 * RW, BT = tile_rows(S), TB = BT * TL::RB, BUF = 2 * TB + 2 * BT * 4, NB = BT / 32 / S;
+    constexpr int BUFS = tile_bufs<OT, D>(S);
     constexpr int ACC = D / 32 * 4096, KB = D / 16, DT = D / 32, AHEAD = sizeof(OT) == 2 && D == 64 ? 2 : 1;
     extern __shared__ __align__(16) char smem[];
     lds_char* lds = (lds_char*)smem;
-    poison_lds(lds, 2 * BUF);
+    poison_lds(lds, BUFS * BUF);
     poison_lds_done();
     PromptAt at;
     int slot;
@@ -182,7 +188,7 @@ __global__ __launch_bounds__(64 * RW * S, (dkv_waves<OT, D>())) void k_prompt_dk
     auto fetch = [&](int i) {
         const int hq = fh, r0 = ft * BT;
         if (++ft > t1) ft = t0, ++fh;
-        lds_char* b = lds + (i & 1) * BUF;
+        lds_char* b = lds + i % BUFS * BUF;
         lq((const char*)((const OT*)a.q + at.tok0 * a.qs[0] + hq * a.qs[1]), r0, b);
         ld((const char*)((const OT*)a.dout + (at.tok0 * a.Hq + hq) * D), r0, b + TB);
 #pragma unroll
@@ -203,10 +209,14 @@ __global__ __launch_bounds__(64 * RW * S, (dkv_waves<OT, D>())) void k_prompt_dk
     TL tl;
     for (int i = 0, t = t0; i < all; ++i, t = t == t1 ? t0 : t + 1) {
         tl.fresh();
+        if (BUFS == 1 && i > 0) {
+            __syncthreads();
+            fetch(i);
+        }
         wait_vm<0>();
         __syncthreads();
-        if (i + 1 < all) fetch(i + 1);
-        const lds_char* qt = lds + (i & 1) * BUF;
+        if (BUFS == 2 && i + 1 < all) fetch(i + 1);
+        const lds_char* qt = lds + i % BUFS * BUF;
         const lds_char* dt_ = qt + TB;
         const lds_char* st = qt + 2 * TB;
 #pragma unroll
@@ -341,7 +351,7 @@ static hipError_t launch_one(F f, long long groups, int threads, int lds, const 
 }
 template <class OT, int D, int RW, int S>
 static hipError_t launch_dq_t(const PromptArgs& a, hipStream_t stream) {
-    constexpr int TILES = 4 * tile_rows(S) * D * (int)sizeof(OT), JOIN = (S - 1) * RW * (D / 32 * 4096);
+    constexpr int TILES = 2 * tile_bufs<OT, D>(S) * tile_rows(S) * D * (int)sizeof(OT), JOIN = (S - 1) * RW * (D / 32 * 4096);
     constexpr int LDS = TILES > JOIN ? TILES : JOIN;
     static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
     const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 32 * RW) * a.Hq;
@@ -350,7 +360,7 @@ static hipError_t launch_dq_t(const PromptArgs& a, hipStream_t stream) {
 }
 template <class OT, int D, int RW, int S>
 static hipError_t launch_dkv_t(const PromptArgs& a, hipStream_t stream) {
-    constexpr int TILES = 4 * tile_rows(S) * (D * (int)sizeof(OT) + 4), JOIN = (S - 1) * RW * (D / 32 * 4096);
+    constexpr int TILES = 2 * tile_bufs<OT, D>(S) * tile_rows(S) * (D * (int)sizeof(OT) + 4), JOIN = (S - 1) * RW * (D / 32 * 4096);
     constexpr int LDS = TILES > JOIN ? TILES : JOIN;
     static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
     const long long n = prompt_slots(a.N, a.T, a.cu != nullptr, 32 * RW) * a.Hkv * a.parts;
@@ -375,8 +385,7 @@ static hipError_t launch_dq_d(const PromptArgs& a, hipStream_t stream) {
         return tasks <= 256 ? launch_dq_t<OT, D, 1, 4>(a, stream) : launch_dq_t<OT, D, 2, 4>(a, stream);
     } else {
         if (S == 1) return launch_dq_t<OT, D, 4, 1>(a, stream);
-        if constexpr (D == 64)
-            if (S == 4) return launch_dq_t<OT, D, 1, 4>(a, stream);
+        if (S == 4) return launch_dq_t<OT, D, 1, 4>(a, stream);
         return launch_dq_t<OT, D, 2, 2>(a, stream);
     }
 }
@@ -389,8 +398,7 @@ static hipError_t launch_dkv_d(const PromptArgs& a, hipStream_t stream) {
         if (S == 2) return launch_dkv_t<OT, D, 2, 2>(a, stream);
         return tasks <= 256 ? launch_dkv_t<OT, D, 1, 4>(a, stream) : launch_dkv_t<OT, D, 2, 4>(a, stream);
     } else {
-        if constexpr (D == 64)
-            if (S == 4) return launch_dkv_t<OT, D, 1, 4>(a, stream);
+        if (S == 4) return launch_dkv_t<OT, D, 1, 4>(a, stream);
         return launch_dkv_t<OT, D, 2, 2>(a, stream);
     }
 }

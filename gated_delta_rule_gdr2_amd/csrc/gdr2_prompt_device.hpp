@@ -239,6 +239,11 @@ __device__ __forceinline__ void add_acc(const lds_char* p, float f, f32x16 (&acc
 }
 // rows of a tile of the other axis: two blocks of 32 for a wave alone, one or two for each of several
 constexpr int tile_rows(int S) { return S == 4 ? 128 : 64; }
+// Tiles of each kind in LDS, the next one on its way while one is worked on; of 128 rows of 512 bytes there is room for one.
+// (4 waves on 32 rows so, 2048 tokens, 8 heads over 2 of 128, fp32: 103 and 336 us forward and backward; 2 waves on 64
+// rows with two tiles of 64 154 and 508.)
+template <class OT, int D>
+constexpr int tile_bufs(int S) { return sizeof(OT) == 4 && D == 128 && S == 4 ? 1 : 2; }
 // the larger, or the sum, of this lane's value and the other half wave's of the same column, by an exchange of half waves
 // in the vector unit
 __device__ __forceinline__ float max_halves(float x) {
