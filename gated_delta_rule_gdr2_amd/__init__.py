@@ -967,8 +967,8 @@ def gdr2_attn_fwd(q, k, v, *, cu_seqlens=None, scale=None, window=0, o=None, lse
     int32 [N+1] on the device, the bounds of N sequences packed along T with B = 1. scale: D ** -0.5 unless
     given; window: only the last ``window`` tokens (0: all). Returns o, or (o, lse) with return_lse or an
     ``lse`` tensor (fp32 [B,T,Hq]), or with save_for_bwd (o, lse, rest) for gdr2_attn_bwd, rest (bf16; None
-    for fp32) being what o's rounding left over. Rows of no sequence are zero, or left as they were in an
-    ``o`` that is passed in."""
+    for fp32) being what o's rounding left over. Rows of no sequence are zero (of lse and rest too), or, where an
+    ``o`` is passed in, left as they were in each."""
     lib = load_library()
     N, T, Hq, Hkv, D, dt, dev, strides = _attn_dims(q, k, v, cu_seqlens)
     new, own_o, rest = [], o is None, None

@@ -8,8 +8,8 @@
 // forming the scores twice. The first one leaves lse log2(e) and -delta for the second.
 //
 // Matrix products bound both (seven of them where a single walk with atomics has five): 2 x 4096 tokens, 16 heads of 128
-// channels, 467 us together, 1030 TFLOP/s counted as seven products, where a large product alone reaches 1198. Packed
-// documents of 64 channels (9 of them, 16 query heads over 4, 2048-token window) 172 us with the sum of the parts.
+// channels, 465 us together, 1030 TFLOP/s counted as seven products, where a large product alone reaches 1198. Packed
+// documents of 64 channels (9 of them, 16 query heads over 4, 2048-token window) 171 us with the sum of the parts.
 #include "gdr2_prompt_device.hpp"
 
 namespace gdr2 {

@@ -5,7 +5,7 @@
 // from memory once for all rows, by loads that go from the pages into LDS, sixteen tokens of a page at a time. Rows are
 // split over workgroups as in gdr2_attn.hip, a unit of the line being a tile. From the rows' registers straight against
 // the cache, four waves side by side (gdr2_tree.hip), 32 sequences of 200 to 16384 tokens with trees of 32, 32 heads over 8
-// of 128, took 200 us: every wave loaded and turned all values by itself. So 113 us and 8.5 for the join, 3.5 TB/s of
+// of 128, took 200 us: every wave loaded and turned all values by itself. So 112 us and 8.4 for the join, 3.6 TB/s of
 // the cache: a workgroup's two tiles fill a compute unit's LDS, so that its loads pause where its waves meet, and where
 // it goes from one row to the next.
 #include "gdr2_prompt_device.hpp"
