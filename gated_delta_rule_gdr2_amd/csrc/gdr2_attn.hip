@@ -104,8 +104,11 @@ __device__ __forceinline__ AttnAt attn_find(const AttnArgs& a, const AttnLine& l
 template <class OT, int D>
 __device__ __forceinline__ void attn_load(const AttnArgs& a, int u, int hkv, const int (&pg)[2], AttnTile<OT, D>& t) {
     attn_ok<OT, D>(pg, t);
-    attn_load_k<OT, D>(a.c, u, hkv, pg, t);
-    attn_load_v<OT, D>(a.c, u, hkv, pg, t);
+#pragma unroll
+    for (int s = 0; s < attn_unit<OT>() / 16; ++s) {
+        attn_load_k<OT, D>(a.c, u, hkv, pg, s, t);
+        attn_load_v<OT, D>(a.c, u, hkv, pg, s, t);
+    }
 }
 
 // Running softmax of a wave: lane (li, lq) holds head li; l is its own tokens' share of the weight.
@@ -214,7 +217,7 @@ __device__ __forceinline__ void attn_update(const AttnArgs& a, const AttnSpan& s
 template <class OT, int D>
 __device__ __forceinline__ void attn_run(const AttnArgs& a, int b, int hr, const AttnSpan& sp, int i0, int n, bool whole,
                                          float* part, float (&sml)[2][AW][16], float (&so)[AW][16][D + 4]) {
-    constexpr int U = attn_unit<OT>(), EV = D / 16;
+    constexpr int EV = D / 16;
     using QT = typename std::conditional<sizeof(OT) == 2, bf16x8, f32x4>::type;
     constexpr int NQ = sizeof(OT) == 2 ? D / 32 : D / 16;
     const int tid = threadIdx.x, l = tid & 63, li = l & 15, lq = l >> 4;

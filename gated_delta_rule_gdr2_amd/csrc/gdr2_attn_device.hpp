@@ -52,47 +52,51 @@ __device__ __forceinline__ void attn_ok(const int (&pg)[2], AttnTile<OT, D>& t) 
     for (int s = 0; s < attn_unit<OT>() / 16; ++s)
         if (pg[s] >= 0) t.ok |= 1 << s;
 }
+// token tile s of the unit
 template <class OT, int D>
-__device__ __forceinline__ void attn_load_k(const Cache& c, int u, int hkv, const int (&pg)[2], AttnTile<OT, D>& t) {
+__device__ __forceinline__ void attn_load_k(const Cache& c, int u, int hkv, const int (&pg)[2], int s, AttnTile<OT, D>& t) {
     const int l = lane_id(), li = l & 15, lq = l >> 4;
-    constexpr int U = attn_unit<OT>();
+    const int tok = (u * attn_unit<OT>() + 16 * s) & (c.page - 1);
+    const long long page = pg[s] >= 0 ? pg[s] : 0;
+    const OT* kp = (const OT*)c.k + page * c.ks[0] + tok * c.ks[1] + hkv * c.ks[2];
+    if constexpr (sizeof(OT) == 2) {
+        const OT* kr = kp + li * c.ks[1] + 8 * lq;
 #pragma unroll
-    for (int s = 0; s < U / 16; ++s) {
-        const int tok = (u * U + 16 * s) & (c.page - 1);
-        const long long page = pg[s] >= 0 ? pg[s] : 0;
-        const OT* kp = (const OT*)c.k + page * c.ks[0] + tok * c.ks[1] + hkv * c.ks[2];
-        if constexpr (sizeof(OT) == 2) {
-            const OT* kr = kp + li * c.ks[1] + 8 * lq;
+        for (int kb = 0; kb < D / 32; ++kb) t.k[s][kb] = *(const bf16x8*)(kr + 32 * kb);
+    } else {
+        const OT* kr = kp + li * c.ks[1] + 4 * lq;
 #pragma unroll
-            for (int kb = 0; kb < D / 32; ++kb) t.k[s][kb] = *(const bf16x8*)(kr + 32 * kb);
-        } else {
-            const OT* kr = kp + li * c.ks[1] + 4 * lq;
-#pragma unroll
-            for (int kb = 0; kb < D / 16; ++kb) t.k[kb] = *(const f32x4*)(kr + 16 * kb);
-        }
+        for (int kb = 0; kb < D / 16; ++kb) t.k[kb] = *(const f32x4*)(kr + 16 * kb);
     }
 }
 template <class OT, int D>
-__device__ __forceinline__ void attn_load_v(const Cache& c, int u, int hkv, const int (&pg)[2], AttnTile<OT, D>& t) {
+__device__ __forceinline__ void attn_load_v(const Cache& c, int u, int hkv, const int (&pg)[2], int s, AttnTile<OT, D>& t) {
     const int l = lane_id(), li = l & 15, lq = l >> 4;
-    constexpr int U = attn_unit<OT>();
+    const int tok = (u * attn_unit<OT>() + 16 * s) & (c.page - 1);
+    const long long page = pg[s] >= 0 ? pg[s] : 0;
+    const OT* vp = (const OT*)c.v + page * c.vs[0] + tok * c.vs[1] + hkv * c.vs[2];
+    if constexpr (sizeof(OT) == 2) {
 #pragma unroll
-    for (int s = 0; s < U / 16; ++s) {
-        const int tok = (u * U + 16 * s) & (c.page - 1);
-        const long long page = pg[s] >= 0 ? pg[s] : 0;
-        const OT* vp = (const OT*)c.v + page * c.vs[0] + tok * c.vs[1] + hkv * c.vs[2];
-        if constexpr (sizeof(OT) == 2) {
+        for (int i = 0; i < 4; ++i)
+            t.v[4 * s + i] = *(const typename AttnTile<OT, D>::VT*)(vp + (4 * lq + i) * c.vs[1] + (D / 16) * li);
+    } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                t.v[4 * s + i] = *(const typename AttnTile<OT, D>::VT*)(vp + (4 * lq + i) * c.vs[1] + (D / 16) * li);
-        } else {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < D / 64; ++j)
-                    t.v[i][j] = *(const f32x4*)(vp + (4 * lq + i) * c.vs[1] + (D / 16) * li + 4 * j);
-        }
+            for (int j = 0; j < D / 64; ++j)
+                t.v[i][j] = *(const f32x4*)(vp + (4 * lq + i) * c.vs[1] + (D / 16) * li + 4 * j);
     }
+}
+// all of the unit
+template <class OT, int D>
+__device__ __forceinline__ void attn_load_k(const Cache& c, int u, int hkv, const int (&pg)[2], AttnTile<OT, D>& t) {
+#pragma unroll
+    for (int s = 0; s < attn_unit<OT>() / 16; ++s) attn_load_k<OT, D>(c, u, hkv, pg, s, t);
+}
+template <class OT, int D>
+__device__ __forceinline__ void attn_load_v(const Cache& c, int u, int hkv, const int (&pg)[2], AttnTile<OT, D>& t) {
+#pragma unroll
+    for (int s = 0; s < attn_unit<OT>() / 16; ++s) attn_load_v<OT, D>(c, u, hkv, pg, s, t);
 }
 
 }  // namespace gdr2

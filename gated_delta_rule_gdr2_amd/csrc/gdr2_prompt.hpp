@@ -64,6 +64,7 @@ inline int prompt_parts(int N, int T, int Hq, int Hkv, bool packed) {
 // and few roundings that balance one another: of 2 heads with one part, both were off by 1.5 times their own rounding on
 // average and by up to 1.8 for 10 tokens, 1.6 for 40, 1.5 for 300, and with two parts by up to 1.2, 1.1 and 1.3; from some 8
 // heads on the average holds for each. For all calls the two cost 482 -> 524 us of the backward of 2 x 4096 tokens.
+// (k_prompt_fwd2 has one part: its sequences' first 64 tokens are a small part of them.)
 inline bool prompt_exacts(const PromptArgs& a) {
     const long long len = prompt_length(a.N, a.T, a.cu != nullptr);
     return (len < a.window ? len : a.window) <= 128 || (long long)a.N * a.Hq <= 8;
