@@ -36,18 +36,29 @@ inline long long prompt_blocks(int N, int T, bool packed) { return prompt_slots(
 // Tokens of a sequence: of packed ones the mean, the lengths being the device's to know.
 inline long long prompt_length(int N, int T, bool packed) { return packed ? ((long long)T + N - 1) / (N > 0 ? N : 1) : T; }
 
-// Waves that share a block's other axis: none share where the longest walk is at most half of what each of the 1024
-// SIMDs has to do anyway, or where two short walks for each are there to hide one another's latency, two where it is no
-// longer than that, else four. `tasks`: walks of one head each; `heads`: heads that a walk goes through one after
-// another. Measured with S = 1, 2, 4, bf16, 128 channels, us, forward and backward:
+// Waves that share a block's other axis. None share where the longest walk is at most half of what each of the 1024 SIMDs
+// has to do anyway; two where it is no longer than that; else four, which end soonest where all blocks are under way at
+// once. More blocks than that (`once`: LDS holds the tiles of as many) take short walks alone and long ones by twos, so
+// that more of them are under way, and in fp32, whose products are the longest, by twos. `tasks`: walks of one head each;
+// `heads`: heads that a walk goes through one after another; es: bytes of an element. Measured with S = 1, 2, 4, us, forward
+// and backward, bf16, 128 channels:
 //     2 x 4096 tokens, 16 heads 166, 210, 258 and 510, 566, 689     1 x 8192, 8 heads over 1 194, 169, 205 and 674, 528, 589
 //     1 x 2048, 16 heads 45, 43, 39 and 166, 120, 112               1 x 512, 16 heads 16, 17, 11 and 60, 50, 36
 //     24 packed of 17 - 700 tokens, 16 heads over 4 31, 45, 61 and 109, 132, 197
-inline int prompt_sharing(const PromptArgs& a, long long tasks, int heads) {
+//     5 x 168, 64 heads over 8 19, 29, 36 and 70, 85, 121           4 x 300, 32 heads 15, 22, 28 and 47, 59, 88
+//     2 x 168, 48 heads 9.9, 11, 18 and 32, 32, 50                  2 x 512, 16 heads 15, 17, 14 and 50, 44, 39
+//     2 x 1024, 16 heads 26, 26, 28 and 82, 70, 79                  16 x 60, 16 heads 8.6, 8.8, 8.3 and 23, 25, 32
+// 64 channels: 4 x 300, 32 heads 10, 11, 14 and 29, 33, 49          1 x 1024, 32 heads 20, 21, 16 and 57, 47, 47
+// fp32, 64:    4 x 300, 32 heads 37, 30, 45 and 107, 88, 137        1 x 130, 4 heads over 2 19, 13, 11 and 53, 37, 30
+// fp32, 128:   2 x 168, 48 heads 32, 23, 35 and 107, 73, 116
+inline int prompt_sharing(const PromptArgs& a, long long tasks, int heads, int es) {
     const long long len = prompt_length(a.N, a.T, a.cu != nullptr), seen = len < a.window ? len : a.window;
     const long long walk = (seen + 63) / 64 * heads;  // tiles of the longest walk
+    const long long once = es == 2 && a.D == 64 ? 1024 : 512;
     const double each = (double)tasks * walk * (seen < len ? 1.0 : 0.5) / 1024.0;
-    return 2.0 * walk <= each || (tasks >= 2048 && walk <= 8) ? 1 : walk <= each ? 2 : 4;
+    if (2.0 * walk <= each || (tasks >= 2048 && walk <= 8)) return 1;
+    if (es == 2 && tasks > once && walk <= 8) return 1;
+    return walk <= each || tasks > once ? 2 : 4;
 }
 
 // Parts that the query heads of a key head are cut in for dK and dV, each walked by itself and added up by a further

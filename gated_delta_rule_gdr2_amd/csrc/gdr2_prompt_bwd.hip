@@ -374,7 +374,7 @@ static hipError_t launch_dkv_t(const PromptArgs& a, hipStream_t stream) {
 template <class OT, int D>
 static hipError_t launch_dq_d(const PromptArgs& a, hipStream_t stream) {
     const long long tasks = prompt_blocks(a.N, a.T, a.cu != nullptr) * a.Hq;
-    const int S = prompt_sharing(a, tasks, 1);
+    const int S = prompt_sharing(a, tasks, 1, sizeof(OT));
     if constexpr (sizeof(OT) == 2) {
         // 256 queries a workgroup from two rounds of them on (2 x 4096 tokens, 16 heads 200 us, with 128 queries 214;
         // 64 channels, 9 packed documents, 92 and 73)
@@ -392,7 +392,7 @@ static hipError_t launch_dq_d(const PromptArgs& a, hipStream_t stream) {
 template <class OT, int D>
 static hipError_t launch_dkv_d(const PromptArgs& a, hipStream_t stream) {
     const long long tasks = prompt_blocks(a.N, a.T, a.cu != nullptr) * a.Hkv * a.parts;
-    const int S = prompt_sharing(a, tasks, (a.G + a.parts - 1) / a.parts);
+    const int S = prompt_sharing(a, tasks, (a.G + a.parts - 1) / a.parts, sizeof(OT));
     if (S == 1) return launch_dkv_t<OT, D, 4, 1>(a, stream);
     if constexpr (sizeof(OT) == 2) {
         if (S == 2) return launch_dkv_t<OT, D, 2, 2>(a, stream);
