@@ -293,7 +293,8 @@ __device__ __forceinline__ void prompt_slot(const PromptArgs& a, int slot, int t
     while (hi - lo > 1) {
         const int step = (hi - lo + 63) / 64, s = lo + lane_id() * step;
         const bool in = s < hi && clamp_int(a.cu[s < hi ? s : lo], 0, a.T) / tile + s <= slot;
-        const int n = __builtin_ctzll(~__ballot(in) | (1ull << 63));
+        const unsigned long long out = ~__ballot(in);
+        const int n = out ? __builtin_ctzll(out) : 64;  // probes before the first that is behind the slot
         lo += max(n - 1, 0) * step;
         hi = min(hi, lo + step);
     }

@@ -460,3 +460,34 @@ def test_refusals():
     with pytest.raises(RuntimeError):
         b(q, k, v, o, lse, do, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert torch.equal(f(q, k, v, window=2 ** 32 + 5), o)
+
+
+MANY = [(1, (1, 1), 64, 127), (1, (4, 2), 64, 128), (1, (4, 2), 128, 126), (1, (4, 2), 128, 256), (1, (2, 1), 128, 65),
+        (1, (2, 1), 64, 512), (1, (8, 8), 128, 320), (1, (2, 1), 128, 4096), (8, (4, 4), 64, 190), (40, (2, 2), 128, 127)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("longer,heads,D,N", MANY)
+def test_more_sequences_than_lanes(dtype, longer, heads, D, N):
+    # A slot's sequence is searched by 64 probes at a time, the last of which is a sequence where N > 63 ceil(N / 64).
+    # Outputs of the caller's, so that rows that nothing is written to show.
+    lens = [longer * ((5 * i) % 23 + (60 if i % 17 == 3 else 0)) for i in range(N - 1)] + [9]
+    cu = bounds(lens)
+    args = make(cu[-1], *heads, D, dtype, seed=40)
+    q, k, v, do = args
+    c = ints(cu)
+    full = lambda x: torch.full_like(x, float("nan"))
+    o, lse, gr = full(q), full(q[..., 0].float()), {n: full(x) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+    ws = torch.full((g2.gdr2_attn_bwd_workspace_bytes(N, cu[-1], *heads, D, True, g2._DT[dtype]),), 255, dtype=torch.uint8, device="cuda")
+    _, _, rest = g2.gdr2_attn_fwd(q, k, v, cu_seqlens=c, o=o, lse=lse, save_for_bwd=True)
+    g2.gdr2_attn_bwd(q, k, v, o, lse, do, rest=rest, cu_seqlens=c, grads=gr, ws=ws)
+    want = check(*args, cu)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert all(torch.equal(gr[n], want[3][n]) for n in gr)
+
+
+def test_long_sequences_more_than_lanes():
+    # 256 queries a workgroup
+    lens = [1030 + i % 5 for i in range(127)] + [300]
+    cu = bounds(lens)
+    check(*make(cu[-1], 2, 1, 128, BF, seed=41), cu)
