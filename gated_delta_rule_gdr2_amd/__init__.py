@@ -23,6 +23,7 @@ import functools
 import os
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 from torch.autograd.function import once_differentiable
 
 __all__ = ["gdr2_fwd", "gdr2_bwd", "gdr2_step", "gdr2_fwd_logits", "gdr2_bwd_logits", "gdr2_step_logits",
@@ -620,9 +621,17 @@ def _accumulation_streams(leaves):
             for t in leaves if t is not None and t.is_leaf and t.requires_grad]
 
 
+def _refuse_tangents(*inputs):
+    """A call that bypasses autograd.Function, since nothing wants a gradient, would drop the tangents of forward-mode
+    differentiation where the function itself refuses them."""
+    if any(t is not None and unpack_dual(t).tangent is not None for t in inputs):
+        raise NotImplementedError("forward-mode differentiation is not supported: an input carries a tangent")
+
+
 class GDR2ScalarFunction(torch.autograd.Function):
     """Autograd wrapper: forward saves the chunks' states in the workspace, backward reuses them. Where no
     gradient is wanted (no_grad, or no input that requires one) it is gdr2_scalar_fwd and saves nothing.
+    Inputs with tangents (forward-mode differentiation) are refused.
 
     Forward and backward may be captured into a graph together, but not while an earlier graph of the same
     leaves, built on another stream, is still alive: their gradients would be accumulated on that stream,
@@ -634,6 +643,7 @@ class GDR2ScalarFunction(torch.autograd.Function):
     def apply(cls, q, k, v, g, beta, h0=None, cu_seqlens=None):
         if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, v, g, beta, h0)):
             return super().apply(q, k, v, g, beta, h0, cu_seqlens)
+        _refuse_tangents(q, k, v, g, beta, h0)
         return gdr2_scalar_fwd(q, k, v, g, beta, h0, cu_seqlens=cu_seqlens)[:2]
 
     @staticmethod
@@ -1035,13 +1045,14 @@ def gdr2_attn_bwd(q, k, v, o, lse, dout, *, rest=None, cu_seqlens=None, scale=No
 
 class GDR2AttnFunction(torch.autograd.Function):
     """Autograd wrapper of gdr2_attn_fwd and gdr2_attn_bwd; apply(q, k, v, cu_seqlens, scale, window) returns o. Where no
-    gradient is wanted it is gdr2_attn_fwd and saves nothing. Capturing forward and backward into a graph: as
-    GDR2ScalarFunction."""
+    gradient is wanted it is gdr2_attn_fwd and saves nothing. Tangents, and capturing forward and backward into a graph:
+    as GDR2ScalarFunction."""
 
     @classmethod
     def apply(cls, q, k, v, cu_seqlens=None, scale=None, window=0):
         if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v)):
             return super().apply(q, k, v, cu_seqlens, scale, window)
+        _refuse_tangents(q, k, v)
         return gdr2_attn_fwd(q, k, v, cu_seqlens=cu_seqlens, scale=scale, window=window)
 
     @staticmethod

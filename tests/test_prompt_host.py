@@ -187,3 +187,27 @@ def test_binding_checks_before_any_call():
               lambda: g2.gdr2_kv_pages(i[0], i[0], i, i[0], i[0, :1], page_size=16, max_tokens=4)):
         with pytest.raises(ValueError):
             f()
+
+
+@pytest.mark.parametrize("grad", [True, False])
+def test_tangents_are_refused(grad):
+    # not dropped, with a derivative of zero as the result, where no gradient is wanted
+    import torch.autograd.forward_ad as fw
+    x = torch.randn(1, 4, 2, 64)
+    gate, state = torch.randn(1, 4, 2), torch.randn(1, 2, 64, 64)
+    with torch.set_grad_enabled(grad), fw.dual_level():
+        dual = lambda t: fw.make_dual(t, torch.ones_like(t))
+        for i in range(3):
+            args = [dual(t) if i == j else t for j, t in enumerate((x, x, x))]
+            with pytest.raises(NotImplementedError):
+                g2.GDR2AttnFunction.apply(*args)
+        plain = (x, x, x, gate, gate, state)
+        for i in range(6):
+            args = [dual(t) if i == j else t for j, t in enumerate(plain)]
+            with pytest.raises(NotImplementedError):
+                g2.GDR2ScalarFunction.apply(*args)
+        for call in (lambda: g2.GDR2AttnFunction.apply(x, x, x), lambda: g2.GDR2ScalarFunction.apply(*plain)):
+            with pytest.raises(ValueError):
+                call()  # without a tangent: CPU tensors
+    with pytest.raises(NotImplementedError):
+        torch.func.jvp(lambda t: g2.GDR2AttnFunction.apply(t, t, t), (x,), (x,))
