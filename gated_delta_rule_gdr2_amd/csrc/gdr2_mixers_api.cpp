@@ -151,6 +151,9 @@ int prompt_shape(int N, int T, int Hq, int Hkv, int D, int dtype, bool packed) {
 }
 bool prompt_none(int N, int T, int Hq) { return N == 0 || T == 0 || Hq == 0; }
 
+// The backward's workspace: lse2 and delta, fp32 [tokens][Hq] each, then parts of dK and dV, from a multiple of 16 bytes on.
+size_t prompt_part_offset(size_t rows) { return (2 * rows * sizeof(float) + 15) / 16 * 16; }
+
 int prompt_fill(gdr2::PromptArgs& a, const long long* strides, const int* cu, int N, int T, int Hq, int Hkv, int D,
                 float scale, int window, int dtype, int zero_rest) {
     if (!isfinite(scale) || window < 0) return GDR2_ERR_VALUE;
@@ -350,7 +353,8 @@ int gdr2_attn_fwd(const void* q, const void* k, const void* v, const long long* 
 size_t gdr2_attn_bwd_workspace_bytes(int N, int T, int Hq, int Hkv, int D, int packed, int dtype) {
     if (prompt_shape(N, T, Hq, Hkv, D, dtype, packed != 0) != GDR2_OK || prompt_none(N, T, Hq)) return 0;
     const size_t tokens = (size_t)(packed ? T : (long long)N * T), parts = gdr2::prompt_parts(N, T, Hq, Hkv, packed != 0);
-    return (2 * tokens * Hq + (parts > 1 ? 2 * parts * tokens * Hkv * D : 0)) * sizeof(float);
+    return parts > 1 ? prompt_part_offset(tokens * Hq) + 2 * parts * tokens * Hkv * D * sizeof(float)
+                     : 2 * tokens * Hq * sizeof(float);
 }
 
 int gdr2_attn_bwd(const void* q, const void* k, const void* v, const long long* strides, const void* o, const float* lse,
@@ -376,7 +380,7 @@ int gdr2_attn_bwd(const void* q, const void* k, const void* v, const long long* 
     a.lse2 = (float*)workspace;
     const size_t rows = (size_t)(packed ? T : (long long)N * T) * Hq;
     a.delta = a.lse2 + rows;
-    a.part = a.delta + rows;
+    a.part = (float*)((char*)workspace + prompt_part_offset(rows));
     a.parts = gdr2::prompt_parts(N, T, Hq, Hkv, packed);
     return gdr2::launch_prompt_bwd(a, dtype == GDR2_DTYPE_BF16, (hipStream_t)stream) == hipSuccess ? GDR2_OK
                                                                                                     : GDR2_ERR_HIP;

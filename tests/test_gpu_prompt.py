@@ -491,3 +491,16 @@ def test_long_sequences_more_than_lanes():
     lens = [1030 + i % 5 for i in range(127)] + [300]
     cu = bounds(lens)
     check(*make(cu[-1], 2, 1, 128, BF, seed=41), cu)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,heads,D", [(33, (3, 1), 64), (45, (5, 1), 128), (7, (9, 3), 64)])
+def test_odd_numbers_of_rows(dtype, T, heads, D):
+    # parts of dK and dV behind an odd number of rows of the workspace, and nothing behind its end
+    args = make(T, *heads, D, dtype, seed=44)
+    q, k, v, do = args
+    o, lse, rest, gr = check(*args, [0, T])
+    n = g2.gdr2_attn_bwd_workspace_bytes(1, T, *heads, D, True, g2._DT[dtype])
+    room = torch.full((n + 256,), 93, dtype=torch.uint8, device="cuda")
+    again = g2.gdr2_attn_bwd(q, k, v, o, lse, do, rest=rest, cu_seqlens=ints([0, T]), ws=room[:n])
+    assert all(torch.equal(again[x], gr[x]) for x in gr) and (room[n:] == 93).all()

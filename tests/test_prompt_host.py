@@ -93,6 +93,15 @@ def test_prompt_workspace_sizes(lib):
     assert bwd(lib, ws_bytes=n - 1) == WS
 
 
+def test_prompt_workspace_parts_are_aligned(lib):
+    # parts of dK and dV, written and read 16 bytes at a time, behind an odd number of rows
+    f = g2.gdr2_attn_bwd_workspace_bytes
+    for T, Hq, rows in ((33, 3, 800), (1, 3, 32), (2, 3, 48), (7, 5, 288)):
+        assert rows % 16 == 0 and 0 <= rows - T * Hq * 8 < 16
+        assert f(1, T, Hq, 1, 64) == rows + 2 * Hq * T * 64 * 4
+        assert bwd(lib, T=T, Hq=Hq, ws_bytes=f(1, T, Hq, 1, 64) - 1) == WS
+
+
 def test_tree_refusals(lib):
     need = g2.gdr2_attn_tree_workspace_bytes(1, 3, 2, 1, 64)
     assert need > 0 and g2.gdr2_attn_tree_workspace_bytes(0, 3, 2, 1, 64) == 0
