@@ -997,7 +997,7 @@ def gdr2_attn_fwd(q, k, v, *, cu_seqlens=None, scale=None, window=0, o=None, lse
         new.append(rest)
     _keep_for(stream, *new)
     if own_o and N == 0:
-        _zero(stream, *new)  # no sequence, and no kernel
+        _zero(stream, *(x for x in (o, lse, rest) if x is not None))  # no sequence, and no kernel
     st = _launch(lib.gdr2_attn_fwd, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), strides, _adr(cu_seqlens),
                  o.data_ptr(), _adr(lse), _adr(rest), N, T, Hq, Hkv, D, D ** -0.5 if scale is None else scale,
                  max(-1, min(window, 0x7fffffff)), dt, int(own_o))

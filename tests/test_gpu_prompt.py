@@ -504,3 +504,12 @@ def test_odd_numbers_of_rows(dtype, T, heads, D):
     room = torch.full((n + 256,), 93, dtype=torch.uint8, device="cuda")
     again = g2.gdr2_attn_bwd(q, k, v, o, lse, do, rest=rest, cu_seqlens=ints([0, T]), ws=room[:n])
     assert all(torch.equal(again[x], gr[x]) for x in gr) and (room[n:] == 93).all()
+
+
+@pytest.mark.parametrize("cu", [[0], [3, 3], [9, 9, 9]])
+def test_rows_of_no_sequence_in_an_lse_of_the_callers(cu):
+    x = torch.randn(1, 9, 4, 64, device="cuda")
+    for own in (True, False):  # zero where o is allocated here, else left as they are
+        o, lse = torch.full_like(x, 7.0), torch.full((1, 9, 4), 7.0, device="cuda")
+        got = g2.gdr2_attn_fwd(x, x, x, cu_seqlens=ints(cu), o=None if own else o, lse=lse)
+        assert got[1] is lse and all((t == (0 if own else 7)).all() for t in got)
