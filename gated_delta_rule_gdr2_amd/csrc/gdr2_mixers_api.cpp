@@ -4,6 +4,7 @@
 #include "../../include/gdr2.h"
 
 #include <hip/hip_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -138,6 +139,10 @@ int attn_shape(int B, int Hq, int Hkv, int D, int dtype) {
 // heads of a head group: the matrix cores' 16 columns at most
 int group_heads(int Hq, int Hkv) { return Hq / Hkv < 16 ? Hq / Hkv : 16; }
 
+// |scale| log2(e), which masked scores of -inf are multiplied by: a scale of zero weighs all that is seen alike, and so does
+// the smallest number above it, times which the largest score is 5e-7, and which leaves -inf what it is.
+float scale2_of(float scale) { return fmaxf((float)(fabs((double)scale) * 1.4426950408889634), FLT_TRUE_MIN); }
+
 // Attention over whole sequences: tokens below 2^31 - 1024 (a tile's last row still fits in 32 bits), and launches of
 // fewer than 2^32 threads at the smallest tile.
 int prompt_shape(int N, int T, int Hq, int Hkv, int D, int dtype, bool packed) {
@@ -170,9 +175,8 @@ int prompt_fill(gdr2::PromptArgs& a, const long long* strides, const int* cu, in
     a.window = window > 0 && window < T ? window : T;
     a.zero_rest = zero_rest;
     a.neg = scale < 0.f;
-    // a scale of zero weighs all that is seen alike, and so does one too small to matter, which leaves -inf what it is
     a.scale = fabsf(scale);
-    a.scale2 = fmaxf((float)(fabs((double)scale) * 1.4426950408889634), 1e-30f);
+    a.scale2 = scale2_of(scale);
     return GDR2_OK;
 }
 
@@ -415,7 +419,7 @@ int gdr2_attn_tree(const void* q, const int* parents, const void* k_cache, const
     a.scale2 = (float)((double)scale * 1.4426950408889634);
     gdr2::tree_rows(a, dtype == GDR2_DTYPE_BF16);
     a.neg = a.wide && scale < 0.f;
-    if (a.wide) a.scale2 = fmaxf(fabsf(a.scale2), 1e-30f);  // as for whole sequences
+    if (a.wide) a.scale2 = scale2_of(scale);
     if (gdr2::tree_line_places(a) > 0x7fffffffLL) return GDR2_ERR_SHAPE;
     const void* const ptrs[] = {q, k_cache, v_cache, o, workspace};
     const void* const words[] = {parents, starts, block_table, lse};

@@ -513,3 +513,37 @@ def test_rows_of_no_sequence_in_an_lse_of_the_callers(cu):
         o, lse = torch.full_like(x, 7.0), torch.full((1, 9, 4), 7.0, device="cuda")
         got = g2.gdr2_attn_fwd(x, x, x, cu_seqlens=ints(cu), o=None if own else o, lse=lse)
         assert got[1] is lse and all((t == (0 if own else 7)).all() for t in got)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,scale", [(60, 2.0 ** -123), (60, -2.0 ** -123), (61, 2.0 ** -125), (50, 2.0 ** -103)])
+def test_small_scales_of_large_scores(dtype, n, scale):
+    # powers of two that come out again: bit for bit what scores of the usual size give
+    cu = [0, 80, 90]
+    q, k, v, do = make(90, 4, 2, 64, dtype, seed=41)
+    kw = dict(cu_seqlens=ints(cu))
+    f = 2.0 ** n
+    want = g2.gdr2_attn_fwd(q, k, v, scale=scale * f * f, save_for_bwd=True, **kw)
+    got = g2.gdr2_attn_fwd(q * f, k * f, v, scale=scale, save_for_bwd=True, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want) if a is not None)
+    a = g2.gdr2_attn_bwd(q, k, v, want[0], want[1], do, rest=want[2], scale=scale * f * f, **kw)
+    b = g2.gdr2_attn_bwd(q * f, k * f, v, want[0], want[1], do, rest=want[2], scale=scale, **kw)
+    assert torch.equal(a["dv"], b["dv"]) and all(torch.equal(a[x], b[x] * f) for x in ("dq", "dk"))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("scale", [0.0, 1e-45, -1e-41])
+def test_scales_of_nothing(dtype, scale):
+    cu = [0, 150, 260]
+    q, k, v, do = make(260, 4, 2, 64, dtype, seed=42)
+    kw = dict(cu_seqlens=ints(cu), scale=scale, window=100)
+    o, lse, rest = g2.gdr2_attn_fwd(q, k, v, save_for_bwd=True, **kw)
+    gr = g2.gdr2_attn_bwd(q, k, v, o, lse, do, rest=rest, **kw)
+    wo, wl, size = ref.attention(q[0], k[0], v[0], cu, scale, 100)
+    near(o[0], wo, size, dtype, "o")
+    assert ((lse[0].double() - wl).abs() <= 1e-5 * wl.abs().clamp(min=1.0)).all()
+    _, _, dv, _, _, sv, _, _ = ref.gradients(q[0], k[0], v[0], do[0], cu, scale, 100)
+    near(gr["dv"][0], dv, sv, dtype, "dv")
+    # the others are the scale times sums of at most 110 terms below 2^16: denormal numbers, which keep few or no bits
+    for x in ("dq", "dk"):
+        assert (gr[x].double().abs() <= abs(scale) * 2.0 ** 23 + 2.0 ** -133).all()

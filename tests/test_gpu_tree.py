@@ -257,6 +257,18 @@ def test_tree_refusals():
         f(q[:, :, :3].contiguous(), p, kc, vc, t, st)
 
 
+@pytest.mark.parametrize("hkv", [4, 1])
+def test_small_scales_of_large_scores(hkv):
+    # powers of two that come out again; up to 32 rows a key head, and more
+    q, parents, kc, vc, table, starts = make([257, 40], 9, 4, hkv, 64, 32, BF, seed=24)
+    f = 2.0 ** 60
+    run = lambda s, scale: g2.gdr2_attn_tree(q * s, ints(parents), kc * s, vc, ints(table), ints(starts), scale=scale, return_lse=True)
+    for scale in (0.125, -0.25):
+        assert all(torch.equal(a, b) for a, b in zip(run(1.0, scale), run(f, scale / f / f)))
+    for scale in (0.0, 1e-45):
+        check(q, parents, kc, vc, table, starts, scale=scale)
+
+
 # ---------------------------------------------------------------- keeping an accepted path
 
 
