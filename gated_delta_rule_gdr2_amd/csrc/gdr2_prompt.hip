@@ -17,28 +17,15 @@
 
 namespace gdr2 {
 
-// RW x 32 queries a workgroup, S waves for each 32 of them, which share the keys; EXACT: queries of few keys in two parts
+// RW x 32 queries of head hq a workgroup, S waves for each 32 of them, which share the keys; EXACT: queries of few keys
+// (prompt_few) in two parts
 template <class OT, int D, int RW, int S, bool EXACT>
-__global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt_fwd(PromptArgs a) {
+__device__ __forceinline__ void prompt_fwd(const PromptArgs& a, const PromptAt& at, int hq, int hk, lds_char* lds) {
     using FR = typename Frag<OT>::type;
     using TL = Tile32<OT, D>;
     constexpr int NW = RW * S, QT = 32 * RW, KT = tile_rows(S), TB = KT * TL::RB, NB = KT / 32 / S;
     constexpr int ACC = D / 32 * 4096;  // bytes of a wave's accumulators
     constexpr int BUFS = tile_bufs<OT, D>(S);
-    extern __shared__ __align__(16) char smem[];
-    lds_char* lds = (lds_char*)smem;
-    poison_lds(lds, 2 * BUFS * TB);
-    poison_lds_done();
-    PromptAt at;
-    int slot;
-    const int hp = prompt_at(a, blockIdx.x, QT, a.Hq, true, at, slot);
-    const int hk = hp % a.Hkv, hq = hk * a.G + hp / a.Hkv;
-    if (a.cu && a.zero_rest) {
-        prompt_zero(a, slot, QT, (OT*)a.o, a.Hq, hq, D);
-        if (a.rest) prompt_zero(a, slot, QT, (OT*)a.rest, a.Hq, hq, D);
-        if (a.lse) prompt_zero(a, slot, QT, a.lse, a.Hq, hq, 1);
-    }
-    if (!at.any) return;
     const int l = lane_id(), h = l >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rw = S == 1 ? w : w % RW, sp = S == 1 ? 0 : w / RW;
     const int q0 = at.tile * QT, last = at.len - 1;
@@ -183,12 +170,33 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
 }
 
 template <class OT, int D, int RW, int S>
+__global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt_fwd(PromptArgs a) {
+    constexpr int QT = 32 * RW;
+    extern __shared__ __align__(16) char smem[];
+    lds_char* lds = (lds_char*)smem;
+    poison_lds(lds, 2 * tile_bufs<OT, D>(S) * tile_rows(S) * D * (int)sizeof(OT));
+    poison_lds_done();
+    PromptAt at;
+    int slot;
+    const int hp = prompt_at(a, blockIdx.x, QT, a.Hq, true, at, slot);
+    const int hk = hp % a.Hkv, hq = hk * a.G + hp / a.Hkv;
+    if (a.cu && a.zero_rest) {
+        prompt_zero(a, slot, QT, (OT*)a.o, a.Hq, hq, D);
+        if (a.rest) prompt_zero(a, slot, QT, (OT*)a.rest, a.Hq, hq, D);
+        if (a.lse) prompt_zero(a, slot, QT, a.lse, a.Hq, hq, 1);
+    }
+    if (!at.any) return;
+    if constexpr (sizeof(OT) == 2)
+        if (prompt_few(a, at.tile * QT)) return prompt_fwd<OT, D, RW, S, true>(a, at, hq, hk, lds);
+    prompt_fwd<OT, D, RW, S, false>(a, at, hq, hk, lds);
+}
+
+template <class OT, int D, int RW, int S>
 static hipError_t launch_fwd_t(const PromptArgs& a, hipStream_t stream) {
     constexpr int TILES = 2 * tile_bufs<OT, D>(S) * tile_rows(S) * D * (int)sizeof(OT), JOIN = (S - 1) * RW * (D / 32 * 4096 + 512);
     constexpr int LDS = TILES > JOIN ? TILES : JOIN;
     static_assert(LDS <= 160 * 1024, "a compute unit's LDS");
-    constexpr bool BF = sizeof(OT) == 2;
-    const auto f = BF && prompt_exacts(a) ? k_prompt_fwd<OT, D, RW, S, BF> : k_prompt_fwd<OT, D, RW, S, false>;
+    const auto f = k_prompt_fwd<OT, D, RW, S>;
     if (LDS > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)f, hipFuncAttributeMaxDynamicSharedMemorySize, LDS);
         if (e != hipSuccess) return e;
@@ -226,6 +234,8 @@ __global__ __launch_bounds__(512, 2) void k_prompt_fwd2(PromptArgs a) {
         if (a.lse) prompt_zero(a, slot, QT, a.lse, a.Hq, hq, 1);
     }
     if (!at.any) return;
+    // queries of few keys, whose walk is short (but for small windows): without turns, in two parts
+    if (prompt_few(a, at.tile * QT)) return prompt_fwd<OT, D, 8, 1, true>(a, at, hq, hk, lds);
     const int l = lane_id(), h = l >> 5, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int q0 = at.tile * QT, last = at.len - 1;
     const int wq0 = q0 + 32 * w, qi = wq0 + (l & 31);

@@ -70,12 +70,17 @@ inline int prompt_parts(int N, int T, int Hq, int Hkv, bool packed) {
     return (int)(p < G ? p : G);
 }
 
-// Calls (bf16) in which queries that see few keys, the first 64 of a sequence, have their weights and weights' gradients in
-// two bf16 parts: those of short sequences, and of few sequences and heads. Such queries hold the most of dq's and dk's size,
-// and few roundings that balance one another: of 2 heads with one part, both were off by 1.5 times their own rounding on
-// average and by up to 1.8 for 10 tokens, 1.6 for 40, 1.5 for 300, and with two parts by up to 1.2, 1.1 and 1.3; from some 8
-// heads on the average holds for each. For all calls the two cost 482 -> 524 us of the backward of 2 x 4096 tokens.
-// (k_prompt_fwd2 has one part: its sequences' first 64 tokens are a small part of them.)
+// Queries that see few keys, the first 64 of a sequence (prompt_few), have their weights in two bf16 parts in the forward
+// (bf16), whatever the call, so that a token's output does not lose precision by the batch it is in: the workgroups that hold
+// such queries take a walk of their own. With it and without, us: 2 x 4096 tokens, 16 heads of 128 150.5 and 149.4, 1 x 16384
+// 1003 and 1001, 24 packed of 17 - 700 tokens 29.8 and 29.1, 2 x 4096 of 64 channels with a window of 2048 76 and 74.4.
+//
+// Calls in which the backward does so too, for weights and their gradients: those of short sequences, and of few sequences and
+// heads. Such queries hold the most of dq's and dk's size, and few roundings that balance one another: of 2 heads with one
+// part, both were off by 1.5 times their own rounding on average and by up to 1.8 for 10 tokens, 1.6 for 40, 1.5 for 300, and
+// with two parts by up to 1.2, 1.1 and 1.3; from some 8 heads on the average over a call's heads holds. For all calls, as in the
+// forward, the backward takes 492 us for 471 (2 x 4096 tokens, 16 heads), 53 for 46 (4 x 300, 32 heads), and 200 for 176 (9
+// packed documents of 64 channels): its registers hold two walks' operands only with spills.
 inline bool prompt_exacts(const PromptArgs& a) {
     const long long len = prompt_length(a.N, a.T, a.cu != nullptr);
     return (len < a.window ? len : a.window) <= 128 || (long long)a.N * a.Hq <= 8;

@@ -195,7 +195,7 @@ __device__ __forceinline__ bf16x8 rest_frag(const f32x16& x, int b, const bf16x8
     for (int e = 0; e < 8; ++e) y[e] = (bf16)(x[8 * b + e] - (float)f[e]);
     return y;
 }
-// Queries of few keys (prompt_exacts).
+// Queries of few keys, from q0 on (prompt_exacts).
 __device__ __forceinline__ bool prompt_few(const PromptArgs& a, int q0) { return q0 < 64 || a.window <= 64; }
 // this lane's column of D rows, held in accumulators, times f: four consecutive elements at a time
 template <class OT, int D>

@@ -330,10 +330,10 @@ int gdr2_kv_append(const void* k, const void* v, void* k_cache, void* v_cache, c
  * only (ignored for fp32), takes what o's rounding left over, o + rest being the result to 16 bits; the backward reads
  * it, where it is given, for sum_c dout_c o_c, whose rounding error would otherwise be the largest part of dq's and dk_'s
  * in rows that see few tokens. Scores, softmax statistics and sums are fp32; with bf16 the weights and their gradients
- * enter the second products as one bf16 each, so that outputs carry two roundings, their own among them. In calls with
- * a mean length or a window of at most 128, or with N Hq of at most 8, the first 64 tokens of each sequence (with a window
- * of at most 64 all) have theirs in two bf16 parts, and carry their own rounding alone (the forward of long sequences
- * with 2^17 tokens times heads and more keeps one).
+ * enter the second products as one bf16 each, so that outputs carry two roundings, their own among them. The first 64
+ * tokens of each sequence (with a window of at most 64 all) have theirs in two bf16 parts, and carry their own rounding
+ * alone: in the forward always, in the backward in calls with a mean length or a window of at most 128, or with N Hq of
+ * at most 8.
  *
  * A value that is infinite or NaN at a token reaches the tokens of its own sequence, also some before it; other
  * sequences are not affected. Results repeat bit for bit; how waves share the work goes by the sizes of the call, so that

@@ -547,3 +547,22 @@ def test_scales_of_nothing(dtype, scale):
     # the others are the scale times sums of at most 110 terms below 2^16: denormal numbers, which keep few or no bits
     for x in ("dq", "dk"):
         assert (gr[x].double().abs() <= abs(scale) * 2.0 ** 23 + 2.0 ** -133).all()
+
+
+FEW = [([300] * 3, (4, 4), 64, 0), ([700, 200, 1000], (16, 4), 128, 0), ([1100] * 4, (32, 32), 128, 0), ([400] * 40, (8, 8), 128, 0),
+       ([500] * 5, (12, 3), 64, 40), ([1024] * 4, (32, 32), 128, 64), ([4096], (1, 1), 128, 0), ([90] * 100, (16, 2), 64, 0)]
+
+
+@pytest.mark.parametrize("lens,heads,D,window", FEW)
+def test_first_tokens_carry_one_rounding_in_any_batch(lens, heads, D, window):
+    # o as in test_short_sequences_carry_one_rounding: of the first 64 tokens, or with a window of at most 64 of all
+    q, k, v, do = make(sum(lens), *heads, D, BF, seed=43)
+    cu = bounds(lens)
+    o, _, rest = g2.gdr2_attn_fwd(q, k, v, cu_seqlens=ints(cu), window=window, save_for_bwd=True)
+    for a, n in zip(cu[:6], lens):
+        at = slice(a, a + (n if window else min(n, 64)))
+        wo, _, size = ref.attention(q[0, at], k[0, at], v[0, at], [0, at.stop - a], D ** -0.5, window)
+        two = (2.0 ** -16 + FP) * size
+        assert ((o[0, at].double() - wo).abs() <= R8 * wo.abs() + (1 + R8) * two + 1e-30).all()
+        both = o[0, at].double() + rest[0, at].double()
+        assert ((both - wo).abs() <= 2.0 ** -16 * wo.abs() + two + 1e-30).all()
