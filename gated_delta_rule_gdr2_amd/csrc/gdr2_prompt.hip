@@ -403,8 +403,9 @@ static hipError_t launch_fwd_d(const PromptArgs& a, hipStream_t stream) {
         // the turns of k_prompt_fwd2 from two rounds of its workgroups on (us against those of four waves: 2 x 4096
         // tokens, 16 heads 143 and 165; 16384 tokens 985 and 1048; 8 x 1024 58 and 58; with 64 channels, whose products
         // are half as long as their softmax, 79 and 56)
-        if (D == 128 && S == 1 && tasks >= 4096 && prompt_length(a.N, a.T, a.cu != nullptr) >= 1024)
-            return launch_fwd2_t<OT, D>(a, stream);
+        if constexpr (D == 128)
+            if (S == 1 && tasks >= 4096 && prompt_length(a.N, a.T, a.cu != nullptr) >= 1024)
+                return launch_fwd2_t<OT, D>(a, stream);
         // sequences that one tile holds: 64 rows of it, while they are few (29 tokens, 16 heads: 6.5 us, of 128 rows 7.8;
         // 6 x 64 tokens, 64 heads 10.1 and, by waves that do not share, 9.5)
         if (a.T <= 64 && tasks <= 512) return launch_fwd_t<OT, D, 2, 2>(a, stream);

@@ -378,8 +378,9 @@ static hipError_t launch_dq_d(const PromptArgs& a, hipStream_t stream) {
     if constexpr (sizeof(OT) == 2) {
         // 256 queries a workgroup from two rounds of them on (2 x 4096 tokens, 16 heads 200 us, with 128 queries 214;
         // 64 channels, 9 packed documents, 92 and 73)
-        if (D == 128 && S == 1 && tasks >= 4096 && prompt_length(a.N, a.T, a.cu != nullptr) >= 1024)
-            return launch_dq_t<OT, D, 8, 1>(a, stream);
+        if constexpr (D == 128)
+            if (S == 1 && tasks >= 4096 && prompt_length(a.N, a.T, a.cu != nullptr) >= 1024)
+                return launch_dq_t<OT, D, 8, 1>(a, stream);
         if (S == 1) return launch_dq_t<OT, D, 4, 1>(a, stream);
         if (S == 2) return launch_dq_t<OT, D, 4, 2>(a, stream);
         return tasks <= 256 ? launch_dq_t<OT, D, 1, 4>(a, stream) : launch_dq_t<OT, D, 2, 4>(a, stream);
