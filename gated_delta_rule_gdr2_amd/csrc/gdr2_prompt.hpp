@@ -38,27 +38,33 @@ inline long long prompt_length(int N, int T, bool packed) { return packed ? ((lo
 
 // Waves that share a block's other axis. None share where the longest walk is at most half of what each of the 1024 SIMDs
 // has to do anyway; two where it is no longer than that; else four, which end soonest where all blocks are under way at
-// once. More blocks than that (`once`: LDS holds the tiles of as many) take short walks alone and long ones by twos, so
-// that more of them are under way, and in fp32, whose products are the longest, by twos. `tasks`: walks of one head each;
-// `heads`: heads that a walk goes through one after another; es: bytes of an element. Measured with S = 1, 2, 4, us, forward
-// and backward, bf16, 128 channels:
-//     2 x 4096 tokens, 16 heads 166, 210, 258 and 510, 566, 689     1 x 8192, 8 heads over 1 194, 169, 205 and 674, 528, 589
-//     1 x 2048, 16 heads 45, 43, 39 and 166, 120, 112               1 x 512, 16 heads 16, 17, 11 and 60, 50, 36
-//     24 packed of 17 - 700 tokens, 16 heads over 4 31, 45, 61 and 109, 132, 197
-//     5 x 168, 64 heads over 8 19, 29, 36 and 70, 85, 121           4 x 300, 32 heads 15, 22, 28 and 47, 59, 88
-//     2 x 168, 48 heads 9.9, 11, 18 and 32, 32, 50                  2 x 512, 16 heads 15, 17, 14 and 50, 44, 39
-//     2 x 1024, 16 heads 26, 26, 28 and 82, 70, 79                  16 x 60, 16 heads 8.6, 8.8, 8.3 and 23, 25, 32
-// 64 channels: 4 x 300, 32 heads 10, 11, 14 and 29, 33, 49          1 x 1024, 32 heads 20, 21, 16 and 57, 47, 47
-// fp32, 64:    4 x 300, 32 heads 37, 30, 45 and 107, 88, 137        1 x 130, 4 heads over 2 19, 13, 11 and 53, 37, 30
-// fp32, 128:   2 x 168, 48 heads 32, 23, 35 and 107, 73, 116
+// once. More blocks than that (`once`: LDS holds the tiles of as many) take short walks alone, middle ones by twos and, up
+// to 1024 of them, long ones by fours; in fp32, whose products are the longest, by twos. A sequence of one tile has nothing
+// to share (in fp32 two share its rows). Of packed sequences the mean length has to do, the lengths being the device's to
+// know: with one of 2000 tokens beside 23 of 5 - 28, 16 heads of 128, the backward takes 176 us alone and 135 by twos.
+// `tasks`: walks of one head each; `heads`: heads that a walk goes through one after another; es: bytes of an element.
+// Measured with S = 1, 2, 4, us, forward and backward, bf16, 128 channels:
+//     2 x 4096 tokens, 16 heads 154, 183, 228 and 478, 533, 640     1 x 8192, 8 heads over 1 182, 163, 193 and 706, 572, 634
+//     1 x 2048, 16 heads 43, 42, 36 and 140, 111, 105               1 x 1152, 16 heads 27, 27, 20 and 88, 72, 59
+//     1 x 2048, 24 heads 48, 44, 56 and 155, 129, 163               1 x 1152, 32 heads 30, 29, 37 and 96, 76, 108
+//     2 x 1024, 16 heads 26, 27, 27 and 83, 70, 79                  1 x 512, 16 heads 15, 17, 11 and 48, 42, 28
+//     24 packed of 17 - 700 tokens, 16 heads over 4 48, 69, 105 and 183, 224, 360
+//     5 x 168, 64 heads over 8 19, 29, 34 and 64, 84, 121           4 x 300, 32 heads 14, 22, 28 and 46, 59, 88
+//     2 x 168, 48 heads 9.6, 12, 18 and 32, 32, 50                  2 x 512, 16 heads 16, 17, 14 and 50, 44, 39
+//     16 x 60, 16 heads 8.0, 8.6, 7.9 and 22, 24, 31                64 x 20, 8 heads 7.6, 8.3, 7.6 and 20, 28, 42
+// 64 channels: 4 x 300, 32 heads 10, 12, 14 and 29, 33, 49          1 x 1024, 32 heads 20, 20, 15 and 56, 46, 46
+// fp32, 64:    4 x 300, 32 heads 38, 31, 46 and 107, 88, 137        1 x 130, 4 heads over 2 18, 12, 10 and 53, 36, 30
+// fp32, 128:   2 x 168, 48 heads 33, 23, 35 and 107, 73, 116        1 x 2048, 16 heads over 4 271, 172, 205 and 924, 558, 663
+//              16 x 64, 16 heads 16, 13, 25 and 51, 43, 80          1 x 60, 16 heads over 4 14, 12, 12 and 46, 38, 40
 inline int prompt_sharing(const PromptArgs& a, long long tasks, int heads, int es) {
     const long long len = prompt_length(a.N, a.T, a.cu != nullptr), seen = len < a.window ? len : a.window;
     const long long walk = (seen + 63) / 64 * heads;  // tiles of the longest walk
     const long long once = es == 2 && a.D == 64 ? 1024 : 512;
     const double each = (double)tasks * walk * (seen < len ? 1.0 : 0.5) / 1024.0;
+    if (a.T <= 64) return es == 2 ? 1 : 2;
     if (2.0 * walk <= each || (tasks >= 2048 && walk <= 8)) return 1;
     if (es == 2 && tasks > once && walk <= 8) return 1;
-    return walk <= each || tasks > once ? 2 : 4;
+    return walk <= each || tasks > (es == 2 && walk > 16 ? 1024 : once) ? 2 : 4;
 }
 
 // Parts that the query heads of a key head are cut in for dK and dV, each walked by itself and added up by a further
