@@ -566,3 +566,43 @@ def test_first_tokens_carry_one_rounding_in_any_batch(lens, heads, D, window):
         assert ((o[0, at].double() - wo).abs() <= R8 * wo.abs() + (1 + R8) * two + 1e-30).all()
         both = o[0, at].double() + rest[0, at].double()
         assert ((both - wo).abs() <= 2.0 ** -16 * wo.abs() + two + 1e-30).all()
+
+
+@pytest.mark.parametrize("heads,D,lens,window", [((4, 2), 64, [33, 37], 20), ((3, 1), 128, [150], 0), ((4, 4), 64, [40, 90, 5], 0)])
+def test_gradients_against_differences_along_themselves(heads, D, lens, window):
+    # fp32: <grad, u> against central differences of L(x) = <o(x), do> with steps h and h / 2, extrapolated, where u is the
+    # gradient (in fp64) on random pieces of it, 8 tokens of a head each, so that <grad, u> is as large as it can be.
+    # Room: o off by 1e-5 normwise, the library's, moves L by 1e-5 |o| |do|, a quotient of step s by that over s and the
+    # extrapolation, (4 (2 / h) + 1 / h) / 3, by three times as much; what the extrapolation leaves is the same
+    # differences' own in fp64. That is less than a fiftieth of <grad, u>: a gradient that is zero, doubled, of the other
+    # sign or lacks one of its pieces' factors is not near it.
+    n = sum(lens)
+    q, k, v, do = make(n, *heads, D, F32, seed=45)
+    cu, sc, c = bounds(lens), D ** -0.5, ints(bounds(lens))
+    f = lambda x: (g2.gdr2_attn_fwd(*x, cu_seqlens=c, window=window).double() * do.double()).sum()
+    f64 = lambda x: (ref.attention(*(t[0] for t in x), cu, sc, window)[0] * do[0].double()).sum()
+    o, lse, _ = g2.gdr2_attn_fwd(q, k, v, cu_seqlens=c, window=window, save_for_bwd=True)
+    gr = g2.gdr2_attn_bwd(q, k, v, o, lse, do, cu_seqlens=c, window=window)
+    exact = ref.gradients(q[0], k[0], v[0], do[0], cu, sc, window)[:3]
+    size = float(o.double().norm() * do.double().norm())
+    gen = torch.Generator().manual_seed(2)
+    for i, name in enumerate(("dq", "dk", "dv")):
+        for part in range(6):
+            g = exact[i][None]
+            on = torch.rand((n + 7) // 8, g.shape[2], generator=gen) < (1.0, 0.5, 0.5, 0.25, 0.25, 0.25)[part]
+            u = g * on.repeat_interleave(8, 0)[:n, :, None].to(g.device)
+            u = u * (0.02 * g.numel() ** 0.5 / float(u.norm()))  # 0.02 an element, were they alike
+
+            def slope(fun, h, wide):
+                x = [[t.double() for t in (q, k, v)] for _ in range(2)]
+                x[0][i], x[1][i] = x[0][i] + h * u, x[1][i] - h * u
+                if not wide:
+                    x = [[t.float() for t in y] for y in x]
+                return float(fun(x[0]) - fun(x[1])) / (2 * h)
+
+            diff = lambda fun, wide: (4 * slope(fun, 0.5, wide) - slope(fun, 1.0, wide)) / 3
+            want, got = float((g * u).sum()), float((gr[name].double() * u).sum())
+            # (the rounding of x + h u to fp32, 2^-24 of 4 h an element at most, moves L by that times |grad|: within 1e-5 too)
+            room = 3 * 1e-5 * size + abs(diff(f64, True) - want)
+            assert want > 50 * room, (name, want, room)
+            assert abs(got - diff(f, False)) <= room, (name, part, got, want, room)
