@@ -17,8 +17,12 @@
 namespace gdr2 {
 
 constexpr int PT = 512;           // threads that hand out the pages
-constexpr int PAGES_SHORT = 4;     // table entries that one thread goes through by itself
-constexpr int SLOTS_FEW = 4096;    // tokens up to which one workgroup writes the slots
+// table entries that one thread goes through by itself. Us with 2, 4 and 8, pages of 16 tokens: 2048 requests of one new token
+// 10.5, 11.6 and 13.2, of 40 tokens (3 or 4 entries) 161, 20 and 21, of 100 (7 or 8) 162, 163 and 24
+constexpr int PAGES_SHORT = 4;
+// tokens up to which one workgroup writes the slots: us so and by a second kernel, 96 requests, one of them a prompt of 1500
+// tokens 8.7 and 9.5, of 3000 11.7 and 9.7, of 5000 15.7 and 10.4, of 12000 31.4 and 10.1
+constexpr int SLOTS_FEW = 4096;
 
 // exclusive prefix sum over the workgroup, and the total; sc: PT / 64 places
 __device__ __forceinline__ long long scan_wg(long long x, long long* sc, long long& total) {

@@ -9,7 +9,10 @@
 //
 // Matrix products bound both (seven of them where a single walk with atomics has five): 2 x 4096 tokens, 16 heads of 128
 // channels, 465 us together, 1030 TFLOP/s counted as seven products, where a large product alone reaches 1198. Packed
-// documents of 64 channels (9 of them, 16 query heads over 4, 2048-token window) 171 us with the sum of the parts.
+// documents of 64 channels (9 of them, 16 query heads over 4, 2048-token window) 173 us with the sum of the parts: vector
+// units busy for 50 % of dQ's cycles and 44 of dK/dV's, matrix cores for 37 and 39, and little of both at once. fp32, 128
+// channels (2048 tokens, 8 heads over 2) 338 us: matrix cores busy for 57 and 61 % of the cycles, vector units for 12; one
+// workgroup a compute unit, whose tile takes 128 of 160 KB of LDS, so that each tile's load is waited out.
 #include "gdr2_prompt_device.hpp"
 
 namespace gdr2 {
@@ -147,8 +150,9 @@ __global__ __launch_bounds__(64 * RW * S, (prompt_waves<OT, D>())) void k_prompt
 
 // ---------------------------------------------------------------- dK, dV: queries in tiles
 // (RW x 32 keys a workgroup, S waves for each 32 of them, which share the queries)
-// Registers leave room for two waves a SIMD at 128 channels, 192 of a lane's 256 being sums and own rows (operands two
-// ahead spilled: 503 us for 480), and for three at 64 (packed documents: the backward 181 us with two, 172 with three). The
+// Registers leave room for two waves a SIMD at 128 channels, 192 of a lane's 256 being sums and own rows, but for 1 to 3 that
+// are spilled outside of the loop, and 5 to 8 that variants with two parts load again inside it (operands two ahead spilled
+// more: 503 us for 480), and for three at 64 (packed documents: the backward 181 us with two, 172 with three). The
 // scheduling barriers keep the compiler from drawing one phase's operands into the one before, which spilled 24.
 template <class OT, int D>
 constexpr int dkv_waves() { return sizeof(OT) == 2 && D == 64 ? 3 : prompt_waves<OT, D>(); }

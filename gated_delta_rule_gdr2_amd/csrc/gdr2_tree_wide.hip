@@ -6,8 +6,14 @@
 // split over workgroups as in gdr2_attn.hip, a unit of the line being a tile. From the rows' registers straight against
 // the cache, four waves side by side (gdr2_tree.hip), 32 sequences of 200 to 16384 tokens with trees of 32, 32 heads over 8
 // of 128, took 200 us: every wave loaded and turned all values by itself. So 112 us and 8.4 for the join, 3.6 TB/s of
-// the cache: a workgroup's two tiles fill a compute unit's LDS, so that its loads pause where its waves meet, and where
-// it goes from one row to the next.
+// the cache. A workgroup's two tiles take 128 of a compute unit's 160 KB of LDS and a third does not fit, so that one tile at
+// most is on its way, and none between a tile's arrival and the sending for the next: waves wait for 38 % of their time,
+// matrix cores are busy for 22 % of the cycles and vector units for 29.
+//
+// Weights enter the second product as one bf16 (the step, and trees of up to 32 rows, take them in two parts): o is off by
+// 2.3e-3 instead of its own rounding's 1.7e-3. Two parts took 127 us for 118 there, 16.6 for 15.9 (one sequence of 777
+// tokens, 12 drafts, 16 heads over 2), 122 for 101 (16 of 4096, 64 drafts, 32 heads over 4), 54 for 44 (64 of 2000, 16 drafts, 32
+// heads over 4 of 64): the products of a tile follow its loads.
 #include "gdr2_prompt_device.hpp"
 #include "gdr2_tree_device.hpp"
 
@@ -328,7 +334,10 @@ template <int D, int RW, int S, int KT>
 static hipError_t launch_wide_t(const TreeArgs& a, hipStream_t stream) {
     using TW = TreeWide<D, RW, S, KT>;
     const auto one = k_tree_wide<D, RW, S, KT, false>, line = k_tree_wide<D, RW, S, KT, true>;
-    // one row a workgroup, without a second kernel, where no row can pass eight tiles
+    // One row a workgroup, without a second kernel, where no row can pass 512 tokens. Few rows end sooner split, many whole; us,
+    // whole and split, 12 drafts, 16 heads over 2 of 128: 1 x 400 tokens 18.6 and 15.0, 8 x 400 18.9 and 16.4, 64 x 400 19.7 and
+    // 24.7; 1 x 777 28.4 and 16.1, 8 x 777 29.0 and 18.1, 64 x 777 27.3 and 31.2; 32 drafts, 32 heads over 8: 8 x 400 19.9 and
+    // 22.9, 64 x 400 43 and 48, 64 x 777 60 and 65
     const long long rows = (long long)a.B * a.Hkv * a.nb;
     const bool whole = tree_max_units(a) <= 512 / KT && rows < (1LL << 32) / (64 * RW * S);
     if (TW::LDS > 65536) {
