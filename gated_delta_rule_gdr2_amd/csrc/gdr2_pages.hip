@@ -22,7 +22,7 @@ constexpr int PT = 512;           // threads that hand out the pages
 constexpr int PAGES_SHORT = 4;
 // tokens up to which one workgroup writes the slots: us so and by a second kernel, 96 requests, one of them a prompt of 1500
 // tokens 8.7 and 9.5, of 3000 11.7 and 9.7, of 5000 15.7 and 10.4, of 12000 31.4 and 10.1
-constexpr int SLOTS_FEW = 4096;
+constexpr int SLOTS_FEW = 2048;
 
 // exclusive prefix sum over the workgroup, and the total; sc: PT / 64 places
 __device__ __forceinline__ long long scan_wg(long long x, long long* sc, long long& total) {

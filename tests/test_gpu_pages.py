@@ -239,3 +239,13 @@ def test_a_server_from_prompt_to_accepted_drafts():
     prompt([0, 0, 60])
     step()
     assert lengths.tolist() == [x[0].shape[0] for x in held]
+
+
+@pytest.mark.parametrize("tokens", [2040, 2041, 2042, 4088, 4089, 4090])
+def test_tokens_around_the_second_kernel(tokens):
+    # slots by the workgroup that hands out the pages, and by a kernel of their own; max_tokens is 7 more
+    lengths, counts = [5, 0, 31, 7], [1, tokens - 12, 10, 1]
+    table = [[3, -1], [-1] * 2, [1, 2], [0, -1]]
+    table = [r + [-1] * 300 for r in table]
+    free = [4 + i for i in range(296)] + [0] * 4
+    check(lengths, counts, table, free, 296, 16, tokens + 7)
