@@ -606,3 +606,26 @@ def test_gradients_against_differences_along_themselves(heads, D, lens, window):
             room = 3 * 1e-5 * size + abs(diff(f64, True) - want)
             assert want > 50 * room, (name, want, room)
             assert abs(got - diff(f, False)) <= room, (name, part, got, want, room)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_of_no_sequence_around_many(dtype):
+    # as test_rows_of_no_sequence, of more sequences than lanes; and bounds out of order among as many stay inside
+    lens = [(3 * i) % 19 for i in range(190)] + [7]
+    cu, n = bounds(lens, 130), sum(lens)
+    args = make(n, 4, 2, 128, dtype, seed=46)
+    want = check(*args, bounds(lens))
+    pad = lambda x: torch.cat([x.new_full((1, 130, *x.shape[2:]), float("nan")), x, x.new_full((1, 77, *x.shape[2:]), float("inf"))], 1)
+    q, k, v, do = (pad(x) for x in args)
+    o, lse, rest = g2.gdr2_attn_fwd(q, k, v, cu_seqlens=ints(cu), save_for_bwd=True)
+    gr = g2.gdr2_attn_bwd(q, k, v, o, lse, do, rest=rest, cu_seqlens=ints(cu))
+    inner = slice(130, 130 + n)
+    for a, b in ((o, want[0]), (lse, want[1]), *((gr[x], want[3][x]) for x in gr)):
+        # (the sizes of the call choose how waves share the work, and with it the order of sums: as test_offsets_past_32_bits)
+        assert normwise(a[:, inner].double(), b.double()) <= (2.0 ** -6 if dtype == BF else 2e-5)
+        assert (a[:, :130] == 0).all() and (a[:, 130 + n:] == 0).all()
+    for bad in ([5, 90, 40] * 30 + [n], [0] * 70 + [2 ** 31 - 1] * 70, list(range(n, 0, -1))[:200], [-9] * 66):
+        o, lse, rest = g2.gdr2_attn_fwd(*args[:3], cu_seqlens=ints(bad), save_for_bwd=True)
+        gr = g2.gdr2_attn_bwd(*args[:3], o, lse, args[3], rest=rest, cu_seqlens=ints(bad))
+        assert o.shape == args[0].shape and gr["dk"].shape == args[1].shape
+    torch.cuda.synchronize()
