@@ -11,8 +11,8 @@
 // channels, 465 us together, 1030 TFLOP/s counted as seven products, where a large product alone reaches 1198. Packed
 // documents of 64 channels (9 of them, 16 query heads over 4, 2048-token window) 173 us with the sum of the parts: vector
 // units busy for 50 % of dQ's cycles and 44 of dK/dV's, matrix cores for 37 and 39, and little of both at once. fp32, 128
-// channels (2048 tokens, 8 heads over 2) 338 us: matrix cores busy for 57 and 61 % of the cycles, vector units for 12; one
-// workgroup a compute unit, whose tile takes 128 of 160 KB of LDS, so that each tile's load is waited out.
+// channels (2048 tokens, 8 heads over 2) 338 us: one wave a SIMD, whose tile takes 128 of 160 KB of LDS, with nothing beside
+// it: matrix cores busy for 57 and 61 % of the cycles, vector units for 12, 15 and 13 % waited.
 #include "gdr2_prompt_device.hpp"
 
 namespace gdr2 {
