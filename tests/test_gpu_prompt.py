@@ -629,3 +629,75 @@ def test_rows_of_no_sequence_around_many(dtype):
         gr = g2.gdr2_attn_bwd(*args[:3], o, lse, args[3], rest=rest, cu_seqlens=ints(bad))
         assert o.shape == args[0].shape and gr["dk"].shape == args[1].shape
     torch.cuda.synchronize()
+
+
+def test_autograd_twice_broadcast_and_of_a_projection():
+    cu = [0, 50, 140]
+    q, k, v, do = make(140, 4, 2, 64, BF, seed=47)
+    c = ints(cu)
+    want = check(q, k, v, do, cu)[3]
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+    o = g2.GDR2AttnFunction.apply(*leaves, c)
+    for _ in range(2):
+        got = torch.autograd.grad(o, leaves, do, retain_graph=True)
+        assert all(torch.equal(a, want[n]) for a, n in zip(got, ("dq", "dk", "dv")))
+    # an output's gradient that is one number, broadcast
+    ones = check(q, k, v, torch.ones_like(do), cu)[3]
+    assert all(torch.equal(a, ones[n]) for a, n in zip(torch.autograd.grad(o.sum(), leaves), ("dq", "dk", "dv")))
+    # parts of one projection's output, and a gradient for keys alone
+    qkv = torch.cat([q, k, v], 2).requires_grad_()
+    a, b, d = qkv[:, :, :4], qkv[:, :, 4:6], qkv[:, :, 6:]
+    g2.GDR2AttnFunction.apply(a, b, d, c).backward(do)
+    assert torch.equal(qkv.grad, torch.cat([want["dq"], want["dk"], want["dv"]], 2))
+    key = k.clone().requires_grad_()
+    g2.GDR2AttnFunction.apply(q, key, v, c).backward(do)
+    assert torch.equal(key.grad, want["dk"])
+    with pytest.raises(RuntimeError):  # no second derivatives
+        g = torch.autograd.grad(g2.GDR2AttnFunction.apply(*leaves, c), leaves, do, create_graph=True)
+        torch.autograd.grad(g[0].sum(), leaves)
+
+
+@pytest.mark.parametrize("dtype,T,heads,D", [(BF, 200, (4, 1), 64), (BF, 1100, (16, 16), 128), (F32, 90, (4, 4), 128)])
+def test_autograd_in_a_graph(dtype, T, heads, D):
+    args = make(T, *heads, D, dtype, seed=48)
+    q, k, v, do = args
+    want = check(*args, [0, T], packed=False)
+    leaves = [x.clone().requires_grad_() for x in (q, k, v)]
+
+    def step():
+        o = g2.GDR2AttnFunction.apply(*leaves)
+        return (o.detach(), *torch.autograd.grad(o, leaves, do))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        for t in got:
+            t.fill_(3)
+        check(*args, [0, T], packed=False)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (want[0], want[3]["dq"], want[3]["dk"], want[3]["dv"])))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_padded_batch(dtype):
+    # sequences of one length, the last tokens of some of them padding with gradients of zero: what comes before does not
+    # depend on it, and neither does it get or give a gradient through it
+    T, lens = 90, [90, 33, 64, 1]
+    q, k, v, do = (x.view(4, T, -1, 64) for x in make(4 * T, 4, 2, 64, dtype, seed=49))
+    keep = torch.arange(T, device="cuda")[None, :] < ints(lens)[:, None]
+    do = do * keep[:, :, None, None]
+    run = lambda *x: (lambda o, lse, rest: (o, g2.gdr2_attn_bwd(*x, o, lse, do, rest=rest)))(*g2.gdr2_attn_fwd(*x, save_for_bwd=True))
+    o, gr = run(q, k, v)
+    other = [torch.where(keep[:, :, None, None], x, 3.0 * x.roll(1, 1)) for x in (q, k, v)]
+    o2, gr2 = run(*other)
+    assert torch.equal(o[keep], o2[keep])
+    for n in gr:
+        assert torch.equal(gr[n][keep], gr2[n][keep]) and not gr[n][~keep].any() and not gr2[n][~keep].any()
